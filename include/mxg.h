@@ -366,6 +366,172 @@ mxg_status_t mxg_dequantize(mxg_format_t fmt, mxg_qlayout_t layout, const void* 
                             const uint8_t* sf, const float* outer, int64_t rows, int64_t cols,
                             void* out, mxg_out_t out_type, mxg_stream_t stream);
 
+/* ------------------------------------------------------------------------- */
+/* 16-bit operators of an expert block: the grouped products on bf16 or fp16 */
+/* tensors, the norms around the block with its gate and residual, and the   */
+/* clipping of the gradients.                                                */
+/* ------------------------------------------------------------------------- */
+
+typedef enum { MXG_F32 = 0, MXG_BF16 = 1, MXG_F16 = 2 } mxg_dtype_t;
+
+/* Grouped products on 16-bit operands as they are: no quantization, no
+ * transposed copies.  in_type is MXG_BF16 or MXG_F16 (A and B alike).  Group g
+ * owns rows off_g .. off_g + M_g - 1 of the ragged matrices; sizes of any
+ * value >= 0 (a workspace of either offsets entry point).
+ *   MXG_FPROP_TN : A = X [M_cap, K], B = W [G, N, K], C [M_cap, N]:
+ *     C[off_g+i, n] = alpha_g sum_k A[off_g+i, k] B[g, n, k] + beta_g C[off_g+i, n]
+ *   MXG_DGRAD_NN : A = dY [M_cap, N], B = W [G, N, K], C = dX [M_cap, K]:
+ *     C[off_g+i, k] = alpha_g sum_n A[off_g+i, n] B[g, n, k] + beta_g C[off_g+i, k]
+ *   MXG_WGRAD_NT : A = dY [M_cap, N], B = X [M_cap, K], C = dW [G, N, K]:
+ *     C[g, n, k] = alpha_g sum_{i in g} A[off_g+i, n] B[off_g+i, k] + beta_g C[g, n, k]
+ *     (an empty group writes beta_g C[g], or zeros).
+ * Sums are FP32; the result is rounded once, to out_type: MXG_F32 or in_type.
+ * G, N, K >= 1 of any value; G <= 1024; M_cap >= 0 (with 0 the pointers of
+ * the ragged matrices may be NULL).
+ * lda, ldb, ldc : elements from one row to the next, 0 for dense rows; W and
+ *             dW hold N rows per expert without a gap (expert stride N * ld).
+ * A, B      : 16-byte aligned, lda and ldb multiples of 8 (so dense operands
+ *             need N and K that are).  C: aligned to its element, any ldc.
+ * alpha, beta : device float[G] or NULL (1 and 0).  C is read only where
+ *             beta_g is not 0.
+ * Rows of the ragged operands at or beyond the live count take no part, and
+ * rows of a ragged C there are not written; a NaN or infinity in one group's
+ * rows reaches no other group.  Negative sizes count as 0 and rows past M_cap
+ * are dropped, each recorded in dev_status.
+ * Errors: INVALID_ARG (nulls, sizes, types, a leading dimension below its row),
+ * ALIGNMENT, UNSUPPORTED_ARCH, LAUNCH. */
+mxg_status_t mxg_grouped_gemm_16bit(mxg_dtype_t in_type, mxg_gemm_mode_t mode, const void* A,
+                                    int64_t lda, const void* B, int64_t ldb,
+                                    const int64_t* group_ws, int G, int64_t M_cap, int64_t N,
+                                    int64_t K, const float* alpha, const float* beta, void* C,
+                                    int64_t ldc, mxg_dtype_t out_type, int32_t* dev_status,
+                                    mxg_stream_t stream);
+
+/* How a block's gate is laid out. */
+typedef enum {
+  MXG_GATE_NONE = 0, /* no gate                                                */
+  MXG_GATE_ROW = 1,  /* float [rows]: one per token (a router's weight)        */
+  MXG_GATE_COL = 2,  /* dtype [cols]: one per channel                          */
+  MXG_GATE_FULL = 3  /* dtype [rows, cols]                                     */
+} mxg_gate_t;
+
+/* The norms after and before a residual block in one pass:
+ *   after  : x' = x + res_scale * gate . (y * ry . w_post)
+ *   before : n  = x' * rx . w_pre
+ * with ry = 1 / sqrt(mean(y^2) + eps) over the row's cols, and rx likewise of
+ * x'.  Without y there is no "after" part (x' = x); without n_out no "before".
+ *   dtype     : type of y, n_out, the weights and the COL / FULL gate
+ *   res_dtype : type of the residual stream x, x_out: dtype or MXG_F32
+ *   ld*       : elements between rows, 0 for cols
+ *   w_post, w_pre : [cols], or NULL for ones
+ *   x_out     : required with y; may be x itself (with the same ld)
+ * n is formed from x' before x' is rounded.  1 <= cols <= 16384, rows >= 0
+ * (0 launches nothing; the [rows, cols] pointers may then be NULL), eps > 0.  Sums are FP32.  Any element alignment; rows
+ * that start on 16 bytes with cols a multiple of 8 take 16-byte accesses. */
+typedef struct {
+  mxg_dtype_t dtype, res_dtype;
+  int64_t rows, cols;
+  const void* x;
+  int64_t ldx;
+  const void* y;
+  int64_t ldy;
+  const void* w_post;
+  const void* gate;
+  int64_t ldg;
+  mxg_gate_t gate_mode;
+  float res_scale;
+  void* x_out;
+  int64_t ldxo;
+  const void* w_pre;
+  void* n_out;
+  int64_t ldn;
+  float eps;
+} mxg_block_norm_t;
+
+/* Errors: INVALID_ARG (nulls, sizes, types, eps, a leading dimension below
+ * cols, neither y nor n_out), ALIGNMENT (a pointer not aligned to its
+ * element), UNSUPPORTED_ARCH, LAUNCH. */
+mxg_status_t mxg_block_norm(const mxg_block_norm_t* desc, mxg_stream_t stream);
+
+/* The gradients of mxg_block_norm.  x is the block's output x' as
+ * mxg_block_norm stored it (x itself without y); dx_out is the gradient with
+ * respect to x' (NULL: zero), dn the one with respect to n (NULL: no "before"
+ * part); at least one of them is given.
+ *   dx [rows, cols] of res_dtype : gradient of x; may be dx_out itself
+ *   dy [rows, cols] of dtype     : gradient of y, required with y; may be y or dn
+ *   dw_post, dw_pre : float [cols] or NULL
+ *   dgate : float [rows] (ROW), float [cols] (COL), dtype [rows, cols] (FULL,
+ *           ld lddg), or NULL.  The sums over rows have a fixed order.
+ * x may be NULL without dn.  rows = 0 writes zeros to dw_post, dw_pre and a COL
+ * dgate. */
+typedef struct {
+  mxg_dtype_t dtype, res_dtype;
+  int64_t rows, cols;
+  const void* x;
+  int64_t ldx;
+  const void* y;
+  int64_t ldy;
+  const void* w_post;
+  const void* gate;
+  int64_t ldg;
+  mxg_gate_t gate_mode;
+  float res_scale;
+  const void* w_pre;
+  float eps;
+  const void* dx_out;
+  int64_t lddxo;
+  const void* dn;
+  int64_t lddn;
+  void* dx;
+  int64_t lddx;
+  void* dy;
+  int64_t lddy;
+  float* dw_post;
+  float* dw_pre;
+  void* dgate;
+  int64_t lddg;
+} mxg_block_norm_grad_t;
+
+/* Bytes of the backward workspace (0 if rows < 0 or cols < 1); 16-byte aligned
+ * device memory whose contents mean nothing before or after the call. */
+size_t mxg_block_norm_workspace_bytes(int64_t rows, int64_t cols);
+
+/* Errors: as mxg_block_norm, plus WORKSPACE_TOO_SMALL. */
+mxg_status_t mxg_block_norm_backward(const mxg_block_norm_grad_t* desc, void* workspace,
+                                     size_t workspace_bytes, mxg_stream_t stream);
+
+/* One gradient of a list: numel elements of src_type at src and, for clipping,
+ * of dst_type at dst (src itself is allowed with the same type; dst otherwise
+ * overlaps no src of the list). */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t numel;
+  mxg_dtype_t src_type, dst_type;
+} mxg_grad_t;
+
+/* Bytes of the workspace of the two calls below (16-byte aligned device
+ * memory, contents meaningless before and after). */
+size_t mxg_grad_workspace_bytes(void);
+
+/* norm[0] = sqrt(sum over the list of g^2): the L2 norm of all gradients as
+ * one vector.  `grads` is a HOST array, read before the call returns; n = 0 or
+ * empty tensors give 0.  Squares are summed in FP32 over short runs and in
+ * FP64 from there on, in a fixed order; magnitudes anywhere in FP32's range
+ * neither overflow nor vanish on the way (the norm itself can pass FP32's).
+ * Errors: INVALID_ARG (nulls, n < 0, numel < 0 or > 2^40, types), ALIGNMENT
+ * (a tensor not aligned to its element, workspace), WORKSPACE_TOO_SMALL,
+ * UNSUPPORTED_ARCH, LAUNCH. */
+mxg_status_t mxg_grad_norm(const mxg_grad_t* grads, int n, float* norm, void* workspace,
+                           size_t workspace_bytes, mxg_stream_t stream);
+
+/* The same norm, and dst = src * min(1, max_norm / (norm + 1e-6)) for every
+ * tensor.  max_norm >= 0 (infinity allowed: nothing is clipped).  An infinite
+ * gradient gives factor 0 (and NaN where 0 meets the infinity), a NaN makes
+ * every output NaN.  Errors: as mxg_grad_norm. */
+mxg_status_t mxg_grad_clip(const mxg_grad_t* grads, int n, float max_norm, float* norm,
+                           void* workspace, size_t workspace_bytes, mxg_stream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* mxg_status_string(mxg_status_t status);
 

@@ -2,6 +2,7 @@
 // device checks and kernel dispatch.  Host code only; no allocation, no
 // synchronisation.
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "mxg_device.cuh"
@@ -34,6 +35,19 @@ cudaError_t launch_grouped_gemm(bool nvfp4, int mode, const void* a_data, const 
                                 int64_t b_ld_bytes, cudaStream_t stream);
 cudaError_t launch_wgrad_no_rows(int G, int64_t N, int64_t K, const float* beta, void* C,
                                  int out_bf16, int num_sms, cudaStream_t stream);
+cudaError_t launch_grouped_gemm16(int in_f16, int mode, const void* A, int64_t lda, const void* B,
+                                  int64_t ldb, const int64_t* group_ws, int G, int64_t M_cap,
+                                  int64_t N, int64_t K, const float* alpha, const float* beta,
+                                  void* C, int64_t ldc, int out_type, int32_t* status, int num_sms,
+                                  cudaStream_t stream);
+int64_t block_norm_ws_bytes(int64_t rows, int64_t cols);
+cudaError_t launch_block_norm(const mxg_block_norm_t& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_block_norm_backward(const mxg_block_norm_grad_t& p, float* ws, int num_sms,
+                                       cudaStream_t stream);
+size_t grad_ws_bytes();
+cudaError_t launch_grad_clip(const mxg_grad_t* grads, int n, bool clip, float max_norm,
+                             float* norm, void* ws, int num_sms, cudaStream_t stream,
+                             int* launches);
 constexpr uint64_t kDefaultWaitNs = 1000000000ull;
 }  // namespace mxg
 
@@ -107,6 +121,73 @@ mxg_status_t operand_shape(const mxg_operand_t* op, int64_t rows, int64_t cols, 
   if (bytes % 16 != 0) return MXG_ERR_ALIGNMENT;
   *ld_bytes = bytes;
   return MXG_OK;
+}
+
+// Bytes of an element, or 0 for a value that is no mxg_dtype_t.
+size_t dtype_bytes(mxg_dtype_t t) {
+  return t == MXG_F32 ? 4 : (t == MXG_BF16 || t == MXG_F16 ? 2 : 0);
+}
+
+bool aligned_to(const void* p, size_t bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
+// The fields that the norms around a block share, in both directions.
+// Fills in the dense leading dimensions.
+template <typename Desc>
+mxg_status_t norm_common(Desc& d) {
+  const size_t e = dtype_bytes(d.dtype), r = dtype_bytes(d.res_dtype);
+  if (e == 0 || r == 0 || (d.res_dtype != d.dtype && d.res_dtype != MXG_F32))
+    return MXG_ERR_INVALID_ARG;
+  if (d.rows < 0 || d.rows > kMaxRows || d.cols < 1 || d.cols > 16384) return MXG_ERR_INVALID_ARG;
+  if (!(d.eps > 0.0f) || std::isinf(d.eps) || !std::isfinite(d.res_scale))
+    return MXG_ERR_INVALID_ARG;
+  if (d.gate_mode < MXG_GATE_NONE || d.gate_mode > MXG_GATE_FULL) return MXG_ERR_INVALID_ARG;
+  if (d.gate_mode != MXG_GATE_NONE && d.rows != 0 && (d.gate == nullptr || d.y == nullptr))
+    return MXG_ERR_INVALID_ARG;
+  // the gradient of a COL gate's row sums reads the gate even without rows
+  if (d.gate_mode == MXG_GATE_COL && d.gate == nullptr) return MXG_ERR_INVALID_ARG;
+  if (d.ldx == 0) d.ldx = d.cols;
+  if (d.ldy == 0) d.ldy = d.cols;
+  if (d.ldg == 0) d.ldg = d.cols;
+  if (d.ldx < d.cols || d.ldy < d.cols || d.ldg < d.cols) return MXG_ERR_INVALID_ARG;
+  const size_t gate_bytes = d.gate_mode == MXG_GATE_ROW ? 4 : e;
+  if (!aligned_to(d.x, r) || !aligned_to(d.y, e) || !aligned_to(d.w_post, e) ||
+      !aligned_to(d.w_pre, e) || !aligned_to(d.gate, gate_bytes))
+    return MXG_ERR_ALIGNMENT;
+  return MXG_OK;
+}
+
+mxg_status_t grad_args(const mxg_grad_t* grads, int n, bool clip, const float* norm,
+                       const void* workspace, size_t workspace_bytes) {
+  if (n < 0 || (n > 0 && grads == nullptr) || norm == nullptr || workspace == nullptr)
+    return MXG_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i) {
+    const mxg_grad_t& t = grads[i];
+    const size_t se = dtype_bytes(t.src_type), de = dtype_bytes(t.dst_type);
+    if (se == 0 || t.numel < 0 || t.numel > (1LL << 40) || (t.numel > 0 && t.src == nullptr))
+      return MXG_ERR_INVALID_ARG;
+    if (clip && (de == 0 || (t.numel > 0 && t.dst == nullptr) ||
+                 (t.dst == t.src && t.numel > 0 && t.dst_type != t.src_type)))
+      return MXG_ERR_INVALID_ARG;
+    if (!aligned_to(t.src, se) || (clip && !aligned_to(t.dst, de))) return MXG_ERR_ALIGNMENT;
+  }
+  if (!aligned_to(norm, 4) || !aligned16(workspace)) return MXG_ERR_ALIGNMENT;
+  if (workspace_bytes < mxg::grad_ws_bytes()) return MXG_ERR_WORKSPACE_TOO_SMALL;
+  return MXG_OK;
+}
+
+mxg_status_t grad_impl(const mxg_grad_t* grads, int n, bool clip, float max_norm, float* norm,
+                       void* workspace, size_t workspace_bytes, mxg_stream_t stream) {
+  mxg_status_t st = grad_args(grads, n, clip, norm, workspace, workspace_bytes);
+  if (st != MXG_OK) return st;
+  int sms = 0;
+  if ((st = current_device(&sms)) != MXG_OK) return st;
+  int launches = 0;
+  const cudaError_t e =
+      mxg::launch_grad_clip(grads, n, clip, max_norm, norm, workspace, sms,
+                            reinterpret_cast<cudaStream_t>(stream), &launches);
+  return launched(e, static_cast<uint64_t>(launches));
 }
 
 }  // namespace
@@ -370,6 +451,120 @@ mxg_status_t mxg_dequantize(mxg_format_t fmt, mxg_qlayout_t layout, const void* 
                                          out_type == MXG_OUT_BF16 ? 1 : 0, sms,
                                          reinterpret_cast<cudaStream_t>(stream)),
                   1);
+}
+
+mxg_status_t mxg_grouped_gemm_16bit(mxg_dtype_t in_type, mxg_gemm_mode_t mode, const void* A,
+                                    int64_t lda, const void* B, int64_t ldb,
+                                    const int64_t* group_ws, int G, int64_t M_cap, int64_t N,
+                                    int64_t K, const float* alpha, const float* beta, void* C,
+                                    int64_t ldc, mxg_dtype_t out_type, int32_t* dev_status,
+                                    mxg_stream_t stream) {
+  const bool wgrad = mode == MXG_WGRAD_NT;
+  // a ragged matrix without rows (M_cap = 0) needs no memory
+  if ((A == nullptr && M_cap != 0) || (B == nullptr && !(wgrad && M_cap == 0)) ||
+      (C == nullptr && !(!wgrad && M_cap == 0)) || group_ws == nullptr || G < 1 || G > 1024)
+    return MXG_ERR_INVALID_ARG;
+  if ((in_type != MXG_BF16 && in_type != MXG_F16) || (out_type != MXG_F32 && out_type != in_type))
+    return MXG_ERR_INVALID_ARG;
+  if (mode != MXG_FPROP_TN && mode != MXG_WGRAD_NT && mode != MXG_DGRAD_NN)
+    return MXG_ERR_INVALID_ARG;
+  if (M_cap < 0 || N < 1 || K < 1 || M_cap > kMaxRows || N > kMaxRows || K > kMaxRows)
+    return MXG_ERR_INVALID_ARG;
+  const int64_t a_cols = mode == MXG_FPROP_TN ? K : N;
+  const int64_t c_cols = mode == MXG_FPROP_TN ? N : K;
+  if (lda == 0) lda = a_cols;
+  if (ldb == 0) ldb = K;
+  if (ldc == 0) ldc = c_cols;
+  // a row stride past 2^36 elements would leave the tensor maps' range
+  constexpr int64_t kMaxLd = 1LL << 36;
+  if (lda < a_cols || ldb < K || ldc < c_cols || lda > kMaxLd || ldb > kMaxLd || ldc > kMaxLd ||
+      N > (1LL << 38) / ldb)
+    return MXG_ERR_INVALID_ARG;
+  if (!aligned16(A) || !aligned16(B) || lda % 8 != 0 || ldb % 8 != 0 ||
+      !aligned_to(C, dtype_bytes(out_type)))
+    return MXG_ERR_ALIGNMENT;
+  int sms = 0;
+  const mxg_status_t st = current_device(&sms);
+  if (st != MXG_OK) return st;
+  if (M_cap == 0 && !wgrad) return MXG_OK;
+  return launched(mxg::launch_grouped_gemm16(
+                      in_type == MXG_F16 ? 1 : 0,
+                      mode == MXG_WGRAD_NT ? 1 : (mode == MXG_DGRAD_NN ? 2 : 0), A, lda, B, ldb,
+                      group_ws, G, M_cap, N, K, alpha, beta, C, ldc, out_type, dev_status, sms,
+                      reinterpret_cast<cudaStream_t>(stream)),
+                  1);
+}
+
+mxg_status_t mxg_block_norm(const mxg_block_norm_t* desc, mxg_stream_t stream) {
+  if (desc == nullptr) return MXG_ERR_INVALID_ARG;
+  mxg_block_norm_t d = *desc;
+  if (d.rows != 0 && (d.x == nullptr || (d.y == nullptr && d.n_out == nullptr) ||
+                      (d.y != nullptr && d.x_out == nullptr)))
+    return MXG_ERR_INVALID_ARG;
+  mxg_status_t st = norm_common(d);
+  if (st == MXG_ERR_INVALID_ARG) return st;
+  if (d.ldxo == 0) d.ldxo = d.cols;
+  if (d.ldn == 0) d.ldn = d.cols;
+  if (d.ldxo < d.cols || d.ldn < d.cols || (d.x_out == d.x && d.x != nullptr && d.ldxo != d.ldx))
+    return MXG_ERR_INVALID_ARG;
+  if (st != MXG_OK) return st;
+  if (!aligned_to(d.x_out, dtype_bytes(d.res_dtype)) || !aligned_to(d.n_out, dtype_bytes(d.dtype)))
+    return MXG_ERR_ALIGNMENT;
+  int sms = 0;
+  if ((st = current_device(&sms)) != MXG_OK) return st;
+  if (d.rows == 0) return MXG_OK;
+  return launched(mxg::launch_block_norm(d, sms, reinterpret_cast<cudaStream_t>(stream)), 1);
+}
+
+size_t mxg_block_norm_workspace_bytes(int64_t rows, int64_t cols) {
+  return rows < 0 || cols < 1 ? 0 : static_cast<size_t>(mxg::block_norm_ws_bytes(rows, cols));
+}
+
+mxg_status_t mxg_block_norm_backward(const mxg_block_norm_grad_t* desc, void* workspace,
+                                     size_t workspace_bytes, mxg_stream_t stream) {
+  if (desc == nullptr) return MXG_ERR_INVALID_ARG;
+  mxg_block_norm_grad_t d = *desc;
+  if (d.rows != 0 && (d.dx == nullptr || (d.dx_out == nullptr && d.dn == nullptr) ||
+                      (d.dn != nullptr && d.x == nullptr) || (d.y != nullptr && d.dy == nullptr)))
+    return MXG_ERR_INVALID_ARG;
+  mxg_status_t st = norm_common(d);
+  if (st == MXG_ERR_INVALID_ARG) return st;
+  if (d.lddxo == 0) d.lddxo = d.cols;
+  if (d.lddn == 0) d.lddn = d.cols;
+  if (d.lddx == 0) d.lddx = d.cols;
+  if (d.lddy == 0) d.lddy = d.cols;
+  if (d.lddg == 0) d.lddg = d.cols;
+  if (d.lddxo < d.cols || d.lddn < d.cols || d.lddx < d.cols || d.lddy < d.cols ||
+      d.lddg < d.cols || (d.dx == d.dx_out && d.dx != nullptr && d.lddx != d.lddxo) ||
+      (d.y != nullptr && ((d.dy == d.y && d.lddy != d.ldy) || (d.dy == d.dn && d.lddy != d.lddn))))
+    return MXG_ERR_INVALID_ARG;
+  if (st != MXG_OK) return st;
+  const size_t e = dtype_bytes(d.dtype), r = dtype_bytes(d.res_dtype);
+  if (!aligned_to(d.dx_out, r) || !aligned_to(d.dx, r) || !aligned_to(d.dn, e) ||
+      !aligned_to(d.dy, e) || !aligned_to(d.dw_post, 4) || !aligned_to(d.dw_pre, 4) ||
+      !aligned_to(d.dgate, d.gate_mode == MXG_GATE_FULL ? e : 4) || !aligned16(workspace))
+    return MXG_ERR_ALIGNMENT;
+  const size_t need = mxg_block_norm_workspace_bytes(d.rows, d.cols);
+  if (workspace_bytes < need) return MXG_ERR_WORKSPACE_TOO_SMALL;
+  if (need > 0 && workspace == nullptr) return MXG_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = current_device(&sms)) != MXG_OK) return st;
+  return launched(mxg::launch_block_norm_backward(d, static_cast<float*>(workspace), sms,
+                                                  reinterpret_cast<cudaStream_t>(stream)),
+                  d.rows > 0 ? 2 : 1);
+}
+
+size_t mxg_grad_workspace_bytes(void) { return mxg::grad_ws_bytes(); }
+
+mxg_status_t mxg_grad_norm(const mxg_grad_t* grads, int n, float* norm, void* workspace,
+                           size_t workspace_bytes, mxg_stream_t stream) {
+  return grad_impl(grads, n, false, 0.0f, norm, workspace, workspace_bytes, stream);
+}
+
+mxg_status_t mxg_grad_clip(const mxg_grad_t* grads, int n, float max_norm, float* norm,
+                           void* workspace, size_t workspace_bytes, mxg_stream_t stream) {
+  if (!(max_norm >= 0.0f)) return MXG_ERR_INVALID_ARG;
+  return grad_impl(grads, n, true, max_norm, norm, workspace, workspace_bytes, stream);
 }
 
 const char* mxg_status_string(mxg_status_t status) {

@@ -27,6 +27,8 @@ MXG_MXFP8_E4M3, MXG_NVFP4_ROWSCALED = 1, 2
 MXG_ROWWISE, MXG_COLWISE, MXG_BOTH = 1, 2, 3
 MXG_FPROP_TN, MXG_WGRAD_NT, MXG_DGRAD_NN = 0, 1, 2
 MXG_OUT_F32, MXG_OUT_BF16 = 0, 1
+MXG_F32, MXG_BF16, MXG_F16 = 0, 1, 2
+MXG_GATE_NONE, MXG_GATE_ROW, MXG_GATE_COL, MXG_GATE_FULL = 0, 1, 2, 3
 MXG_DEV_NEG_SIZE, MXG_DEV_MISALIGNED, MXG_DEV_SUM_OVER_CAPACITY = 1, 2, 4
 MXG_DEV_BOUNDS, MXG_DEV_TIMEOUT = 8, 16
 STATUS_NAMES = {0: "MXG_OK", 1: "MXG_ERR_INVALID_ARG", 2: "MXG_ERR_ALIGNMENT",
@@ -44,6 +46,37 @@ class Operand(ctypes.Structure):
     """mxg_operand_t"""
     _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("outer", ctypes.c_void_p),
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld", ctypes.c_int64)]
+
+
+class BlockNorm(ctypes.Structure):
+    """mxg_block_norm_t"""
+    _fields_ = [("dtype", ctypes.c_int), ("res_dtype", ctypes.c_int), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("w_post", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("gate_mode", ctypes.c_int),
+                ("res_scale", ctypes.c_float), ("x_out", ctypes.c_void_p),
+                ("ldxo", ctypes.c_int64), ("w_pre", ctypes.c_void_p), ("n_out", ctypes.c_void_p),
+                ("ldn", ctypes.c_int64), ("eps", ctypes.c_float)]
+
+
+class BlockNormGrad(ctypes.Structure):
+    """mxg_block_norm_grad_t"""
+    _fields_ = [("dtype", ctypes.c_int), ("res_dtype", ctypes.c_int), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("w_post", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("gate_mode", ctypes.c_int),
+                ("res_scale", ctypes.c_float), ("w_pre", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("dx_out", ctypes.c_void_p), ("lddxo", ctypes.c_int64),
+                ("dn", ctypes.c_void_p), ("lddn", ctypes.c_int64), ("dx", ctypes.c_void_p),
+                ("lddx", ctypes.c_int64), ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+                ("dw_post", ctypes.c_void_p), ("dw_pre", ctypes.c_void_p),
+                ("dgate", ctypes.c_void_p), ("lddg", ctypes.c_int64)]
+
+
+class Grad(ctypes.Structure):
+    """mxg_grad_t"""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("src_type", ctypes.c_int), ("dst_type", ctypes.c_int)]
 
 
 def _operand(T, elems_per_byte: int) -> Operand:
@@ -106,6 +139,21 @@ def load() -> ctypes.CDLL:
         L.mxg_grouped_gemm_unaligned.argtypes = [c_int, ctypes.POINTER(Operand),
                                                  ctypes.POINTER(Operand), vp, c_int, i64, i64, i64,
                                                  vp, vp, vp, vp, c_int, vp, vp]
+        L.mxg_grouped_gemm_16bit.restype = c_int
+        L.mxg_grouped_gemm_16bit.argtypes = [c_int, c_int, vp, i64, vp, i64, vp, c_int, i64, i64,
+                                             i64, vp, vp, vp, i64, c_int, vp, vp]
+        L.mxg_block_norm.restype = c_int
+        L.mxg_block_norm.argtypes = [ctypes.POINTER(BlockNorm), vp]
+        L.mxg_block_norm_workspace_bytes.restype = sz
+        L.mxg_block_norm_workspace_bytes.argtypes = [i64, i64]
+        L.mxg_block_norm_backward.restype = c_int
+        L.mxg_block_norm_backward.argtypes = [ctypes.POINTER(BlockNormGrad), vp, sz, vp]
+        L.mxg_grad_workspace_bytes.restype = sz
+        L.mxg_grad_workspace_bytes.argtypes = []
+        L.mxg_grad_norm.restype = c_int
+        L.mxg_grad_norm.argtypes = [vp, c_int, vp, vp, sz, vp]
+        L.mxg_grad_clip.restype = c_int
+        L.mxg_grad_clip.argtypes = [vp, c_int, ctypes.c_float, vp, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -238,6 +286,168 @@ def mxg_grouped_gemm_unaligned(mode: int, A: tuple, B: tuple, group_ws: torch.Te
                                              out_type, _p(dev_status), _s(stream)))
 
 
+# ------------------------------------------------ 16-bit operators of an expert block
+_DTYPES = {torch.float32: MXG_F32, torch.bfloat16: MXG_BF16, torch.float16: MXG_F16}
+
+
+def _ld(t) -> int:
+    """Elements between the rows of a matrix whose rows are contiguous."""
+    if t is None or t.dim() < 2:
+        return 0
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("rows must be contiguous (stride %d between their elements)" % t.stride(-1))
+    # the stride of a dimension of size 1 says nothing
+    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
+
+
+def _ld_experts(t) -> int:
+    """The same for [G, N, K] whose experts follow one another without a gap."""
+    ld = _ld(t)
+    if t.dim() == 3 and t.shape[0] > 1 and t.stride(0) != t.shape[1] * ld:
+        raise ValueError("experts must lie one after the other (stride %d, want %d)"
+                         % (t.stride(0), t.shape[1] * ld))
+    return ld
+
+
+def mxg_grouped_gemm_16bit(mode: int, A: torch.Tensor, B: torch.Tensor, group_ws: torch.Tensor,
+                           G: int, M_cap: int, N: int, K: int, alpha=None, beta=None,
+                           C: torch.Tensor = None, dev_status=None, stream=None) -> None:
+    """A, B: bf16 or fp16 device tensors (rows may be strided; weights [G, N, K]
+    or [G*N, K]); C: fp32 or the operands' type."""
+    if (A.dtype != B.dtype or A.dtype not in (torch.bfloat16, torch.float16)
+            or C.dtype not in _DTYPES):
+        raise ValueError("operands of one 16-bit type, C of that or fp32: got %s, %s, %s"
+                         % (A.dtype, B.dtype, C.dtype))
+    assert group_ws.dtype == torch.int64
+    _check("mxg_grouped_gemm_16bit",
+           load().mxg_grouped_gemm_16bit(_DTYPES[A.dtype], mode, _p(A), _ld(A), _p(B),
+                                         _ld_experts(B), _p(group_ws), G, M_cap, N, K, _p(alpha),
+                                         _p(beta), _p(C), _ld_experts(C), _DTYPES[C.dtype],
+                                         _p(dev_status), _s(stream)))
+
+
+def _norm_types(x, others, f32) -> tuple:
+    """(dtype, res_dtype) of the norms around a block; x is of the residual stream."""
+    kinds = {t.dtype for t in others if t is not None}
+    if len(kinds) != 1 or not kinds <= set(_DTYPES) or x.dtype not in _DTYPES:
+        raise ValueError("y, n, the weights and the gate have one type: got %s" % kinds)
+    if any(t is not None and t.dtype != torch.float32 for t in f32):
+        raise ValueError("the ROW gate and the gradients of broadcast inputs are fp32")
+    return _DTYPES[kinds.pop()], _DTYPES[x.dtype]
+
+
+def _rows_of(x, others) -> None:
+    if any(t is not None and t.shape != x.shape for t in others):
+        raise ValueError("the [rows, cols] tensors differ in shape: %s"
+                         % [tuple(t.shape) for t in others if t is not None])
+
+
+def _cols_of(cols, others) -> None:
+    if any(t is not None and (t.numel() != cols or not t.is_contiguous()) for t in others):
+        raise ValueError("the weights are contiguous vectors of %d" % cols)
+
+
+def _gate_of(gate, gate_mode, rows, cols) -> None:
+    want = {MXG_GATE_ROW: rows, MXG_GATE_COL: cols, MXG_GATE_FULL: rows * cols}.get(gate_mode)
+    if gate is not None and (gate.numel() != want or
+                             (gate_mode != MXG_GATE_FULL and not gate.is_contiguous())):
+        raise ValueError("a gate (or its gradient) of mode %d has %s elements" % (gate_mode, want))
+
+
+def mxg_block_norm(x: torch.Tensor, y=None, w_post=None, gate=None, gate_mode: int = MXG_GATE_NONE,
+                   res_scale: float = 1.0, x_out=None, w_pre=None, n_out=None, eps: float = 1e-6,
+                   stream=None) -> None:
+    """x, y, x_out, n_out: [rows, cols] (rows may be strided)."""
+    rows, cols = x.shape
+    row = gate_mode == MXG_GATE_ROW
+    dtype, res = _norm_types(x, (y, n_out, w_post, w_pre, None if row else gate),
+                             (gate if row else None,))
+    _rows_of(x, (y, x_out, n_out))
+    _cols_of(cols, (w_post, w_pre))
+    _gate_of(gate, gate_mode, rows, cols)
+    if x_out is not None and x_out.dtype != x.dtype:
+        raise ValueError("x and x_out have one type")
+    d = BlockNorm(dtype, res, rows, cols, _p(x), _ld(x), _p(y), _ld(y), _p(w_post), _p(gate),
+                  _ld(gate), gate_mode, res_scale, _p(x_out), _ld(x_out), _p(w_pre), _p(n_out),
+                  _ld(n_out), eps)
+    _check("mxg_block_norm", load().mxg_block_norm(ctypes.byref(d), _s(stream)))
+
+
+def mxg_block_norm_workspace_bytes(rows: int, cols: int) -> int:
+    return load().mxg_block_norm_workspace_bytes(rows, cols)
+
+
+def mxg_block_norm_backward(x: torch.Tensor, y=None, w_post=None, gate=None,
+                            gate_mode: int = MXG_GATE_NONE, res_scale: float = 1.0, w_pre=None,
+                            eps: float = 1e-6, dx_out=None, dn=None, dx=None, dy=None,
+                            dw_post=None, dw_pre=None, dgate=None, workspace=None,
+                            stream=None) -> None:
+    """x: the block's output as mxg_block_norm stored it (x_out)."""
+    rows, cols = x.shape
+    row, full = gate_mode == MXG_GATE_ROW, gate_mode == MXG_GATE_FULL
+    dtype, res = _norm_types(x, (y, dn, dy, w_post, w_pre, None if row else gate,
+                                 dgate if full else None),
+                             (gate if row else None, None if full else dgate, dw_post, dw_pre))
+    _rows_of(x, (y, dx_out, dn, dx, dy))
+    _cols_of(cols, (w_post, w_pre, dw_post, dw_pre))
+    _gate_of(gate, gate_mode, rows, cols)
+    _gate_of(dgate, gate_mode, rows, cols)
+    if any(t is not None and t.dtype != x.dtype for t in (dx_out, dx)):
+        raise ValueError("x, dx_out and dx have one type")
+    d = BlockNormGrad(dtype, res, rows, cols, _p(x), _ld(x), _p(y), _ld(y), _p(w_post), _p(gate),
+                      _ld(gate), gate_mode, res_scale, _p(w_pre), eps, _p(dx_out), _ld(dx_out),
+                      _p(dn), _ld(dn), _p(dx), _ld(dx), _p(dy), _ld(dy), _p(dw_post), _p(dw_pre),
+                      _p(dgate), _ld(dgate))
+    _check("mxg_block_norm_backward",
+           load().mxg_block_norm_backward(ctypes.byref(d), _p(workspace),
+                                          0 if workspace is None else workspace.nbytes, _s(stream)))
+
+
+def mxg_grad_workspace_bytes() -> int:
+    return load().mxg_grad_workspace_bytes()
+
+
+class GradList:
+    """An array of mxg_grad_t over tensors that it keeps alive (grad_list)."""
+
+    def __init__(self, src, dst):
+        for t in (*src, *dst):
+            if not t.is_contiguous() or t.dtype not in _DTYPES:
+                raise ValueError("gradients are contiguous fp32, bf16 or fp16 tensors")
+        if len(src) != len(dst) or any(s.numel() != d.numel() for s, d in zip(src, dst)):
+            raise ValueError("one destination of the same size for each gradient")
+        self.tensors = (tuple(src), tuple(dst))
+        self.n = len(src)
+        self.array = (Grad * max(1, self.n))(*[
+            Grad(_p(s), _p(d), s.numel(), _DTYPES[s.dtype], _DTYPES[d.dtype])
+            for s, d in zip(src, dst)])
+        self.address = ctypes.addressof(self.array)
+
+
+def grad_list(src, dst=None) -> GradList:
+    """The list mxg_grad_norm and mxg_grad_clip take: gradients, and where their
+    clipped values go (default: in place).  It can be used again as long as the
+    gradients stay in the same tensors."""
+    src = list(src)
+    return GradList(src, src if dst is None else list(dst))
+
+
+def mxg_grad_norm(grads: GradList, norm: torch.Tensor, workspace: torch.Tensor,
+                  stream=None) -> None:
+    assert norm.dtype == torch.float32
+    _check("mxg_grad_norm",
+           load().mxg_grad_norm(grads.address, grads.n, _p(norm), _p(workspace),
+                                workspace.nbytes, _s(stream)))
+
+
+def mxg_grad_clip(grads: GradList, max_norm: float, norm: torch.Tensor, workspace: torch.Tensor,
+                  stream=None) -> None:
+    assert norm.dtype == torch.float32
+    _check("mxg_grad_clip",
+           load().mxg_grad_clip(grads.address, grads.n, max_norm, _p(norm), _p(workspace),
+                                workspace.nbytes, _s(stream)))
+
+
 def mxg_status_string(code: int) -> str:
     return load().mxg_status_string(code).decode()
 
@@ -293,3 +503,12 @@ def alloc_nvfp4(rows: int, cols: int, device="cuda", rowwise=True, colwise=False
         out["sf_col"] = torch.empty(rows * cols // 16, dtype=torch.uint8, device=device)
         out["outer_col"] = torch.empty((G, cols), dtype=torch.float32, device=device)
     return out
+
+
+def alloc_block_norm_workspace(rows: int, cols: int, device="cuda") -> torch.Tensor:
+    return torch.empty(max(16, mxg_block_norm_workspace_bytes(rows, cols)), dtype=torch.uint8,
+                       device=device)
+
+
+def alloc_grad_workspace(device="cuda") -> torch.Tensor:
+    return torch.empty(mxg_grad_workspace_bytes(), dtype=torch.uint8, device=device)
