@@ -186,8 +186,6 @@ namespace {
 
 constexpr int kSmallList = 64, kLargeList = 512;
 
-int64_t elem_bytes(int type) { return type == MXG_F32 ? 4 : 2; }
-
 // Fills one launch's list from grads[*next ...]; empty tensors are skipped.
 template <int CAP>
 void fill(GradList<CAP>& l, const mxg_grad_t* grads, int n, int* next) {
