@@ -338,7 +338,8 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
 
   // ------------------------------------------------------------ producers (both CTAs)
   if (warp == 0) {
-    if (lane == 0) {
+    {
+      const uint32_t leader = elect_leader();
       prefetch_tmap(&tmap_a);
       prefetch_tmap(&tmap_b);
       uint32_t stage = 0, phase = 0, issued = 0, parity = 0, tail_issued = 0, tail_parity = 0;
@@ -350,16 +351,17 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
         if (rank == 0) {
           // the unit's shape, for the MMA thread
           const int slot = static_cast<int>(n & 1), par = static_cast<int>((n >> 1) & 1);
-          if (!mbar_wait(info_empty_bar(slot), par ^ 1, abort_flag, p.status)) break;
-          info_word[slot] = static_cast<uint64_t>(static_cast<uint32_t>(kb_count)) |
-                            (static_cast<uint64_t>((last + 15) / 16) << 32) |
-                            (static_cast<uint64_t>(t.n_mma) << 40);
-          mbar_arrive(info_full_bar(slot));
+          if (!mbar_wait_warp(info_empty_bar(slot), par ^ 1, abort_flag, p.status)) break;
+          if (leader)
+            info_word[slot] = static_cast<uint64_t>(static_cast<uint32_t>(kb_count)) |
+                              (static_cast<uint64_t>((last + 15) / 16) << 32) |
+                              (static_cast<uint64_t>(t.n_mma) << 40);
+          mbar_arrive_if(info_full_bar(slot), leader);
         }
         const int32_t b_at = t.j0 + (t.n_mma / 2) * static_cast<int32_t>(rank);
         const int32_t a_at = t.i0 + 128 * static_cast<int32_t>(rank);
         for (int32_t kb = 0; kb < kb_count; ++kb) {
-          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status)) {
+          if (!mbar_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, p.status)) {
             ok = false;
             break;
           }
@@ -368,33 +370,33 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
           if (MODE == 1 && kb + 1 == kb_count && (last & 15) != 0) {
             // rows of the next group in the last MMA step: this CTA's bytes
             // land on its own barrier, and its mask warp passes them on
-            mbar_arrive_expect_tx(land_bar(stage), Cfg::kStageBytes);
+            mbar_arrive_expect_tx_if(land_bar(stage), Cfg::kStageBytes, leader);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              tma_load_2d(sa + 8192 * c, &tmap_a, land_bar(stage), a_at + 64 * c, t.row0 + k0);
-              tma_load_2d(sb + 8192 * c, &tmap_b, land_bar(stage), b_at + 64 * c, t.row0 + k0);
+              tma_load_2d_if(sa + 8192 * c, &tmap_a, land_bar(stage), a_at + 64 * c, t.row0 + k0, leader);
+              tma_load_2d_if(sb + 8192 * c, &tmap_b, land_bar(stage), b_at + 64 * c, t.row0 + k0, leader);
             }
             tail_issued |= 1u << stage;
             tail_parity ^= 1u << stage;
           } else {
-            if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * Cfg::kStageBytes);
+            if (rank == 0) mbar_arrive_expect_tx_if(full_bar(stage), 2 * Cfg::kStageBytes, leader);
             const uint32_t fb = mapa_shared(full_bar(stage), 0);
             if constexpr (A_MN) {
 #pragma unroll
               for (int c = 0; c < 2; ++c)
-                tma_load_2d_pair(sa + 8192 * c, &tmap_a, fb, a_at + 64 * c, t.row0 + k0);
+                tma_load_2d_pair_if(sa + 8192 * c, &tmap_a, fb, a_at + 64 * c, t.row0 + k0, leader);
             } else {
-              tma_load_2d_pair(sa, &tmap_a, fb, k0, t.row0 + a_at);
+              tma_load_2d_pair_if(sa, &tmap_a, fb, k0, t.row0 + a_at, leader);
             }
             if constexpr (MODE == 0) {
-              tma_load_3d_pair(sb, &tmap_b, fb, k0, b_at, t.g);
+              tma_load_3d_pair_if(sb, &tmap_b, fb, k0, b_at, t.g, leader);
             } else {
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
                 if constexpr (MODE == 2)
-                  tma_load_3d_pair(sb + 8192 * c, &tmap_b, fb, b_at + 64 * c, k0, t.g);
+                  tma_load_3d_pair_if(sb + 8192 * c, &tmap_b, fb, b_at + 64 * c, k0, t.g, leader);
                 else
-                  tma_load_2d_pair(sb + 8192 * c, &tmap_b, fb, b_at + 64 * c, t.row0 + k0);
+                  tma_load_2d_pair_if(sb + 8192 * c, &tmap_b, fb, b_at + 64 * c, t.row0 + k0, leader);
               }
             }
           }
@@ -416,26 +418,28 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
   }
   // ------------------------------------------------------------ MMA issuer (even CTA)
   else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const uint32_t leader = elect_leader();
       uint32_t stage = 0, phase = 0;
       bool ok = true;
       int64_t n = 0;
       for (int64_t u = unit0; ok && u < total; u += ustride, ++n) {
         const int slot = static_cast<int>(n & 1);
         const uint32_t par = static_cast<uint32_t>((n >> 1) & 1);
-        if (!mbar_wait(info_full_bar(slot), par, abort_flag, p.status)) break;
+        if (!mbar_wait_warp(info_full_bar(slot), par, abort_flag, p.status)) break;
         const uint64_t info = info_word[slot];
-        mbar_arrive(info_empty_bar(slot));
+        __syncwarp();  // every lane has read the word
+        mbar_arrive_if(info_empty_bar(slot), leader);
         const int32_t kb_count = static_cast<int32_t>(info & 0xFFFFFFFFu);
         const int last_mmas = static_cast<int>((info >> 32) & 0xFFu);
         const uint32_t n_mma = static_cast<uint32_t>(info >> 40);
         const uint32_t idesc = p.idesc | ((n_mma >> 3) << 17);
         // the accumulator's previous unit has been read out
-        if (!mbar_wait_cluster(tempty_bar(slot), par ^ 1u, abort_flag, p.status)) break;
+        if (!mbar_wait_warp<true>(tempty_bar(slot), par ^ 1u, abort_flag, p.status)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + 256u * slot;
         for (int32_t kb = 0; kb < kb_count; ++kb) {
-          if (!mbar_wait(full_bar(stage), phase, abort_flag, p.status)) {
+          if (!mbar_wait_warp(full_bar(stage), phase, abort_flag, p.status)) {
             ok = false;
             break;
           }
@@ -446,19 +450,20 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
 #pragma unroll
           for (int kk = 0; kk < Cfg::kMmas; ++kk) {
             if (kk >= nmma) break;
-            tc_mma_f16_pair(d, ad + kk * kStep16<A_MN>, bd + kk * kStep16<B_MN>, idesc,
-                            (kb > 0 || kk > 0) ? 1u : 0u);
+            tc_mma_f16_pair_if(d, ad + kk * kStep16<A_MN>, bd + kk * kStep16<B_MN>, idesc,
+                               (kb > 0 || kk > 0) ? 1u : 0u, leader);
           }
-          tc_commit_pair_mc(empty_bar(stage), 0x3);
+          tc_commit_pair_mc_if(empty_bar(stage), 0x3, leader);
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        tc_commit_pair_mc(tfull_bar(slot), 0x3);
+        tc_commit_pair_mc_if(tfull_bar(slot), 0x3, leader);
       }
-      tc_commit_pair(drain_bar);
+      if (leader) tc_commit_pair(drain_bar);
+      __syncwarp();
       drain16(drain_bar, 0, p.status);
     }
   }
@@ -473,7 +478,7 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
       stage = (stage + static_cast<uint32_t>(kb_count - 1)) % S;
       if ((last & 15) != 0) {
         const uint32_t par = (used >> stage) & 1u;
-        if (!mbar_wait(land_bar(stage), par, abort_flag, p.status)) break;
+        if (!mbar_wait_warp(land_bar(stage), par, abort_flag, p.status)) break;
         // rows last .. end of the 16: whole 128-byte rows, which the swizzle
         // permutes only within themselves
         const uint32_t bytes = static_cast<uint32_t>(((last + 15) & ~15) - last) * 128u;
@@ -484,7 +489,7 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
         fence_proxy_async_shared();
         __syncwarp();
         if (rank == 0) {
-          if (!mbar_wait_cluster(odd_bar(stage), par, abort_flag, p.status)) break;
+          if (!mbar_wait_warp<true>(odd_bar(stage), par, abort_flag, p.status)) break;
           if (lane == 0) mbar_arrive(full_bar(stage));
         } else if (lane == 0) {
           mbar_arrive_cluster(mapa_shared(odd_bar(stage), 0));
@@ -506,7 +511,7 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
       const bool has_k = t.kdim > 0;
       const float alpha = p.alpha ? p.alpha[t.g] : 1.0f;
       const float beta = p.beta ? p.beta[t.g] : 0.0f;
-      if (!mbar_wait(tfull_bar(slot), static_cast<uint32_t>((n >> 1) & 1), abort_flag, p.status))
+      if (!mbar_wait_warp(tfull_bar(slot), static_cast<uint32_t>((n >> 1) & 1), abort_flag, p.status))
         break;
       tc_fence_after();
       uint32_t v[4][32];

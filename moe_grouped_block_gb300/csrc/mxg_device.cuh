@@ -105,22 +105,6 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
   return ok != 0;
 }
 
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
-                                                  volatile int* abort_flag, int32_t* status,
-                                                  uint64_t timeout_ns = kWaitTimeoutNs) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
-  for (uint32_t it = 0;; ++it) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if ((it & 15u) == 15u && globaltimer() - t0 > timeout_ns) {
-      *abort_flag = 1;
-      status_set(status, MXG_DEV_TIMEOUT);
-      return false;
-    }
-  }
-}
-
 // ---------------------------------------------------------------- proxies
 __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -389,26 +373,149 @@ __device__ __forceinline__ void tc_mma_nvf4_pair(uint32_t d_tmem, uint64_t adesc
       : "memory");
 }
 
-// D(tmem) (+)= A(smem) * B(smem)^T on the pair, 16-bit operands (the
-// instruction descriptor names the type), FP32 accumulation.
-__device__ __forceinline__ void tc_mma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                                uint32_t idesc, uint32_t accumulate) {
+// ---------------------------------------------------------------- one lane of a converged warp
+// The forms below are reached by a whole converged warp and executed by the
+// lane whose `leader` is set (elect_leader).  Written this way, with no branch
+// around them, their operands stay in uniform registers: behind a branch on
+// the lane number every one of these instructions first moves its descriptors
+// and addresses over from vector registers.
+__device__ __forceinline__ uint32_t elect_leader() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r;
+}
+
+// Bounded wait of a whole converged warp; every lane gets the same answer.
+// CLUSTER: threads of another CTA arrive on the barrier.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity,
+                                               volatile int* abort_flag, int32_t* status,
+                                               uint64_t timeout_ns = kWaitTimeoutNs) {
+  auto ready = [&] {
+    const bool r = CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+    return __all_sync(0xFFFFFFFFu, r) != 0;
+  };
+  if (ready()) return true;
+  const uint64_t t0 = globaltimer();
+  for (uint32_t it = 0;; ++it) {
+    if (ready()) return true;
+    bool late = false;
+    if ((it & 15u) == 15u) late = globaltimer() - t0 > timeout_ns;
+    if (__any_sync(0xFFFFFFFFu, late)) {
+      *abort_flag = 1;
+      status_set(status, MXG_DEV_TIMEOUT);
+      return false;
+    }
+    if (__any_sync(0xFFFFFFFFu, *abort_flag != 0)) return false;
+  }
+}
+
+__device__ __forceinline__ void mbar_arrive_if(uint32_t bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+      "r"(leader)
       : "memory");
 }
 
-// The same on one CTA.
-__device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                           uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mbar_arrive_expect_tx_if(uint32_t bar, uint32_t bytes,
+                                                         uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes), "r"(leader)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d_if(uint32_t dst, const void* tmap, uint32_t bar,
+                                               int32_t c0, int32_t c1, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+      "l"(tmap), "r"(bar), "r"(c0), "r"(c1), "r"(leader)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_if(uint32_t dst, const void* tmap, uint32_t bar,
+                                               int32_t c0, int32_t c1, int32_t c2,
+                                               uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+      "l"(tmap), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(leader)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d_pair_if(uint32_t dst, const void* tmap,
+                                                    uint32_t cluster_bar, int32_t c0, int32_t c1,
+                                                    uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+      "bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+      "l"(tmap), "r"(cluster_bar), "r"(c0), "r"(c1), "r"(leader)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair_if(uint32_t dst, const void* tmap,
+                                                    uint32_t cluster_bar, int32_t c0, int32_t c1,
+                                                    int32_t c2, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+      "bytes [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+      "l"(tmap), "r"(cluster_bar), "r"(c0), "r"(c1), "r"(c2), "r"(leader)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_if(uint32_t bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          bar),
+      "r"(leader)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_pair_mc_if(uint32_t bar, uint16_t cta_mask,
+                                                     uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;\n\t}" ::"r"(bar),
+      "h"(cta_mask), "r"(leader)
+      : "memory");
+}
+
+// D(tmem) (+)= A(smem) * B(smem)^T, 16-bit operands (the instruction
+// descriptor names the type), FP32 accumulation: on the pair, and on one CTA.
+__device__ __forceinline__ void tc_mma_f16_pair_if(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                   uint32_t idesc, uint32_t accumulate,
+                                                   uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_f16_if(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t accumulate,
+                                              uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
 }
 
