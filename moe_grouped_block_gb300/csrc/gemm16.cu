@@ -4,23 +4,31 @@
 //   wgrad  C[g, n, k]    = alpha_g * sum_{i in g} A[off_g+i, n] B[off_g+i, k] + beta_g * C
 // Group g owns rows off_g .. off_g + M_g - 1 (any M_g >= 0, read on the device).
 //
-// A 2-CTA cluster computes 256 x 256 output units with the cta_group::2 MMA;
-// CTA r holds 128 rows of the unit's A tile and half of its B tile.  Warp 0
-// loads (TMA), warp 1 of the even CTA issues the MMAs, warps 2-9 are the
-// epilogue (one TMEM lane quarter and 128 columns each).  The two 256-column
-// accumulators fill tensor memory, so that the epilogue of a unit runs under
-// the MMAs of the next one.  The clusters are persistent and walk the units
-// in a static order derived from the group sizes on the device.
+// Every mode is C = R Q^T with R giving the rows of C (the operand A of the
+// interface) and Q its columns (B).  A 2-CTA cluster computes units of up to
+// 256 rows times 256 columns with the cta_group::2 MMA, transposed: Q is the
+// MMA's 256-row operand (128 rows a CTA) and R its other one, whose width is
+// any multiple of 32.  So the ragged side costs multiples of 32 rows, not of
+// the tile -- with 64 groups of some 500 rows, whole 256-row tiles computed
+// 1.7 times the rows there are -- a few rows are one narrow MMA beside the
+// weights' stream, and an accumulator lane is a column of C, so that a warp
+// stores 32 neighbouring columns of a row at any alignment of C.
+//
+// Warp 0 loads (TMA), warp 1 of the even CTA issues the MMAs, warps 2-9 are
+// the epilogue.  Two 256-column accumulators fill tensor memory, so that the
+// epilogue of a unit runs under the MMAs of the next one.  The clusters are
+// persistent and walk the units in a static order derived from the group
+// sizes on the device.
 //
 // Neither operand is transposed in memory: where the contraction runs along
-// rows (B of dgrad, both of wgrad) the tile is loaded as 64-row boxes of 64
+// rows (Q of dgrad, both of wgrad) the tile is loaded as 64-row boxes of 64
 // columns and the MMA reads it MN-major.
 //
 // Contraction tails.  Past N or K the copies fill zeros (for the weights the
 // tensor map has the expert as its third dimension, so that a box never runs
 // into the next expert).  Only wgrad's contraction ends at a device-side
 // number: the rows of the next group that share the last 16-row MMA step are
-// zeroed in shared memory, in A and in B (a zero against their NaN would not
+// zeroed in shared memory, in both operands (a zero against a NaN would not
 // be zero), by warp 10 while earlier stages are multiplied.
 #include <atomic>
 
@@ -39,9 +47,11 @@ struct Gemm16Params {
   int32_t M_cap, N, K;
   int32_t out_cols;  // columns of C: N for fprop, K for dgrad and wgrad
   int32_t G;
-  int32_t out_type;  // mxg_dtype_t
-  uint32_t idesc;    // operand types and majors (M and N are added per unit)
-  int32_t c_vec;     // bytes of the widest aligned access to rows of C: 32, 16 or 0
+  int32_t out_type;     // mxg_dtype_t
+  uint32_t idesc;       // operand types and majors, M = 256; N is added per unit
+  int32_t tile_rows;    // rows of C per unit: a multiple of 32, at most 256
+  int32_t stages;       // pipeline stages, ...
+  int32_t stage_bytes;  // ... each a 128-row tile of Q and half the unit's rows of R
 };
 
 // Row offsets of the groups and their first units, by one warp: negative
@@ -96,31 +106,33 @@ __device__ __forceinline__ void group_tables16(const int64_t* group_ws, int G, i
   if (lane == 0 && blockIdx.x == 0) status_set(status, bits);
 }
 
-// Work unit u of the pair kernel: 256 rows times 256 columns of C.
+// Work unit u: `rows` rows of C from i0 on, 256 columns from j0 on.
 struct Unit16 {
   int32_t g;
-  int32_t row0;       // first row of the group in the ragged operands
-  int32_t i0, j0;     // first row (within the group, or of dW_g) and column of C
-  int32_t rows_left;  // rows of C from i0 on that belong to the group / dW_g
-  int32_t kdim;       // contraction length
-  int32_t n_mma;      // columns the MMAs compute: 256, fewer in the last column unit
+  int32_t row0;   // first row of the group in the ragged operands
+  int32_t i0, j0; // first row (within the group, or of dW_g) and column of C
+  int32_t rows;   // rows of the unit
+  int32_t n_mma;  // the same, rounded up to 32: the MMAs' width
+  int32_t kdim;   // contraction length
 };
 
-constexpr int kTile16 = 256;
+constexpr int kCols16 = 256;
 
 template <int MODE>
 __device__ __forceinline__ Unit16 map_unit16(int64_t u, const Gemm16Params& p,
                                              const int32_t* row_off, const int32_t* unit_off) {
   Unit16 t;
-  const int32_t cu = (p.out_cols + kTile16 - 1) / kTile16;
+  const uint32_t cu = (static_cast<uint32_t>(p.out_cols) + kCols16 - 1) / kCols16;
+  uint32_t i, j, tiles;
+  int32_t total;  // rows of C in this group
   if constexpr (MODE == 1) {
-    const uint32_t per = static_cast<uint32_t>((p.N + kTile16 - 1) / kTile16) * cu;
+    tiles = static_cast<uint32_t>(p.N + p.tile_rows - 1) / p.tile_rows;
+    const uint32_t per = tiles * cu;
     t.g = static_cast<int32_t>(static_cast<uint32_t>(u) / per);
     const uint32_t local = static_cast<uint32_t>(u) - t.g * per;
-    const uint32_t iu = local / cu;
-    t.i0 = static_cast<int32_t>(iu) * kTile16;
-    t.j0 = static_cast<int32_t>(local - iu * cu) * kTile16;
-    t.rows_left = p.N - t.i0;
+    i = local / cu;
+    j = local - i * cu;
+    total = p.N;
     t.row0 = row_off[t.g];
     t.kdim = row_off[t.g + 1] - t.row0;
   } else {
@@ -135,98 +147,49 @@ __device__ __forceinline__ Unit16 map_unit16(int64_t u, const Gemm16Params& p,
     t.g = lo;
     t.row0 = row_off[lo];
     t.kdim = MODE == 0 ? p.K : p.N;
-    const int32_t rows = row_off[lo + 1] - t.row0;
-    const uint32_t ru = static_cast<uint32_t>((rows + kTile16 - 1) / kTile16);
+    total = row_off[lo + 1] - t.row0;
+    tiles = static_cast<uint32_t>(total + p.tile_rows - 1) / p.tile_rows;
     const uint32_t local = static_cast<uint32_t>(u) - unit_off[lo];
     // column unit, then row unit, so that the clusters in flight share weight
     // tiles and the group's rows stay in L2; where those rows are more than an
     // L2 budget, blocks of column units that fit it, each walked row unit by
     // row unit
-    uint32_t j = local / ru, i = local - j * ru;
+    j = local / tiles;
+    i = local - j * tiles;
     constexpr int64_t kL2Budget = 32ll << 20;
-    if (static_cast<int64_t>(rows) * t.kdim * 2 > kL2Budget) {
-      int64_t cb = kL2Budget / (static_cast<int64_t>(kTile16) * t.kdim * 2);
+    if (static_cast<int64_t>(total) * t.kdim * 2 > kL2Budget) {
+      int64_t cb = kL2Budget / (static_cast<int64_t>(kCols16) * t.kdim * 2);
       cb = cb < 1 ? 1 : (cb > cu ? cu : cb);
-      const uint32_t b = static_cast<uint32_t>(cb), blk = local / (ru * b);
-      const uint32_t width = (blk + 1) * b <= static_cast<uint32_t>(cu) ? b : cu - blk * b;
-      const uint32_t rem = local - blk * ru * b;
+      const uint32_t b = static_cast<uint32_t>(cb), blk = local / (tiles * b);
+      const uint32_t width = (blk + 1) * b <= cu ? b : cu - blk * b;
+      const uint32_t rem = local - blk * tiles * b;
       i = rem / width;
       j = blk * b + (rem - i * width);
     }
-    t.i0 = static_cast<int32_t>(i) * kTile16;
-    t.j0 = static_cast<int32_t>(j) * kTile16;
-    t.rows_left = rows - t.i0;
   }
-  const int32_t left = p.out_cols - t.j0;
-  t.n_mma = left >= kTile16 ? kTile16 : (left + 31) / 32 * 32;
+  // the group's rows in equal shares (multiples of 32): a narrow last unit
+  // would stream its weights for few products
+  const int32_t share = ((total + static_cast<int32_t>(tiles) - 1) / static_cast<int32_t>(tiles) + 31) & ~31;
+  t.i0 = static_cast<int32_t>(i) * share;
+  t.j0 = static_cast<int32_t>(j) * kCols16;
+  t.rows = max(0, min(share, total - t.i0));
+  t.n_mma = max(32, (t.rows + 31) & ~31);
   return t;
 }
 
-// 16 columns of one output row: alpha * acc + beta * old, stored as the output
-// type.  `n`: columns of the 16 that exist.
+// One column (of this lane) and up to 32 rows of C: alpha * acc + beta * old.
 template <typename T>
-__device__ __forceinline__ void store_cols16(T* dst, const uint32_t* acc, int n, int vec, bool has_k,
-                                             float alpha, float beta) {
-  float f[16];
+__device__ __forceinline__ void store_column16(T* dst, int64_t ldc, const uint32_t (&acc)[32],
+                                               int rows, bool has_k, float alpha, float beta) {
 #pragma unroll
-  for (int e = 0; e < 16; ++e) f[e] = has_k ? alpha * __uint_as_float(acc[e]) : 0.0f;
-  if (n >= 16 && vec != 0) {
-    if (beta != 0.0f) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float o[8];
-        unpack8<T>(load8<T>(dst + 8 * h), o);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[8 * h + e] += beta * o[e];
-      }
+  for (int e = 0; e < 32; ++e) {
+    if (e < rows) {
+      float v = has_k ? alpha * __uint_as_float(acc[e]) : 0.0f;
+      if (beta != 0.0f) v += beta * to_f32(*dst);
+      *dst = from_f32<T>(v);
     }
-    if (vec == 32) {
-      if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(f[8 * h + e]);
-          st_global_32B(dst + 8 * h, w);
-        }
-      } else {
-        uint32_t w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = pack2<T>(f[2 * e], f[2 * e + 1]);
-        st_global_32B(dst, w);
-      }
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float o[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = f[8 * h + e];
-        store8<T>(dst + 8 * h, o);
-      }
-    }
-    return;
+    dst += ldc;
   }
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (e < n) {
-      float v = f[e];
-      if (beta != 0.0f) v += beta * to_f32(dst[e]);
-      dst[e] = from_f32<T>(v);
-    }
-}
-
-__device__ __forceinline__ void store_row16(const Gemm16Params& p, int64_t row, int32_t col,
-                                            const uint32_t* acc, bool has_k, float alpha,
-                                            float beta) {
-  const int n = p.out_cols - col;
-  if (n <= 0) return;
-  const int64_t at = row * p.ldc + col;
-  if (p.out_type == MXG_F32)
-    store_cols16(static_cast<float*>(p.C) + at, acc, n, p.c_vec, has_k, alpha, beta);
-  else if (p.out_type == MXG_BF16)
-    store_cols16(static_cast<Bf16*>(p.C) + at, acc, n, p.c_vec, has_k, alpha, beta);
-  else
-    store_cols16(static_cast<F16*>(p.C) + at, acc, n, p.c_vec, has_k, alpha, beta);
 }
 
 // Bounded wait used only while tearing down: ignores the abort flag.
@@ -241,26 +204,25 @@ __device__ __forceinline__ void drain16(uint32_t bar, uint32_t parity, int32_t* 
 }
 
 struct Pair16 {
-  static constexpr int kStages = 6;
-  static constexpr int kBK = 64;                   // contraction elements per stage
-  static constexpr int kOperand = 128 * kBK * 2;   // bytes of A, and of B, per CTA and stage
-  static constexpr int kStageBytes = 2 * kOperand;
+  static constexpr int kMaxStages = 12;
+  static constexpr int kBK = 64;                 // contraction elements per stage
+  static constexpr int kQBytes = 128 * kBK * 2;  // Q per CTA and stage
   static constexpr int kMmas = kBK / 16;
   static constexpr int kEpiWarps = 8;
   static constexpr int kMaskWarp = 2 + kEpiWarps;
   static constexpr int threads(int mode) { return 32 * (kMaskWarp + (mode == 1 ? 1 : 0)); }
   // full[S], empty[S], land[S], odd_masked[S], tfull[2], tempty[2],
   // info_full[2], info_empty[2], drain; two unit words; TMEM base, abort flag
-  static constexpr int kBars = 4 * kStages + 9;
+  static constexpr int kBars = 4 * kMaxStages + 9;
   static constexpr int kBarBytes = 8 * (kBars + 2) + 16;
-  static size_t smem_bytes(int G) {
-    return 1024 + static_cast<size_t>(kStages) * kStageBytes + kBarBytes + 8 * (G + 1);
-  }
+  // the barriers and tables lie before the stages
+  static constexpr int kSmemMax = 227 * 1024;
+  static int header_bytes(int G) { return (kBarBytes + 8 * (G + 1) + 1023) / 1024 * 1024; }
 };
 
-// Descriptor of a 128-row K-major tile (rows of 128 bytes, 128-byte swizzle),
-// or of an MN-major one: chunks of 64 rows of 128 bytes (64 values along M or
-// N a row), 8192 bytes apart, 8-row groups 1024 bytes apart.
+// Descriptor of a K-major tile (rows of 128 bytes, 128-byte swizzle), or of an
+// MN-major one: chunks of 64 rows of 128 bytes (64 values along M or N a row),
+// 8192 bytes apart, 8-row groups 1024 bytes apart.
 template <bool MN>
 __device__ __forceinline__ uint64_t tile_desc16(uint32_t saddr) {
   return MN ? smem_desc(saddr, 8192, 1024, 2) : smem_desc(saddr, 16, 1024, 2);
@@ -271,23 +233,24 @@ constexpr uint32_t kStep16 = MN ? 2048 / 16 : 32 / 16;
 
 template <int MODE>
 __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
-    gemm16_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
-                       const __grid_constant__ CUtensorMap tmap_b, const Gemm16Params p) {
+    gemm16_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                       const __grid_constant__ CUtensorMap tmap_r, const Gemm16Params p) {
   using Cfg = Pair16;
-  constexpr int S = Cfg::kStages, BK = Cfg::kBK;
-  constexpr bool A_MN = MODE == 1, B_MN = MODE != 0;
+  constexpr int S = Cfg::kMaxStages, BK = Cfg::kBK;
+  constexpr bool Q_MN = MODE != 0, R_MN = MODE == 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * Cfg::kStageBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
   uint64_t* info_word = bars + Cfg::kBars;
   uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(info_word + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_s + 1);
-  int32_t* row_off = reinterpret_cast<int32_t*>(smem + S * Cfg::kStageBytes + Cfg::kBarBytes);
+  int32_t* row_off = reinterpret_cast<int32_t*>(smem + Cfg::kBarBytes);
   int32_t* unit_off = row_off + (p.G + 1);
 
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
-  const uint32_t smem_base = smem_u32(smem);
+  const uint32_t stage0 = smem_u32(smem) + ((Cfg::kBarBytes + 8 * (p.G + 1) + 1023) & ~1023);
+  const uint32_t stages = p.stages, stage_bytes = p.stage_bytes;
   const uint32_t rank = cluster_ctarank();
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   auto full_bar = [&](int s) { return bar(s); };
@@ -323,7 +286,7 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
     tmem_relinquish_pair();
   }
   if (warp == 1)
-    group_tables16(p.group_ws, p.G, p.M_cap, kTile16, (p.out_cols + kTile16 - 1) / kTile16,
+    group_tables16(p.group_ws, p.G, p.M_cap, p.tile_rows, (p.out_cols + kCols16 - 1) / kCols16,
                    row_off, unit_off, p.status);
   tc_fence_before();
   __syncthreads();
@@ -332,88 +295,84 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
   const uint32_t tmem_base = *tmem_base_s;
   const int64_t unit0 = blockIdx.x >> 1, ustride = gridDim.x >> 1;
   const int64_t total =
-      MODE == 1 ? static_cast<int64_t>(p.G) * ((p.N + kTile16 - 1) / kTile16) *
-                      ((p.out_cols + kTile16 - 1) / kTile16)
+      MODE == 1 ? static_cast<int64_t>(p.G) * ((p.N + p.tile_rows - 1) / p.tile_rows) *
+                      ((p.out_cols + kCols16 - 1) / kCols16)
                 : unit_off[p.G];
 
   // ------------------------------------------------------------ producers (both CTAs)
   if (warp == 0) {
-    {
-      const uint32_t leader = elect_leader();
-      prefetch_tmap(&tmap_a);
-      prefetch_tmap(&tmap_b);
-      uint32_t stage = 0, phase = 0, issued = 0, parity = 0, tail_issued = 0, tail_parity = 0;
-      bool ok = true;
-      for (int64_t u = unit0, n = 0; ok && u < total; u += ustride, ++n) {
-        const Unit16 t = map_unit16<MODE>(u, p, row_off, unit_off);
-        const int32_t kb_count = (t.kdim + BK - 1) / BK;
-        const int32_t last = t.kdim - (kb_count - 1) * BK;  // elements of the last block
-        if (rank == 0) {
-          // the unit's shape, for the MMA thread
-          const int slot = static_cast<int>(n & 1), par = static_cast<int>((n >> 1) & 1);
-          if (!mbar_wait_warp(info_empty_bar(slot), par ^ 1, abort_flag, p.status)) break;
-          if (leader)
-            info_word[slot] = static_cast<uint64_t>(static_cast<uint32_t>(kb_count)) |
-                              (static_cast<uint64_t>((last + 15) / 16) << 32) |
-                              (static_cast<uint64_t>(t.n_mma) << 40);
-          mbar_arrive_if(info_full_bar(slot), leader);
+    const uint32_t leader = elect_leader();
+    prefetch_tmap(&tmap_q);
+    prefetch_tmap(&tmap_r);
+    uint32_t stage = 0, phase = 0, issued = 0, parity = 0, tail_issued = 0, tail_parity = 0;
+    const bool two = stage_bytes > Cfg::kQBytes + 8192;  // MN-major R: a second chunk
+    bool ok = true;
+    for (int64_t u = unit0, n = 0; ok && u < total; u += ustride, ++n) {
+      const Unit16 t = map_unit16<MODE>(u, p, row_off, unit_off);
+      const int32_t kb_count = (t.kdim + BK - 1) / BK;
+      const int32_t last = t.kdim - (kb_count - 1) * BK;  // elements of the last block
+      if (rank == 0) {
+        // the unit's shape, for the MMA warp
+        const int slot = static_cast<int>(n & 1), par = static_cast<int>((n >> 1) & 1);
+        if (!mbar_wait_warp(info_empty_bar(slot), par ^ 1, abort_flag, p.status)) break;
+        if (leader)
+          info_word[slot] = static_cast<uint64_t>(static_cast<uint32_t>(kb_count)) |
+                            (static_cast<uint64_t>((last + 15) / 16) << 32) |
+                            (static_cast<uint64_t>(t.n_mma) << 40);
+        mbar_arrive_if(info_full_bar(slot), leader);
+      }
+      const int32_t q_at = t.j0 + 128 * static_cast<int32_t>(rank);
+      const int32_t r_at = t.i0 + (t.n_mma / 2) * static_cast<int32_t>(rank);
+      for (int32_t kb = 0; kb < kb_count; ++kb) {
+        if (!mbar_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, p.status)) {
+          ok = false;
+          break;
         }
-        const int32_t b_at = t.j0 + (t.n_mma / 2) * static_cast<int32_t>(rank);
-        const int32_t a_at = t.i0 + 128 * static_cast<int32_t>(rank);
-        for (int32_t kb = 0; kb < kb_count; ++kb) {
-          if (!mbar_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sa = smem_base + stage * Cfg::kStageBytes, sb = sa + Cfg::kOperand;
-          const int32_t k0 = kb * BK;
-          if (MODE == 1 && kb + 1 == kb_count && (last & 15) != 0) {
-            // rows of the next group in the last MMA step: this CTA's bytes
-            // land on its own barrier, and its mask warp passes them on
-            mbar_arrive_expect_tx_if(land_bar(stage), Cfg::kStageBytes, leader);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              tma_load_2d_if(sa + 8192 * c, &tmap_a, land_bar(stage), a_at + 64 * c, t.row0 + k0, leader);
-              tma_load_2d_if(sb + 8192 * c, &tmap_b, land_bar(stage), b_at + 64 * c, t.row0 + k0, leader);
-            }
-            tail_issued |= 1u << stage;
-            tail_parity ^= 1u << stage;
+        const uint32_t sq = stage0 + stage * stage_bytes, sr = sq + Cfg::kQBytes;
+        const int32_t k0 = kb * BK;
+        if (MODE == 1 && kb + 1 == kb_count && (last & 15) != 0) {
+          // rows of the next group in the last MMA step: this CTA's bytes
+          // land on its own barrier, and its mask warp passes them on
+          const uint32_t lb = land_bar(stage);
+          mbar_arrive_expect_tx_if(lb, stage_bytes, leader);
+          tma_load_2d_if(sq, &tmap_q, lb, q_at, t.row0 + k0, leader);
+          tma_load_2d_if(sq + 8192, &tmap_q, lb, q_at + 64, t.row0 + k0, leader);
+          tma_load_2d_if(sr, &tmap_r, lb, r_at, t.row0 + k0, leader);
+          if (two) tma_load_2d_if(sr + 8192, &tmap_r, lb, r_at + 64, t.row0 + k0, leader);
+          tail_issued |= 1u << stage;
+          tail_parity ^= 1u << stage;
+        } else {
+          if (rank == 0) mbar_arrive_expect_tx_if(full_bar(stage), 2 * stage_bytes, leader);
+          const uint32_t fb = mapa_shared(full_bar(stage), 0);
+          if constexpr (MODE == 0) {
+            tma_load_3d_pair_if(sq, &tmap_q, fb, k0, q_at, t.g, leader);
+          } else if constexpr (MODE == 2) {
+            tma_load_3d_pair_if(sq, &tmap_q, fb, q_at, k0, t.g, leader);
+            tma_load_3d_pair_if(sq + 8192, &tmap_q, fb, q_at + 64, k0, t.g, leader);
           } else {
-            if (rank == 0) mbar_arrive_expect_tx_if(full_bar(stage), 2 * Cfg::kStageBytes, leader);
-            const uint32_t fb = mapa_shared(full_bar(stage), 0);
-            if constexpr (A_MN) {
-#pragma unroll
-              for (int c = 0; c < 2; ++c)
-                tma_load_2d_pair_if(sa + 8192 * c, &tmap_a, fb, a_at + 64 * c, t.row0 + k0, leader);
-            } else {
-              tma_load_2d_pair_if(sa, &tmap_a, fb, k0, t.row0 + a_at, leader);
-            }
-            if constexpr (MODE == 0) {
-              tma_load_3d_pair_if(sb, &tmap_b, fb, k0, b_at, t.g, leader);
-            } else {
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                if constexpr (MODE == 2)
-                  tma_load_3d_pair_if(sb + 8192 * c, &tmap_b, fb, b_at + 64 * c, k0, t.g, leader);
-                else
-                  tma_load_2d_pair_if(sb + 8192 * c, &tmap_b, fb, b_at + 64 * c, t.row0 + k0, leader);
-              }
-            }
+            tma_load_2d_pair_if(sq, &tmap_q, fb, q_at, t.row0 + k0, leader);
+            tma_load_2d_pair_if(sq + 8192, &tmap_q, fb, q_at + 64, t.row0 + k0, leader);
           }
-          issued |= 1u << stage;
-          parity = (parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
+          if constexpr (MODE == 1) {
+            tma_load_2d_pair_if(sr, &tmap_r, fb, r_at, t.row0 + k0, leader);
+            if (two) tma_load_2d_pair_if(sr + 8192, &tmap_r, fb, r_at + 64, t.row0 + k0, leader);
+          } else {
+            tma_load_2d_pair_if(sr, &tmap_r, fb, k0, t.row0 + r_at, leader);
           }
         }
+        issued |= 1u << stage;
+        parity = (parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      // every copy has landed before the CTAs may exit: the even CTA's full
-      // barriers count both CTAs' bytes; masked stages count their own
-      for (int s = 0; s < S; ++s) {
-        if (rank == 0 && (issued >> s & 1u)) drain16(full_bar(s), (parity >> s) & 1u, p.status);
-        if (tail_issued >> s & 1u) drain16(land_bar(s), (~tail_parity >> s) & 1u, p.status);
-      }
+    }
+    // every copy has landed before the CTAs may exit: the even CTA's full
+    // barriers count both CTAs' bytes; masked stages count their own
+    for (int s = 0; s < S; ++s) {
+      if (rank == 0 && (issued >> s & 1u)) drain16(full_bar(s), (parity >> s) & 1u, p.status);
+      if (tail_issued >> s & 1u) drain16(land_bar(s), (~tail_parity >> s) & 1u, p.status);
     }
   }
   // ------------------------------------------------------------ MMA issuer (even CTA)
@@ -444,17 +403,17 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_base + stage * Cfg::kStageBytes, sb = sa + Cfg::kOperand;
-          const uint64_t ad = tile_desc16<A_MN>(sa), bd = tile_desc16<B_MN>(sb);
+          const uint32_t sq = stage0 + stage * stage_bytes, sr = sq + Cfg::kQBytes;
+          const uint64_t qd = tile_desc16<Q_MN>(sq), rd = tile_desc16<R_MN>(sr);
           const int nmma = kb + 1 == kb_count ? last_mmas : Cfg::kMmas;
 #pragma unroll
           for (int kk = 0; kk < Cfg::kMmas; ++kk) {
             if (kk >= nmma) break;
-            tc_mma_f16_pair_if(d, ad + kk * kStep16<A_MN>, bd + kk * kStep16<B_MN>, idesc,
+            tc_mma_f16_pair_if(d, qd + kk * kStep16<Q_MN>, rd + kk * kStep16<R_MN>, idesc,
                                (kb > 0 || kk > 0) ? 1u : 0u, leader);
           }
           tc_commit_pair_mc_if(empty_bar(stage), 0x3, leader);
-          if (++stage == S) {
+          if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -475,17 +434,16 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
       const int32_t kb_count = (t.kdim + BK - 1) / BK;
       if (kb_count == 0) continue;
       const int32_t last = t.kdim - (kb_count - 1) * BK;
-      stage = (stage + static_cast<uint32_t>(kb_count - 1)) % S;
+      stage = (stage + static_cast<uint32_t>(kb_count - 1)) % stages;
       if ((last & 15) != 0) {
         const uint32_t par = (used >> stage) & 1u;
         if (!mbar_wait_warp(land_bar(stage), par, abort_flag, p.status)) break;
         // rows last .. end of the 16: whole 128-byte rows, which the swizzle
         // permutes only within themselves
         const uint32_t bytes = static_cast<uint32_t>(((last + 15) & ~15) - last) * 128u;
-        const uint32_t at = smem_base + stage * Cfg::kStageBytes + static_cast<uint32_t>(last) * 128u;
+        const uint32_t at = stage0 + stage * stage_bytes + static_cast<uint32_t>(last) * 128u;
         for (uint32_t o = lane * 16; o < bytes; o += 512)
-#pragma unroll
-          for (uint32_t c = 0; c < 4; ++c) st_shared_v4(at + 8192 * c + o, 0, 0, 0, 0);
+          for (uint32_t c = 0; c < stage_bytes; c += 8192) st_shared_v4(at + c + o, 0, 0, 0, 0);
         fence_proxy_async_shared();
         __syncwarp();
         if (rank == 0) {
@@ -496,14 +454,13 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
         }
         used ^= 1u << stage;
       }
-      stage = (stage + 1) % S;
+      stage = (stage + 1) % stages;
     }
   }
   // ------------------------------------------------------------ epilogue (both CTAs)
   else {
-    const uint32_t ew = warp - 2;
-    const uint32_t quarter = warp & 3u;  // TMEM lanes 32 * quarter .. + 31
-    const uint32_t col0 = 128u * (ew >> 2);
+    // lane quarter = 32 columns of C, every other chunk of 32 rows
+    const uint32_t quarter = warp & 3u, half = (warp - 2) >> 2;
     int64_t n = 0;
     for (int64_t u = unit0; u < total; u += ustride, ++n) {
       const Unit16 t = map_unit16<MODE>(u, p, row_off, unit_off);
@@ -511,27 +468,38 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
       const bool has_k = t.kdim > 0;
       const float alpha = p.alpha ? p.alpha[t.g] : 1.0f;
       const float beta = p.beta ? p.beta[t.g] : 0.0f;
-      if (!mbar_wait_warp(tfull_bar(slot), static_cast<uint32_t>((n >> 1) & 1), abort_flag, p.status))
+      if (!mbar_wait_warp(tfull_bar(slot), static_cast<uint32_t>((n >> 1) & 1), abort_flag,
+                          p.status))
         break;
       tc_fence_after();
-      uint32_t v[4][32];
-      if (has_k) {
-        const uint32_t taddr = tmem_base + ((32u * quarter) << 16) + 256u * slot + col0;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(taddr + 32 * c, v[c]);
-        tmem_ld_wait();
+      const uint32_t taddr = tmem_base + ((32u * quarter) << 16) + 256u * slot;
+      const int32_t col = t.j0 + static_cast<int32_t>(128 * rank + 32 * quarter + lane);
+      const int64_t row =
+          (MODE == 1 ? static_cast<int64_t>(t.g) * p.N : static_cast<int64_t>(t.row0)) + t.i0;
+      const bool in = col < p.out_cols;
+      for (int32_t c = 32 * static_cast<int32_t>(half); c < t.rows; c += 64) {
+        uint32_t v[32];
+        if (has_k) {
+          tmem_ld32(taddr + static_cast<uint32_t>(c), v);
+          tmem_ld_wait();
+        }
+        if (in) {
+          const int64_t at = (row + c) * p.ldc + col;
+          const int left = t.rows - c;
+          if (p.out_type == MXG_F32)
+            store_column16(static_cast<float*>(p.C) + at, p.ldc, v, left, has_k, alpha, beta);
+          else if (p.out_type == MXG_BF16)
+            store_column16(static_cast<Bf16*>(p.C) + at, p.ldc, v, left, has_k, alpha, beta);
+          else
+            store_column16(static_cast<F16*>(p.C) + at, p.ldc, v, left, has_k, alpha, beta);
+        }
+        __syncwarp();
       }
+      // the loads have completed: the accumulator may be overwritten.  Relaxed:
+      // a release would wait for the stores
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(slot), 0));
-      const int32_t r = static_cast<int32_t>(128 * rank + 32 * quarter + lane);
-      if (r < t.rows_left) {
-        const int64_t row = (MODE == 1 ? static_cast<int64_t>(t.g) * p.N : t.row0) + t.i0 + r;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          store_row16(p, row, t.j0 + static_cast<int32_t>(col0) + 16 * k, &v[k >> 1][16 * (k & 1)],
-                      has_k, alpha, beta);
-      }
     }
   }
 
@@ -551,7 +519,7 @@ namespace {
 constexpr int kMaxDev16 = 64;
 
 // Clusters of the pair kernel that the device holds at once, asked once per
-// device (with the shared memory of the largest group table).
+// device, with all the shared memory there is.
 template <int MODE>
 int pair_clusters(int num_sms) {
   static std::atomic<int> known[kMaxDev16];
@@ -560,7 +528,7 @@ int pair_clusters(int num_sms) {
   int c = known[dev].load(std::memory_order_relaxed);
   if (c != 0) return c;
   auto kern = gemm16_pair_kernel<MODE>;
-  const int smem = static_cast<int>(Pair16::smem_bytes(1024));
+  const int smem = Pair16::kSmemMax;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
@@ -579,8 +547,8 @@ int pair_clusters(int num_sms) {
 }
 
 template <int MODE>
-cudaError_t launch_pair16(const CUtensorMap& ta, const CUtensorMap& tb, const Gemm16Params& p,
-                          int64_t max_units, int num_sms, cudaStream_t stream) {
+cudaError_t launch_pair16(const CUtensorMap& tq, const CUtensorMap& tr, const Gemm16Params& p,
+                          int smem, int64_t max_units, int num_sms, cudaStream_t stream) {
   const int clusters = pair_clusters<MODE>(num_sms);
   if (clusters < 1) return cudaErrorInvalidConfiguration;
   const int64_t n = max_units < clusters ? max_units : clusters;
@@ -591,11 +559,11 @@ cudaError_t launch_pair16(const CUtensorMap& ta, const CUtensorMap& tb, const Ge
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(2 * n));
   cfg.blockDim = dim3(Pair16::threads(MODE));
-  cfg.dynamicSmemBytes = Pair16::smem_bytes(p.G);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemm16_pair_kernel<MODE>, ta, tb, p);
+  return cudaLaunchKernelEx(&cfg, gemm16_pair_kernel<MODE>, tq, tr, p);
 }
 
 // A ragged matrix [rows, cols] of 16-bit elements, boxes of 64 columns.
@@ -627,41 +595,47 @@ cudaError_t launch_grouped_gemm16(int in_f16, int mode, const void* A, int64_t l
   p.G = G;
   p.out_type = out_type;
   // FP32 accumulation (bit 4), operand types (bits 7 and 10: 0 fp16, 1 bf16),
-  // MN-major operands (bits 15 and 16), M = 256 (bit 24)
-  p.idesc = (1u << 4) | (in_f16 ? 0u : (1u << 7) | (1u << 10)) | (mode == 1 ? 1u << 15 : 0u) |
-            (mode != 0 ? 1u << 16 : 0u) | ((256u >> 4) << 24);
-  const int64_t size = out_type == MXG_F32 ? 4 : 2;
-  const uintptr_t c_at = reinterpret_cast<uintptr_t>(C) | static_cast<uintptr_t>(ldc * size);
-  p.c_vec = (c_at & 31u) == 0 ? 32 : ((c_at & 15u) == 0 ? 16 : 0);
+  // MN-major Q and R (bits 15 and 16), M = 256 (bit 24)
+  p.idesc = (1u << 4) | (in_f16 ? 0u : (1u << 7) | (1u << 10)) | (mode != 0 ? 1u << 15 : 0u) |
+            (mode == 1 ? 1u << 16 : 0u) | ((256u >> 4) << 24);
+  // units as tall as the rows can be, up to 256; what few rows leave free of a
+  // stage goes to more stages, i.e. more of the weights in flight
+  const int64_t c_rows = mode == 1 ? N : M_cap;
+  p.tile_rows = c_rows >= 256 ? 256 : static_cast<int32_t>((c_rows + 31) / 32 * 32);
+  const int r_bytes = mode == 1 ? (p.tile_rows > 128 ? 16384 : 8192) : p.tile_rows / 2 * 128;
+  p.stage_bytes = Pair16::kQBytes + r_bytes;
+  const int header = Pair16::header_bytes(G) + 1024;
+  p.stages = (Pair16::kSmemMax - header) / p.stage_bytes;
+  if (p.stages > Pair16::kMaxStages) p.stages = Pair16::kMaxStages;
+  const int smem = header + p.stages * p.stage_bytes;
 
   // without rows no copy is made: any aligned address serves the tensor maps
-  if (M_cap == 0) {
-    A = group_ws;
-    B = mode == 1 ? group_ws : B;
-  }
-  CUtensorMap ta, tb;
-  const int64_t a_cols = mode == 0 ? K : N;
-  if (!ragged_map(&ta, A, a_cols, M_cap, lda, mode == 1 ? 64 : 128)) return cudaErrorInvalidValue;
+  if (M_cap == 0) A = B = reinterpret_cast<const void*>(uintptr_t{1} << 20);
+  CUtensorMap tq, tr;
+  const int64_t r_cols = mode == 0 ? K : N;
+  if (!ragged_map(&tr, A, r_cols, M_cap, lda,
+                  mode == 1 ? 64u : static_cast<uint32_t>(p.tile_rows / 2)))
+    return cudaErrorInvalidValue;
   if (mode == 1) {
-    if (!ragged_map(&tb, B, K, M_cap, ldb, 64)) return cudaErrorInvalidValue;
+    if (!ragged_map(&tq, B, K, M_cap, ldb, 64)) return cudaErrorInvalidValue;
   } else {
     const uint64_t dims[3] = {static_cast<uint64_t>(K), static_cast<uint64_t>(N),
                               static_cast<uint64_t>(G)};
     const uint64_t strides[2] = {static_cast<uint64_t>(ldb) * 2, static_cast<uint64_t>(N * ldb) * 2};
     const uint32_t box[3] = {64, mode == 0 ? 128u : 64u, 1};
-    if (!make_tmap_3d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT16, B, dims, strides, box,
+    if (!make_tmap_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT16, B, dims, strides, box,
                       CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
-  const int64_t cu = (p.out_cols + kTile16 - 1) / kTile16;
+  const int64_t cu = (p.out_cols + kCols16 - 1) / kCols16;
   // an upper bound: the sizes are on the device
   const int64_t live = M_cap < G ? M_cap : G;
-  const int64_t units = mode == 1 ? G * ((N + kTile16 - 1) / kTile16) * cu
-                                  : ((M_cap + live * (kTile16 - 1)) / kTile16) * cu;
+  const int64_t units = mode == 1 ? G * ((N + p.tile_rows - 1) / p.tile_rows) * cu
+                                  : ((M_cap + live * (p.tile_rows - 1)) / p.tile_rows) * cu;
   if (units > INT32_MAX) return cudaErrorInvalidValue;
-  if (mode == 0) return launch_pair16<0>(ta, tb, p, units, num_sms, stream);
-  if (mode == 1) return launch_pair16<1>(ta, tb, p, units, num_sms, stream);
-  return launch_pair16<2>(ta, tb, p, units, num_sms, stream);
+  if (mode == 0) return launch_pair16<0>(tq, tr, p, smem, units, num_sms, stream);
+  if (mode == 1) return launch_pair16<1>(tq, tr, p, smem, units, num_sms, stream);
+  return launch_pair16<2>(tq, tr, p, smem, units, num_sms, stream);
 }
 
 }  // namespace mxg
