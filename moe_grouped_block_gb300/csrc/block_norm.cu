@@ -11,84 +11,97 @@
 
 namespace mxg {
 
-template <typename T, typename R, bool VEC, int ITER, int MAXT>
-__global__ void __launch_bounds__(MAXT) block_norm_kernel(const mxg_block_norm_t p, int team,
+// COMMON: both parts and no full gate, known when compiled -- with these left to
+// run time, a row costs a thread some 200 instructions beside the arithmetic on
+// its 8 or 16 columns, a third of all.
+template <typename T, typename R, bool VEC, int ITER, int MAXT, bool COMMON>
+__global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const mxg_block_norm_t p, int team,
                                                           int depth) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float red[2][32];
   const int nt = blockDim.x, teams = nt / team;
-  const int lane = threadIdx.x % team, cols = static_cast<int>(p.cols);
+  const int lane = threadIdx.x % team, team_id = threadIdx.x / team;
+  const int cols = static_cast<int>(p.cols);
   const float inv = 1.0f / static_cast<float>(cols);
-  const bool has_y = p.y != nullptr, has_n = p.n_out != nullptr;
-  const bool full = p.gate_mode == MXG_GATE_FULL;
+  const bool has_y = COMMON || p.y != nullptr, has_n = COMMON || p.n_out != nullptr;
+  const bool full = !COMMON && p.gate_mode == MXG_GATE_FULL;
   const int r_bytes = kHalves<R> * nt * 16, t_bytes = kHalves<T> * nt * 16;
   const int at_g = r_bytes + t_bytes;
   const int chunk_bytes = r_bytes + (has_y ? t_bytes : 0) + (full ? t_bytes : 0);
+  const int slot_bytes = ITER * chunk_bytes, ring_bytes = depth * slot_bytes;
   const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
-  const int64_t base0 = static_cast<int64_t>(blockIdx.x) * teams;
-  const int team_id = threadIdx.x / team;
-  uint8_t* mine = ring + threadIdx.x * 16;
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * 16, end = mine + ring_bytes;
+  if (VEC) ring_clear(mine, ring_bytes, nt);
+  const int c0 = RowIo<T, VEC>::col(0, 0, lane, team);
+  const int dc = RowIo<T, VEC>::col(1, 0, lane, team) - c0;  // from one chunk to the next
 
-  auto slot_at = [&](int slot, int it) { return mine + (slot * ITER + it) * chunk_bytes; };
-  auto fill = [&](int64_t base, int slot) {
-    const int64_t row = base + team_id;
-    const int limit = row < p.rows ? cols : 0;
+  int64_t f_row = static_cast<int64_t>(blockIdx.x) * teams + team_id;  // the row filled next
+  uint32_t f_at = mine;                                                // and where to
+  const R* x = static_cast<const R*>(p.x) + f_row * p.ldx + c0;
+  const T* y = static_cast<const T*>(p.y) + f_row * p.ldy + c0;
+  R* x_out = static_cast<R*>(p.x_out) + f_row * p.ldxo;
+  T* n_out = static_cast<T*>(p.n_out) + f_row * p.ldn;
+  const int64_t dx = step * p.ldx, dy = step * p.ldy, dxo = step * p.ldxo, dn = step * p.ldn;
+  auto fill = [&] {
+    if (f_row < p.rows) {
+      const T* g = static_cast<const T*>(p.gate) + f_row * p.ldg + c0;
 #pragma unroll
-    for (int it = 0; it < ITER; ++it) {
-      uint8_t* at = slot_at(slot, it);
-      ring_fill<R, VEC>(at, static_cast<const R*>(p.x) + row * p.ldx, limit, it, lane, team, nt);
-      if (has_y)
-        ring_fill<T, VEC>(at + r_bytes, static_cast<const T*>(p.y) + row * p.ldy, limit, it, lane,
-                          team, nt);
-      if (full)
-        ring_fill<T, VEC>(at + at_g, static_cast<const T*>(p.gate) + row * p.ldg, limit, it, lane,
-                          team, nt);
+      for (int it = 0; it < ITER; ++it) {
+        const uint32_t at = f_at + it * chunk_bytes;
+        const bool in = c0 + it * dc < cols;
+        ring_fill<R, VEC>(at, x + it * dc, in, cols, it, lane, team, nt);
+        if (has_y) ring_fill<T, VEC>(at + r_bytes, y + it * dc, in, cols, it, lane, team, nt);
+        if (full) ring_fill<T, VEC>(at + at_g, g + it * dc, in, cols, it, lane, team, nt);
+      }
+    } else {
+      ring_clear(f_at, slot_bytes, nt);  // a team past the last row adds nothing
     }
     if (VEC) cp_async_commit();
+    f_row += step;
+    x += dx;
+    y += dy;
+    if ((f_at += slot_bytes) == end) f_at = mine;
   };
-  for (int d = 0; d < depth - 1; ++d) fill(base0 + d * step, d);
-  const Weight<T, VEC, ITER> w_post(has_y ? p.w_post : nullptr, cols, lane, team);
-  const Weight<T, VEC, ITER> g_col(p.gate_mode == MXG_GATE_COL ? p.gate : nullptr, cols, lane, team);
-  const Weight<T, VEC, ITER> w_pre(has_n ? p.w_pre : nullptr, cols, lane, team);
+  int64_t row = f_row;
+  for (int d = 0; d < depth - 1; ++d) fill();
+  using W = Weight<T, VEC, ITER, MAXT <= 512>;
+  const W w_post(p.w_post, cols, lane, team);
+  const W g_col(p.gate_mode == MXG_GATE_COL ? p.gate : nullptr, cols, lane, team);
+  const W w_pre(p.w_pre, cols, lane, team);
 
-  int slot = 0;
-  for (int64_t base = base0; base < p.rows; base += step) {
-    const int64_t row = base + team_id;
-    const bool live = row < p.rows;
-    const int limit = live ? cols : 0;  // a team past the last row loads and stores nothing
-    const int ahead = slot + depth - 1 >= depth ? slot - 1 : slot + depth - 1;
-    fill(base + (depth - 1) * step, ahead);
+  uint32_t at0 = mine;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * teams; base < p.rows; base += step) {
+    const int limit = row < p.rows ? cols : 0;  // a team past the last row stores nothing
+    fill();
     if (VEC) cp_async_wait(depth - 1);
 
-    F2 x[ITER][4];
+    F2 s[ITER][4];  // the stream
 #pragma unroll
-    for (int it = 0; it < ITER; ++it)
-      ring_read<R, VEC>(slot_at(slot, it), limit, it, lane, team, nt, x[it]);
+    for (int it = 0; it < ITER; ++it) ring_read<R>(at0 + it * chunk_bytes, nt, s[it]);
     if (has_y) {
-      F2 y[ITER][4], q = 0;
+      F2 b[ITER][4], q = 0;  // the block's output
 #pragma unroll
       for (int it = 0; it < ITER; ++it) {
-        ring_read<T, VEC>(slot_at(slot, it) + r_bytes, limit, it, lane, team, nt, y[it]);
+        ring_read<T>(at0 + it * chunk_bytes + r_bytes, nt, b[it]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q = fma2(y[it][i], y[it][i], q);
+        for (int i = 0; i < 4; ++i) q = fma2(b[it][i], b[it][i], q);
       }
-      float s[1] = {sum2(q)};
-      team_sum(s, red[0], team);
-      float r = rsqrtf(s[0] * inv + p.eps) * p.res_scale;
-      if (p.gate_mode == MXG_GATE_ROW && live) r *= static_cast<const float*>(p.gate)[row];
+      float r = rsqrtf(team_sum(sum2(q), red[0], team) * inv + p.eps) * p.res_scale;
+      if (p.gate_mode == MXG_GATE_ROW && limit != 0) r *= static_cast<const float*>(p.gate)[row];
+      const F2 r2 = f2(r);
 #pragma unroll
       for (int it = 0; it < ITER; ++it) {
-        w_post.apply(it, y[it]);
-        g_col.apply(it, y[it]);
+        w_post.apply(it, b[it]);
+        if (p.gate_mode == MXG_GATE_COL) g_col.apply(it, b[it]);
         if (full) {
           F2 g[4];
-          ring_read<T, VEC>(slot_at(slot, it) + at_g, limit, it, lane, team, nt, g);
+          ring_read<T>(at0 + it * chunk_bytes + at_g, nt, g);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[it][i] = mul2(y[it][i], g[i]);
+          for (int i = 0; i < 4; ++i) b[it][i] = mul2(b[it][i], g[i]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[it][i] = fma2(y[it][i], f2(r), x[it][i]);
-        RowIo<R, VEC>::store(static_cast<R*>(p.x_out) + row * p.ldxo, limit, it, lane, team, x[it]);
+        for (int i = 0; i < 4; ++i) s[it][i] = fma2(b[it][i], r2, s[it][i]);
+        RowIo<R, VEC>::store(x_out, limit, it, lane, team, s[it]);
       }
     }
     if (has_n) {
@@ -96,36 +109,39 @@ __global__ void __launch_bounds__(MAXT) block_norm_kernel(const mxg_block_norm_t
 #pragma unroll
       for (int it = 0; it < ITER; ++it)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q = fma2(x[it][i], x[it][i], q);
-      float s[1] = {sum2(q)};
-      team_sum(s, red[1], team);
-      const float r = rsqrtf(s[0] * inv + p.eps);
+        for (int i = 0; i < 4; ++i) q = fma2(s[it][i], s[it][i], q);
+      const F2 r2 = f2(rsqrtf(team_sum(sum2(q), red[1], team) * inv + p.eps));
 #pragma unroll
       for (int it = 0; it < ITER; ++it) {
-        w_pre.apply(it, x[it]);
+        w_pre.apply(it, s[it]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[it][i] = mul2(x[it][i], f2(r));
-        RowIo<T, VEC>::store(static_cast<T*>(p.n_out) + row * p.ldn, limit, it, lane, team, x[it]);
+        for (int i = 0; i < 4; ++i) s[it][i] = mul2(s[it][i], r2);
+        RowIo<T, VEC>::store(n_out, limit, it, lane, team, s[it]);
       }
     }
     // one buffer in use: order its reuse
     if (team > 32 && !(has_y && has_n)) __syncthreads();
-    if (++slot >= depth) slot = 0;
+    row += step;
+    x_out += dxo;
+    n_out += dn;
+    if ((at0 += slot_bytes) == end) at0 = mine;
   }
 }
 
 namespace {
 
-template <typename T, typename R, bool VEC>
+constexpr int kWaves = 2;
+
+template <typename T, typename R, bool VEC, bool COMMON>
 cudaError_t forward_rows(const mxg_block_norm_t& p, const RowShape& r, int64_t grid, int smem,
                          int depth, cudaStream_t stream) {
   if (r.iter == 1)
-    return launch_rows(block_norm_kernel<T, R, VEC, 1, 256>, grid, r.threads, smem, stream, p,
-                       r.team, depth);
+    return launch_rows(block_norm_kernel<T, R, VEC, 1, 256, COMMON>, grid, r.threads, smem, stream,
+                       p, r.team, depth);
   if (r.threads <= 512)
-    return launch_rows(block_norm_kernel<T, R, VEC, 2, 512>, grid, r.threads, smem, stream, p,
-                       r.team, depth);
-  return launch_rows(block_norm_kernel<T, R, VEC, 2, 1024>, grid, r.threads, smem, stream, p,
+    return launch_rows(block_norm_kernel<T, R, VEC, 2, 512, COMMON>, grid, r.threads, smem, stream,
+                       p, r.team, depth);
+  return launch_rows(block_norm_kernel<T, R, VEC, 2, 1024, COMMON>, grid, r.threads, smem, stream, p,
                      r.team, depth);
 }
 
@@ -137,17 +153,21 @@ cudaError_t norm_forward(const mxg_block_norm_t& p, int num_sms, cudaStream_t st
                    aligned_rows(p.n_out, p.ldn, sizeof(T)) && aligned_rows(p.w_post, 0, sizeof(T)) &&
                    aligned_rows(p.w_pre, 0, sizeof(T)) &&
                    (p.gate_mode < MXG_GATE_COL || aligned_rows(p.gate, full ? p.ldg : 0, sizeof(T)));
-  const RowShape r = row_shape(p.cols, 256);
-  const int ctas = std::max(1, std::min(8, 768 / r.threads));  // per SM
+  const RowShape r = row_shape(p.cols, 256, 2048);
+  // CTAs an SM holds at once (64 to 72 registers a thread at 8 columns, 115 at
+  // 16), and a few times as many in the grid
+  const int ctas = std::max(1, std::min(16, (r.iter == 1 ? 896 : 512) / r.threads));
   const int64_t teams = r.threads / r.team;
-  const int64_t grid =
-      std::min<int64_t>((p.rows + teams - 1) / teams, static_cast<int64_t>(num_sms) * ctas);
+  const int64_t grid = std::min<int64_t>((p.rows + teams - 1) / teams,
+                                         static_cast<int64_t>(num_sms) * ctas * kWaves);
   // at most 192 KB a slot: 16384 columns of three fp32 inputs
   const int slot = r.threads * 8 * r.iter *
                    static_cast<int>(sizeof(R) + (p.y ? sizeof(T) : 0) + (full ? sizeof(T) : 0));
   const int depth = std::max(1, std::min(vec ? 4 : 2, kRowSmem / ctas / slot));
-  if (vec) return forward_rows<T, R, true>(p, r, grid, slot * depth, depth, stream);
-  return forward_rows<T, R, false>(p, r, grid, slot * depth, depth, stream);
+  if (!vec) return forward_rows<T, R, false, false>(p, r, grid, slot * depth, depth, stream);
+  if (p.y != nullptr && p.n_out != nullptr && !full)
+    return forward_rows<T, R, true, true>(p, r, grid, slot * depth, depth, stream);
+  return forward_rows<T, R, true, false>(p, r, grid, slot * depth, depth, stream);
 }
 
 }  // namespace

@@ -7,10 +7,11 @@
 //   dgate = s t . yh . w_post, summed over the axes the gate is broadcast along
 // rx and ry are made again from x' and y, which are read anyway.
 //
-// One pass over the rows (rows.cuh): a first reduction gives rx, ry and
-// mean(a . xh), a second one mean(b . yh).  The column sums of a CTA's rows stay
-// in registers and leave one partial row per CTA; a second kernel adds those in
-// a fixed order.
+// One pass over the rows (rows.cuh).  Two reductions make a row: rx, ry and
+// mean(a . xh), then mean(b . yh).  The first is taken a row ahead, together with
+// the second one of the row before, so that a row costs one barrier.  The
+// column sums of a CTA's rows stay in registers and leave one partial row per
+// CTA; a second kernel adds those in a fixed order.
 #include "rows.cuh"
 
 namespace mxg {
@@ -20,6 +21,7 @@ namespace mxg {
 constexpr int kNormMaxSms = 160;
 constexpr int kBwdCta = 128;  // CTA size of the narrow rows
 
+constexpr int kWaves = 1;
 static int bwd_ctas(const RowShape& r) { return std::max(1, std::min(8, 512 / r.threads)); }
 
 // Column sums of this CTA's rows go to the workspace [block][2][cols]:
@@ -27,61 +29,78 @@ static int bwd_ctas(const RowShape& r) { return std::max(1, std::min(8, 512 / r.
 // rows (row, full) and 1 otherwise; the finish kernel applies what is constant
 // down a column.
 // lean: dx' and a full gate do not come through the ring (rows so wide that it
-// would not hold them).
-template <typename T, typename R, bool VEC, int ITER, int MAXT>
-__global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const mxg_block_norm_grad_t p,
+// would not hold two of them).
+// COMMON: all inputs, no full gate and not lean, known when compiled.
+template <typename T, typename R, bool VEC, int ITER, int MAXT, bool COMMON>
+__global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(const mxg_block_norm_grad_t p,
                                                               float* ws, int team, int depth,
-                                                              bool lean) {
+                                                              bool is_lean) {
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float red[2][96];
+  __shared__ float red[3][128];
   const int nt = blockDim.x, teams = nt / team;
-  const int lane = threadIdx.x % team, cols = static_cast<int>(p.cols);
+  const int lane = threadIdx.x % team, team_id = threadIdx.x / team;
+  const int cols = static_cast<int>(p.cols);
   const float inv = 1.0f / static_cast<float>(cols);
-  const bool has_y = p.y != nullptr, has_n = p.dn != nullptr, has_x = p.dx_out != nullptr;
-  const bool full = p.gate_mode == MXG_GATE_FULL;
+  const bool has_y = COMMON || p.y != nullptr, has_n = COMMON || p.dn != nullptr;
+  const bool has_x = COMMON || p.dx_out != nullptr;
+  const bool full = !COMMON && p.gate_mode == MXG_GATE_FULL, lean = !COMMON && is_lean;
   const int r_bytes = kHalves<R> * nt * 16, t_bytes = kHalves<T> * nt * 16;
   // places of x', dn, y, dx' and the gate in a chunk
   const int at_n = has_n ? r_bytes : 0, at_y = at_n + (has_n ? t_bytes : 0);
   const int at_x = at_y + (has_y ? t_bytes : 0), at_g = at_x + (has_x && !lean ? r_bytes : 0);
   const int chunk_bytes = at_g + (full && !lean ? t_bytes : 0);
+  const int slot_bytes = ITER * chunk_bytes, ring_bytes = depth * slot_bytes;
   const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
-  const int64_t base0 = static_cast<int64_t>(blockIdx.x) * teams;
-  const int team_id = threadIdx.x / team;
-  uint8_t* mine = ring + threadIdx.x * 16;
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * 16, end = mine + ring_bytes;
+  if (VEC) ring_clear(mine, ring_bytes, nt);
+  const int c0 = RowIo<T, VEC>::col(0, 0, lane, team);
+  const int dc = RowIo<T, VEC>::col(1, 0, lane, team) - c0;  // from one chunk to the next
 
-  auto slot_at = [&](int slot, int it) { return mine + (slot * ITER + it) * chunk_bytes; };
-  auto fill = [&](int64_t base, int slot) {
-    const int64_t row = base + team_id;
-    const int limit = row < p.rows ? cols : 0;
+  int64_t f_row = static_cast<int64_t>(blockIdx.x) * teams + team_id;  // the row filled next
+  uint32_t f_at = mine;                                                // and where to
+  const R* x = static_cast<const R*>(p.x) + f_row * p.ldx + c0;
+  const T* n = static_cast<const T*>(p.dn) + f_row * p.lddn + c0;
+  const T* y = static_cast<const T*>(p.y) + f_row * p.ldy + c0;
+  const R* d = static_cast<const R*>(p.dx_out) + f_row * p.lddxo + c0;
+  R* dx = static_cast<R*>(p.dx) + f_row * p.lddx;
+  T* dy = static_cast<T*>(p.dy) + f_row * p.lddy;
+  auto fill = [&] {
+    if (f_row < p.rows) {
+      const T* g = static_cast<const T*>(p.gate) + f_row * p.ldg + c0;
 #pragma unroll
-    for (int it = 0; it < ITER; ++it) {
-      uint8_t* at = slot_at(slot, it);
-      if (has_n) {
-        ring_fill<R, VEC>(at, static_cast<const R*>(p.x) + row * p.ldx, limit, it, lane, team, nt);
-        ring_fill<T, VEC>(at + at_n, static_cast<const T*>(p.dn) + row * p.lddn, limit, it, lane,
-                          team, nt);
+      for (int it = 0; it < ITER; ++it) {
+        const uint32_t at = f_at + it * chunk_bytes;
+        const int o = it * dc;
+        const bool in = c0 + o < cols;
+        if (has_n) {
+          ring_fill<R, VEC>(at, x + o, in, cols, it, lane, team, nt);
+          ring_fill<T, VEC>(at + at_n, n + o, in, cols, it, lane, team, nt);
+        }
+        if (has_y) ring_fill<T, VEC>(at + at_y, y + o, in, cols, it, lane, team, nt);
+        if (has_x && !lean) ring_fill<R, VEC>(at + at_x, d + o, in, cols, it, lane, team, nt);
+        if (full && !lean) ring_fill<T, VEC>(at + at_g, g + o, in, cols, it, lane, team, nt);
       }
-      if (has_y)
-        ring_fill<T, VEC>(at + at_y, static_cast<const T*>(p.y) + row * p.ldy, limit, it, lane,
-                          team, nt);
-      if (has_x && !lean)
-        ring_fill<R, VEC>(at + at_x, static_cast<const R*>(p.dx_out) + row * p.lddxo, limit, it,
-                          lane, team, nt);
-      if (full && !lean)
-        ring_fill<T, VEC>(at + at_g, static_cast<const T*>(p.gate) + row * p.ldg, limit, it, lane,
-                          team, nt);
+    } else {
+      ring_clear(f_at, slot_bytes, nt);  // a team past the last row adds nothing
     }
     if (VEC) cp_async_commit();
+    f_row += step;
+    x += step * p.ldx;
+    n += step * p.lddn;
+    y += step * p.ldy;
+    d += step * p.lddxo;
+    if ((f_at += slot_bytes) == end) f_at = mine;
   };
-  for (int d = 0; d < depth - 1; ++d) fill(base0 + d * step, d);
+  int64_t row = f_row;
+  for (int d = 0; d < depth - 1; ++d) fill();
 
-  const Weight<T, VEC, ITER> w_pre(has_n ? p.w_pre : nullptr, cols, lane, team);
-  // w_post times a gate per channel, in fp32
-  F2 wg[ITER][4];
-  {
-    const Weight<T, VEC, ITER> w_post(has_y ? p.w_post : nullptr, cols, lane, team);
-    const Weight<T, VEC, ITER> g_col(p.gate_mode == MXG_GATE_COL ? p.gate : nullptr, cols, lane,
-                                     team);
+  constexpr bool REG = MAXT <= 512;
+  using W = Weight<T, VEC, ITER, REG>;
+  const W w_pre(p.w_pre, cols, lane, team);
+  const W w_post(p.w_post, cols, lane, team);
+  const W g_col(p.gate_mode == MXG_GATE_COL ? p.gate : nullptr, cols, lane, team);
+  F2 wg[REG ? ITER : 1][4];  // w_post times a gate per channel, in fp32
+  if constexpr (REG) {
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
 #pragma unroll
@@ -90,97 +109,112 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const mxg_block_no
       g_col.apply(it, wg[it]);
     }
   }
+  auto times_wg = [&](int it, F2(&f)[4]) {
+    if constexpr (REG) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], wg[it][i]);
+    } else {
+      w_post.apply(it, f);
+      g_col.apply(it, f);
+    }
+  };
 
-  F2 s0[ITER][4] = {}, s1[ITER][4] = {};
-  int slot = 0;
-  for (int64_t base = base0; base < p.rows; base += step) {
-    const int64_t row = base + team_id;
-    const bool live = row < p.rows;
-    const int limit = live ? cols : 0;
-    const int ahead = slot + depth - 1 >= depth ? slot - 1 : slot + depth - 1;
-    fill(base + (depth - 1) * step, ahead);
-    if (VEC) cp_async_wait(depth - 1);
-    auto get_r = [&](int at, int it, F2(&f)[4]) {
-      ring_read<R, VEC>(slot_at(slot, it) + at, limit, it, lane, team, nt, f);
-    };
-    auto get_t = [&](int at, int it, F2(&f)[4]) {
-      ring_read<T, VEC>(slot_at(slot, it) + at, limit, it, lane, team, nt, f);
-    };
-    auto get_gate = [&](int it, F2(&f)[4]) {
-      if (lean)
-        unpack8<T>(RowIo<T, VEC>::load(static_cast<const T*>(p.gate) + row * p.ldg, limit, it, lane,
-                                       team),
-                   f);
-      else
-        get_t(at_g, it, f);
-    };
-
-    // ---- the sums that need nothing else
-    F2 v0 = 0, v1 = 0, v2 = 0;
+  // this thread's share of sum x'^2, sum a . x' and sum y^2 of the row at `at0`
+  auto row_sums = [&](uint32_t at0, float(&v)[4]) {
+    F2 v1 = 0, v2 = 0, v3 = 0;
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
+      const uint32_t at = at0 + it * chunk_bytes;
       if (has_n) {
         F2 x[4], a[4];
-        get_r(0, it, x);
-        get_t(at_n, it, a);
+        ring_read<R>(at, nt, x);
+        ring_read<T>(at + at_n, nt, a);
         w_pre.apply(it, a);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          v0 = fma2(x[i], x[i], v0);
-          v1 = fma2(a[i], x[i], v1);
+          v1 = fma2(x[i], x[i], v1);
+          v2 = fma2(a[i], x[i], v2);
         }
       }
       if (has_y) {
         F2 y[4];
-        get_t(at_y, it, y);
+        ring_read<T>(at + at_y, nt, y);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v2 = fma2(y[i], y[i], v2);
+        for (int i = 0; i < 4; ++i) v3 = fma2(y[i], y[i], v3);
       }
     }
-    float v[3] = {sum2(v0), sum2(v1), sum2(v2)};
-    team_sum(v, red[0], team);
-    const float rx = rsqrtf(v[0] * inv + p.eps), ry = rsqrtf(v[2] * inv + p.eps);
-    const float c = v[1] * inv * rx;  // mean(a . xh)
+    v[1] = sum2(v1);
+    v[2] = sum2(v2);
+    v[3] = sum2(v3);
+  };
+
+  F2 s0[ITER][4] = {}, s1[ITER][4] = {};
+  uint32_t at0 = mine;
+  const bool ahead = depth > 1;  // the ring holds the next row too
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (ahead) {
+    if (VEC) cp_async_wait(depth - 2);
+    row_sums(at0, v);
+    team_sum4(v, red[2], team);
+  }
+  int parity = 0;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * teams; base < p.rows; base += step) {
+    const int limit = row < p.rows ? cols : 0;
+    const uint32_t next = at0 + slot_bytes == end ? mine : at0 + slot_bytes;
+    fill();
+    if (!ahead) {
+      if (VEC) cp_async_wait(0);
+      row_sums(at0, v);
+      team_sum4(v, red[2], team);
+    }
+    const float rx = rsqrtf(v[1] * inv + p.eps), ry = rsqrtf(v[3] * inv + p.eps);
+    const float c = v[2] * inv * rx;  // mean(a . xh)
 
     // ---- t, its column sums, and the sum for dy
-    const float gr = p.gate_mode == MXG_GATE_ROW && live ? static_cast<const float*>(p.gate)[row]
-                                                         : 1.0f;
+    const float gr = p.gate_mode == MXG_GATE_ROW && limit != 0
+                         ? static_cast<const float*>(p.gate)[row]
+                         : 1.0f;
+    const F2 rx2 = f2(rx), k2 = f2(-rx * rx * c), gy2 = f2(gr * ry);
     F2 t[ITER][4], q2 = 0;
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
-      zero4(t[it]);
-      if (has_x) {
-        if (lean)
-          unpack8<R>(RowIo<R, VEC>::load(static_cast<const R*>(p.dx_out) + row * p.lddxo, limit, it,
-                                         lane, team),
-                     t[it]);
-        else
-          get_r(at_x, it, t[it]);
-      }
+      const uint32_t at = at0 + it * chunk_bytes;
+      if (!has_x)
+        zero4(t[it]);
+      else if (lean)
+        unpack8<R>(RowIo<R, VEC>::load(static_cast<const R*>(p.dx_out) + row * p.lddxo, limit, it,
+                                       lane, team),
+                   t[it]);
+      else
+        ring_read<R>(at + at_x, nt, t[it]);
       if (has_n) {
         F2 x[4], a[4];
-        get_r(0, it, x);
-        get_t(at_n, it, a);
+        ring_read<R>(at, nt, x);
+        ring_read<T>(at + at_n, nt, a);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s0[it][i] = fma2(mul2(a[i], x[i]), f2(rx), s0[it][i]);
+        for (int i = 0; i < 4; ++i) s0[it][i] = fma2(mul2(a[i], x[i]), rx2, s0[it][i]);
         w_pre.apply(it, a);
         // rx (a - xh c) = rx a - (rx rx c) x'
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          t[it][i] = fma2(x[i], f2(-rx * rx * c), fma2(a[i], f2(rx), t[it][i]));
+        for (int i = 0; i < 4; ++i) t[it][i] = fma2(x[i], k2, fma2(a[i], rx2, t[it][i]));
       }
-      RowIo<R, VEC>::store(static_cast<R*>(p.dx) + row * p.lddx, limit, it, lane, team, t[it]);
+      RowIo<R, VEC>::store(dx, limit, it, lane, team, t[it]);
       if (has_y) {
         F2 y[4];
-        get_t(at_y, it, y);
+        ring_read<T>(at + at_y, nt, y);
         if (full) {
           F2 g[4];
-          get_gate(it, g);
+          if (lean)
+            unpack8<T>(RowIo<T, VEC>::load(static_cast<const T*>(p.gate) + row * p.ldg, limit, it,
+                                           lane, team),
+                       g);
+          else
+            ring_read<T>(at + at_g, nt, g);
           if (p.dgate != nullptr) {
             F2 dg[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dg[i] = mul2(mul2(t[it][i], wg[it][i]), mul2(y[i], f2(p.res_scale * ry)));
+            for (int i = 0; i < 4; ++i) dg[i] = mul2(t[it][i], mul2(y[i], f2(p.res_scale * ry)));
+            times_wg(it, dg);
             RowIo<T, VEC>::store(static_cast<T*>(p.dgate) + row * p.lddg, limit, it, lane, team,
                                  dg);
           }
@@ -188,33 +222,38 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const mxg_block_no
           for (int i = 0; i < 4; ++i) t[it][i] = mul2(t[it][i], g[i]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const F2 ty = mul2(t[it][i], y[i]);
-          s1[it][i] = fma2(ty, f2(gr * ry), s1[it][i]);
-          t[it][i] = mul2(t[it][i], wg[it][i]);  // b but for the factor of the whole row
-          q2 = fma2(t[it][i], y[i], q2);
-        }
+        for (int i = 0; i < 4; ++i) s1[it][i] = fma2(mul2(t[it][i], y[i]), gy2, s1[it][i]);
+        times_wg(it, t[it]);  // b but for the factor of the whole row
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q2 = fma2(t[it][i], y[i], q2);
       }
     }
+    v[0] = sum2(q2);
+    if (ahead) {
+      if (VEC) cp_async_wait(depth - 2);
+      row_sums(next, v);
+    }
+    team_sum4(v, red[parity], team);
+    parity ^= 1;
     if (has_y) {
-      float q[1] = {sum2(q2)};
-      team_sum(q, red[1], team);
-      if (p.gate_mode == MXG_GATE_ROW && p.dgate != nullptr && lane == 0 && live)
-        static_cast<float*>(p.dgate)[row] = p.res_scale * ry * q[0];
-      const float fr = p.res_scale * gr * ry, m = q[0] * inv * ry;  // m: mean(b . yh) / f
+      if (p.gate_mode == MXG_GATE_ROW && p.dgate != nullptr && lane == 0 && limit != 0)
+        static_cast<float*>(p.dgate)[row] = p.res_scale * ry * v[0];
+      // dy = fr (b - y ry m) with m = mean(b . yh)
+      const float fr = p.res_scale * gr * ry, m = v[0] * inv * ry;
+      const F2 fr2 = f2(fr), my2 = f2(-fr * ry * m);
 #pragma unroll
       for (int it = 0; it < ITER; ++it) {
         F2 y[4];
-        get_t(at_y, it, y);
+        ring_read<T>(at0 + it * chunk_bytes + at_y, nt, y);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          t[it][i] = mul2(fma2(y[i], f2(-ry * m), t[it][i]), f2(fr));
-        RowIo<T, VEC>::store(static_cast<T*>(p.dy) + row * p.lddy, limit, it, lane, team, t[it]);
+        for (int i = 0; i < 4; ++i) t[it][i] = fma2(y[i], my2, mul2(t[it][i], fr2));
+        RowIo<T, VEC>::store(dy, limit, it, lane, team, t[it]);
       }
-    } else if (team > 32) {
-      __syncthreads();
     }
-    if (++slot >= depth) slot = 0;
+    row += step;
+    dx += step * p.lddx;
+    dy += step * p.lddy;
+    at0 = next;
   }
 
   // ---- this CTA's partial row
@@ -248,7 +287,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const mxg_block_no
 
 // Column sums of `blocks` partial rows, in a fixed order: 32 columns a CTA,
 // kSlices threads a column.
-constexpr int kSlices = 16;
+constexpr int kSlices = 32;
 template <typename T>
 __global__ void __launch_bounds__(32 * kSlices)
     block_norm_bwd_finish_kernel(const mxg_block_norm_grad_t p, const float* ws, int blocks) {
@@ -285,17 +324,17 @@ __global__ void __launch_bounds__(32 * kSlices)
 
 namespace {
 
-template <typename T, typename R, bool VEC>
+template <typename T, typename R, bool VEC, bool COMMON>
 cudaError_t backward_rows(const mxg_block_norm_grad_t& p, float* ws, const RowShape& r,
                           int64_t grid, int smem, int depth, bool lean, cudaStream_t stream) {
   if (r.iter == 1)
-    return launch_rows(block_norm_bwd_kernel<T, R, VEC, 1, 256>, grid, r.threads, smem, stream, p,
-                       ws, r.team, depth, lean);
+    return launch_rows(block_norm_bwd_kernel<T, R, VEC, 1, 512, COMMON>, grid, r.threads, smem,
+                       stream, p, ws, r.team, depth, lean);
   if (r.threads <= 512)
-    return launch_rows(block_norm_bwd_kernel<T, R, VEC, 2, 512>, grid, r.threads, smem, stream, p,
-                       ws, r.team, depth, lean);
-  return launch_rows(block_norm_bwd_kernel<T, R, VEC, 2, 1024>, grid, r.threads, smem, stream, p,
-                     ws, r.team, depth, lean);
+    return launch_rows(block_norm_bwd_kernel<T, R, VEC, 2, 512, COMMON>, grid, r.threads, smem,
+                       stream, p, ws, r.team, depth, lean);
+  return launch_rows(block_norm_bwd_kernel<T, R, VEC, 2, 1024, COMMON>, grid, r.threads, smem,
+                     stream, p, ws, r.team, depth, lean);
 }
 
 template <typename T, typename R>
@@ -310,25 +349,28 @@ cudaError_t norm_backward(const mxg_block_norm_grad_t& p, float* ws, int num_sms
                    aligned_rows(p.w_pre, 0, sizeof(T)) &&
                    (p.gate_mode < MXG_GATE_COL || aligned_rows(p.gate, full ? p.ldg : 0, sizeof(T))) &&
                    (!full || aligned_rows(p.dgate, p.lddg, sizeof(T)));
-  const RowShape r = row_shape(p.cols, kBwdCta);
+  const RowShape r = row_shape(p.cols, kBwdCta, 4096);
   const int ctas = bwd_ctas(r);
   const int64_t teams = r.threads / r.team;
   const int64_t grid = std::min<int64_t>((p.rows + teams - 1) / teams,
-                                         static_cast<int64_t>(std::min(num_sms, kNormMaxSms)) * ctas);
+                                         static_cast<int64_t>(std::min(num_sms, kNormMaxSms)) * ctas * kWaves);
   if (grid > 0) {
     const int chunk = r.threads * 8 * r.iter;
     const int core = static_cast<int>((p.dn ? sizeof(R) + sizeof(T) : 0) + (p.y ? sizeof(T) : 0));
     const int rest = static_cast<int>((p.dx_out ? sizeof(R) : 0) + (full ? sizeof(T) : 0));
-    const bool lean = chunk * (core + rest) > kRowSmem;  // the core is at most 192 KB
+    // without dx' and a full gate where the ring could not hold two rows else;
+    // the rest is at most 192 KB a row
+    const bool lean = chunk * (core + rest) * 2 > kRowSmem && core > 0;
     const int slot = chunk * (core + (lean ? 0 : rest));
-    const int depth =
-        slot == 0 ? 1 : std::max(1, std::min(vec ? 4 : 2, kRowSmem / ctas / slot));
+    const int depth = std::max(1, std::min(vec ? 4 : 2, kRowSmem / ctas / slot));
     // narrow rows: the teams' column sums meet where the ring was
     const int sums = teams > 1 ? static_cast<int>(teams * 2 * p.cols * sizeof(float)) : 0;
     const int smem = std::max(slot * depth, sums);
+    const bool common = vec && p.y && p.dn && p.dx_out && !full && !lean;
     const cudaError_t e =
-        vec ? backward_rows<T, R, true>(p, ws, r, grid, smem, depth, lean, stream)
-            : backward_rows<T, R, false>(p, ws, r, grid, smem, depth, lean, stream);
+        common ? backward_rows<T, R, true, true>(p, ws, r, grid, smem, depth, lean, stream)
+        : vec  ? backward_rows<T, R, true, false>(p, ws, r, grid, smem, depth, lean, stream)
+               : backward_rows<T, R, false, false>(p, ws, r, grid, smem, depth, lean, stream);
     if (e != cudaSuccess) return e;
   }
   block_norm_bwd_finish_kernel<T>
@@ -340,8 +382,8 @@ cudaError_t norm_backward(const mxg_block_norm_grad_t& p, float* ws, int num_sms
 }  // namespace
 
 int64_t block_norm_ws_bytes(int64_t rows, int64_t cols) {
-  const RowShape r = row_shape(cols, kBwdCta);
-  return std::min<int64_t>(rows, static_cast<int64_t>(kNormMaxSms) * bwd_ctas(r)) * 2 * cols * 4;
+  const RowShape r = row_shape(cols, kBwdCta, 4096);
+  return std::min<int64_t>(rows, static_cast<int64_t>(kNormMaxSms) * bwd_ctas(r) * kWaves) * 2 * cols * 4;
 }
 
 cudaError_t launch_block_norm_backward(const mxg_block_norm_grad_t& p, float* ws, int num_sms,

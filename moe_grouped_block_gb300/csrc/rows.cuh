@@ -23,10 +23,8 @@ struct RowShape {
   int iter;     // chunks of 8 columns per thread
 };
 
-// Above 2048 columns 16 a thread: a row's reductions cost a warp some 60
-// instructions whatever its width, and at 8 columns a thread (512 threads on
-// 4096 columns) they were a third of all that was issued.
-inline RowShape row_shape(int64_t cols, int small_cta) {
+// `wide`: columns above which a thread takes 16 of them.
+inline RowShape row_shape(int64_t cols, int small_cta, int64_t wide) {
   RowShape r;
   if (cols <= 256) {
     r.team = 8;
@@ -34,7 +32,7 @@ inline RowShape row_shape(int64_t cols, int small_cta) {
     r.threads = small_cta;
     r.iter = 1;
   } else {
-    r.iter = cols > 2048 ? 2 : 1;
+    r.iter = cols > wide ? 2 : 1;
     r.team = static_cast<int>((cols + 8 * r.iter - 1) / (8 * r.iter) + 31) / 32 * 32;
     r.threads = r.team;
   }
@@ -177,39 +175,50 @@ struct RowIo {
 };
 
 // ---------------------------------------------------------------- the ring
-// Slot, then chunk, then input, then 16-byte half, then thread.
+// Slot, then chunk, then input, then 16-byte half, then thread.  Its addresses
+// are 32-bit shared-memory ones: as generic pointers they cost two instructions
+// at each of the dozen places that form one for a row.
 template <typename T>
 constexpr int kHalves = static_cast<int>(sizeof(T)) / 2;
 
-// One chunk of an input into the ring: asynchronously where rows come in
-// vectors, through registers where they do not.  Columns past `cols` are left
-// out (VEC) or zero.
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+
+// One chunk of an input into the ring, `src` being the thread's first column of
+// it: copied asynchronously where rows come in vectors, through registers where
+// they do not.  `in`: the chunk lies in the row (VEC).
 template <typename T, bool VEC>
-__device__ __forceinline__ void ring_fill(uint8_t* at, const T* row, int cols, int it, int lane,
-                                          int team, int nt) {
+__device__ __forceinline__ void ring_fill(uint32_t at, const T* src, bool in, int cols, int it,
+                                          int lane, int team, int nt) {
   if constexpr (VEC) {
-    const int c = RowIo<T, VEC>::col(it, 0, lane, team);
-    if (c < cols)
+    if (in)
 #pragma unroll
       for (int h = 0; h < kHalves<T>; ++h)
-        cp_async_16_l2(smem_u32(at + h * nt * 16),
-                       reinterpret_cast<const uint8_t*>(row + c) + 16 * h);
+        cp_async_16_l2(at + h * nt * 16, reinterpret_cast<const uint8_t*>(src) + 16 * h);
   } else {
-    const Raw8<T> v = RowIo<T, VEC>::load(row, cols, it, lane, team);
-    *reinterpret_cast<uint4*>(at) = v.q;
-    if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(at + nt * 16) = v.r;
+    const Raw8<T> v =
+        RowIo<T, VEC>::load(src - RowIo<T, VEC>::col(it, 0, lane, team), cols, it, lane, team);
+    st_shared_v4(at, v.q.x, v.q.y, v.q.z, v.q.w);
+    if constexpr (sizeof(T) == 4) st_shared_v4(at + nt * 16, v.r.x, v.r.y, v.r.z, v.r.w);
   }
 }
-// A chunk back out of it; 0 for a thread whose columns are past `cols`.
-template <typename T, bool VEC>
-__device__ __forceinline__ void ring_read(const uint8_t* at, int cols, int it, int lane, int team,
-                                          int nt, F2 (&f)[4]) {
-  Raw8<T> v{};
-  if (RowIo<T, VEC>::col(it, 0, lane, team) < cols) {
-    v.q = *reinterpret_cast<const uint4*>(at);
-    if constexpr (sizeof(T) == 4) v.r = *reinterpret_cast<const uint4*>(at + nt * 16);
-  }
+// A chunk back out of it.
+template <typename T>
+__device__ __forceinline__ void ring_read(uint32_t at, int nt, F2 (&f)[4]) {
+  Raw8<T> v;
+  v.q = lds16(at);
+  if constexpr (sizeof(T) == 4) v.r = lds16(at + nt * 16);
   unpack8<T>(v, f);
+}
+// Zeros in this thread's pieces of `bytes` bytes of the ring.
+__device__ __forceinline__ void ring_clear(uint32_t mine, int bytes, int nt) {
+  for (int o = 0; o < bytes; o += nt * 16) st_shared_v4(mine + o, 0, 0, 0, 0);
 }
 
 // All but the newest `n` groups of this thread's copies have landed.
@@ -224,62 +233,96 @@ __device__ __forceinline__ void cp_async_wait(int n) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// A thread's columns of a weight, kept in registers as they lie in memory: read
-// again for each row, they come from L2, since the ring leaves L1 little room.
-template <typename T, bool VEC, int ITER>
+// A thread's columns of a weight (ones where there is none).  REG: kept in
+// registers as they lie in memory -- read again for each row, they come from L2,
+// since the ring leaves L1 little room.  Rows of over 8192 columns have no
+// registers to spare and do that.
+template <typename T, bool VEC, int ITER, bool REG>
 struct Weight {
-  Raw8<T> raw[ITER];
-  bool present;
+  Raw8<T> raw[REG ? ITER : 1];
+  const T* at;
+  int cols, lane, team;
   __device__ __forceinline__ Weight(const void* w, int cols, int lane, int team)
-      : present(w != nullptr) {
+      : at(static_cast<const T*>(w)), cols(cols), lane(lane), team(team) {
+    if constexpr (REG) {
+      F2 one[4] = {f2(1.0f), f2(1.0f), f2(1.0f), f2(1.0f)};
 #pragma unroll
-    for (int it = 0; it < ITER; ++it)
-      raw[it] = RowIo<T, VEC>::load(static_cast<const T*>(w), present ? cols : 0, it, lane, team);
+      for (int it = 0; it < ITER; ++it)
+        raw[it] = w != nullptr ? RowIo<T, VEC>::load(at, cols, it, lane, team) : pack8<T>(one);
+    }
   }
   // f *= weight
   __device__ __forceinline__ void apply(int it, F2 (&f)[4]) const {
-    if (!present) return;
     F2 w[4];
-    unpack8<T>(raw[it], w);
+    if constexpr (REG) {
+      unpack8<T>(raw[it], w);
+    } else {
+      if (at == nullptr) return;
+      unpack8<T>(RowIo<T, VEC>::load(at, cols, it, lane, team), w);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], w[i]);
   }
 };
 
 // ---------------------------------------------------------------- sums
-// Sums of NV values over the team, in a fixed order.  For teams of more than a
-// warp (the whole CTA) `buf` holds 32 * NV floats, and is written again only
-// after another team_sum on another buffer, or a barrier, has passed.
-template <int NV>
-__device__ __forceinline__ void team_sum(float (&v)[NV], float* buf, int team) {
-  if (team >= 32) {
+// Sums over the team, in a fixed order, of one value or of four.  For teams of
+// more than a warp (the whole CTA) `buf` holds 32 floats a value, and is written
+// again only after another such sum on another buffer, or a barrier, has
+// passed.
+__device__ __forceinline__ float lanes_sum(float v, int span) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], d);
-    if (team == 32) return;
-    const int warps = team >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) buf[i * 32 + w] = v[i];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = lane < warps ? buf[i * 32 + lane] : 0.0f;
-    // 8 warps: three steps in lanes 0-7, read from lane 0
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-      if (d < warps)
-#pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], d);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, v[i], 0);
-  } else {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-      if (d < team)
-#pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], d);
+  for (int d = 16; d > 0; d >>= 1)
+    if (d < span) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  return v;
+}
+
+__device__ __forceinline__ float team_sum(float v, float* buf, int team) {
+  if (team < 32) return lanes_sum(v, team);
+  v = lanes_sum(v, 32);
+  if (team == 32) return v;
+  const int warps = team >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) buf[w] = v;
+  __syncthreads();
+  v = lane < warps ? buf[lane] : 0.0f;
+  if (warps <= 8) {
+    v = lanes_sum(v, 8);
+    return __shfl_sync(0xFFFFFFFFu, v, 0);
   }
+  return lanes_sum(v, 32);
+}
+
+// Four at once.  Within a warp the lanes halve the values between them as they
+// halve the span, so that four sums cost 6 shuffles and not 20.
+__device__ __forceinline__ void team_sum4(float (&v)[4], float* buf, int team) {
+  if (team < 32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = lanes_sum(v[i], team);
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  const bool h16 = (lane & 16) != 0, h8 = (lane & 8) != 0;
+  // lanes with bit 4 take values 2 and 3, the others 0 and 1; bit 3 then
+  // chooses within the pair
+  float a = h16 ? v[2] : v[0], b = h16 ? v[3] : v[1];
+  a += __shfl_xor_sync(0xFFFFFFFFu, h16 ? v[0] : v[2], 16);
+  b += __shfl_xor_sync(0xFFFFFFFFu, h16 ? v[1] : v[3], 16);
+  float s = h8 ? b : a;
+  s += __shfl_xor_sync(0xFFFFFFFFu, h8 ? a : b, 8);
+  s = lanes_sum(s, 8);
+  if (team > 32) {
+    const int warps = team >> 5, w = threadIdx.x >> 5, j = lane & 7;
+    float* mine = buf + (lane >> 3) * 32;
+    if (j == 0) mine[w] = s;
+    __syncthreads();
+    s = j < warps ? mine[j] : 0.0f;
+#pragma unroll
+    for (int k = 8; k < 32; k += 8)
+      if (j + k < warps) s += mine[j + k];
+    s = lanes_sum(s, 8);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, s, 8 * i);
 }
 
 }  // namespace mxg
