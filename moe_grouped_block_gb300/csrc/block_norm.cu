@@ -69,11 +69,18 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const mxg_block_nor
   const W g_col(p.gate_mode == MXG_GATE_COL ? p.gate : nullptr, cols, lane, team);
   const W w_pre(p.w_pre, cols, lane, team);
 
+  // a row's gate is asked for a row ahead: its latency is that of memory
+  const bool g_row = p.gate_mode == MXG_GATE_ROW;
+  auto row_gate = [&](int64_t r) {
+    return g_row && r < p.rows ? static_cast<const float*>(p.gate)[r] : 1.0f;
+  };
+  float gr = row_gate(row);
   uint32_t at0 = mine;
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * teams; base < p.rows; base += step) {
     const int limit = row < p.rows ? cols : 0;  // a team past the last row stores nothing
     fill();
     if (VEC) cp_async_wait(depth - 1);
+    const float gr_next = row_gate(row + step);
 
     F2 s[ITER][4];  // the stream
 #pragma unroll
@@ -86,8 +93,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const mxg_block_nor
 #pragma unroll
         for (int i = 0; i < 4; ++i) q = fma2(b[it][i], b[it][i], q);
       }
-      float r = rsqrtf(team_sum(sum2(q), red[0], team) * inv + p.eps) * p.res_scale;
-      if (p.gate_mode == MXG_GATE_ROW && limit != 0) r *= static_cast<const float*>(p.gate)[row];
+      const float r = rsqrtf(team_sum(sum2(q), red[0], team) * inv + p.eps) * p.res_scale * gr;
       const F2 r2 = f2(r);
 #pragma unroll
       for (int it = 0; it < ITER; ++it) {
@@ -121,6 +127,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const mxg_block_nor
     }
     // one buffer in use: order its reuse
     if (team > 32 && !(has_y && has_n)) __syncthreads();
+    gr = gr_next;
     row += step;
     x_out += dxo;
     n_out += dn;

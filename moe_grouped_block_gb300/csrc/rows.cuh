@@ -161,8 +161,16 @@ struct RowIo {
       const int c = col(it, 0, lane, team);
       if (c < cols) {
         const Raw8<T> v = pack8<T>(f);
+        if constexpr (sizeof(T) == 4) {
+          // whole 32-byte sectors, where the row allows it
+          if ((reinterpret_cast<uintptr_t>(row) & 31u) == 0) {
+            const uint32_t w[8] = {v.q.x, v.q.y, v.q.z, v.q.w, v.r.x, v.r.y, v.r.z, v.r.w};
+            st_global_32B(row + c, w);
+            return;
+          }
+          reinterpret_cast<uint4*>(row + c)[1] = v.r;
+        }
         reinterpret_cast<uint4*>(row + c)[0] = v.q;
-        if constexpr (sizeof(T) == 4) reinterpret_cast<uint4*>(row + c)[1] = v.r;
       }
     } else {
 #pragma unroll
