@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(const mxg_block
   const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
   const uint32_t mine = smem_u32(ring) + threadIdx.x * 16, end = mine + ring_bytes;
   if (VEC) ring_clear(mine, ring_bytes, nt);
+  grid_launch_dependents();
   const int c0 = RowIo<T, VEC>::col(0, 0, lane, team);
   const int dc = RowIo<T, VEC>::col(1, 0, lane, team) - c0;  // from one chunk to the next
 
@@ -325,6 +326,7 @@ template <typename T>
 __global__ void __launch_bounds__(32 * kSlices)
     block_norm_bwd_finish_kernel(const mxg_block_norm_grad_t p, const float* ws, int blocks) {
   __shared__ float part[2][kSlices][32];
+  grid_wait_for_previous();
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int cols = static_cast<int>(p.cols), c = blockIdx.x * 32 + lane;
   float a0 = 0.0f, a1 = 0.0f;
@@ -406,10 +408,9 @@ cudaError_t norm_backward(const mxg_block_norm_grad_t& p, float* ws, int num_sms
                : backward_rows<T, R, false, false>(p, ws, r, grid, smem, depth, lean, stream);
     if (e != cudaSuccess) return e;
   }
-  block_norm_bwd_finish_kernel<T>
-      <<<static_cast<unsigned>((p.cols + 31) / 32), 32 * kSlices, 0, stream>>>(
-          p, ws, static_cast<int>(grid));
-  return cudaGetLastError();
+  return launch_after(grid > 0, block_norm_bwd_finish_kernel<T>,
+                      static_cast<unsigned>((p.cols + 31) / 32), 32 * kSlices, 0, stream, p,
+                      static_cast<const float*>(ws), static_cast<int>(grid));
 }
 
 }  // namespace
