@@ -175,8 +175,15 @@ def _p(t) -> int | None:
     return t.data_ptr()
 
 
+# the handle alone of the current stream of a device: making the Stream object
+# costs 6 us, as much as the rest of a call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _s(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -292,12 +299,16 @@ _DTYPES = {torch.float32: MXG_F32, torch.bfloat16: MXG_BF16, torch.float16: MXG_
 
 def _ld(t) -> int:
     """Elements between the rows of a matrix whose rows are contiguous."""
-    if t is None or t.dim() < 2:
+    if t is None:
         return 0
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError("rows must be contiguous (stride %d between their elements)" % t.stride(-1))
+    stride = t.stride()
+    if len(stride) < 2:
+        return 0
+    rows, cols = t.shape[-2:]
+    if stride[-1] != 1 and cols > 1:
+        raise ValueError("rows must be contiguous (stride %d between their elements)" % stride[-1])
     # the stride of a dimension of size 1 says nothing
-    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
+    return stride[-2] if rows > 1 else max(stride[-2], cols)
 
 
 def _ld_experts(t) -> int:
@@ -326,32 +337,45 @@ def mxg_grouped_gemm_16bit(mode: int, A: torch.Tensor, B: torch.Tensor, group_ws
                                          _p(dev_status), _s(stream)))
 
 
-def _norm_types(x, others, f32) -> tuple:
-    """(dtype, res_dtype) of the norms around a block; x is of the residual stream."""
-    kinds = {t.dtype for t in others if t is not None}
-    if len(kinds) != 1 or not kinds <= set(_DTYPES) or x.dtype not in _DTYPES:
-        raise ValueError("y, n, the weights and the gate have one type: got %s" % kinds)
-    if any(t is not None and t.dtype != torch.float32 for t in f32):
-        raise ValueError("the ROW gate and the gradients of broadcast inputs are fp32")
-    return _DTYPES[kinds.pop()], _DTYPES[x.dtype]
+def _same_type(tensors) -> int:
+    """The mxg_dtype_t of those that are given."""
+    kind = None
+    for t in tensors:
+        if t is not None and t.dtype is not kind:
+            if kind is not None:
+                raise ValueError("tensors of one type expected: got %s and %s" % (kind, t.dtype))
+            kind = t.dtype
+    if kind not in _DTYPES:
+        raise ValueError("expected fp32, bf16 or fp16: got %s" % kind)
+    return _DTYPES[kind]
 
 
-def _rows_of(x, others) -> None:
-    if any(t is not None and t.shape != x.shape for t in others):
-        raise ValueError("the [rows, cols] tensors differ in shape: %s"
-                         % [tuple(t.shape) for t in others if t is not None])
+def _same_shape(x, tensors) -> None:
+    shape = x.shape
+    for t in tensors:
+        if t is not None and t.shape != shape:
+            raise ValueError("the [rows, cols] tensors differ in shape: %s and %s"
+                             % (tuple(shape), tuple(t.shape)))
 
 
-def _cols_of(cols, others) -> None:
-    if any(t is not None and (t.numel() != cols or not t.is_contiguous()) for t in others):
-        raise ValueError("the weights are contiguous vectors of %d" % cols)
+def _vector(t, n: int, f32: bool = False) -> None:
+    """A contiguous vector of n elements, or none."""
+    if t is not None and (t.numel() != n or not t.is_contiguous() or
+                          (f32 and t.dtype is not torch.float32)):
+        raise ValueError("expected a contiguous vector of %d%s: got %s of %s"
+                         % (n, " fp32 elements" if f32 else "", tuple(t.shape), t.dtype))
 
 
-def _gate_of(gate, gate_mode, rows, cols) -> None:
-    want = {MXG_GATE_ROW: rows, MXG_GATE_COL: cols, MXG_GATE_FULL: rows * cols}.get(gate_mode)
-    if gate is not None and (gate.numel() != want or
-                             (gate_mode != MXG_GATE_FULL and not gate.is_contiguous())):
-        raise ValueError("a gate (or its gradient) of mode %d has %s elements" % (gate_mode, want))
+def _gate(gate, mode: int, x, broadcast_f32: bool) -> None:
+    """A gate of the given mode or (broadcast_f32) its gradient."""
+    if gate is None:
+        return
+    if mode == MXG_GATE_ROW:
+        _vector(gate, x.shape[0], True)
+    elif mode == MXG_GATE_COL:
+        _vector(gate, x.shape[1], broadcast_f32)
+    elif mode != MXG_GATE_FULL or gate.shape != x.shape:
+        raise ValueError("a gate of mode %d does not have the shape %s" % (mode, tuple(gate.shape)))
 
 
 def mxg_block_norm(x: torch.Tensor, y=None, w_post=None, gate=None, gate_mode: int = MXG_GATE_NONE,
@@ -359,17 +383,16 @@ def mxg_block_norm(x: torch.Tensor, y=None, w_post=None, gate=None, gate_mode: i
                    stream=None) -> None:
     """x, y, x_out, n_out: [rows, cols] (rows may be strided)."""
     rows, cols = x.shape
-    row = gate_mode == MXG_GATE_ROW
-    dtype, res = _norm_types(x, (y, n_out, w_post, w_pre, None if row else gate),
-                             (gate if row else None,))
-    _rows_of(x, (y, x_out, n_out))
-    _cols_of(cols, (w_post, w_pre))
-    _gate_of(gate, gate_mode, rows, cols)
-    if x_out is not None and x_out.dtype != x.dtype:
-        raise ValueError("x and x_out have one type")
+    full = gate_mode == MXG_GATE_FULL
+    dtype = _same_type((y, n_out, w_post, w_pre, gate if gate_mode >= MXG_GATE_COL else None))
+    res = _same_type((x, x_out))
+    _same_shape(x, (y, x_out, n_out))
+    _vector(w_post, cols)
+    _vector(w_pre, cols)
+    _gate(gate, gate_mode, x, False)
     d = BlockNorm(dtype, res, rows, cols, _p(x), _ld(x), _p(y), _ld(y), _p(w_post), _p(gate),
-                  _ld(gate), gate_mode, res_scale, _p(x_out), _ld(x_out), _p(w_pre), _p(n_out),
-                  _ld(n_out), eps)
+                  _ld(gate) if full else 0, gate_mode, res_scale, _p(x_out), _ld(x_out), _p(w_pre),
+                  _p(n_out), _ld(n_out), eps)
     _check("mxg_block_norm", load().mxg_block_norm(ctypes.byref(d), _s(stream)))
 
 
@@ -384,20 +407,21 @@ def mxg_block_norm_backward(x: torch.Tensor, y=None, w_post=None, gate=None,
                             stream=None) -> None:
     """x: the block's output as mxg_block_norm stored it (x_out)."""
     rows, cols = x.shape
-    row, full = gate_mode == MXG_GATE_ROW, gate_mode == MXG_GATE_FULL
-    dtype, res = _norm_types(x, (y, dn, dy, w_post, w_pre, None if row else gate,
-                                 dgate if full else None),
-                             (gate if row else None, None if full else dgate, dw_post, dw_pre))
-    _rows_of(x, (y, dx_out, dn, dx, dy))
-    _cols_of(cols, (w_post, w_pre, dw_post, dw_pre))
-    _gate_of(gate, gate_mode, rows, cols)
-    _gate_of(dgate, gate_mode, rows, cols)
-    if any(t is not None and t.dtype != x.dtype for t in (dx_out, dx)):
-        raise ValueError("x, dx_out and dx have one type")
+    full = gate_mode == MXG_GATE_FULL
+    dtype = _same_type((y, dn, dy, w_post, w_pre, gate if gate_mode >= MXG_GATE_COL else None,
+                        dgate if full else None))
+    res = _same_type((x, dx_out, dx))
+    _same_shape(x, (y, dx_out, dn, dx, dy))
+    _vector(w_post, cols)
+    _vector(w_pre, cols)
+    _vector(dw_post, cols, True)
+    _vector(dw_pre, cols, True)
+    _gate(gate, gate_mode, x, False)
+    _gate(dgate, gate_mode, x, True)
     d = BlockNormGrad(dtype, res, rows, cols, _p(x), _ld(x), _p(y), _ld(y), _p(w_post), _p(gate),
-                      _ld(gate), gate_mode, res_scale, _p(w_pre), eps, _p(dx_out), _ld(dx_out),
-                      _p(dn), _ld(dn), _p(dx), _ld(dx), _p(dy), _ld(dy), _p(dw_post), _p(dw_pre),
-                      _p(dgate), _ld(dgate))
+                      _ld(gate) if full else 0, gate_mode, res_scale, _p(w_pre), eps, _p(dx_out),
+                      _ld(dx_out), _p(dn), _ld(dn), _p(dx), _ld(dx), _p(dy), _ld(dy), _p(dw_post),
+                      _p(dw_pre), _p(dgate), _ld(dgate) if full else 0)
     _check("mxg_block_norm_backward",
            load().mxg_block_norm_backward(ctypes.byref(d), _p(workspace),
                                           0 if workspace is None else workspace.nbytes, _s(stream)))
@@ -408,7 +432,7 @@ def mxg_grad_workspace_bytes() -> int:
 
 
 class GradList:
-    """An array of mxg_grad_t over tensors that it keeps alive (grad_list)."""
+    """An array of mxg_grad_t over tensors that it keeps alive (see grad_list)."""
 
     def __init__(self, src, dst):
         for t in (*src, *dst):
