@@ -30,6 +30,7 @@
 // number: the rows of the next group that share the last 16-row MMA step are
 // zeroed in shared memory, in both operands (a zero against a NaN would not
 // be zero), by warp 10 while earlier stages are multiplied.
+#include <algorithm>
 #include <atomic>
 
 #include "elem.cuh"
@@ -50,8 +51,11 @@ struct Gemm16Params {
   int32_t out_type;     // mxg_dtype_t
   uint32_t idesc;       // operand types and majors, M = 256; N is added per unit
   int32_t tile_rows;    // rows of C per unit: a multiple of 32, at most 256
+  int32_t tile_cols;    // columns of C per unit: 256 or 128
+  int32_t col_units;    // units side by side
   int32_t stages;       // pipeline stages, ...
-  int32_t stage_bytes;  // ... each a 128-row tile of Q and half the unit's rows of R
+  int32_t q_bytes;      // ... each half the unit's columns of Q ...
+  int32_t stage_bytes;  // ... and half its rows of R
 };
 
 // Row offsets of the groups and their first units, by one warp: negative
@@ -106,7 +110,7 @@ __device__ __forceinline__ void group_tables16(const int64_t* group_ws, int G, i
   if (lane == 0 && blockIdx.x == 0) status_set(status, bits);
 }
 
-// Work unit u: `rows` rows of C from i0 on, 256 columns from j0 on.
+// Work unit u: `rows` rows of C from i0 on, p.tile_cols columns from j0 on.
 struct Unit16 {
   int32_t g;
   int32_t row0;   // first row of the group in the ragged operands
@@ -116,13 +120,11 @@ struct Unit16 {
   int32_t kdim;   // contraction length
 };
 
-constexpr int kCols16 = 256;
-
 template <int MODE>
 __device__ __forceinline__ Unit16 map_unit16(int64_t u, const Gemm16Params& p,
                                              const int32_t* row_off, const int32_t* unit_off) {
   Unit16 t;
-  const uint32_t cu = (static_cast<uint32_t>(p.out_cols) + kCols16 - 1) / kCols16;
+  const uint32_t cu = static_cast<uint32_t>(p.col_units);
   uint32_t i, j, tiles;
   int32_t total;  // rows of C in this group
   if constexpr (MODE == 1) {
@@ -158,7 +160,7 @@ __device__ __forceinline__ Unit16 map_unit16(int64_t u, const Gemm16Params& p,
     i = local - j * tiles;
     constexpr int64_t kL2Budget = 32ll << 20;
     if (static_cast<int64_t>(total) * t.kdim * 2 > kL2Budget) {
-      int64_t cb = kL2Budget / (static_cast<int64_t>(kCols16) * t.kdim * 2);
+      int64_t cb = kL2Budget / (static_cast<int64_t>(p.tile_cols) * t.kdim * 2);
       cb = cb < 1 ? 1 : (cb > cu ? cu : cb);
       const uint32_t b = static_cast<uint32_t>(cb), blk = local / (tiles * b);
       const uint32_t width = (blk + 1) * b <= cu ? b : cu - blk * b;
@@ -171,7 +173,7 @@ __device__ __forceinline__ Unit16 map_unit16(int64_t u, const Gemm16Params& p,
   // would stream its weights for few products
   const int32_t share = ((total + static_cast<int32_t>(tiles) - 1) / static_cast<int32_t>(tiles) + 31) & ~31;
   t.i0 = static_cast<int32_t>(i) * share;
-  t.j0 = static_cast<int32_t>(j) * kCols16;
+  t.j0 = static_cast<int32_t>(j) * p.tile_cols;
   t.rows = max(0, min(share, total - t.i0));
   t.n_mma = max(32, (t.rows + 31) & ~31);
   return t;
@@ -217,7 +219,6 @@ __device__ __forceinline__ void drain16(uint32_t bar, uint32_t parity, int32_t* 
 struct Pair16 {
   static constexpr int kMaxStages = 12;
   static constexpr int kBK = 64;                 // contraction elements per stage
-  static constexpr int kQBytes = 128 * kBK * 2;  // Q per CTA and stage
   static constexpr int kMmas = kBK / 16;
   static constexpr int kEpiWarps = 8;
   static constexpr int kMaskWarp = 2 + kEpiWarps;
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
 
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
   const uint32_t stage0 = smem_u32(smem) + ((Cfg::kBarBytes + 8 * (p.G + 1) + 1023) & ~1023);
-  const uint32_t stages = p.stages, stage_bytes = p.stage_bytes;
+  const uint32_t stages = p.stages, stage_bytes = p.stage_bytes, q_bytes = p.q_bytes;
   const uint32_t rank = cluster_ctarank();
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   auto full_bar = [&](int s) { return bar(s); };
@@ -296,9 +297,16 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
     tmem_alloc_pair(smem_u32(tmem_base_s), 512);
     tmem_relinquish_pair();
   }
+  if (warp == 0) {
+    prefetch_tmap(&tmap_q);
+    prefetch_tmap(&tmap_r);
+  }
+  // from here on memory is read: what came before on the stream is done
+  grid_launch_dependents();
+  grid_wait_for_previous();
   if (warp == 1)
-    group_tables16(p.group_ws, p.G, p.M_cap, p.tile_rows, (p.out_cols + kCols16 - 1) / kCols16,
-                   row_off, unit_off, p.status);
+    group_tables16(p.group_ws, p.G, p.M_cap, p.tile_rows, p.col_units, row_off, unit_off,
+                   p.status);
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // the even CTA's barriers exist before the odd CTA's copies signal them
@@ -306,17 +314,15 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
   const uint32_t tmem_base = *tmem_base_s;
   const int64_t unit0 = blockIdx.x >> 1, ustride = gridDim.x >> 1;
   const int64_t total =
-      MODE == 1 ? static_cast<int64_t>(p.G) * ((p.N + p.tile_rows - 1) / p.tile_rows) *
-                      ((p.out_cols + kCols16 - 1) / kCols16)
+      MODE == 1 ? static_cast<int64_t>(p.G) * ((p.N + p.tile_rows - 1) / p.tile_rows) * p.col_units
                 : unit_off[p.G];
 
   // ------------------------------------------------------------ producers (both CTAs)
   if (warp == 0) {
     const uint32_t leader = elect_leader();
-    prefetch_tmap(&tmap_q);
-    prefetch_tmap(&tmap_r);
     uint32_t stage = 0, phase = 0, issued = 0, parity = 0, tail_issued = 0, tail_parity = 0;
-    const bool two = stage_bytes > Cfg::kQBytes + 8192;  // MN-major R: a second chunk
+    // MN-major: a second chunk of 64
+    const bool two_q = q_bytes > 8192, two_r = stage_bytes - q_bytes > 8192;
     bool ok = true;
     for (int64_t u = unit0, n = 0; ok && u < total; u += ustride, ++n) {
       const Unit16 t = map_unit16<MODE>(u, p, row_off, unit_off);
@@ -332,14 +338,14 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
                             (static_cast<uint64_t>(t.n_mma) << 40);
         mbar_arrive_if(info_full_bar(slot), leader);
       }
-      const int32_t q_at = t.j0 + 128 * static_cast<int32_t>(rank);
+      const int32_t q_at = t.j0 + p.tile_cols / 2 * static_cast<int32_t>(rank);
       const int32_t r_at = t.i0 + (t.n_mma / 2) * static_cast<int32_t>(rank);
       for (int32_t kb = 0; kb < kb_count; ++kb) {
         if (!mbar_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, p.status)) {
           ok = false;
           break;
         }
-        const uint32_t sq = stage0 + stage * stage_bytes, sr = sq + Cfg::kQBytes;
+        const uint32_t sq = stage0 + stage * stage_bytes, sr = sq + q_bytes;
         const int32_t k0 = kb * BK;
         if (MODE == 1 && kb + 1 == kb_count && (last & 15) != 0) {
           // rows of the next group in the last MMA step: this CTA's bytes
@@ -347,9 +353,9 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
           const uint32_t lb = land_bar(stage);
           mbar_arrive_expect_tx_if(lb, stage_bytes, leader);
           tma_load_2d_if(sq, &tmap_q, lb, q_at, t.row0 + k0, leader);
-          tma_load_2d_if(sq + 8192, &tmap_q, lb, q_at + 64, t.row0 + k0, leader);
+          if (two_q) tma_load_2d_if(sq + 8192, &tmap_q, lb, q_at + 64, t.row0 + k0, leader);
           tma_load_2d_if(sr, &tmap_r, lb, r_at, t.row0 + k0, leader);
-          if (two) tma_load_2d_if(sr + 8192, &tmap_r, lb, r_at + 64, t.row0 + k0, leader);
+          if (two_r) tma_load_2d_if(sr + 8192, &tmap_r, lb, r_at + 64, t.row0 + k0, leader);
           tail_issued |= 1u << stage;
           tail_parity ^= 1u << stage;
         } else {
@@ -359,14 +365,15 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
             tma_load_3d_pair_if(sq, &tmap_q, fb, k0, q_at, t.g, leader);
           } else if constexpr (MODE == 2) {
             tma_load_3d_pair_if(sq, &tmap_q, fb, q_at, k0, t.g, leader);
-            tma_load_3d_pair_if(sq + 8192, &tmap_q, fb, q_at + 64, k0, t.g, leader);
+            if (two_q) tma_load_3d_pair_if(sq + 8192, &tmap_q, fb, q_at + 64, k0, t.g, leader);
           } else {
             tma_load_2d_pair_if(sq, &tmap_q, fb, q_at, t.row0 + k0, leader);
-            tma_load_2d_pair_if(sq + 8192, &tmap_q, fb, q_at + 64, t.row0 + k0, leader);
+            if (two_q)
+              tma_load_2d_pair_if(sq + 8192, &tmap_q, fb, q_at + 64, t.row0 + k0, leader);
           }
           if constexpr (MODE == 1) {
             tma_load_2d_pair_if(sr, &tmap_r, fb, r_at, t.row0 + k0, leader);
-            if (two) tma_load_2d_pair_if(sr + 8192, &tmap_r, fb, r_at + 64, t.row0 + k0, leader);
+            if (two_r) tma_load_2d_pair_if(sr + 8192, &tmap_r, fb, r_at + 64, t.row0 + k0, leader);
           } else {
             tma_load_2d_pair_if(sr, &tmap_r, fb, k0, t.row0 + r_at, leader);
           }
@@ -414,7 +421,7 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
             break;
           }
           tc_fence_after();
-          const uint32_t sq = stage0 + stage * stage_bytes, sr = sq + Cfg::kQBytes;
+          const uint32_t sq = stage0 + stage * stage_bytes, sr = sq + q_bytes;
           const uint64_t qd = tile_desc16<Q_MN>(sq), rd = tile_desc16<R_MN>(sr);
           const int nmma = kb + 1 == kb_count ? last_mmas : Cfg::kMmas;
 #pragma unroll
@@ -484,10 +491,11 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
         break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((32u * quarter) << 16) + 256u * slot;
-      const int32_t col = t.j0 + static_cast<int32_t>(128 * rank + 32 * quarter + lane);
+      const int32_t lane_col = static_cast<int32_t>(32 * quarter + lane);
+      const int32_t col = t.j0 + p.tile_cols / 2 * static_cast<int32_t>(rank) + lane_col;
       const int64_t row =
           (MODE == 1 ? static_cast<int64_t>(t.g) * p.N : static_cast<int64_t>(t.row0)) + t.i0;
-      const bool in = col < p.out_cols;
+      const bool in = lane_col < p.tile_cols / 2 && col < p.out_cols;
       for (int32_t c = 32 * static_cast<int32_t>(half); c < t.rows; c += 64) {
         uint32_t v[32];
         if (has_k) {
@@ -567,16 +575,19 @@ cudaError_t launch_pair16(const CUtensorMap& tq, const CUtensorMap& tr, const Ge
   if (clusters < 1) return cudaErrorInvalidConfiguration;
   const int64_t n = max_units < clusters ? max_units : clusters;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  // set up beside the kernel before it, where that one allows it
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(2 * n));
   cfg.blockDim = dim3(Pair16::threads(MODE));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, gemm16_pair_kernel<MODE>, tq, tr, p);
 }
 
@@ -612,16 +623,37 @@ cudaError_t launch_grouped_gemm16(int in_f16, int mode, const void* A, int64_t l
   // MN-major Q and R (bits 15 and 16), M = 256 (bit 24)
   p.idesc = (1u << 4) | (in_f16 ? 0u : (1u << 7) | (1u << 10)) | (mode != 0 ? 1u << 15 : 0u) |
             (mode == 1 ? 1u << 16 : 0u) | ((256u >> 4) << 24);
-  // units as tall as the rows can be, up to 256; what few rows leave free of a
-  // stage goes to more stages, i.e. more of the weights in flight
+  // Units of 256 x 256, or as many rows as there can be; while twice as many
+  // still find a cluster each, their longer side is halved, down to 64 rows and
+  // 128 columns (one row through 4096 x 4096: 23 us in 16 units, 20 us in 32; in
+  // 64 of 64 columns 25 us).  The MMA always runs on 256 columns; the lanes of
+  // those that a unit does not have are not read.  What small units leave free of
+  // a stage goes to more stages, i.e. more of the operands in flight.
   const int64_t c_rows = mode == 1 ? N : M_cap;
   p.tile_rows = c_rows >= 256 ? 256 : static_cast<int32_t>((c_rows + 31) / 32 * 32);
+  p.tile_cols = 256;
+  // an upper bound: the sizes are on the device
+  const int64_t live = M_cap < G ? M_cap : G;
+  auto count = [&] {
+    const int64_t cu = (p.out_cols + p.tile_cols - 1) / p.tile_cols;
+    return mode == 1 ? G * ((N + p.tile_rows - 1) / p.tile_rows) * cu
+                     : (M_cap + live * (p.tile_rows - 1)) / p.tile_rows * cu;
+  };
+  while (count() * 2 <= num_sms / 2 && (p.tile_cols > 128 || p.tile_rows > 64)) {
+    if (p.tile_cols > 128 && (p.tile_cols >= p.tile_rows || p.tile_rows <= 64))
+      p.tile_cols /= 2;
+    else
+      p.tile_rows = (p.tile_rows / 2 + 31) / 32 * 32;
+  }
+  p.col_units = (p.out_cols + p.tile_cols - 1) / p.tile_cols;
+  p.q_bytes = p.tile_cols / 2 * 128;
   const int r_bytes = mode == 1 ? (p.tile_rows > 128 ? 16384 : 8192) : p.tile_rows / 2 * 128;
-  p.stage_bytes = Pair16::kQBytes + r_bytes;
+  p.stage_bytes = p.q_bytes + r_bytes;
   const int header = Pair16::header_bytes(G) + 1024;
   p.stages = (Pair16::kSmemMax - header) / p.stage_bytes;
   if (p.stages > Pair16::kMaxStages) p.stages = Pair16::kMaxStages;
-  const int smem = header + p.stages * p.stage_bytes;
+  // the MMA reads 16 KB from each tile of Q on, however many columns are in it
+  const int smem = header + (p.stages - 1) * p.stage_bytes + std::max(p.stage_bytes, 16384);
 
   // without rows no copy is made: any aligned address serves the tensor maps
   if (M_cap == 0) A = B = reinterpret_cast<const void*>(uintptr_t{1} << 20);
@@ -636,16 +668,12 @@ cudaError_t launch_grouped_gemm16(int in_f16, int mode, const void* A, int64_t l
     const uint64_t dims[3] = {static_cast<uint64_t>(K), static_cast<uint64_t>(N),
                               static_cast<uint64_t>(G)};
     const uint64_t strides[2] = {static_cast<uint64_t>(ldb) * 2, static_cast<uint64_t>(N * ldb) * 2};
-    const uint32_t box[3] = {64, mode == 0 ? 128u : 64u, 1};
+    const uint32_t box[3] = {64, mode == 0 ? static_cast<uint32_t>(p.tile_cols / 2) : 64u, 1};
     if (!make_tmap_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT16, B, dims, strides, box,
                       CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
-  const int64_t cu = (p.out_cols + kCols16 - 1) / kCols16;
-  // an upper bound: the sizes are on the device
-  const int64_t live = M_cap < G ? M_cap : G;
-  const int64_t units = mode == 1 ? G * ((N + p.tile_rows - 1) / p.tile_rows) * cu
-                                  : ((M_cap + live * (p.tile_rows - 1)) / p.tile_rows) * cu;
+  const int64_t units = count();
   if (units > INT32_MAX) return cudaErrorInvalidValue;
   if (mode == 0) return launch_pair16<0>(tq, tr, p, smem, units, num_sms, stream);
   if (mode == 1) return launch_pair16<1>(tq, tr, p, smem, units, num_sms, stream);
