@@ -184,12 +184,12 @@ __device__ __forceinline__ Unit16 map_unit16(int64_t u, const Gemm16Params& p,
 // row in the way, a 256 x 256 unit's epilogue took 10 k cycles, as long as the
 // MMAs of a 1408-long contraction.
 template <typename T>
-__device__ __forceinline__ void store_column16(T* dst, int64_t ldc, const uint32_t (&acc)[32],
+__device__ __forceinline__ void store_column16(T* dst, int64_t ldc, const float (&acc)[32],
                                                int rows, float alpha, float beta) {
   if (rows >= 32 && beta == 0.0f) {
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
-      *dst = from_f32<T>(alpha * __uint_as_float(acc[e]));
+      *dst = from_f32<T>(alpha * acc[e]);
       dst += ldc;
     }
     return;
@@ -197,7 +197,7 @@ __device__ __forceinline__ void store_column16(T* dst, int64_t ldc, const uint32
 #pragma unroll
   for (int e = 0; e < 32; ++e) {
     if (e < rows) {
-      float v = alpha * __uint_as_float(acc[e]);
+      float v = alpha * acc[e];
       if (beta != 0.0f) v += beta * to_f32(*dst);
       *dst = from_f32<T>(v);
     }
@@ -243,7 +243,16 @@ __device__ __forceinline__ uint64_t tile_desc16(uint32_t saddr) {
 template <bool MN>
 constexpr uint32_t kStep16 = MN ? 2048 / 16 : 32 / 16;
 
-template <int MODE>
+// SEG: K blocks that are summed in tensor memory at a time, 0 for all of them.
+// The tensor cores add to an accumulator by truncation, so a sum over k elements
+// comes out some 0.7 k / 16 2^-24 too small (measured: 9e-6 over 8192, 3.8e-5 over
+// 32768): nothing beside the rounding of a 16-bit output, but more than an fp32
+// one should lose.  For those the epilogue warps take the accumulator over after
+// every SEG blocks and add it up in registers, rounding to nearest: 4.9e-7 over
+// 32768 with 8 blocks (512 elements).  wgrad of 8 experts of 14336 x 4096, 16381
+// rows, into fp32: 1156 us so, 1160 us without; with 6 blocks 1204 us, with 4,
+// where the MMAs catch up with the epilogue's stores, 1269 us.
+template <int MODE, int SEG>
 __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
     gemm16_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
                        const __grid_constant__ CUtensorMap tmap_r, const Gemm16Params p) {
@@ -397,13 +406,14 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
   else if (warp == 1) {
     if (rank == 0) {
       const uint32_t leader = elect_leader();
-      uint32_t stage = 0, phase = 0;
+      uint32_t stage = 0, phase = 0, seg = 0;  // seg: accumulators filled so far
       bool ok = true;
       int64_t n = 0;
       for (int64_t u = unit0; ok && u < total; u += ustride, ++n) {
         const int slot = static_cast<int>(n & 1);
-        const uint32_t par = static_cast<uint32_t>((n >> 1) & 1);
-        if (!mbar_wait_warp(info_full_bar(slot), par, abort_flag, p.status)) break;
+        if (!mbar_wait_warp(info_full_bar(slot), static_cast<uint32_t>((n >> 1) & 1), abort_flag,
+                            p.status))
+          break;
         const uint64_t info = info_word[slot];
         __syncwarp();  // every lane has read the word
         mbar_arrive_if(info_empty_bar(slot), leader);
@@ -411,33 +421,42 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
         const int last_mmas = static_cast<int>((info >> 32) & 0xFFu);
         const uint32_t n_mma = static_cast<uint32_t>(info >> 40);
         const uint32_t idesc = p.idesc | ((n_mma >> 3) << 17);
-        // the accumulator's previous unit has been read out
-        if (!mbar_wait_warp<true>(tempty_bar(slot), par ^ 1u, abort_flag, p.status)) break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + 256u * slot;
-        for (int32_t kb = 0; kb < kb_count; ++kb) {
-          if (!mbar_wait_warp(full_bar(stage), phase, abort_flag, p.status)) {
+        int32_t kb = 0;
+        do {
+          // the accumulator has been read out since it was last filled
+          const uint32_t acc = seg & 1u;
+          if (!mbar_wait_warp<true>(tempty_bar(acc), ((seg >> 1) & 1u) ^ 1u, abort_flag, p.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sq = stage0 + stage * stage_bytes, sr = sq + q_bytes;
-          const uint64_t qd = tile_desc16<Q_MN>(sq), rd = tile_desc16<R_MN>(sr);
-          const int nmma = kb + 1 == kb_count ? last_mmas : Cfg::kMmas;
+          const uint32_t d = tmem_base + 256u * acc;
+          const int32_t kb0 = kb, kb1 = SEG != 0 ? min(kb_count, kb + SEG) : kb_count;
+          for (; kb < kb1; ++kb) {
+            if (!mbar_wait_warp(full_bar(stage), phase, abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sq = stage0 + stage * stage_bytes, sr = sq + q_bytes;
+            const uint64_t qd = tile_desc16<Q_MN>(sq), rd = tile_desc16<R_MN>(sr);
+            const int nmma = kb + 1 == kb_count ? last_mmas : Cfg::kMmas;
 #pragma unroll
-          for (int kk = 0; kk < Cfg::kMmas; ++kk) {
-            if (kk >= nmma) break;
-            tc_mma_f16_pair_if(d, qd + kk * kStep16<Q_MN>, rd + kk * kStep16<R_MN>, idesc,
-                               (kb > 0 || kk > 0) ? 1u : 0u, leader);
+            for (int kk = 0; kk < Cfg::kMmas; ++kk) {
+              if (kk >= nmma) break;
+              tc_mma_f16_pair_if(d, qd + kk * kStep16<Q_MN>, rd + kk * kStep16<R_MN>, idesc,
+                                 (kb > kb0 || kk > 0) ? 1u : 0u, leader);
+            }
+            tc_commit_pair_mc_if(empty_bar(stage), 0x3, leader);
+            if (++stage == stages) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          tc_commit_pair_mc_if(empty_bar(stage), 0x3, leader);
-          if (++stage == stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-        if (!ok) break;
-        tc_commit_pair_mc_if(tfull_bar(slot), 0x3, leader);
+          if (!ok) break;
+          tc_commit_pair_mc_if(tfull_bar(acc), 0x3, leader);
+          ++seg;
+        } while (kb < kb_count);
       }
       if (leader) tc_commit_pair(drain_bar);
       __syncwarp();
@@ -479,49 +498,97 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
   else {
     // lane quarter = 32 columns of C, every other chunk of 32 rows
     const uint32_t quarter = warp & 3u, half = (warp - 2) >> 2;
-    int64_t n = 0;
-    for (int64_t u = unit0; u < total; u += ustride, ++n) {
+    uint32_t seg = 0;
+    bool ok = true;
+    for (int64_t u = unit0; ok && u < total; u += ustride) {
       const Unit16 t = map_unit16<MODE>(u, p, row_off, unit_off);
-      const int slot = static_cast<int>(n & 1);
       const bool has_k = t.kdim > 0;
       const float alpha = p.alpha ? p.alpha[t.g] : 1.0f;
       const float beta = p.beta ? p.beta[t.g] : 0.0f;
-      if (!mbar_wait_warp(tfull_bar(slot), static_cast<uint32_t>((n >> 1) & 1), abort_flag,
-                          p.status))
-        break;
-      tc_fence_after();
-      const uint32_t taddr = tmem_base + ((32u * quarter) << 16) + 256u * slot;
       const int32_t lane_col = static_cast<int32_t>(32 * quarter + lane);
       const int32_t col = t.j0 + p.tile_cols / 2 * static_cast<int32_t>(rank) + lane_col;
       const int64_t row =
           (MODE == 1 ? static_cast<int64_t>(t.g) * p.N : static_cast<int64_t>(t.row0)) + t.i0;
       const bool in = lane_col < p.tile_cols / 2 && col < p.out_cols;
-      for (int32_t c = 32 * static_cast<int32_t>(half); c < t.rows; c += 64) {
-        uint32_t v[32];
-        if (has_k) {
-          tmem_ld32(taddr + static_cast<uint32_t>(c), v);
-          tmem_ld_wait();
-        } else {
+      const int32_t c0 = 32 * static_cast<int32_t>(half);
+      auto store = [&](int32_t c, const float(&v)[32]) {
+        if (!in) return;
+        const int64_t at = (row + c) * p.ldc + col;
+        if (SEG != 0 || p.out_type == MXG_F32)
+          store_column16(static_cast<float*>(p.C) + at, p.ldc, v, t.rows - c, alpha, beta);
+        else if (p.out_type == MXG_BF16)
+          store_column16(static_cast<Bf16*>(p.C) + at, p.ldc, v, t.rows - c, alpha, beta);
+        else
+          store_column16(static_cast<F16*>(p.C) + at, p.ldc, v, t.rows - c, alpha, beta);
+      };
+      // the next accumulator, and the word that it may be filled again.  That
+      // arrival is relaxed: a release would wait for the stores
+      auto take = [&] {
+        const uint32_t acc = seg & 1u;
+        if (!mbar_wait_warp(tfull_bar(acc), (seg >> 1) & 1u, abort_flag, p.status)) return false;
+        tc_fence_after();
+        return true;
+      };
+      auto give = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(seg & 1u), 0));
+        ++seg;
+      };
+      const uint32_t lanes = tmem_base + ((32u * quarter) << 16);
+      if constexpr (SEG == 0) {
+        if (!(ok = take())) break;
+        const uint32_t taddr = lanes + 256u * (seg & 1u);
+        for (int32_t c = c0; c < t.rows; c += 64) {
+          float v[32];
+          if (has_k) {
+            uint32_t w[32];
+            tmem_ld32(taddr + static_cast<uint32_t>(c), w);
+            tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0;
+            for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(w[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+          }
+          store(c, v);
+          __syncwarp();
         }
-        if (in) {
-          const int64_t at = (row + c) * p.ldc + col;
-          const int left = t.rows - c;
-          if (p.out_type == MXG_F32)
-            store_column16(static_cast<float*>(p.C) + at, p.ldc, v, left, alpha, beta);
-          else if (p.out_type == MXG_BF16)
-            store_column16(static_cast<Bf16*>(p.C) + at, p.ldc, v, left, alpha, beta);
-          else
-            store_column16(static_cast<F16*>(p.C) + at, p.ldc, v, left, alpha, beta);
-        }
+        give();
+      } else {
+        float v[4][32];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[m][e] = 0.0f;
+        int32_t k = 0;
+        do {
+          if (!(ok = take())) break;
+          const uint32_t taddr = lanes + 256u * (seg & 1u) + static_cast<uint32_t>(c0);
+          if (has_k) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              if (c0 + 64 * m < t.rows) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  uint32_t w[16];
+                  tmem_ld16(taddr + 64 * m + 16 * h, w);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) v[m][16 * h + e] += __uint_as_float(w[e]);
+                }
+              }
+            }
+          }
+          give();
+          k += SEG * BK;
+        } while (k < t.kdim);
+        if (!ok) break;
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          if (c0 + 64 * m < t.rows) store(c0 + 64 * m, v[m]);
         __syncwarp();
       }
-      // the loads have completed: the accumulator may be overwritten.  Relaxed:
-      // a release would wait for the stores
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(slot), 0));
     }
   }
 
@@ -539,17 +606,18 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
 namespace {
 
 constexpr int kMaxDev16 = 64;
+constexpr int kSeg16 = 8;  // K blocks an fp32 output's sum stays in tensor memory
 
 // Clusters of the pair kernel that the device holds at once, asked once per
 // device, with all the shared memory there is.
-template <int MODE>
+template <int MODE, int SEG>
 int pair_clusters(int num_sms) {
   static std::atomic<int> known[kMaxDev16];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev16) return 0;
   int c = known[dev].load(std::memory_order_relaxed);
   if (c != 0) return c;
-  auto kern = gemm16_pair_kernel<MODE>;
+  auto kern = gemm16_pair_kernel<MODE, SEG>;
   const int smem = Pair16::kSmemMax;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return 0;
@@ -568,10 +636,10 @@ int pair_clusters(int num_sms) {
   return c;
 }
 
-template <int MODE>
+template <int MODE, int SEG>
 cudaError_t launch_pair16(const CUtensorMap& tq, const CUtensorMap& tr, const Gemm16Params& p,
                           int smem, int64_t max_units, int num_sms, cudaStream_t stream) {
-  const int clusters = pair_clusters<MODE>(num_sms);
+  const int clusters = pair_clusters<MODE, SEG>(num_sms);
   if (clusters < 1) return cudaErrorInvalidConfiguration;
   const int64_t n = max_units < clusters ? max_units : clusters;
   cudaLaunchConfig_t cfg = {};
@@ -588,7 +656,7 @@ cudaError_t launch_pair16(const CUtensorMap& tq, const CUtensorMap& tr, const Ge
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gemm16_pair_kernel<MODE>, tq, tr, p);
+  return cudaLaunchKernelEx(&cfg, gemm16_pair_kernel<MODE, SEG>, tq, tr, p);
 }
 
 // A ragged matrix [rows, cols] of 16-bit elements, boxes of 64 columns.
@@ -675,9 +743,14 @@ cudaError_t launch_grouped_gemm16(int in_f16, int mode, const void* A, int64_t l
   }
   const int64_t units = count();
   if (units > INT32_MAX) return cudaErrorInvalidValue;
-  if (mode == 0) return launch_pair16<0>(tq, tr, p, smem, units, num_sms, stream);
-  if (mode == 1) return launch_pair16<1>(tq, tr, p, smem, units, num_sms, stream);
-  return launch_pair16<2>(tq, tr, p, smem, units, num_sms, stream);
+  if (out_type == MXG_F32) {
+    if (mode == 0) return launch_pair16<0, kSeg16>(tq, tr, p, smem, units, num_sms, stream);
+    if (mode == 1) return launch_pair16<1, kSeg16>(tq, tr, p, smem, units, num_sms, stream);
+    return launch_pair16<2, kSeg16>(tq, tr, p, smem, units, num_sms, stream);
+  }
+  if (mode == 0) return launch_pair16<0, 0>(tq, tr, p, smem, units, num_sms, stream);
+  if (mode == 1) return launch_pair16<1, 0>(tq, tr, p, smem, units, num_sms, stream);
+  return launch_pair16<2, 0>(tq, tr, p, smem, units, num_sms, stream);
 }
 
 }  // namespace mxg

@@ -289,6 +289,20 @@ def test_long_contraction(mode):
     check(run(mode, A, B, sizes, N, K, torch.float32).cpu(), ref, mag, kd, torch.float32)
 
 
+def test_fp32_outputs_of_very_long_sums():
+    """Sums of 32768 products.  512 of them are added at a time by truncation --
+    32 additions, each losing less than 2^-23 of the sum so far -- and the 64 such
+    sums by rounding to nearest: 32 2^-23 + 64 2^-24 = 8e-6 of the result at most,
+    and half of that for sums that grow (added by truncation alone, the 2048 steps
+    lost 4e-5)."""
+    g = torch.Generator(device=DEV).manual_seed(20)
+    dy = torch.randn(32768, 264, generator=g, device=DEV).to(torch.bfloat16)
+    x = torch.randn(32768, 136, generator=g, device=DEV).to(torch.bfloat16)
+    C = run(WGRAD, dy, x, [32768], 264, 136, torch.float32)
+    ref = dy.double().t() @ x.double()
+    assert float((C[0].double() - ref).norm() / ref.norm()) <= 4e-6
+
+
 def test_outputs_past_32_bits():
     """C of more than 2^31 elements, an odd last group."""
     N, K, sizes = 32776, 64, [40000, 25537]
