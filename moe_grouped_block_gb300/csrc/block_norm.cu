@@ -170,7 +170,9 @@ cudaError_t norm_forward(const mxg_block_norm_t& p, int num_sms, cudaStream_t st
   // at most 192 KB a slot: 16384 columns of three fp32 inputs
   const int slot = r.threads * 8 * r.iter *
                    static_cast<int>(sizeof(R) + (p.y ? sizeof(T) : 0) + (full ? sizeof(T) : 0));
-  const int depth = std::max(1, std::min(vec ? 4 : 2, kRowSmem / ctas / slot));
+  const int64_t each = (p.rows + grid * teams - 1) / (grid * teams);  // rows a team walks
+  const int depth = static_cast<int>(
+      std::max<int64_t>(1, std::min<int64_t>({vec ? 4 : 2, kRowSmem / ctas / slot, each})));
   if (!vec) return forward_rows<T, R, false, false>(p, r, grid, slot * depth, depth, stream);
   if (p.y != nullptr && p.n_out != nullptr && !full)
     return forward_rows<T, R, true, true>(p, r, grid, slot * depth, depth, stream);

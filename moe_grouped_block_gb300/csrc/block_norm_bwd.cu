@@ -397,7 +397,9 @@ cudaError_t norm_backward(const mxg_block_norm_grad_t& p, float* ws, int num_sms
     // the rest is at most 192 KB a row
     const bool lean = chunk * (core + rest) * 2 > kRowSmem && core > 0;
     const int slot = chunk * (core + (lean ? 0 : rest));
-    const int depth = std::max(1, std::min(vec ? 4 : 2, kRowSmem / ctas / slot));
+    const int64_t each = (p.rows + grid * teams - 1) / (grid * teams);  // rows a team walks
+    const int depth = static_cast<int>(
+        std::max<int64_t>(1, std::min<int64_t>({vec ? 4 : 2, kRowSmem / ctas / slot, each})));
     // narrow rows: the teams' column sums meet where the ring was
     const int sums = teams > 1 ? static_cast<int>(teams * 2 * p.cols * sizeof(float)) : 0;
     const int smem = std::max(slot * depth, sums);
