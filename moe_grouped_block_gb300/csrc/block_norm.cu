@@ -65,9 +65,9 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const mxg_block_nor
   int64_t row = f_row;
   for (int d = 0; d < depth - 1; ++d) fill();
   using W = Weight<T, VEC, ITER, MAXT <= 512>;
-  const W w_post(p.w_post, cols, lane, team);
-  const W g_col(p.gate_mode == MXG_GATE_COL ? p.gate : nullptr, cols, lane, team);
-  const W w_pre(p.w_pre, cols, lane, team);
+  const W w_post(p.w_post, 0, cols, lane, team);
+  const W g_col(p.gate_mode == MXG_GATE_COL ? p.gate : nullptr, 0, cols, lane, team);
+  const W w_pre(p.w_pre, 0, cols, lane, team);
 
   // a row's gate is asked for a row ahead: its latency is that of memory
   const bool g_row = p.gate_mode == MXG_GATE_ROW;
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const mxg_block_nor
 #pragma unroll
         for (int i = 0; i < 4; ++i) q = fma2(b[it][i], b[it][i], q);
       }
-      const float r = rsqrtf(team_sum(sum2(q), red[0], team) * inv + p.eps) * p.res_scale * gr;
+      const float r = rsqrtf(team_sum<1>(sum2(q), red[0], team) * inv + p.eps) * p.res_scale * gr;
       const F2 r2 = f2(r);
 #pragma unroll
       for (int it = 0; it < ITER; ++it) {
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const mxg_block_nor
       for (int it = 0; it < ITER; ++it)
 #pragma unroll
         for (int i = 0; i < 4; ++i) q = fma2(s[it][i], s[it][i], q);
-      const F2 r2 = f2(rsqrtf(team_sum(sum2(q), red[1], team) * inv + p.eps));
+      const F2 r2 = f2(rsqrtf(team_sum<1>(sum2(q), red[1], team) * inv + p.eps));
 #pragma unroll
       for (int it = 0; it < ITER; ++it) {
         w_pre.apply(it, s[it]);
@@ -137,18 +137,19 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const mxg_block_nor
 
 namespace {
 
-constexpr int kWaves = 2;
+// up to 98 registers a thread at 8 columns, 115 at 16 (64 in CTAs of 1024)
+constexpr RowLimits kFwdLimits = {256, {256, 1024}, {640, 512}, 1 << 30};
 
 template <typename T, typename R, bool VEC, bool COMMON>
 cudaError_t forward_rows(const mxg_block_norm_t& p, const RowShape& r, int64_t grid, int smem,
                          int depth, cudaStream_t stream) {
   if (r.iter == 1)
-    return launch_rows(block_norm_kernel<T, R, VEC, 1, 256, COMMON>, grid, r.threads, smem, stream,
-                       p, r.team, depth);
+    return launch_rows(block_norm_kernel<T, R, VEC, 1, 256, COMMON>, r, grid, smem, stream, p,
+                       r.team, depth);
   if (r.threads <= 512)
-    return launch_rows(block_norm_kernel<T, R, VEC, 2, 512, COMMON>, grid, r.threads, smem, stream,
-                       p, r.team, depth);
-  return launch_rows(block_norm_kernel<T, R, VEC, 2, 1024, COMMON>, grid, r.threads, smem, stream, p,
+    return launch_rows(block_norm_kernel<T, R, VEC, 2, 512, COMMON>, r, grid, smem, stream, p,
+                       r.team, depth);
+  return launch_rows(block_norm_kernel<T, R, VEC, 2, 1024, COMMON>, r, grid, smem, stream, p,
                      r.team, depth);
 }
 
@@ -160,23 +161,27 @@ cudaError_t norm_forward(const mxg_block_norm_t& p, int num_sms, cudaStream_t st
                    aligned_rows(p.n_out, p.ldn, sizeof(T)) && aligned_rows(p.w_post, 0, sizeof(T)) &&
                    aligned_rows(p.w_pre, 0, sizeof(T)) &&
                    (p.gate_mode < MXG_GATE_COL || aligned_rows(p.gate, full ? p.ldg : 0, sizeof(T)));
-  const RowShape r = row_shape(p.cols, 256, 2048);
-  // CTAs an SM holds at once (64 to 72 registers a thread at 8 columns, 115 at
-  // 16), and a few times as many in the grid
-  const int ctas = std::max(1, std::min(16, (r.iter == 1 ? 896 : 512) / r.threads));
+  const RowShape r = row_shape(p.cols, kFwdLimits);
+  // twice as many CTAs as an SM holds where that is more than one, so that the
+  // slower SMs end up with fewer (16384 x 4096: 92 us, 96 us with one wave; 4096
+  // x 8192, one CTA an SM: 97 us with two, 95 us with one)
+  const int ctas = row_ctas(r, kFwdLimits, 16);
+  const int waves = ctas > 1 ? 2 : 1;
   const int64_t teams = r.threads / r.team;
   const int64_t grid = std::min<int64_t>((p.rows + teams - 1) / teams,
-                                         static_cast<int64_t>(num_sms) * ctas * kWaves);
+                                         static_cast<int64_t>(num_sms) * ctas * waves);
   // at most 192 KB a slot: 16384 columns of three fp32 inputs
   const int slot = r.threads * 8 * r.iter *
                    static_cast<int>(sizeof(R) + (p.y ? sizeof(T) : 0) + (full ? sizeof(T) : 0));
   const int64_t each = (p.rows + grid * teams - 1) / (grid * teams);  // rows a team walks
   const int depth = static_cast<int>(
       std::max<int64_t>(1, std::min<int64_t>({vec ? 4 : 2, kRowSmem / ctas / slot, each})));
-  if (!vec) return forward_rows<T, R, false, false>(p, r, grid, slot * depth, depth, stream);
-  if (p.y != nullptr && p.n_out != nullptr && !full)
-    return forward_rows<T, R, true, true>(p, r, grid, slot * depth, depth, stream);
-  return forward_rows<T, R, true, false>(p, r, grid, slot * depth, depth, stream);
+  const bool common = p.y != nullptr && p.n_out != nullptr && !full;
+  if (!vec)
+    return common ? forward_rows<T, R, false, true>(p, r, grid, slot * depth, depth, stream)
+                  : forward_rows<T, R, false, false>(p, r, grid, slot * depth, depth, stream);
+  return common ? forward_rows<T, R, true, true>(p, r, grid, slot * depth, depth, stream)
+                : forward_rows<T, R, true, false>(p, r, grid, slot * depth, depth, stream);
 }
 
 }  // namespace

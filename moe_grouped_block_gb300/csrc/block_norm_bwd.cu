@@ -12,6 +12,10 @@
 // the second one of the row before, so that a row costs one barrier.  The
 // column sums of a CTA's rows stay in registers and leave one partial row per
 // CTA; a second kernel adds those in a fixed order.
+//
+// Rows of more than 8192 columns are shared by two CTAs, whose warps post their
+// sums to each other: one of 1024 threads would leave 64 registers a thread, and
+// spilled 400 bytes (4096 x 16384: 346 us so, 207 us shared).
 #include "rows.cuh"
 
 namespace mxg {
@@ -19,10 +23,7 @@ namespace mxg {
 // CTAs of the backward kernel: as many partial rows as the workspace has room
 // for.  160 bounds the SM count; a thread takes some 120 registers.
 constexpr int kNormMaxSms = 160;
-constexpr int kBwdCta = 128;  // CTA size of the narrow rows
-
-constexpr int kWaves = 1;
-static int bwd_ctas(const RowShape& r) { return std::max(1, std::min(8, 512 / r.threads)); }
+constexpr RowLimits kBwdLimits = {128, {512, 512}, {512, 512}, 8192};
 
 // Column sums of this CTA's rows go to the workspace [block][2][cols]:
 // S0 = sum dn . xh, S1 = sum t . u . yh with u the gate where it varies over
@@ -31,16 +32,20 @@ static int bwd_ctas(const RowShape& r) { return std::max(1, std::min(8, 512 / r.
 // lean: dx' and a full gate do not come through the ring (rows so wide that it
 // would not hold two of them).
 // COMMON: all inputs, no full gate and not lean, known when compiled.
-template <typename T, typename R, bool VEC, int ITER, int MAXT, bool COMMON>
-__global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(const mxg_block_norm_grad_t p,
+template <typename T, typename R, bool VEC, int ITER, int SPLIT, bool COMMON>
+__global__ void __launch_bounds__(512, 1) block_norm_bwd_kernel(const mxg_block_norm_grad_t p,
                                                               float* ws, int team, int depth,
                                                               bool is_lean) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float red[3][128];
   const int nt = blockDim.x, teams = nt / team;
   const int lane = threadIdx.x % team, team_id = threadIdx.x / team;
-  const int cols = static_cast<int>(p.cols);
-  const float inv = 1.0f / static_cast<float>(cols);
+  // this CTA's columns: cols of them from off on
+  const int64_t off = SPLIT == 1 ? 0 : cluster_ctarank() * cols_per_cta(p.cols, SPLIT);
+  const int cols = static_cast<int>(SPLIT == 1 ? p.cols
+                                               : min(p.cols - off, cols_per_cta(p.cols, SPLIT)));
+  const float inv = 1.0f / static_cast<float>(p.cols);
+  const int64_t block = blockIdx.x / SPLIT;
   const bool has_y = COMMON || p.y != nullptr, has_n = COMMON || p.dn != nullptr;
   const bool has_x = COMMON || p.dx_out != nullptr;
   const bool full = !COMMON && p.gate_mode == MXG_GATE_FULL, lean = !COMMON && is_lean;
@@ -50,20 +55,20 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(const mxg_block
   const int at_x = at_y + (has_y ? t_bytes : 0), at_g = at_x + (has_x && !lean ? r_bytes : 0);
   const int chunk_bytes = at_g + (full && !lean ? t_bytes : 0);
   const int slot_bytes = ITER * chunk_bytes, ring_bytes = depth * slot_bytes;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+  const int64_t step = static_cast<int64_t>(gridDim.x / SPLIT) * teams;
   const uint32_t mine = smem_u32(ring) + threadIdx.x * 16, end = mine + ring_bytes;
   if (VEC) ring_clear(mine, ring_bytes, nt);
   grid_launch_dependents();
   const int c0 = RowIo<T, VEC>::col(0, 0, lane, team);
   const int dc = RowIo<T, VEC>::col(1, 0, lane, team) - c0;  // from one chunk to the next
 
-  int64_t f_row = static_cast<int64_t>(blockIdx.x) * teams + team_id;  // the row filled next
-  const R* x = static_cast<const R*>(p.x) + f_row * p.ldx + c0;
-  const T* n = static_cast<const T*>(p.dn) + f_row * p.lddn + c0;
-  const T* y = static_cast<const T*>(p.y) + f_row * p.ldy + c0;
-  const R* d = static_cast<const R*>(p.dx_out) + f_row * p.lddxo + c0;
-  R* dx = static_cast<R*>(p.dx) + f_row * p.lddx;
-  T* dy = static_cast<T*>(p.dy) + f_row * p.lddy;
+  int64_t f_row = block * teams + team_id;  // the row filled next
+  const R* x = static_cast<const R*>(p.x) + f_row * p.ldx + off + c0;
+  const T* n = static_cast<const T*>(p.dn) + f_row * p.lddn + off + c0;
+  const T* y = static_cast<const T*>(p.y) + f_row * p.ldy + off + c0;
+  const R* d = static_cast<const R*>(p.dx_out) + f_row * p.lddxo + off + c0;
+  R* dx = static_cast<R*>(p.dx) + f_row * p.lddx + off;
+  T* dy = static_cast<T*>(p.dy) + f_row * p.lddy + off;
   // One row into the slot at `to`, in two parts: what is read until t is made,
   // and what is read after that.  EARLY: a thread refills its own pieces of a
   // slot as soon as it has read them, so that a ring of two rows still has one in
@@ -89,7 +94,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(const mxg_block
       if (!EARLY && has_y) ring_fill<T, VEC>(at + at_y, y + o, in, cols, it, lane, team, nt);
       if (has_x && !lean) ring_fill<R, VEC>(at + at_x, d + o, in, cols, it, lane, team, nt);
       if (full && !lean)
-        ring_fill<T, VEC>(at + at_g, static_cast<const T*>(p.gate) + f_row * p.ldg + c0 + o, in,
+        ring_fill<T, VEC>(at + at_g, static_cast<const T*>(p.gate) + f_row * p.ldg + off + c0 + o, in,
                           cols, it, lane, team, nt);
     }
   };
@@ -117,13 +122,13 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(const mxg_block
     fill_late(mine + i * slot_bytes);
   }
 
-  constexpr bool REG = MAXT <= 512;
-  using W = Weight<T, VEC, ITER, REG>;
-  const W w_pre(p.w_pre, cols, lane, team);
-  const W w_post(p.w_post, cols, lane, team);
-  const W g_col(p.gate_mode == MXG_GATE_COL ? p.gate : nullptr, cols, lane, team);
-  F2 wg[REG ? ITER : 1][4];  // w_post times a gate per channel, in fp32
-  if constexpr (REG) {
+  if (SPLIT > 1) cluster_sync();  // both are there before one writes to the other
+  using W = Weight<T, VEC, ITER>;
+  const W w_pre(p.w_pre, off, cols, lane, team);
+  F2 wg[ITER][4];  // w_post times a gate per channel, in fp32
+  {
+    const W w_post(p.w_post, off, cols, lane, team);
+    const W g_col(p.gate_mode == MXG_GATE_COL ? p.gate : nullptr, off, cols, lane, team);
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
 #pragma unroll
@@ -133,13 +138,8 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(const mxg_block
     }
   }
   auto times_wg = [&](int it, F2(&f)[4]) {
-    if constexpr (REG) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], wg[it][i]);
-    } else {
-      w_post.apply(it, f);
-      g_col.apply(it, f);
-    }
+    for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], wg[it][i]);
   };
 
   // this thread's share of sum x'^2, sum a . x' and sum y^2 of the row at `at0`
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(const mxg_block
   if (ahead) {
     if (VEC) cp_async_wait(EARLY ? depth - 1 : depth - 2);
     row_sums(at0, v);
-    team_sum4(v, red[2], team);
+    team_sum4<SPLIT>(v, red[2], team);
   }
   // a row's gate is asked for a row ahead: its latency is that of memory
   const bool g_row = p.gate_mode == MXG_GATE_ROW;
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(const mxg_block
   };
   float gr = row_gate(row);
   int parity = 0;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * teams; base < p.rows; base += step) {
+  for (int64_t base = block * teams; base < p.rows; base += step) {
     const int limit = row < p.rows ? cols : 0;
     const uint32_t next = at0 + slot_bytes == end ? mine : at0 + slot_bytes;
     if (!EARLY) {
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(const mxg_block
     if (!ahead) {
       if (VEC) cp_async_wait(0);
       row_sums(at0, v);
-      team_sum4(v, red[2], team);
+      team_sum4<SPLIT>(v, red[2], team);
     }
     const float rx = rsqrtf(v[1] * inv + p.eps), ry = rsqrtf(v[3] * inv + p.eps);
     const float c = v[2] * inv * rx;  // mean(a . xh)
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(const mxg_block
       if (!has_x)
         zero4(t[it]);
       else if (lean)
-        unpack8<R>(RowIo<R, VEC>::load(static_cast<const R*>(p.dx_out) + row * p.lddxo, limit, it,
+        unpack8<R>(RowIo<R, VEC>::load(static_cast<const R*>(p.dx_out) + row * p.lddxo + off, limit, it,
                                        lane, team),
                    t[it]);
       else
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(const mxg_block
         if (full) {
           F2 g[4];
           if (lean)
-            unpack8<T>(RowIo<T, VEC>::load(static_cast<const T*>(p.gate) + row * p.ldg, limit, it,
+            unpack8<T>(RowIo<T, VEC>::load(static_cast<const T*>(p.gate) + row * p.ldg + off, limit, it,
                                            lane, team),
                        g);
           else
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(const mxg_block
 #pragma unroll
             for (int i = 0; i < 4; ++i) dg[i] = mul2(t[it][i], mul2(y[i], f2(p.res_scale * ry)));
             times_wg(it, dg);
-            RowIo<T, VEC>::store(static_cast<T*>(p.dgate) + row * p.lddg, limit, it, lane, team,
+            RowIo<T, VEC>::store(static_cast<T*>(p.dgate) + row * p.lddg + off, limit, it, lane, team,
                                  dg);
           }
 #pragma unroll
@@ -265,10 +265,10 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(const mxg_block
       if (VEC) cp_async_wait(depth - 2);
       row_sums(next, v);
     }
-    team_sum4(v, red[parity], team);
+    team_sum4<SPLIT>(v, red[parity], team);
     parity ^= 1;
     if (has_y) {
-      if (g_row && p.dgate != nullptr && lane == 0 && limit != 0)
+      if (g_row && p.dgate != nullptr && lane == 0 && off == 0 && limit != 0)
         static_cast<float*>(p.dgate)[row] = p.res_scale * ry * v[0];
       // dy = fr (b - y ry m) with m = mean(b . yh)
       const float fr = p.res_scale * gr * ry, m = v[0] * inv * ry;
@@ -290,12 +290,13 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(const mxg_block
     at0 = next;
   }
 
-  // ---- this CTA's partial row
-  float* out = ws + static_cast<int64_t>(blockIdx.x) * 2 * cols;
+  // ---- this CTA's part of a partial row
+  const int64_t total = p.cols;
+  float* out = ws + block * 2 * total + off;
   if (teams > 1) {  // several teams: their sums meet in shared memory (the ring is done with)
     if (VEC) cp_async_wait(0);
     __syncthreads();
-    out = reinterpret_cast<float*>(ring) + team_id * 2 * cols;
+    out = reinterpret_cast<float*>(ring) + team_id * 2 * total;
   }
 #pragma unroll
   for (int it = 0; it < ITER; ++it)
@@ -304,13 +305,13 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(const mxg_block
       const int at = RowIo<T, VEC>::col(it, e, lane, team);
       if (at < cols) {
         out[at] = e & 1 ? f2_hi(s0[it][e >> 1]) : f2_lo(s0[it][e >> 1]);
-        out[cols + at] = e & 1 ? f2_hi(s1[it][e >> 1]) : f2_lo(s1[it][e >> 1]);
+        out[total + at] = e & 1 ? f2_hi(s1[it][e >> 1]) : f2_lo(s1[it][e >> 1]);
       }
     }
   if (teams > 1) {
     __syncthreads();
     const float* sums = reinterpret_cast<const float*>(ring);
-    out = ws + static_cast<int64_t>(blockIdx.x) * 2 * cols;
+    out = ws + block * 2 * total;
     for (int i = threadIdx.x; i < 2 * cols; i += nt) {
       float s = 0.0f;
       for (int k = 0; k < teams; ++k) s += sums[k * 2 * cols + i];
@@ -362,14 +363,14 @@ namespace {
 template <typename T, typename R, bool VEC, bool COMMON>
 cudaError_t backward_rows(const mxg_block_norm_grad_t& p, float* ws, const RowShape& r,
                           int64_t grid, int smem, int depth, bool lean, cudaStream_t stream) {
+  if (r.split > 1)
+    return launch_rows(block_norm_bwd_kernel<T, R, VEC, 2, 2, COMMON>, r, grid, smem, stream, p, ws,
+                       r.team, depth, lean);
   if (r.iter == 1)
-    return launch_rows(block_norm_bwd_kernel<T, R, VEC, 1, 512, COMMON>, grid, r.threads, smem,
-                       stream, p, ws, r.team, depth, lean);
-  if (r.threads <= 512)
-    return launch_rows(block_norm_bwd_kernel<T, R, VEC, 2, 512, COMMON>, grid, r.threads, smem,
-                       stream, p, ws, r.team, depth, lean);
-  return launch_rows(block_norm_bwd_kernel<T, R, VEC, 2, 1024, COMMON>, grid, r.threads, smem,
-                     stream, p, ws, r.team, depth, lean);
+    return launch_rows(block_norm_bwd_kernel<T, R, VEC, 1, 1, COMMON>, r, grid, smem, stream, p, ws,
+                       r.team, depth, lean);
+  return launch_rows(block_norm_bwd_kernel<T, R, VEC, 2, 1, COMMON>, r, grid, smem, stream, p, ws,
+                     r.team, depth, lean);
 }
 
 template <typename T, typename R>
@@ -384,11 +385,11 @@ cudaError_t norm_backward(const mxg_block_norm_grad_t& p, float* ws, int num_sms
                    aligned_rows(p.w_pre, 0, sizeof(T)) &&
                    (p.gate_mode < MXG_GATE_COL || aligned_rows(p.gate, full ? p.ldg : 0, sizeof(T))) &&
                    (!full || aligned_rows(p.dgate, p.lddg, sizeof(T)));
-  const RowShape r = row_shape(p.cols, kBwdCta, 4096);
-  const int ctas = bwd_ctas(r);
+  const RowShape r = row_shape(p.cols, kBwdLimits);
+  const int ctas = row_ctas(r, kBwdLimits, 8);
   const int64_t teams = r.threads / r.team;
   const int64_t grid = std::min<int64_t>((p.rows + teams - 1) / teams,
-                                         static_cast<int64_t>(std::min(num_sms, kNormMaxSms)) * ctas * kWaves);
+                                         static_cast<int64_t>(std::min(num_sms, kNormMaxSms) / r.split) * ctas);
   if (grid > 0) {
     const int chunk = r.threads * 8 * r.iter;
     const int core = static_cast<int>((p.dn ? sizeof(R) + sizeof(T) : 0) + (p.y ? sizeof(T) : 0));
@@ -403,11 +404,13 @@ cudaError_t norm_backward(const mxg_block_norm_grad_t& p, float* ws, int num_sms
     // narrow rows: the teams' column sums meet where the ring was
     const int sums = teams > 1 ? static_cast<int>(teams * 2 * p.cols * sizeof(float)) : 0;
     const int smem = std::max(slot * depth, sums);
-    const bool common = vec && p.y && p.dn && p.dx_out && !full && !lean;
+    // (16 odd columns a thread spill less with the general code)
+    const bool common = p.y && p.dn && p.dx_out && !full && !lean && (vec || r.iter == 1);
     const cudaError_t e =
-        common ? backward_rows<T, R, true, true>(p, ws, r, grid, smem, depth, lean, stream)
-        : vec  ? backward_rows<T, R, true, false>(p, ws, r, grid, smem, depth, lean, stream)
-               : backward_rows<T, R, false, false>(p, ws, r, grid, smem, depth, lean, stream);
+        vec ? (common ? backward_rows<T, R, true, true>(p, ws, r, grid, smem, depth, lean, stream)
+                      : backward_rows<T, R, true, false>(p, ws, r, grid, smem, depth, lean, stream))
+            : (common ? backward_rows<T, R, false, true>(p, ws, r, grid, smem, depth, lean, stream)
+                      : backward_rows<T, R, false, false>(p, ws, r, grid, smem, depth, lean, stream));
     if (e != cudaSuccess) return e;
   }
   return launch_after(grid > 0, block_norm_bwd_finish_kernel<T>,
@@ -418,8 +421,8 @@ cudaError_t norm_backward(const mxg_block_norm_grad_t& p, float* ws, int num_sms
 }  // namespace
 
 int64_t block_norm_ws_bytes(int64_t rows, int64_t cols) {
-  const RowShape r = row_shape(cols, kBwdCta, 4096);
-  return std::min<int64_t>(rows, static_cast<int64_t>(kNormMaxSms) * bwd_ctas(r) * kWaves) * 2 * cols * 4;
+  const RowShape r = row_shape(cols, kBwdLimits);
+  return std::min<int64_t>(rows, static_cast<int64_t>(kNormMaxSms) * row_ctas(r, kBwdLimits, 8)) * 2 * cols * 4;
 }
 
 cudaError_t launch_block_norm_backward(const mxg_block_norm_grad_t& p, float* ws, int num_sms,

@@ -21,22 +21,55 @@ struct RowShape {
   int team;     // threads per row
   int threads;  // per CTA: one team, or several of at most a warp
   int iter;     // chunks of 8 columns per thread
+  int split;    // CTAs (a cluster) that share a row
 };
 
-// `wide`: columns above which a thread takes 16 of them.
-inline RowShape row_shape(int64_t cols, int small_cta, int64_t wide) {
+// Columns of a row that one CTA of a cluster of `split` holds: a multiple of 8
+// (the last one may have fewer).
+__host__ __device__ inline int64_t cols_per_cta(int64_t cols, int split) {
+  return split == 1 ? cols : (cols + 8 * split - 1) / (8 * split) * 8;
+}
+
+// What a kernel lets row_shape choose from.
+struct RowLimits {
+  int small_cta;  // CTA size of narrow rows
+  int team[2];    // threads a row may take with 8, and with 16, columns a thread
+  int fit[2];     // threads an SM holds of either kernel
+  int split_at;   // columns above which two CTAs share a row
+};
+
+// 8 or 16 columns a thread, whichever keeps more of an SM's threads on columns;
+// where both do alike, 8.
+inline RowShape row_shape(int64_t cols, const RowLimits& lim) {
   RowShape r;
+  r.split = cols > lim.split_at ? 2 : 1;
+  cols = cols_per_cta(cols, r.split);
   if (cols <= 256) {
     r.team = 8;
     while (r.team * 8 < cols) r.team *= 2;
-    r.threads = small_cta;
+    r.threads = lim.small_cta;
     r.iter = 1;
-  } else {
-    r.iter = cols > wide ? 2 : 1;
-    r.team = static_cast<int>((cols + 8 * r.iter - 1) / (8 * r.iter) + 31) / 32 * 32;
-    r.threads = r.team;
+    return r;
+  }
+  double best = -1.0;
+  for (int iter = 1; iter <= 2; ++iter) {
+    const int64_t busy = (cols + 8 * iter - 1) / (8 * iter);
+    const int team = static_cast<int>((busy + 31) / 32 * 32);
+    if (team > lim.team[iter - 1]) continue;
+    const int fit = lim.fit[iter - 1];
+    const double used = static_cast<double>(std::max(1, fit / team) * busy) / fit;
+    if (used > best + 1e-9) {
+      best = used;
+      r.iter = iter;
+      r.team = r.threads = team;
+    }
   }
   return r;
+}
+
+// CTAs an SM holds at once.
+inline int row_ctas(const RowShape& r, const RowLimits& lim, int most) {
+  return std::max(1, std::min(most, lim.fit[r.iter - 1] / r.threads));
 }
 
 constexpr int kRowSmem = 220 * 1024;  // of an SM's 227 KB, for the rings of its CTAs
@@ -45,18 +78,28 @@ inline bool aligned_rows(const void* p, int64_t ld, size_t size) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * static_cast<int64_t>(size)) % 16 == 0;
 }
 
-// Launches `kern` with its ring; more than 48 KB of shared memory in all has to be
-// asked for.
+// Launches `kern` with its ring, in clusters of `split`; more than 48 KB of
+// shared memory in all has to be asked for.
 template <typename Kern, typename... Args>
-cudaError_t launch_rows(Kern kern, int64_t grid, int threads, int smem, cudaStream_t stream,
-                        Args... args) {
+cudaError_t launch_rows(Kern kern, const RowShape& r, int64_t grid, int smem, cudaStream_t stream,
+                        const Args&... args) {
   if (smem > 40 * 1024) {  // 48 KB with the static part
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  kern<<<static_cast<unsigned>(grid), threads, smem, stream>>>(args...);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(r.split);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid * r.split));
+  cfg.blockDim = dim3(static_cast<unsigned>(r.threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = r.split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 // ---------------------------------------------------------------- fp32 pairs
@@ -243,15 +286,19 @@ __device__ __forceinline__ void cp_async_wait(int n) {
 
 // A thread's columns of a weight (ones where there is none).  REG: kept in
 // registers as they lie in memory -- read again for each row, they come from L2,
-// since the ring leaves L1 little room.  Rows of over 8192 columns have no
-// registers to spare and do that.
-template <typename T, bool VEC, int ITER, bool REG>
+// since the ring leaves L1 little room.  The forward pass on rows of over 8192
+// columns has no registers to spare and does that.
+template <typename T, bool VEC, int ITER, bool REG = true>
 struct Weight {
   Raw8<T> raw[REG ? ITER : 1];
   const T* at;
   int cols, lane, team;
-  __device__ __forceinline__ Weight(const void* w, int cols, int lane, int team)
-      : at(static_cast<const T*>(w)), cols(cols), lane(lane), team(team) {
+  // `w` is read from the CTA's first column, `off`, on
+  __device__ __forceinline__ Weight(const void* w, int64_t off, int cols, int lane, int team)
+      : at(w != nullptr ? static_cast<const T*>(w) + off : nullptr),
+        cols(cols),
+        lane(lane),
+        team(team) {
     if constexpr (REG) {
       F2 one[4] = {f2(1.0f), f2(1.0f), f2(1.0f), f2(1.0f)};
 #pragma unroll
@@ -285,15 +332,36 @@ __device__ __forceinline__ float lanes_sum(float v, int span) {
   return v;
 }
 
+// A CTA's barrier, or the cluster's where two CTAs share a row.
+template <int SPLIT>
+__device__ __forceinline__ void team_sync() {
+  if constexpr (SPLIT == 1)
+    __syncthreads();
+  else
+    cluster_sync();
+}
+// A warp's sum into place `at` of the buffer of every CTA that shares the row.
+template <int SPLIT>
+__device__ __forceinline__ void team_post(float* buf, int at, float v) {
+  buf[at] = v;
+  if constexpr (SPLIT == 2)
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(
+                     mapa_shared(smem_u32(buf + at), cluster_ctarank() ^ 1u)),
+                 "f"(v)
+                 : "memory");
+}
+
+// SPLIT 2: CTAs of at most 16 warps; rank r's warps take places 16 r and on.
+template <int SPLIT>
 __device__ __forceinline__ float team_sum(float v, float* buf, int team) {
-  if (team < 32) return lanes_sum(v, team);
+  if (SPLIT == 1 && team < 32) return lanes_sum(v, team);
   v = lanes_sum(v, 32);
-  if (team == 32) return v;
+  if (SPLIT == 1 && team == 32) return v;
   const int warps = team >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) buf[w] = v;
-  __syncthreads();
-  v = lane < warps ? buf[lane] : 0.0f;
-  if (warps <= 8) {
+  if (lane == 0) team_post<SPLIT>(buf, SPLIT == 1 ? w : 16 * cluster_ctarank() + w, v);
+  team_sync<SPLIT>();
+  v = (SPLIT == 1 ? lane : (lane & 15)) < warps ? buf[lane] : 0.0f;
+  if (SPLIT == 1 && warps <= 8) {
     v = lanes_sum(v, 8);
     return __shfl_sync(0xFFFFFFFFu, v, 0);
   }
@@ -302,8 +370,9 @@ __device__ __forceinline__ float team_sum(float v, float* buf, int team) {
 
 // Four at once.  Within a warp the lanes halve the values between them as they
 // halve the span, so that four sums cost 6 shuffles and not 20.
+template <int SPLIT>
 __device__ __forceinline__ void team_sum4(float (&v)[4], float* buf, int team) {
-  if (team < 32) {
+  if (SPLIT == 1 && team < 32) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = lanes_sum(v[i], team);
     return;
@@ -318,15 +387,18 @@ __device__ __forceinline__ void team_sum4(float (&v)[4], float* buf, int team) {
   float s = h8 ? b : a;
   s += __shfl_xor_sync(0xFFFFFFFFu, h8 ? a : b, 8);
   s = lanes_sum(s, 8);
-  if (team > 32) {
+  if (SPLIT > 1 || team > 32) {
     const int warps = team >> 5, w = threadIdx.x >> 5, j = lane & 7;
     float* mine = buf + (lane >> 3) * 32;
-    if (j == 0) mine[w] = s;
-    __syncthreads();
-    s = j < warps ? mine[j] : 0.0f;
+    if (j == 0) team_post<SPLIT>(mine, SPLIT == 1 ? w : 16 * cluster_ctarank() + w, s);
+    team_sync<SPLIT>();
+    s = 0.0f;
 #pragma unroll
-    for (int k = 8; k < 32; k += 8)
-      if (j + k < warps) s += mine[j + k];
+    for (int k = 0; k < 16; k += 8)
+      if (j + k < warps) {
+        s += mine[j + k];
+        if (SPLIT > 1) s += mine[16 + j + k];
+      }
     s = lanes_sum(s, 8);
   }
 #pragma unroll
