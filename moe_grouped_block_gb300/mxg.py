@@ -298,12 +298,13 @@ _DTYPES = {torch.float32: MXG_F32, torch.bfloat16: MXG_BF16, torch.float16: MXG_
 
 
 def _ld(t) -> int:
-    """Elements between the rows of a matrix whose rows are contiguous."""
-    if t is None:
+    """Elements between the rows of a matrix whose rows are contiguous; 0 where
+    they follow one another."""
+    if t is None or t.is_contiguous():
         return 0
     stride = t.stride()
     if len(stride) < 2:
-        return 0
+        raise ValueError("a vector must be contiguous")
     rows, cols = t.shape[-2:]
     if stride[-1] != 1 and cols > 1:
         raise ValueError("rows must be contiguous (stride %d between their elements)" % stride[-1])
@@ -314,7 +315,7 @@ def _ld(t) -> int:
 def _ld_experts(t) -> int:
     """The same for [G, N, K] whose experts follow one another without a gap."""
     ld = _ld(t)
-    if t.dim() == 3 and t.shape[0] > 1 and t.stride(0) != t.shape[1] * ld:
+    if ld and t.dim() == 3 and t.shape[0] > 1 and t.stride(0) != t.shape[1] * ld:
         raise ValueError("experts must lie one after the other (stride %d, want %d)"
                          % (t.stride(0), t.shape[1] * ld))
     return ld
