@@ -2,7 +2,7 @@
 // bf16 / fp16 / fp32 storage and fp32 registers, one element or 8 at a time.
 #pragma once
 
-#include "mxg_device.cuh"
+#include "device16.cuh"
 
 namespace mxg {
 
@@ -11,22 +11,6 @@ struct Bf16 {
 };
 struct F16 {
   uint16_t bits;
-};
-
-// mxg_dtype_t of a storage type
-template <typename T>
-struct ElemOf;
-template <>
-struct ElemOf<float> {
-  static constexpr int kType = MXG_F32;
-};
-template <>
-struct ElemOf<Bf16> {
-  static constexpr int kType = MXG_BF16;
-};
-template <>
-struct ElemOf<F16> {
-  static constexpr int kType = MXG_F16;
 };
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
@@ -130,18 +114,4 @@ __device__ __forceinline__ void unpack8(const Raw8<T>& v, float (&f)[8]) {
     unpack2<T>(v.q.w, f[6], f[7]);
   }
 }
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
-  uint4* q = reinterpret_cast<uint4*>(p);
-  if constexpr (sizeof(T) == 4) {
-    q[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                      __float_as_uint(f[3]));
-    q[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
-                      __float_as_uint(f[7]));
-  } else {
-    q[0] = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]),
-                      pack2<T>(f[6], f[7]));
-  }
-}
-
 }  // namespace mxg

@@ -34,7 +34,7 @@
 #include <atomic>
 
 #include "elem.cuh"
-#include "mxg_host.h"
+#include "host16.h"
 
 namespace mxg {
 
@@ -737,8 +737,7 @@ cudaError_t launch_grouped_gemm16(int in_f16, int mode, const void* A, int64_t l
                               static_cast<uint64_t>(G)};
     const uint64_t strides[2] = {static_cast<uint64_t>(ldb) * 2, static_cast<uint64_t>(N * ldb) * 2};
     const uint32_t box[3] = {64, mode == 0 ? static_cast<uint32_t>(p.tile_cols / 2) : 64u, 1};
-    if (!make_tmap_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT16, B, dims, strides, box,
-                      CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!make_tmap_3d_swizzled(&tq, B, dims, strides, box))
       return cudaErrorInvalidValue;
   }
   const int64_t units = count();

@@ -17,7 +17,7 @@
 #include <type_traits>
 
 #include "elem.cuh"
-#include "mxg_host.h"
+#include "host16.h"
 
 namespace mxg {
 

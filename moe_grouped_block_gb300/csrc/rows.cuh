@@ -13,7 +13,7 @@
 #include <algorithm>
 
 #include "elem.cuh"
-#include "mxg_host.h"
+#include "host16.h"
 
 namespace mxg {
 
