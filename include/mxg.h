@@ -397,7 +397,8 @@ typedef enum { MXG_F32 = 0, MXG_BF16 = 1, MXG_F16 = 2 } mxg_dtype_t;
  * Rows of the ragged operands at or beyond the live count take no part, and
  * rows of a ragged C there are not written; a NaN or infinity in one group's
  * rows reaches no other group.  Negative sizes count as 0 and rows past M_cap
- * are dropped, each recorded in dev_status.
+ * are dropped, each recorded in dev_status (as is TIMEOUT, a pipeline wait that
+ * ran out).
  * Errors: INVALID_ARG (nulls, sizes, types, a leading dimension below its row),
  * ALIGNMENT, UNSUPPORTED_ARCH, LAUNCH. */
 mxg_status_t mxg_grouped_gemm_16bit(mxg_dtype_t in_type, mxg_gemm_mode_t mode, const void* A,

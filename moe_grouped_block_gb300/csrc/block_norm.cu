@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const mxg_block_nor
 #pragma unroll
         for (int i = 0; i < 4; ++i) q = fma2(b[it][i], b[it][i], q);
       }
-      const float r = rsqrtf(team_sum<1>(sum2(q), red[0], team) * inv + p.eps) * p.res_scale * gr;
+      const float r = rsqrtf(team_sum(sum2(q), red[0], team) * inv + p.eps) * p.res_scale * gr;
       const F2 r2 = f2(r);
 #pragma unroll
       for (int it = 0; it < ITER; ++it) {
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const mxg_block_nor
       for (int it = 0; it < ITER; ++it)
 #pragma unroll
         for (int i = 0; i < 4; ++i) q = fma2(s[it][i], s[it][i], q);
-      const F2 r2 = f2(rsqrtf(team_sum<1>(sum2(q), red[1], team) * inv + p.eps));
+      const F2 r2 = f2(rsqrtf(team_sum(sum2(q), red[1], team) * inv + p.eps));
 #pragma unroll
       for (int it = 0; it < ITER; ++it) {
         w_pre.apply(it, s[it]);

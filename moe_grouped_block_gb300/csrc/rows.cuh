@@ -353,24 +353,23 @@ __device__ __forceinline__ void team_post(float* buf, int at, float v) {
                  : "memory");
 }
 
-// SPLIT 2: CTAs of at most 16 warps; rank r's warps take places 16 r and on.
-template <int SPLIT>
 __device__ __forceinline__ float team_sum(float v, float* buf, int team) {
-  if (SPLIT == 1 && team < 32) return lanes_sum(v, team);
+  if (team < 32) return lanes_sum(v, team);
   v = lanes_sum(v, 32);
-  if (SPLIT == 1 && team == 32) return v;
+  if (team == 32) return v;
   const int warps = team >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) team_post<SPLIT>(buf, SPLIT == 1 ? w : 16 * cluster_ctarank() + w, v);
-  team_sync<SPLIT>();
-  v = (SPLIT == 1 ? lane : (lane & 15)) < warps ? buf[lane] : 0.0f;
-  if (SPLIT == 1 && warps <= 8) {
+  if (lane == 0) buf[w] = v;
+  __syncthreads();
+  v = lane < warps ? buf[lane] : 0.0f;
+  if (warps <= 8) {
     v = lanes_sum(v, 8);
     return __shfl_sync(0xFFFFFFFFu, v, 0);
   }
   return lanes_sum(v, 32);
 }
 
-// Four at once.  Within a warp the lanes halve the values between them as they
+// Four at once, for CTAs of at most 16 warps (SPLIT 2: rank r's warps take places
+// 16 r and on).  Within a warp the lanes halve the values between them as they
 // halve the span, so that four sums cost 6 shuffles and not 20.
 template <int SPLIT>
 __device__ __forceinline__ void team_sum4(float (&v)[4], float* buf, int team) {
