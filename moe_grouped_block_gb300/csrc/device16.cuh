@@ -166,6 +166,16 @@ __device__ __forceinline__ void tc_mma_f16_pair_if(uint32_t d_tmem, uint64_t ade
       : "memory");
 }
 
+// fp32 words in shared memory, this CTA's and another one's of the cluster
+__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // ---------------------------------------------------------------- copies
 // cp_async_16 past L1, for data that is read once.
 __device__ __forceinline__ void cp_async_16_l2(uint32_t dst, const void* src) {

@@ -20,6 +20,10 @@
 // persistent and walk the units in a static order derived from the group
 // sizes on the device.
 //
+// Where there are few units and a long contraction, clusters of 4 or 8 CTAs take
+// one unit each and their pairs a part of its contraction.  They join the parts
+// in shared memory, each pair adding and storing some of the rows.
+//
 // Neither operand is transposed in memory: where the contraction runs along
 // rows (Q of dgrad, both of wgrad) the tile is loaded as 64-row boxes of 64
 // columns and the MMA reads it MN-major.
@@ -32,6 +36,7 @@
 // be zero), by warp 10 while earlier stages are multiplied.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "elem.cuh"
 #include "host16.h"
@@ -56,6 +61,7 @@ struct Gemm16Params {
   int32_t stages;       // pipeline stages, ...
   int32_t q_bytes;      // ... each half the unit's columns of Q ...
   int32_t stage_bytes;  // ... and half its rows of R
+  int32_t splits;       // pairs of CTAs that share a unit's contraction: 1, 2 or 4
 };
 
 // Row offsets of the groups and their first units, by one warp: negative
@@ -117,12 +123,14 @@ struct Unit16 {
   int32_t i0, j0; // first row (within the group, or of dW_g) and column of C
   int32_t rows;   // rows of the unit
   int32_t n_mma;  // the same, rounded up to 32: the MMAs' width
-  int32_t kdim;   // contraction length
+  int32_t k0;     // this pair's share of the contraction: its start ...
+  int32_t kdim;   // ... and length
 };
 
-template <int MODE>
+template <int MODE, bool SPLIT>
 __device__ __forceinline__ Unit16 map_unit16(int64_t u, const Gemm16Params& p,
-                                             const int32_t* row_off, const int32_t* unit_off) {
+                                             const int32_t* row_off, const int32_t* unit_off,
+                                             int32_t pair) {
   Unit16 t;
   const uint32_t cu = static_cast<uint32_t>(p.col_units);
   uint32_t i, j, tiles;
@@ -176,6 +184,12 @@ __device__ __forceinline__ Unit16 map_unit16(int64_t u, const Gemm16Params& p,
   t.j0 = static_cast<int32_t>(j) * p.tile_cols;
   t.rows = max(0, min(share, total - t.i0));
   t.n_mma = max(32, (t.rows + 31) & ~31);
+  t.k0 = 0;
+  if constexpr (SPLIT) {  // whole K blocks each
+    const int32_t blocks = (t.kdim + 63) / 64;
+    t.k0 = blocks * pair / p.splits * 64;
+    t.kdim = min(t.kdim, blocks * (pair + 1) / p.splits * 64) - t.k0;
+  }
   return t;
 }
 
@@ -252,7 +266,7 @@ constexpr uint32_t kStep16 = MN ? 2048 / 16 : 32 / 16;
 // 32768 with 8 blocks (512 elements).  wgrad of 8 experts of 14336 x 4096, 16381
 // rows, into fp32: 1156 us so, 1160 us without; with 6 blocks 1204 us, with 4,
 // where the MMAs catch up with the epilogue's stores, 1269 us.
-template <int MODE, int SEG>
+template <int MODE, int SEG, bool SPLIT>
 __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
     gemm16_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
                        const __grid_constant__ CUtensorMap tmap_r, const Gemm16Params p) {
@@ -272,7 +286,9 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
   const uint32_t stage0 = smem_u32(smem) + ((Cfg::kBarBytes + 8 * (p.G + 1) + 1023) & ~1023);
   const uint32_t stages = p.stages, stage_bytes = p.stage_bytes, q_bytes = p.q_bytes;
-  const uint32_t rank = cluster_ctarank();
+  // of a pair, its place in the pair and the cluster's rank of its even CTA
+  const uint32_t rank = cluster_ctarank() & 1u, even = SPLIT ? cluster_ctarank() & ~1u : 0u;
+  const int32_t pair = static_cast<int32_t>(even >> 1);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   auto full_bar = [&](int s) { return bar(s); };
   auto empty_bar = [&](int s) { return bar(S + s); };
@@ -321,7 +337,8 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
   cluster_sync();  // the even CTA's barriers exist before the odd CTA's copies signal them
   tc_fence_after();
   const uint32_t tmem_base = *tmem_base_s;
-  const int64_t unit0 = blockIdx.x >> 1, ustride = gridDim.x >> 1;
+  const uint32_t cluster_ctas = SPLIT ? 2 * static_cast<uint32_t>(p.splits) : 2u;
+  const int64_t unit0 = blockIdx.x / cluster_ctas, ustride = gridDim.x / cluster_ctas;
   const int64_t total =
       MODE == 1 ? static_cast<int64_t>(p.G) * ((p.N + p.tile_rows - 1) / p.tile_rows) * p.col_units
                 : unit_off[p.G];
@@ -334,7 +351,7 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
     const bool two_q = q_bytes > 8192, two_r = stage_bytes - q_bytes > 8192;
     bool ok = true;
     for (int64_t u = unit0, n = 0; ok && u < total; u += ustride, ++n) {
-      const Unit16 t = map_unit16<MODE>(u, p, row_off, unit_off);
+      const Unit16 t = map_unit16<MODE, SPLIT>(u, p, row_off, unit_off, pair);
       const int32_t kb_count = (t.kdim + BK - 1) / BK;
       const int32_t last = t.kdim - (kb_count - 1) * BK;  // elements of the last block
       if (rank == 0) {
@@ -355,7 +372,7 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
           break;
         }
         const uint32_t sq = stage0 + stage * stage_bytes, sr = sq + q_bytes;
-        const int32_t k0 = kb * BK;
+        const int32_t k0 = t.k0 + kb * BK;
         if (MODE == 1 && kb + 1 == kb_count && (last & 15) != 0) {
           // rows of the next group in the last MMA step: this CTA's bytes
           // land on its own barrier, and its mask warp passes them on
@@ -369,7 +386,7 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
           tail_parity ^= 1u << stage;
         } else {
           if (rank == 0) mbar_arrive_expect_tx_if(full_bar(stage), 2 * stage_bytes, leader);
-          const uint32_t fb = mapa_shared(full_bar(stage), 0);
+          const uint32_t fb = mapa_shared(full_bar(stage), even);
           if constexpr (MODE == 0) {
             tma_load_3d_pair_if(sq, &tmap_q, fb, k0, q_at, t.g, leader);
           } else if constexpr (MODE == 2) {
@@ -406,6 +423,7 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
   else if (warp == 1) {
     if (rank == 0) {
       const uint32_t leader = elect_leader();
+      const uint16_t pair_mask = static_cast<uint16_t>(0x3u << even);
       uint32_t stage = 0, phase = 0, seg = 0;  // seg: accumulators filled so far
       bool ok = true;
       int64_t n = 0;
@@ -447,14 +465,14 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
               tc_mma_f16_pair_if(d, qd + kk * kStep16<Q_MN>, rd + kk * kStep16<R_MN>, idesc,
                                  (kb > kb0 || kk > 0) ? 1u : 0u, leader);
             }
-            tc_commit_pair_mc_if(empty_bar(stage), 0x3, leader);
+            tc_commit_pair_mc_if(empty_bar(stage), pair_mask, leader);
             if (++stage == stages) {
               stage = 0;
               phase ^= 1u;
             }
           }
           if (!ok) break;
-          tc_commit_pair_mc_if(tfull_bar(acc), 0x3, leader);
+          tc_commit_pair_mc_if(tfull_bar(acc), pair_mask, leader);
           ++seg;
         } while (kb < kb_count);
       }
@@ -467,7 +485,7 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
   else if (MODE == 1 && warp == Cfg::kMaskWarp) {
     uint32_t stage = 0, used = 0;  // used: parity of each stage's masked uses so far
     for (int64_t u = unit0; u < total; u += ustride) {
-      const Unit16 t = map_unit16<MODE>(u, p, row_off, unit_off);
+      const Unit16 t = map_unit16<MODE, SPLIT>(u, p, row_off, unit_off, pair);
       const int32_t kb_count = (t.kdim + BK - 1) / BK;
       if (kb_count == 0) continue;
       const int32_t last = t.kdim - (kb_count - 1) * BK;
@@ -487,7 +505,7 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
           if (!mbar_wait_warp<true>(odd_bar(stage), par, abort_flag, p.status)) break;
           if (lane == 0) mbar_arrive(full_bar(stage));
         } else if (lane == 0) {
-          mbar_arrive_cluster(mapa_shared(odd_bar(stage), 0));
+          mbar_arrive_cluster(mapa_shared(odd_bar(stage), even));
         }
         used ^= 1u << stage;
       }
@@ -499,9 +517,9 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
     // lane quarter = 32 columns of C, every other chunk of 32 rows
     const uint32_t quarter = warp & 3u, half = (warp - 2) >> 2;
     uint32_t seg = 0;
-    bool ok = true;
+    bool ok = true, joined = !SPLIT;
     for (int64_t u = unit0; ok && u < total; u += ustride) {
-      const Unit16 t = map_unit16<MODE>(u, p, row_off, unit_off);
+      const Unit16 t = map_unit16<MODE, SPLIT>(u, p, row_off, unit_off, pair);
       const bool has_k = t.kdim > 0;
       const float alpha = p.alpha ? p.alpha[t.g] : 1.0f;
       const float beta = p.beta ? p.beta[t.g] : 0.0f;
@@ -532,15 +550,53 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
       auto give = [&] {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(seg & 1u), 0));
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(seg & 1u), even));
         ++seg;
       };
       const uint32_t lanes = tmem_base + ((32u * quarter) << 16);
+      // Pairs that share the contraction: chunk m (of this warp's four) of the
+      // sums is wanted by pair m % splits.  The others put theirs into the
+      // stages of that pair's CTA, once no pair copies or multiplies any more
+      // (a cluster has one unit only), and it adds them in the pairs' order.
+      auto join = [&](auto&& chunk) {
+        const int32_t S = p.splits, per = 4 / S;
+        auto place = [&](int32_t from, int32_t m) {
+          return stage0 + static_cast<uint32_t>(((from * per + m / S) * 2 + static_cast<int32_t>(half)) * 32 * 128 +
+                                                lane_col) * 4u;
+        };
+        __syncwarp();
+        cluster_sync();
+#pragma unroll
+        for (int32_t m = 0; m < 4; ++m) {
+          const int32_t to = m & (S - 1);
+          if (c0 + 64 * m >= t.rows || to == pair) continue;
+          float v[32];
+          chunk(m, v);
+          const uint32_t dst = mapa_shared(place(pair < to ? pair : pair - 1, m), 2 * to + rank);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) st_cluster_f32(dst + e * 512, v[e]);
+        }
+        __syncwarp();
+        cluster_sync();
+#pragma unroll
+        for (int32_t m = 0; m < 4; ++m) {
+          if (c0 + 64 * m >= t.rows || (m & (S - 1)) != pair) continue;
+          float v[32];
+          chunk(m, v);
+          for (int32_t from = 0; from < S - 1; ++from) {
+            const uint32_t src = place(from, m);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] += ld_shared_f32(src + e * 512);
+          }
+          store(c0 + 64 * m, v);
+          __syncwarp();
+        }
+        joined = true;
+      };
       if constexpr (SEG == 0) {
         if (!(ok = take())) break;
         const uint32_t taddr = lanes + 256u * (seg & 1u);
-        for (int32_t c = c0; c < t.rows; c += 64) {
-          float v[32];
+        auto read = [&](int32_t c, float(&v)[32]) {
           if (has_k) {
             uint32_t w[32];
             tmem_ld32(taddr + static_cast<uint32_t>(c), w);
@@ -551,8 +607,16 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = 0.0f;
           }
-          store(c, v);
-          __syncwarp();
+        };
+        if constexpr (SPLIT) {
+          join([&](int32_t m, float(&v)[32]) { read(c0 + 64 * m, v); });
+        } else {
+          for (int32_t c = c0; c < t.rows; c += 64) {
+            float v[32];
+            read(c, v);
+            store(c, v);
+            __syncwarp();
+          }
         }
         give();
       } else {
@@ -584,12 +648,29 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
           k += SEG * BK;
         } while (k < t.kdim);
         if (!ok) break;
+        if constexpr (SPLIT) {
+          join([&](int32_t m, float(&w)[32]) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
-          if (c0 + 64 * m < t.rows) store(c0 + 64 * m, v[m]);
-        __syncwarp();
+            for (int e = 0; e < 32; ++e) w[e] = v[m][e];
+          });
+        } else {
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            if (c0 + 64 * m < t.rows) store(c0 + 64 * m, v[m]);
+          __syncwarp();
+        }
       }
     }
+    if (!joined) {  // no unit, or given up
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
+  }
+  if (SPLIT && (warp < 2 || warp == Cfg::kMaskWarp)) {  // the epilogues' join
+    __syncwarp();
+    cluster_sync();
+    cluster_sync();
   }
 
   // ------------------------------------------------------------ teardown
@@ -608,55 +689,67 @@ namespace {
 constexpr int kMaxDev16 = 64;
 constexpr int kSeg16 = 8;  // K blocks an fp32 output's sum stays in tensor memory
 
-// Clusters of the pair kernel that the device holds at once, asked once per
+// Clusters of 2 * splits CTAs that the device holds at once, asked once per
 // device, with all the shared memory there is.
-template <int MODE, int SEG>
-int pair_clusters(int num_sms) {
-  static std::atomic<int> known[kMaxDev16];
+int pair_clusters(int splits, int num_sms) {
+  static std::atomic<int> known[3][kMaxDev16];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev16) return 0;
-  int c = known[dev].load(std::memory_order_relaxed);
+  std::atomic<int>& slot = known[splits >> 1][dev];
+  int c = slot.load(std::memory_order_relaxed);
   if (c != 0) return c;
-  auto kern = gemm16_pair_kernel<MODE, SEG>;
-  const int smem = Pair16::kSmemMax;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  auto kern = gemm16_pair_kernel<1, kSeg16, true>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Pair16::kSmemMax) !=
+      cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(2 * splits);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(num_sms & ~1));
-  cfg.blockDim = dim3(Pair16::threads(MODE));
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3(static_cast<unsigned>(num_sms / (2 * splits) * 2 * splits));
+  cfg.blockDim = dim3(Pair16::threads(1));
+  cfg.dynamicSmemBytes = Pair16::kSmemMax;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&c, kern, &cfg) != cudaSuccess || c < 1) c = num_sms / 2;
-  known[dev].store(c, std::memory_order_relaxed);
+  if (cudaOccupancyMaxActiveClusters(&c, kern, &cfg) != cudaSuccess || c < 1)
+    c = num_sms / (2 * splits);
+  slot.store(c, std::memory_order_relaxed);
   return c;
 }
 
-template <int MODE, int SEG>
+template <int MODE, int SEG, bool SPLIT>
 cudaError_t launch_pair16(const CUtensorMap& tq, const CUtensorMap& tr, const Gemm16Params& p,
                           int smem, int64_t max_units, int num_sms, cudaStream_t stream) {
-  const int clusters = pair_clusters<MODE, SEG>(num_sms);
+  static std::atomic<bool> ready[kMaxDev16];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev16)
+    return cudaErrorInvalidDevice;
+  if (!ready[dev].load(std::memory_order_relaxed)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(gemm16_pair_kernel<MODE, SEG, SPLIT>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, Pair16::kSmemMax);
+    if (e != cudaSuccess) return e;
+    ready[dev].store(true, std::memory_order_relaxed);
+  }
+  const int clusters = pair_clusters(p.splits, num_sms);
   if (clusters < 1) return cudaErrorInvalidConfiguration;
   const int64_t n = max_units < clusters ? max_units : clusters;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(2 * p.splits);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   // set up beside the kernel before it, where that one allows it
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * n));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * p.splits * n));
   cfg.blockDim = dim3(Pair16::threads(MODE));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gemm16_pair_kernel<MODE, SEG>, tq, tr, p);
+  return cudaLaunchKernelEx(&cfg, gemm16_pair_kernel<MODE, SEG, SPLIT>, tq, tr, p);
 }
 
 // A ragged matrix [rows, cols] of 16-bit elements, boxes of 64 columns.
@@ -693,8 +786,8 @@ cudaError_t launch_grouped_gemm16(int in_f16, int mode, const void* A, int64_t l
             (mode == 1 ? 1u << 16 : 0u) | ((256u >> 4) << 24);
   // Units of 256 x 256, or as many rows as there can be; while twice as many
   // still find a cluster each, their longer side is halved, down to 64 rows and
-  // 128 columns (one row through 4096 x 4096: 23 us in 16 units, 20 us in 32; in
-  // 64 of 64 columns 25 us).  The MMA always runs on 256 columns; the lanes of
+  // 128 columns (one row through 4096 x 4096 unshared: 23 us in 16 units, 20 us in
+  // 32; in 64 of 64 columns 25 us).  The MMA always runs on 256 columns; the lanes of
   // those that a unit does not have are not read.  What small units leave free of
   // a stage goes to more stages, i.e. more of the operands in flight.
   const int64_t c_rows = mode == 1 ? N : M_cap;
@@ -707,7 +800,21 @@ cudaError_t launch_grouped_gemm16(int in_f16, int mode, const void* A, int64_t l
     return mode == 1 ? G * ((N + p.tile_rows - 1) / p.tile_rows) * cu
                      : (M_cap + live * (p.tile_rows - 1)) / p.tile_rows * cu;
   };
-  while (count() * 2 <= num_sms / 2 && (p.tile_cols > 128 || p.tile_rows > 64)) {
+  // Where units are few and the contraction is long, 4 or 2 pairs share a unit's
+  // -- as many as leave each cluster one unit at most, and each pair 8 K blocks of
+  // 64, or 16 where it has more than 64 rows to join (one row through 4096 x 4096:
+  // 14.9 us by two pairs, 19.5 us by one; through 1024 x 4096: 10.3 us by four,
+  // 18.4 us; 16 rows through 1024 x 2048: 9.2 us by four, 10.3 us by two; wgrad of
+  // 512 x 512 over 2048 rows: 13.1 us by four, 11.3 us by two, 12.3 us by one).
+  // The length of wgrad's is known on average only.
+  const int64_t k_avg = mode == 0 ? K : mode == 2 ? N : live > 0 ? M_cap / live : 0;
+  p.splits = 1;
+  for (int s = 4; s > 1 && p.splits == 1; s /= 2)
+    if ((k_avg + 63) / 64 >= s * (p.tile_rows <= 64 ? 8 : 16) &&
+        count() <= pair_clusters(s, num_sms))
+      p.splits = s;
+  const int most = p.splits == 1 ? num_sms / 2 : pair_clusters(p.splits, num_sms);
+  while (count() * 2 <= most && (p.tile_cols > 128 || p.tile_rows > 64)) {
     if (p.tile_cols > 128 && (p.tile_cols >= p.tile_rows || p.tile_rows <= 64))
       p.tile_cols /= 2;
     else
@@ -721,7 +828,9 @@ cudaError_t launch_grouped_gemm16(int in_f16, int mode, const void* A, int64_t l
   p.stages = (Pair16::kSmemMax - header) / p.stage_bytes;
   if (p.stages > Pair16::kMaxStages) p.stages = Pair16::kMaxStages;
   // the MMA reads 16 KB from each tile of Q on, however many columns are in it
-  const int smem = header + (p.stages - 1) * p.stage_bytes + std::max(p.stage_bytes, 16384);
+  int smem = header + (p.stages - 1) * p.stage_bytes + std::max(p.stage_bytes, 16384);
+  // the sums of the other pairs: 32 rows of 128 columns eight times over, less its own share
+  if (p.splits > 1) smem = std::max(smem, header + (p.splits - 1) * (8 / p.splits) * 16384);
 
   // without rows no copy is made: any aligned address serves the tensor maps
   if (M_cap == 0) A = B = reinterpret_cast<const void*>(uintptr_t{1} << 20);
@@ -742,14 +851,18 @@ cudaError_t launch_grouped_gemm16(int in_f16, int mode, const void* A, int64_t l
   }
   const int64_t units = count();
   if (units > INT32_MAX) return cudaErrorInvalidValue;
-  if (out_type == MXG_F32) {
-    if (mode == 0) return launch_pair16<0, kSeg16>(tq, tr, p, smem, units, num_sms, stream);
-    if (mode == 1) return launch_pair16<1, kSeg16>(tq, tr, p, smem, units, num_sms, stream);
-    return launch_pair16<2, kSeg16>(tq, tr, p, smem, units, num_sms, stream);
-  }
-  if (mode == 0) return launch_pair16<0, 0>(tq, tr, p, smem, units, num_sms, stream);
-  if (mode == 1) return launch_pair16<1, 0>(tq, tr, p, smem, units, num_sms, stream);
-  return launch_pair16<2, 0>(tq, tr, p, smem, units, num_sms, stream);
+  auto launch = [&](auto seg, auto split) {
+    constexpr int SEG = decltype(seg)::value;
+    constexpr bool SPLIT = decltype(split)::value;
+    if (mode == 0) return launch_pair16<0, SEG, SPLIT>(tq, tr, p, smem, units, num_sms, stream);
+    if (mode == 1) return launch_pair16<1, SEG, SPLIT>(tq, tr, p, smem, units, num_sms, stream);
+    return launch_pair16<2, SEG, SPLIT>(tq, tr, p, smem, units, num_sms, stream);
+  };
+  using Whole = std::integral_constant<int, 0>;
+  using Parts = std::integral_constant<int, kSeg16>;
+  if (out_type == MXG_F32)
+    return p.splits > 1 ? launch(Parts{}, std::true_type{}) : launch(Parts{}, std::false_type{});
+  return p.splits > 1 ? launch(Whole{}, std::true_type{}) : launch(Whole{}, std::false_type{});
 }
 
 }  // namespace mxg

@@ -349,6 +349,60 @@ def test_same_bits_every_time():
             assert torch.equal(first, run(mode, A, B, sizes, N, K, torch.float32))
 
 
+SHARED = [  # mode, sizes, N, K: few outputs, long contractions
+    ("fprop", [1], 1000, 4104), ("fprop", [33], 520, 4100), ("fprop", [100], 520, 4100),
+    ("fprop", [300], 300, 4096), ("fprop", [5, 0, 3], 256, 2100), ("fprop", [40], 4088, 1030),
+    ("dgrad", [1], 4104, 1000), ("dgrad", [257], 4097, 264), ("dgrad", [0, 20, 70], 1100, 700),
+    ("wgrad", [5000], 300, 200), ("wgrad", [2048], 512, 512), ("wgrad", [1, 0, 40, 7, 9000], 129, 70),
+    ("wgrad", [4500, 4400, 4200], 50, 1032),
+]
+
+
+@pytest.mark.parametrize("case", SHARED, ids=lambda c: "%s_%s_%d_%d" % (c[0], len(c[1]), c[2], c[3]))
+def test_shared_contractions(case):
+    mode, sizes, N, K = case
+    mode, G, M = MODES[mode], len(sizes), sum(sizes)
+    cap = M + 5
+    a, b, A, B = inputs(mode, sizes, N, K, torch.bfloat16, 21, cap=cap)
+    alpha, beta = [0.5 + g for g in range(G)], [(-1.0) ** g * (g % 3) for g in range(G)]
+    g = torch.Generator().manual_seed(22)
+    c = torch.randn(*{FPROP: (cap, N), DGRAD: (cap, K), WGRAD: (G, N, K)}[mode], generator=g)
+    for out in (torch.float32, torch.bfloat16):
+        ref, mag, kd = reference(mode, a, b, sizes)
+        C = run(mode, A, B, sizes, N, K, out, cap=cap)
+        live = C if mode == WGRAD else C[:M]
+        check(live.cpu(), ref, mag, kd, out)
+        if mode != WGRAD:
+            assert (C[M:] == 7.0).all()
+        assert torch.equal(C, run(mode, A, B, sizes, N, K, out, cap=cap))
+        old = c.to(out)
+        ref, mag, kd = reference(mode, a, b, sizes, alpha, beta, old)
+        C = run(mode, A, B, sizes, N, K, out, cap=cap, alpha=alpha, beta=beta, c=old)
+        check((C if mode == WGRAD else C[:M]).cpu(), ref, mag, kd, out)
+    a, b, A, B = inputs(mode, sizes, N, K, torch.float16, 23, integers=True)
+    ref, _, _ = reference(mode, a, b, sizes)
+    assert torch.equal(run(mode, A, B, sizes, N, K, torch.float32).cpu().double(), ref)
+
+
+def test_shared_contractions_with_sizes_that_do_not_fit():
+    """Clusters without a unit, and sizes past the capacity or below zero."""
+    N, K = 256, 4096
+    a, b, A, B = inputs(FPROP, [2, 3, 1], N, K, torch.bfloat16, 24)
+    for sizes, taken in (([2, 3, 1], [2, 3, 1]), ([0, 0, 0], [0, 0, 0]), ([-4, 2, 0], [0, 2, 0]),
+                         ([3, 900, 1], [3, 3, 0])):
+        ws = torch.tensor(sizes + [0, 0, 0, 0], dtype=torch.int64, device=DEV)
+        C = torch.full((6, N), 7.0, device=DEV)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        mxg.mxg_grouped_gemm_16bit(FPROP, A, B, ws, 3, 6, N, K, None, None, C, dev_status=status)
+        torch.cuda.synchronize()
+        m = sum(taken)
+        if m:
+            ref, mag, kd = reference(FPROP, a, b, taken)
+            check(C[:m].cpu(), ref, mag, kd, torch.float32)
+        assert (C[m:] == 7.0).all()
+        assert bool(status.item()) == (sizes != taken)
+
+
 def test_binding_refusals():
     x = torch.zeros(16, 64, dtype=torch.bfloat16, device=DEV)
     w = torch.zeros(2, 32, 64, dtype=torch.bfloat16, device=DEV)
