@@ -8,6 +8,10 @@
 // the same order -- and scales.  Both are bound by memory; the second walks the
 // chunks backwards, so that it finds in L2 what the first read last.
 //
+// 1.41 G bf16 elements in 24 tensors: 1.28 ms, 6.6 TB/s for the three passes over
+// 2.8 GB (a copy reaches 6.78); nothing stays in an L2 of 126 MB but the last 4 %
+// read.  48 tensors of 1 to 262147 elements: 10.3 us, the two kernels' latency.
+//
 // Squares are summed in fp32 over 8 elements, over a thread's share of a chunk
 // (8 or fewer such sums) and over a warp, and in fp64 from there on.  A sum of 8
 // outside [2^-96, 2^120] -- where fp32 squares have overflowed, or may have lost
