@@ -700,8 +700,8 @@ namespace {
 constexpr int kMaxDev16 = 64;
 constexpr int kSeg16 = 8;  // K blocks an fp32 output's sum stays in tensor memory
 
-// Clusters of 2 * splits CTAs that the device holds at once, asked once per
-// device, with all the shared memory there is.
+// Clusters of 2 * splits CTAs that the device holds at once (-1: none of more
+// than a pair), asked once per device, with all the shared memory there is.
 int pair_clusters(int splits, int num_sms) {
   static std::atomic<int> known[3][kMaxDev16];
   int dev = 0;
@@ -724,7 +724,7 @@ int pair_clusters(int splits, int num_sms) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaOccupancyMaxActiveClusters(&c, kern, &cfg) != cudaSuccess || c < 1)
-    c = num_sms / (2 * splits);
+    c = splits == 1 ? num_sms / 2 : -1;
   slot.store(c, std::memory_order_relaxed);
   return c;
 }
