@@ -166,6 +166,14 @@ __device__ __forceinline__ void tc_mma_f16_pair_if(uint32_t d_tmem, uint64_t ade
       : "memory");
 }
 
+// cluster_sync in two halves, by whole warps
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // fp32 words in shared memory, this CTA's and another one's of the cluster
 __device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");

@@ -69,62 +69,75 @@ struct Gemm16Params {
   int32_t tile_rows;    // rows of C per unit: a multiple of 32, at most 256
   int32_t tile_cols;    // columns of C per unit: 256 or 128
   int32_t col_units;    // units side by side
+  uint32_t w_shape;     // unit_shape of dW's rows
   int32_t stages;       // pipeline stages, ...
   int32_t q_bytes;      // ... each half the unit's columns of Q ...
   int32_t stage_bytes;  // ... and half its rows of R
   int32_t splits;       // pairs of CTAs that share a unit's contraction: 1, 2 or 4
 };
 
-// Row offsets of the groups and their first units, by one warp: negative
-// sizes count as 0 and rows past M_cap are dropped, so that no access leaves
-// the operands.  A unit is `rows_per_unit` rows of a group times one of
-// `col_units` column ranges.
-__device__ __forceinline__ void group_tables16(const int64_t* group_ws, int G, int64_t M_cap,
-                                               int rows_per_unit, int64_t col_units,
+// The rows of a group (or of dW_g) in units of equal shares: a narrow last unit
+// would stream its weights for few products.  `tiles` of them, `share` rows each, a
+// multiple of 32; packed into a word.
+__host__ __device__ __forceinline__ uint32_t unit_shape(uint32_t rows, uint32_t tile_rows) {
+  const uint32_t tiles = (rows + tile_rows - 1) / tile_rows;
+  const uint32_t share = tiles == 0 ? 0 : ((rows + tiles - 1) / tiles + 31) / 32;  // <= 8
+  return tiles << 4 | share;
+}
+
+// Row offsets of the groups, the shape of their units and their first ones, by
+// one warp: negative sizes count as 0 and rows past M_cap are dropped, so that no
+// access leaves the operands.  A unit is a share of a group's rows times one of
+// `col_units` column ranges.  32-bit sums that stop at one row past the capacity:
+// with 64-bit ones and divisions a call took 0.5 us longer.
+__device__ __forceinline__ void group_tables16(const int64_t* group_ws, int G, uint32_t M_cap,
+                                               uint32_t tile_rows, uint32_t col_units,
                                                int32_t* row_off, int32_t* unit_off,
-                                               int32_t* status) {
-  const uint32_t lane = lane_id();
-  int64_t carry_rows = 0, carry_units = 0;
-  int32_t bits = 0;
-  auto scan = [&](int64_t v) {
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, d);
-      if (lane >= static_cast<uint32_t>(d)) v += u;
-    }
-    return v;
-  };
+                                               uint32_t* shape, int32_t* status) {
+  const uint32_t lane = lane_id(), most = M_cap + 1;
+  uint32_t carry_rows = 0, carry_units = 0;
+  bool neg = false, over = false;
   for (int base = 0; base < G; base += 32) {
     const int g = base + static_cast<int>(lane);
-    int64_t s = 0;
-    if (g < G) {
-      s = group_ws[g];
-      if (s < 0) {
-        s = 0;
-        bits |= MXG_DEV_NEG_SIZE;
-      }
-      if (s > M_cap) s = M_cap + 1;  // keeps the sum small, still past the capacity
+    const int64_t size = g < G ? group_ws[g] : 0;
+    neg |= size < 0;
+    const uint32_t s = size < 0 ? 0u : size > M_cap ? most : static_cast<uint32_t>(size);
+    uint32_t incl = s;  // all terms are at most `most`, which is below 2^31 + 1
+    auto add = [&](uint32_t a, uint32_t b) { return a > most - b ? most : a + b; };
+#pragma unroll
+    for (uint32_t d = 1; d < 32; d <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if (lane >= d) incl = add(incl, u);
     }
-    const int64_t incl = scan(s);
-    const int64_t before = min(carry_rows + incl - s, M_cap);
-    const int64_t after = min(carry_rows + incl, M_cap);
-    if (carry_rows + incl > M_cap && s > 0) bits |= MXG_DEV_SUM_OVER_CAPACITY;
-    const int64_t units = (after - before + rows_per_unit - 1) / rows_per_unit * col_units;
-    const int64_t uincl = scan(units);
+    incl = add(incl, carry_rows);
+    uint32_t excl = __shfl_up_sync(0xFFFFFFFFu, incl, 1);
+    if (lane == 0) excl = carry_rows;
+    const uint32_t before = min(excl, M_cap), after = min(incl, M_cap);
+    over |= incl > M_cap && s > 0;
+    const uint32_t word = unit_shape(after - before, tile_rows);
+    uint32_t units = (word >> 4) * col_units;
+    const uint32_t own = units;
+#pragma unroll
+    for (uint32_t d = 1; d < 32; d <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, units, d);
+      if (lane >= d) units += u;
+    }
     if (g < G) {
       row_off[g] = static_cast<int32_t>(before);
-      unit_off[g] = static_cast<int32_t>(carry_units + uincl - units);
+      unit_off[g] = static_cast<int32_t>(carry_units + units - own);
+      shape[g] = word;
     }
-    carry_rows += __shfl_sync(0xFFFFFFFFu, incl, 31);
-    carry_units += __shfl_sync(0xFFFFFFFFu, uincl, 31);
+    carry_rows = __shfl_sync(0xFFFFFFFFu, incl, 31);
+    carry_units += __shfl_sync(0xFFFFFFFFu, units, 31);
   }
   if (lane == 0) {
     row_off[G] = static_cast<int32_t>(min(carry_rows, M_cap));
     unit_off[G] = static_cast<int32_t>(carry_units);
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) bits |= __shfl_xor_sync(0xFFFFFFFFu, bits, d);
-  if (lane == 0 && blockIdx.x == 0) status_set(status, bits);
+  neg = __any_sync(0xFFFFFFFFu, neg);
+  over = __any_sync(0xFFFFFFFFu, over);
+  if ((neg || over) && lane == 0 && blockIdx.x == 0)
+    status_set(status, (neg ? MXG_DEV_NEG_SIZE : 0) | (over ? MXG_DEV_SUM_OVER_CAPACITY : 0));
 }
 
 // Work unit u: `rows` rows of C from i0 on, p.tile_cols columns from j0 on.
@@ -141,14 +154,14 @@ struct Unit16 {
 template <int MODE, bool SPLIT>
 __device__ __forceinline__ Unit16 map_unit16(int64_t u, const Gemm16Params& p,
                                              const int32_t* row_off, const int32_t* unit_off,
-                                             int32_t pair) {
+                                             const uint32_t* shape, int32_t pair) {
   Unit16 t;
   const uint32_t cu = static_cast<uint32_t>(p.col_units);
-  uint32_t i, j, tiles;
+  uint32_t i, j, word;
   int32_t total;  // rows of C in this group
   if constexpr (MODE == 1) {
-    tiles = static_cast<uint32_t>(p.N + p.tile_rows - 1) / p.tile_rows;
-    const uint32_t per = tiles * cu;
+    word = p.w_shape;
+    const uint32_t per = (word >> 4) * cu;
     t.g = static_cast<int32_t>(static_cast<uint32_t>(u) / per);
     const uint32_t local = static_cast<uint32_t>(u) - t.g * per;
     i = local / cu;
@@ -157,19 +170,22 @@ __device__ __forceinline__ Unit16 map_unit16(int64_t u, const Gemm16Params& p,
     t.row0 = row_off[t.g];
     t.kdim = row_off[t.g + 1] - t.row0;
   } else {
-    int lo = 0, hi = p.G;  // largest g with unit_off[g] <= u
-    while (hi - lo > 1) {
+    int lo = 0, hi = p.G;  // largest g with unit_off[g] <= u: halving, then 32 at once
+    while (hi - lo > 32) {
       const int mid = (lo + hi) >> 1;
       if (unit_off[mid] <= u)
         lo = mid;
       else
         hi = mid;
     }
+    const int at = lo + static_cast<int>(lane_id());
+    lo += __popc(__ballot_sync(0xFFFFFFFFu, at < hi && unit_off[min(at, p.G)] <= u)) - 1;
     t.g = lo;
     t.row0 = row_off[lo];
     t.kdim = MODE == 0 ? p.K : p.N;
     total = row_off[lo + 1] - t.row0;
-    tiles = static_cast<uint32_t>(total + p.tile_rows - 1) / p.tile_rows;
+    word = shape[lo];
+    const uint32_t tiles = word >> 4;
     const uint32_t local = static_cast<uint32_t>(u) - unit_off[lo];
     // column unit, then row unit, so that the clusters in flight share weight
     // tiles and the group's rows stay in L2; where those rows are more than an
@@ -188,9 +204,7 @@ __device__ __forceinline__ Unit16 map_unit16(int64_t u, const Gemm16Params& p,
       j = blk * b + (rem - i * width);
     }
   }
-  // the group's rows in equal shares (multiples of 32): a narrow last unit
-  // would stream its weights for few products
-  const int32_t share = ((total + static_cast<int32_t>(tiles) - 1) / static_cast<int32_t>(tiles) + 31) & ~31;
+  const int32_t share = static_cast<int32_t>(word & 15u) * 32;
   t.i0 = static_cast<int32_t>(i) * share;
   t.j0 = static_cast<int32_t>(j) * p.tile_cols;
   t.rows = max(0, min(share, total - t.i0));
@@ -254,7 +268,7 @@ struct Pair16 {
   static constexpr int kBarBytes = 8 * (kBars + 2) + 16;
   // the barriers and tables lie before the stages
   static constexpr int kSmemMax = 227 * 1024;
-  static int header_bytes(int G) { return (kBarBytes + 8 * (G + 1) + 1023) / 1024 * 1024; }
+  static int header_bytes(int G) { return (kBarBytes + 12 * (G + 1) + 1023) / 1024 * 1024; }
 };
 
 // Descriptor of a K-major tile (rows of 128 bytes, 128-byte swizzle), or of an
@@ -293,9 +307,10 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_s + 1);
   int32_t* row_off = reinterpret_cast<int32_t*>(smem + Cfg::kBarBytes);
   int32_t* unit_off = row_off + (p.G + 1);
+  uint32_t* shape = reinterpret_cast<uint32_t*>(unit_off + (p.G + 1));
 
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
-  const uint32_t stage0 = smem_u32(smem) + ((Cfg::kBarBytes + 8 * (p.G + 1) + 1023) & ~1023);
+  const uint32_t stage0 = smem_u32(smem) + ((Cfg::kBarBytes + 12 * (p.G + 1) + 1023) & ~1023);
   const uint32_t stages = p.stages, stage_bytes = p.stage_bytes, q_bytes = p.q_bytes;
   // of a pair, its place in the pair and the cluster's rank of its even CTA
   const uint32_t rank = cluster_ctarank() & 1u, even = SPLIT ? cluster_ctarank() & ~1u : 0u;
@@ -337,21 +352,24 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
     prefetch_tmap(&tmap_q);
     prefetch_tmap(&tmap_r);
   }
+  __syncwarp();
+  cluster_arrive();  // the barriers are there for the cluster's other CTAs
   // from here on memory is read: what came before on the stream is done
   grid_launch_dependents();
   grid_wait_for_previous();
   if (warp == 1)
-    group_tables16(p.group_ws, p.G, p.M_cap, p.tile_rows, p.col_units, row_off, unit_off,
-                   p.status);
+    group_tables16(p.group_ws, p.G, static_cast<uint32_t>(p.M_cap),
+                   static_cast<uint32_t>(p.tile_rows), static_cast<uint32_t>(p.col_units), row_off,
+                   unit_off, shape, p.status);
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // the even CTA's barriers exist before the odd CTA's copies signal them
+  cluster_wait();  // the even CTA's barriers exist before the odd CTA's copies signal them
   tc_fence_after();
   const uint32_t tmem_base = *tmem_base_s;
   const uint32_t cluster_ctas = SPLIT ? 2 * static_cast<uint32_t>(p.splits) : 2u;
   const int64_t unit0 = blockIdx.x / cluster_ctas, ustride = gridDim.x / cluster_ctas;
   const int64_t total =
-      MODE == 1 ? static_cast<int64_t>(p.G) * ((p.N + p.tile_rows - 1) / p.tile_rows) * p.col_units
+      MODE == 1 ? static_cast<int64_t>(p.G) * (p.w_shape >> 4) * p.col_units
                 : unit_off[p.G];
 
   // ------------------------------------------------------------ producers (both CTAs)
@@ -362,7 +380,7 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
     const bool two_q = q_bytes > 8192, two_r = stage_bytes - q_bytes > 8192;
     bool ok = true;
     for (int64_t u = unit0, n = 0; ok && u < total; u += ustride, ++n) {
-      const Unit16 t = map_unit16<MODE, SPLIT>(u, p, row_off, unit_off, pair);
+      const Unit16 t = map_unit16<MODE, SPLIT>(u, p, row_off, unit_off, shape, pair);
       const int32_t kb_count = (t.kdim + BK - 1) / BK;
       const int32_t last = t.kdim - (kb_count - 1) * BK;  // elements of the last block
       if (rank == 0) {
@@ -496,7 +514,7 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
   else if (MODE == 1 && warp == Cfg::kMaskWarp) {
     uint32_t stage = 0, used = 0;  // used: parity of each stage's masked uses so far
     for (int64_t u = unit0; u < total; u += ustride) {
-      const Unit16 t = map_unit16<MODE, SPLIT>(u, p, row_off, unit_off, pair);
+      const Unit16 t = map_unit16<MODE, SPLIT>(u, p, row_off, unit_off, shape, pair);
       const int32_t kb_count = (t.kdim + BK - 1) / BK;
       if (kb_count == 0) continue;
       const int32_t last = t.kdim - (kb_count - 1) * BK;
@@ -530,7 +548,7 @@ __global__ void __launch_bounds__(Pair16::threads(MODE), 1)
     uint32_t seg = 0;
     bool ok = true, joined = !SPLIT;
     for (int64_t u = unit0; ok && u < total; u += ustride) {
-      const Unit16 t = map_unit16<MODE, SPLIT>(u, p, row_off, unit_off, pair);
+      const Unit16 t = map_unit16<MODE, SPLIT>(u, p, row_off, unit_off, shape, pair);
       const bool has_k = t.kdim > 0;
       const float alpha = p.alpha ? p.alpha[t.g] : 1.0f;
       const float beta = p.beta ? p.beta[t.g] : 0.0f;
@@ -832,6 +850,7 @@ cudaError_t launch_grouped_gemm16(int in_f16, int mode, const void* A, int64_t l
       p.tile_rows = (p.tile_rows / 2 + 31) / 32 * 32;
   }
   p.col_units = (p.out_cols + p.tile_cols - 1) / p.tile_cols;
+  p.w_shape = unit_shape(static_cast<uint32_t>(N), static_cast<uint32_t>(p.tile_rows));
   p.q_bytes = p.tile_cols / 2 * 128;
   const int r_bytes = mode == 1 ? (p.tile_rows > 128 ? 16384 : 8192) : p.tile_rows / 2 * 128;
   p.stage_bytes = p.q_bytes + r_bytes;
