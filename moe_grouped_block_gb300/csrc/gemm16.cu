@@ -29,7 +29,7 @@
 // columns and the MMA reads it MN-major.
 //
 // What bounds it.  With a few rows, the weights' bytes: 16 rows through 7 of 8
-// experts of 14336 x 4096, 128 us at 6.4 TB/s of the 6.78 that a copy reaches.
+// experts of 14336 x 4096, 126 us at 6.5 TB/s of the 6.78 that a copy reaches.
 // With many, the tensor cores and the power they draw: 16384 rows through 8 such
 // experts in 1.03 ms when run for milliseconds (1.87 PFLOP/s; the tensor pipe is
 // active 92 % of the time), in 1.19 ms when run for seconds, at 1.4 kW and some
@@ -832,9 +832,10 @@ cudaError_t launch_grouped_gemm16(int in_f16, int mode, const void* A, int64_t l
   // Where units are few and the contraction is long, 4 or 2 pairs share a unit's
   // -- as many as leave each cluster one unit at most, and each pair 8 K blocks of
   // 64, or 16 where it has more than 64 rows to join (one row through 4096 x 4096:
-  // 14.9 us by two pairs, 19.5 us by one; through 1024 x 4096: 10.3 us by four,
-  // 18.4 us; 16 rows through 1024 x 2048: 9.2 us by four, 10.3 us by two; wgrad of
-  // 512 x 512 over 2048 rows: 13.1 us by four, 11.3 us by two, 12.3 us by one).
+  // 14.7 us by two pairs, 19.4 us by one; through 1024 x 4096: 10.3 us by four,
+  // 12.8 us by two, 17.9 us by one; 16 rows through 1024 x 2048: 8.7, 9.7 and
+  // 11.8 us; wgrad of 512 x 512 over 2048 rows: 12.5 us by four, 10.8 us by two,
+  // 11.8 us by one; 128 rows through 1024 x 1024: 8.2 us by two, 7.7 us by one).
   // The length of wgrad's is known on average only.
   const int64_t k_avg = mode == 0 ? K : mode == 2 ? N : live > 0 ? M_cap / live : 0;
   p.splits = 1;
