@@ -309,6 +309,9 @@ def _ld(t) -> int:
     if stride[-1] != 1 and cols > 1:
         raise ValueError("rows must be contiguous (stride %d between their elements)" % stride[-1])
     # the stride of a dimension of size 1 says nothing
+    if rows > 1 and stride[-2] < cols:
+        raise ValueError("rows overlap (stride %d, %d elements): a broadcast matrix has to be "
+                         "materialised" % (stride[-2], cols))
     return stride[-2] if rows > 1 else max(stride[-2], cols)
 
 
