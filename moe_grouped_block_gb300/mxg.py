@@ -12,6 +12,7 @@ for the shapes include/mxg.h documents.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 
@@ -315,30 +316,95 @@ def _ld(t) -> int:
     return stride[-2] if rows > 1 else max(stride[-2], cols)
 
 
-def _ld_experts(t) -> int:
-    """The same for [G, N, K] whose experts follow one another without a gap."""
-    ld = _ld(t)
-    if ld and t.dim() == 3 and t.shape[0] > 1 and t.stride(0) != t.shape[1] * ld:
-        raise ValueError("experts must lie one after the other (stride %d, want %d)"
-                         % (t.stride(0), t.shape[1] * ld))
+def _operand16(t, name: str, rows: int, cols: int, per: int = 0) -> int:
+    """Elements between the rows of the `rows` x `cols` matrix that t holds -- or of
+    experts of `per` rows each, one after the other -- and 0 where they are dense.
+    t may have more rows, and more columns in a row; a contiguous t counts as its
+    reshape."""
+    if rows > 1 and t.shape == ((rows // per, per, cols) if per else (rows, cols)):
+        if t.is_contiguous():
+            return 0  # as nearly all are
+    if rows < 0 or cols < 1:
+        return 0  # the library refuses the sizes
+    shape, stride = t.shape, t.stride()
+    dense = t.is_contiguous() and _reshapes_to(shape, rows, cols, per)
+    if not dense:
+        have = shape[0] * shape[1] if len(shape) == 3 else shape[0]
+        if (len(shape) not in (2, 3) or shape[-1] < cols or have < rows
+                or (len(shape) == 3 and per and shape[1] != per)):
+            raise ValueError("%s: expected %s: got %s" % (name, [rows // per, per, cols] if per else
+                                                          [rows, cols], tuple(shape)))
+        if stride[-1] != 1 and cols > 1:
+            raise ValueError("%s: rows must be contiguous (stride %d between their elements)"
+                             % (name, stride[-1]))
+    if rows <= 1:  # no stride to keep: any multiple of 8 serves
+        return (cols + 7) // 8 * 8
+    if dense:
+        return 0
+    one = len(shape) == 3 and shape[1] == 1
+    ld = stride[0] if one else stride[-2]
+    if ld < cols:
+        raise ValueError("%s: rows overlap (stride %d, %d elements)" % (name, ld, cols))
+    if len(shape) == 3 and rows > shape[1] and stride[0] != shape[1] * ld:
+        raise ValueError("%s: experts must lie one after the other (stride %d, want %d)"
+                         % (name, stride[0], shape[1] * ld))
     return ld
+
+
+def _reshapes_to(shape, rows: int, cols: int, per: int) -> bool:
+    """Whether a contiguous tensor of this shape starts with `rows` dense rows: its last
+    dimensions together are the columns, or its elements are just as many."""
+    n = math.prod(shape)
+    if n < rows * cols:
+        return False
+    if len(shape) == 1:
+        return True
+    if len(shape) == 3 and per and shape[-1] == cols:
+        return shape[1] == per
+    width = 1
+    for d in reversed(shape):
+        width *= d
+        if width >= cols:
+            break
+    return width == cols or (n == rows * cols and shape[-1] % cols == 0)
+
+
+def _per_group(t, name: str, G: int) -> None:
+    """alpha or beta: a contiguous fp32 vector of at least G elements."""
+    if not isinstance(t, int) and (t.dtype is not torch.float32 or t.numel() < G
+                                   or not t.is_contiguous()):
+        raise ValueError("%s: expected %d contiguous fp32 elements: got %s of %s"
+                         % (name, G, tuple(t.shape), t.dtype))
 
 
 def mxg_grouped_gemm_16bit(mode: int, A: torch.Tensor, B: torch.Tensor, group_ws: torch.Tensor,
                            G: int, M_cap: int, N: int, K: int, alpha=None, beta=None,
                            C: torch.Tensor = None, dev_status=None, stream=None) -> None:
-    """A, B: bf16 or fp16 device tensors (rows may be strided; weights [G, N, K]
-    or [G*N, K]); C: fp32 or the operands' type."""
+    """A, B: bf16 or fp16 device tensors of at least the rows and columns that the mode
+    implies ([M_cap, N or K]; weights [G, N, K] or [G*N, K]), of which the first ones
+    count; rows may be strided.  C: fp32 or the operands' type."""
     if (A.dtype != B.dtype or A.dtype not in (torch.bfloat16, torch.float16)
             or C.dtype not in _DTYPES):
         raise ValueError("operands of one 16-bit type, C of that or fp32: got %s, %s, %s"
                          % (A.dtype, B.dtype, C.dtype))
     assert group_ws.dtype == torch.int64
+    if group_ws.numel() < G or not group_ws.is_contiguous():
+        raise ValueError("group_ws: expected the workspace of %d groups: got %s"
+                         % (G, tuple(group_ws.shape)))
+    for v, name in ((alpha, "alpha"), (beta, "beta")):
+        if v is not None:
+            _per_group(v, name, G)
+    if mode == MXG_WGRAD_NT:
+        lda, ldb = _operand16(A, "A", M_cap, N), _operand16(B, "B", M_cap, K)
+        ldc = _operand16(C, "C", G * N, K, N)
+    else:
+        fprop = mode == MXG_FPROP_TN
+        lda, ldb = _operand16(A, "A", M_cap, K if fprop else N), _operand16(B, "B", G * N, K, N)
+        ldc = _operand16(C, "C", M_cap, N if fprop else K)
     _check("mxg_grouped_gemm_16bit",
-           load().mxg_grouped_gemm_16bit(_DTYPES[A.dtype], mode, _p(A), _ld(A), _p(B),
-                                         _ld_experts(B), _p(group_ws), G, M_cap, N, K, _p(alpha),
-                                         _p(beta), _p(C), _ld_experts(C), _DTYPES[C.dtype],
-                                         _p(dev_status), _s(stream)))
+           load().mxg_grouped_gemm_16bit(_DTYPES[A.dtype], mode, _p(A), lda, _p(B), ldb,
+                                         _p(group_ws), G, M_cap, N, K, _p(alpha), _p(beta), _p(C),
+                                         ldc, _DTYPES[C.dtype], _p(dev_status), _s(stream)))
 
 
 def _same_type(tensors) -> int:
