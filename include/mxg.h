@@ -493,8 +493,9 @@ typedef struct {
   int64_t lddg;
 } mxg_block_norm_grad_t;
 
-/* Bytes of the backward workspace (0 if rows < 0 or cols < 1); 16-byte aligned
- * device memory whose contents mean nothing before or after the call. */
+/* Bytes of the backward workspace (0 for sizes that the call refuses: rows < 0,
+ * cols < 1 or > 16384); 16-byte aligned device memory whose contents mean nothing
+ * before or after the call. */
 size_t mxg_block_norm_workspace_bytes(int64_t rows, int64_t cols);
 
 /* Errors: as mxg_block_norm, plus WORKSPACE_TOO_SMALL. */

@@ -96,6 +96,7 @@ mxg_status_t launched(cudaError_t e, uint64_t n) {
 // The kernels index rows (and the padded rows of groups of any size) with
 // 32-bit integers in their group tables.
 constexpr int64_t kMaxRows = 0x7FFFFF80LL;
+constexpr int64_t kMaxNormCols = 16384;  // of the norms around a block
 
 // Arguments of the offsets entry points.  Bounds on the multiplier (2^31)
 // and on the capacity (2^62, and capacity * last_dim within int64) keep every
@@ -139,7 +140,8 @@ mxg_status_t norm_common(Desc& d) {
   const size_t e = dtype_bytes(d.dtype), r = dtype_bytes(d.res_dtype);
   if (e == 0 || r == 0 || (d.res_dtype != d.dtype && d.res_dtype != MXG_F32))
     return MXG_ERR_INVALID_ARG;
-  if (d.rows < 0 || d.rows > kMaxRows || d.cols < 1 || d.cols > 16384) return MXG_ERR_INVALID_ARG;
+  if (d.rows < 0 || d.rows > kMaxRows || d.cols < 1 || d.cols > kMaxNormCols)
+    return MXG_ERR_INVALID_ARG;
   if (!(d.eps > 0.0f) || std::isinf(d.eps) || !std::isfinite(d.res_scale))
     return MXG_ERR_INVALID_ARG;
   if (d.gate_mode < MXG_GATE_NONE || d.gate_mode > MXG_GATE_FULL) return MXG_ERR_INVALID_ARG;
@@ -517,7 +519,9 @@ mxg_status_t mxg_block_norm(const mxg_block_norm_t* desc, mxg_stream_t stream) {
 }
 
 size_t mxg_block_norm_workspace_bytes(int64_t rows, int64_t cols) {
-  return rows < 0 || cols < 1 ? 0 : static_cast<size_t>(mxg::block_norm_ws_bytes(rows, cols));
+  // a width that the calls refuse has no shape of teams to ask for
+  if (rows < 0 || cols < 1 || cols > kMaxNormCols) return 0;
+  return static_cast<size_t>(mxg::block_norm_ws_bytes(rows, cols));
 }
 
 mxg_status_t mxg_block_norm_backward(const mxg_block_norm_grad_t* desc, void* workspace,
