@@ -316,14 +316,13 @@ def _ld(t) -> int:
     return stride[-2] if rows > 1 else max(stride[-2], cols)
 
 
-def _operand16(t, name: str, rows: int, cols: int, per: int = 0) -> int:
-    """Elements between the rows of the `rows` x `cols` matrix that t holds -- or of
-    experts of `per` rows each, one after the other -- and 0 where they are dense.
-    t may have more rows, and more columns in a row; a contiguous t counts as its
-    reshape."""
-    if rows > 1 and t.shape == ((rows // per, per, cols) if per else (rows, cols)):
-        if t.is_contiguous():
-            return 0  # as nearly all are
+def _operand16(t, name: str, want: tuple) -> int:
+    """Elements between the rows of the matrix [rows, cols] that t holds, or of the
+    experts [G, rows, cols] one after the other, and 0 where they are dense.  t may
+    have more rows (or experts), and more columns in a row; a contiguous t counts as
+    its reshape."""
+    per = want[1] if len(want) == 3 else 0
+    rows, cols = want[0] * (per or 1), want[-1]
     if rows < 0 or cols < 1:
         return 0  # the library refuses the sizes
     shape, stride = t.shape, t.stride()
@@ -332,8 +331,7 @@ def _operand16(t, name: str, rows: int, cols: int, per: int = 0) -> int:
         have = shape[0] * shape[1] if len(shape) == 3 else shape[0]
         if (len(shape) not in (2, 3) or shape[-1] < cols or have < rows
                 or (len(shape) == 3 and per and shape[1] != per)):
-            raise ValueError("%s: expected %s: got %s" % (name, [rows // per, per, cols] if per else
-                                                          [rows, cols], tuple(shape)))
+            raise ValueError("%s: expected %s: got %s" % (name, want, tuple(shape)))
         if stride[-1] != 1 and cols > 1:
             raise ValueError("%s: rows must be contiguous (stride %d between their elements)"
                              % (name, stride[-1]))
@@ -394,13 +392,17 @@ def mxg_grouped_gemm_16bit(mode: int, A: torch.Tensor, B: torch.Tensor, group_ws
     for v, name in ((alpha, "alpha"), (beta, "beta")):
         if v is not None:
             _per_group(v, name, G)
+    a = (M_cap, K if mode == MXG_FPROP_TN else N)
     if mode == MXG_WGRAD_NT:
-        lda, ldb = _operand16(A, "A", M_cap, N), _operand16(B, "B", M_cap, K)
-        ldc = _operand16(C, "C", G * N, K, N)
+        b, c = (M_cap, K), (G, N, K)
     else:
-        fprop = mode == MXG_FPROP_TN
-        lda, ldb = _operand16(A, "A", M_cap, K if fprop else N), _operand16(B, "B", G * N, K, N)
-        ldc = _operand16(C, "C", M_cap, N if fprop else K)
+        b, c = (G, N, K), (M_cap, N if mode == MXG_FPROP_TN else K)
+    # (a dense single row of a width that is no multiple of 8 is given a stride that is)
+    if ((not (N | K) & 7 or (M_cap > 1 and N > 1)) and A.shape == a and B.shape == b
+            and C.shape == c and A.is_contiguous() and B.is_contiguous() and C.is_contiguous()):
+        lda = ldb = ldc = 0  # as nearly all are
+    else:
+        lda, ldb, ldc = _operand16(A, "A", a), _operand16(B, "B", b), _operand16(C, "C", c)
     _check("mxg_grouped_gemm_16bit",
            load().mxg_grouped_gemm_16bit(_DTYPES[A.dtype], mode, _p(A), lda, _p(B), ldb,
                                          _p(group_ws), G, M_cap, N, K, _p(alpha), _p(beta), _p(C),
