@@ -145,12 +145,12 @@ template <typename T, typename R, bool VEC, bool COMMON>
 cudaError_t forward_rows(const mxg_block_norm_t& p, const RowShape& r, int64_t grid, int smem,
                          int depth, cudaStream_t stream) {
   if (r.iter == 1)
-    return launch_rows(block_norm_kernel<T, R, VEC, 1, 256, COMMON>, r, grid, smem, stream, p,
+    return launch_rows<block_norm_kernel<T, R, VEC, 1, 256, COMMON>>(r, grid, smem, stream, p,
                        r.team, depth);
   if (r.threads <= 512)
-    return launch_rows(block_norm_kernel<T, R, VEC, 2, 512, COMMON>, r, grid, smem, stream, p,
+    return launch_rows<block_norm_kernel<T, R, VEC, 2, 512, COMMON>>(r, grid, smem, stream, p,
                        r.team, depth);
-  return launch_rows(block_norm_kernel<T, R, VEC, 2, 1024, COMMON>, r, grid, smem, stream, p,
+  return launch_rows<block_norm_kernel<T, R, VEC, 2, 1024, COMMON>>(r, grid, smem, stream, p,
                      r.team, depth);
 }
 

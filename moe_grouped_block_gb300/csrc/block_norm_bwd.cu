@@ -369,12 +369,12 @@ template <typename T, typename R, bool VEC, bool COMMON>
 cudaError_t backward_rows(const mxg_block_norm_grad_t& p, float* ws, const RowShape& r,
                           int64_t grid, int smem, int depth, bool lean, cudaStream_t stream) {
   if (r.split > 1)
-    return launch_rows(block_norm_bwd_kernel<T, R, VEC, 2, 2, COMMON>, r, grid, smem, stream, p, ws,
+    return launch_rows<block_norm_bwd_kernel<T, R, VEC, 2, 2, COMMON>>(r, grid, smem, stream, p, ws,
                        r.team, depth, lean);
   if (r.iter == 1)
-    return launch_rows(block_norm_bwd_kernel<T, R, VEC, 1, 1, COMMON>, r, grid, smem, stream, p, ws,
+    return launch_rows<block_norm_bwd_kernel<T, R, VEC, 1, 1, COMMON>>(r, grid, smem, stream, p, ws,
                        r.team, depth, lean);
-  return launch_rows(block_norm_bwd_kernel<T, R, VEC, 2, 1, COMMON>, r, grid, smem, stream, p, ws,
+  return launch_rows<block_norm_bwd_kernel<T, R, VEC, 2, 1, COMMON>>(r, grid, smem, stream, p, ws,
                      r.team, depth, lean);
 }
 

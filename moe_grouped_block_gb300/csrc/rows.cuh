@@ -11,6 +11,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 
 #include "elem.cuh"
 #include "host16.h"
@@ -80,15 +81,24 @@ inline bool aligned_rows(const void* p, int64_t ld, size_t size) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * static_cast<int64_t>(size)) % 16 == 0;
 }
 
-// Launches `kern` with its ring, in clusters of `split`; more than 48 KB of
-// shared memory in all has to be asked for.
-template <typename Kern, typename... Args>
-cudaError_t launch_rows(Kern kern, const RowShape& r, int64_t grid, int smem, cudaStream_t stream,
+// Launches KERN with its ring, in clusters of `split`.  The shared memory that a
+// kernel may be launched with belongs to the kernel, for all host threads: it is set
+// once per device, to the most that any shape takes.  Set for each launch to what
+// that one takes, another thread's launch of a larger shape was refused now and then
+// (2761 of 30000 with three threads).
+template <auto KERN, typename... Args>
+cudaError_t launch_rows(const RowShape& r, int64_t grid, int smem, cudaStream_t stream,
                         const Args&... args) {
-  if (smem > 40 * 1024) {  // 48 KB with the static part
+  constexpr int kMaxDev = 64;
+  static std::atomic<bool> ready[kMaxDev];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev)
+    return cudaErrorInvalidDevice;
+  if (!ready[dev].load(std::memory_order_acquire)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem);
     if (e != cudaSuccess) return e;
+    ready[dev].store(true, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -101,7 +111,7 @@ cudaError_t launch_rows(Kern kern, const RowShape& r, int64_t grid, int smem, cu
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = r.split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
+  return cudaLaunchKernelEx(&cfg, KERN, args...);
 }
 
 // ---------------------------------------------------------------- fp32 pairs
