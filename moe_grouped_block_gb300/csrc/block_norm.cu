@@ -140,6 +140,7 @@ namespace {
 
 // up to 98 registers a thread at 8 columns, 115 at 16 (64 in CTAs of 1024)
 constexpr RowLimits kFwdLimits = {256, {256, 1024}, {640, 512}, 1 << 30};
+static_assert(kFwdLimits.split_at >= kMaxRowCols, "the forward kernel's rows are not shared");
 
 template <typename T, typename R, bool VEC, bool COMMON>
 cudaError_t forward_rows(const mxg_block_norm_t& p, const RowShape& r, int64_t grid, int smem,

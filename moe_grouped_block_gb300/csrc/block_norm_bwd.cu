@@ -29,6 +29,9 @@ namespace mxg {
 // for.  160 bounds the SM count; a thread takes some 120 registers.
 constexpr int kNormMaxSms = 160;
 constexpr RowLimits kBwdLimits = {128, {512, 512}, {512, 512}, 8192};
+// A shared row runs the kernel of 16 columns a thread, and its ring is sized by the
+// columns a thread that row_shape gives: 16 wherever a CTA's part is not narrow.
+static_assert(kBwdLimits.split_at >= 2 * kNarrowCols, "a shared row has 16 columns a thread");
 
 // Column sums of this CTA's rows go to the workspace [block][2][cols]:
 // S0 = sum dn . xh, S1 = sum t . u . yh with u the gate where it varies over

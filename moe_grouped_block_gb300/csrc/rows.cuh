@@ -31,6 +31,9 @@ __host__ __device__ inline int64_t cols_per_cta(int64_t cols, int split) {
   return split == 1 ? cols : (cols + 8 * split - 1) / (8 * split) * 8;
 }
 
+constexpr int kMaxRowCols = 16384;  // the widest row that a call accepts
+constexpr int kNarrowCols = 256;    // up to which a team is a warp or less
+
 // What a kernel lets row_shape choose from.
 struct RowLimits {
   int small_cta;  // CTA size of narrow rows
@@ -41,12 +44,12 @@ struct RowLimits {
 };
 
 // 8 or 16 columns a thread, whichever keeps more of an SM's threads on columns;
-// where both do alike, 8.
+// where both do alike, 8.  1 <= cols <= kMaxRowCols.
 inline RowShape row_shape(int64_t cols, const RowLimits& lim) {
-  RowShape r;
+  RowShape r = {32, 32, 1, 1};
   r.split = cols > lim.split_at ? 2 : 1;
   cols = cols_per_cta(cols, r.split);
-  if (cols <= 256) {
+  if (cols <= kNarrowCols) {
     r.team = 8;
     while (r.team * 8 < cols) r.team *= 2;
     r.threads = lim.small_cta;
