@@ -528,8 +528,9 @@ mxg_status_t mxg_grad_norm(const mxg_grad_t* grads, int n, float* norm, void* wo
                            size_t workspace_bytes, mxg_stream_t stream);
 
 /* The same norm, and dst = src * min(1, max_norm / (norm + 1e-6)) for every
- * tensor.  max_norm >= 0 (infinity allowed: nothing is clipped).  An infinite
- * gradient gives factor 0 (and NaN where 0 meets the infinity), a NaN makes
+ * tensor, also where the norm or the factor leaves FP32's range.  max_norm >= 0;
+ * with an infinite one the factor is 1, whatever the norm.  With a finite one an
+ * infinite gradient gives factor 0 (and NaN where 0 meets the infinity).  A NaN makes
  * every output NaN.  Errors: as mxg_grad_norm. */
 mxg_status_t mxg_grad_clip(const mxg_grad_t* grads, int n, float max_norm, float* norm,
                            void* workspace, size_t workspace_bytes, mxg_stream_t stream);

@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(32) grad_norm_kernel(const double* partial, in
 
 // ---------------------------------------------------------------- clipping
 template <typename T, typename D>
-__device__ __forceinline__ void chunk_scale(const GradEntry& e, const Chunk& k, float factor) {
+__device__ __forceinline__ void chunk_scale(const GradEntry& e, const Chunk& k, float2 factor) {
   constexpr int P = kPer16<T>;
   const T* src = static_cast<const T*>(e.src) + k.at;
   D* dst = static_cast<D*>(e.dst) + k.at;
@@ -247,7 +247,7 @@ __device__ __forceinline__ void chunk_scale(const GradEntry& e, const Chunk& k, 
     float f[P];
     unpack16<T>(v[i], f);
 #pragma unroll
-    for (int j = 0; j < P; ++j) f[j] *= factor;
+    for (int j = 0; j < P; ++j) f[j] = f[j] * factor.x * factor.y;
     if (e.dst_vec) {  // 8 or 4 elements of 4 or 2 bytes: 8 bytes at least
       uint32_t w[P * sizeof(D) / 4];
 #pragma unroll
@@ -272,26 +272,42 @@ __device__ __forceinline__ void chunk_scale(const GradEntry& e, const Chunk& k, 
   }
   const int rest = tid < k.head ? tid - k.head : whole + (tid - 32);
   if (tid < k.head || (tid >= 32 && tid - 32 < k.n - whole))
-    dst[rest] = from_f32<D>(to_f32(src[rest]) * factor);
+    dst[rest] = from_f32<D>(to_f32(src[rest]) * factor.x * factor.y);
+}
+
+// min(1, max_norm / (norm + 1e-6)) as a product x y that is applied factor by factor:
+// x = 1, but where the quotient is no normal fp32 number -- a norm may pass fp32's
+// range.  There x = 2^-100 or 2^-126 and y makes up for it: g x is exact unless the
+// result is below the smallest subnormal, and y keeps its bits down to quotients of
+// 2^-252, whose results are fp32 subnormals or 0.
+__device__ __forceinline__ float2 clip_factor(float max_norm, double norm) {
+  if (isinf(max_norm))  // nothing is clipped, whatever the norm
+    return make_float2(1.0f, isnan(norm) ? static_cast<float>(norm) : 1.0f);
+  const double to = norm + 1e-6;
+  const float f = max_norm / static_cast<float>(to);
+  if (f < 0x1p-126f && !isinf(norm)) {
+    const double q = static_cast<double>(max_norm) / to;
+    return q < 0x1p-226 ? make_float2(0x1p-126f, static_cast<float>(q * 0x1p126))
+                        : make_float2(0x1p-100f, static_cast<float>(q * 0x1p100));
+  }
+  return make_float2(1.0f, f > 1.0f ? 1.0f : f);  // NaN stays NaN
 }
 
 template <int CAP, typename S, typename D>
 __global__ void __launch_bounds__(kThreads, std::is_void<S>::value ? 1 : 3)
     grad_scale_kernel(const __grid_constant__ GradList<CAP> list, const double* partial,
                       int partials, float max_norm, float* norm) {
-  __shared__ float shared_factor;
+  __shared__ float2 shared_factor;
   grid_wait_for_previous();  // the partial sums
   if (threadIdx.x < 32) {
     const double total = norm_of(partial, partials);
     if (threadIdx.x == 0) {
       if (norm != nullptr && blockIdx.x == 0) *norm = static_cast<float>(total);
-      // a norm past fp32's range gives factor 0, as an infinite one does
-      const float f = max_norm / static_cast<float>(total + 1e-6);
-      shared_factor = f > 1.0f ? 1.0f : f;  // NaN stays NaN
+      shared_factor = clip_factor(max_norm, total);
     }
   }
   __syncthreads();
-  const float factor = shared_factor;
+  const float2 factor = shared_factor;
   for (int c = list.chunks - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
     const GradEntry& e = list.e[find_entry(list, c)];
     const Chunk k = chunk_of(e, c);
