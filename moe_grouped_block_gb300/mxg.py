@@ -381,8 +381,8 @@ def mxg_grouped_gemm_16bit(mode: int, A: torch.Tensor, B: torch.Tensor, group_ws
     """A, B: bf16 or fp16 device tensors of at least the rows and columns that the mode
     implies ([M_cap, N or K]; weights [G, N, K] or [G*N, K]), of which the first ones
     count; rows may be strided.  C: fp32 or the operands' type."""
-    if (A.dtype != B.dtype or A.dtype not in (torch.bfloat16, torch.float16)
-            or C.dtype not in _DTYPES):
+    kind, out = _DTYPES.get(A.dtype), _DTYPES.get(C.dtype)
+    if not kind or out is None or B.dtype is not A.dtype:  # MXG_F32 is 0
         raise ValueError("operands of one 16-bit type, C of that or fp32: got %s, %s, %s"
                          % (A.dtype, B.dtype, C.dtype))
     assert group_ws.dtype == torch.int64
@@ -404,9 +404,9 @@ def mxg_grouped_gemm_16bit(mode: int, A: torch.Tensor, B: torch.Tensor, group_ws
     else:
         lda, ldb, ldc = _operand16(A, "A", a), _operand16(B, "B", b), _operand16(C, "C", c)
     _check("mxg_grouped_gemm_16bit",
-           load().mxg_grouped_gemm_16bit(_DTYPES[A.dtype], mode, _p(A), lda, _p(B), ldb,
-                                         _p(group_ws), G, M_cap, N, K, _p(alpha), _p(beta), _p(C),
-                                         ldc, _DTYPES[C.dtype], _p(dev_status), _s(stream)))
+           load().mxg_grouped_gemm_16bit(kind, mode, _p(A), lda, _p(B), ldb, _p(group_ws), G,
+                                         M_cap, N, K, _p(alpha), _p(beta), _p(C), ldc, out,
+                                         _p(dev_status), _s(stream)))
 
 
 def _same_type(tensors) -> int:
