@@ -49,7 +49,8 @@ def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) 
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    headers = sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [HEADER]
+    headers = sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")))
+    headers.append(HEADER)
     objs = []
     jobs = []
     for src in sources:
