@@ -386,6 +386,9 @@ typedef enum { MXG_F32 = 0, MXG_BF16 = 1, MXG_F16 = 2 } mxg_dtype_t;
  *     C[g, n, k] = alpha_g sum_{i in g} A[off_g+i, n] B[off_g+i, k] + beta_g C[g, n, k]
  *     (an empty group writes beta_g C[g], or zeros).
  * Sums are FP32; the result is rounded once, to out_type: MXG_F32 or in_type.
+ * The tensor cores add by truncation: an FP32 result takes over their sums every
+ * 512 products and adds those rounding to nearest, a 16-bit one (whose own
+ * rounding is larger) is the whole contraction's truncated sum.
  * G, N, K >= 1 of any value; G <= 1024; M_cap >= 0 (with 0 the pointers of
  * the ragged matrices may be NULL).
  * lda, ldb, ldc : elements from one row to the next, 0 for dense rows; W and
@@ -427,8 +430,9 @@ typedef enum {
  *   w_post, w_pre : [cols], or NULL for ones
  *   x_out     : required with y; may be x itself (with the same ld)
  * n is formed from x' before x' is rounded.  1 <= cols <= 16384, rows >= 0
- * (0 launches nothing; the [rows, cols] pointers may then be NULL), eps > 0.  Sums are FP32.  Any element alignment; rows
- * that start on 16 bytes with cols a multiple of 8 take 16-byte accesses. */
+ * (0 launches nothing; the [rows, cols] pointers may then be NULL), eps > 0.  Sums
+ * are FP32.  Any element alignment; rows that start on 16 bytes with cols a
+ * multiple of 8 take 16-byte accesses. */
 typedef struct {
   mxg_dtype_t dtype, res_dtype;
   int64_t rows, cols;

@@ -15,7 +15,7 @@
 //
 // Memory is the bound: 16384 x 4096 in bf16 takes 137 us, 5.9 TB/s of the 6.78
 // that a copy reaches, the second kernel's 7 us among them.  2777 x 7168 beside an
-// fp32 stream: 85 us, 4.2 TB/s -- one CTA an SM, whose ring holds two rows, and a
+// fp32 stream: 88 us, 4.1 TB/s -- one CTA an SM, whose ring holds two rows, and a
 // barrier every row.
 //
 // Rows of more than 8192 columns are shared by two CTAs, whose warps post their

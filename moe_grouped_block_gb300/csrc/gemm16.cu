@@ -33,9 +33,9 @@
 // With many, the tensor cores and the power they draw: 16384 rows through 8 such
 // experts in 1.03 ms when run for milliseconds (1.87 PFLOP/s; the tensor pipe is
 // active 92 % of the time), in 1.19 ms when run for seconds, at 1.4 kW and some
-// 1.4 GHz.  dgrad of 32768 rows over 63 experts of 1408 x 2048: 138-150 us, 105 us
-// at full clock; its narrower units (210 rows on average) cost 509 cycles a K
-// block where 420 multiply.  wgrad of the 8 experts into fp32: 1.16 ms, 600 cycles
+// 1.4 GHz.  dgrad of 32768 rows over 63 experts of 1408 x 2048: 138-150 us, 158-162
+// us when run for seconds; its narrower units (210 rows on average) cost 509 cycles
+// a K block where 420 multiply.  wgrad of the 8 experts into fp32: 1.16 ms, 600 cycles
 // a K block against 494 without the 1.9 GB it stores: with both operands MN-major,
 // stores and operand reads meet in shared memory.
 //
@@ -221,7 +221,9 @@ __device__ __forceinline__ Unit16 map_unit16(int64_t u, const Gemm16Params& p,
 // One column (of this lane) and up to 32 rows of C: alpha * acc + beta * old.
 // The whole chunk without beta is straight-line code: with its two tests per
 // row in the way, a 256 x 256 unit's epilogue took 10 k cycles, as long as the
-// MMAs of a 1408-long contraction.
+// MMAs of a 1408-long contraction.  With beta each row waits for its old value in
+// turn: wgrad of 16384 rows, 8 experts of 14336 x 4096, into fp32 takes 1.09 ms
+// without beta and 6.5 ms with it.
 template <typename T>
 __device__ __forceinline__ void store_column16(T* dst, int64_t ldc, const float (&acc)[32],
                                                int rows, float alpha, float beta) {
