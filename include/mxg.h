@@ -539,6 +539,231 @@ mxg_status_t mxg_grad_norm(const mxg_grad_t* grads, int n, float* norm, void* wo
 mxg_status_t mxg_grad_clip(const mxg_grad_t* grads, int n, float max_norm, float* norm,
                            void* workspace, size_t workspace_bytes, mxg_stream_t stream);
 
+/* ------------------------------------------------------------------------- */
+/* Around the products of an expert block: the routing of tokens to experts  */
+/* with its balance loss, the rows moved there and back, and the gated       */
+/* activation between the products with its inputs kept in 8 bits.           */
+/* ------------------------------------------------------------------------- */
+
+/* What a router's logit l becomes: MXG_SCORE_SOFTMAX: s_e = exp(l_e) / sum_i
+ * exp(l_i); MXG_SCORE_SIGMOID: s_e = 1 / (1 + exp(-l_e)). */
+typedef enum { MXG_SCORE_SOFTMAX = 0, MXG_SCORE_SIGMOID = 1 } mxg_score_t;
+
+/* Routing of `tokens` tokens to k of `experts` experts each, with the counts,
+ * the balance loss and, where wanted, the rows that the tokens take.
+ *   logits : [tokens, experts] of dtype, ld elements between rows (0: dense)
+ *   mask   : uint8 [tokens], 0 for a token that takes no part (padding), or NULL
+ * For each token the k experts of the largest logits, in falling order; the
+ * lower expert first where logits are equal (-0 equals 0), NaN above infinity.
+ * A logit of -infinity is never chosen.
+ *   expert : int32 [tokens, k]; -1 where there is none: a masked token, a
+ *            token whose logits are all -infinity (it counts as masked), or
+ *            less than k logits above -infinity
+ *   weight : float [tokens, k] = scale * s_e, or with `normalize` scale * s_e /
+ *            (the sum of the token's chosen s); 0 where there is no expert
+ *   counts : int32 [experts], tokens of each expert
+ * The balance loss, with p = s / (sum of the token's s), n the tokens that take
+ * part and P_e = (sum over them of p_e) / n:
+ *   slope  : float [experts], balance * experts / n * counts_e / (sum of counts)
+ *            -- the loss's derivative with respect to each p_e, for
+ *            mxg_route_backward -- or NULL
+ *   loss   : float [1], n * sum_e slope_e P_e, or NULL
+ * (0 without any such token; the counts have no gradient).  A NaN
+ * among a token's logits -- with MXG_SCORE_SOFTMAX +infinity too -- is chosen first
+ * and makes the weights and shares that depend on it, and the loss, NaN.
+ * Rows, where row_of and group_ws are given (both or neither): sorted by
+ * expert, an expert's in the order of the tokens, each expert's group padded at
+ * its end to a multiple of `align` rows (1 <= align <= 1024):
+ *   row_of   : int32 [tokens, k], -1 where there is no expert
+ *   group_ws : int64 [2 experts + 1], the padded sizes and the offsets times
+ *              last_dim as the offsets entry points write them
+ * Rows at or beyond rows_capacity, rounded down to a multiple of align, are
+ * dropped: row_of -1, MXG_DEV_SUM_OVER_CAPACITY in dev_status.  tokens * k +
+ * experts * (align - 1) rows always suffice.
+ * 1 <= experts <= 1024, 1 <= k <= min(experts, 32), tokens >= 0 and tokens * k
+ * and rows_capacity up to 2^31 - 128; scale and balance finite.  Sums are FP32
+ * and of a fixed order.  Any element alignment; logits whose rows start on 16
+ * bytes with experts a multiple of 8 take 16-byte accesses. */
+typedef struct {
+  mxg_dtype_t dtype;
+  int64_t tokens;
+  int32_t experts, k;
+  const void* logits;
+  int64_t ld;
+  const uint8_t* mask;
+  mxg_score_t score;
+  int32_t normalize;
+  float scale, balance;
+  int32_t* expert;
+  float* weight;
+  int32_t* counts;
+  float* loss;
+  float* slope;
+  int32_t* row_of;
+  int64_t* group_ws;
+  int32_t align;
+  int64_t rows_capacity, last_dim;
+} mxg_route_t;
+
+/* Bytes of the workspace of mxg_route and mxg_route_rows (0 for sizes that they
+ * refuse); 16-byte aligned device memory whose contents mean nothing before or
+ * after the call. */
+size_t mxg_route_workspace_bytes(int64_t tokens, int experts, int k);
+
+/* Errors: INVALID_ARG (nulls, sizes, types, ld < experts, last_dim < 1, or
+ * rows_capacity * last_dim beyond int64), ALIGNMENT (a pointer not aligned to
+ * its element, workspace), WORKSPACE_TOO_SMALL, UNSUPPORTED_ARCH, LAUNCH. */
+mxg_status_t mxg_route(const mxg_route_t* desc, void* workspace, size_t workspace_bytes,
+                       int32_t* dev_status, mxg_stream_t stream);
+
+/* The counts and rows of mxg_route for experts chosen elsewhere: expert int32
+ * [tokens, k], any value outside [0, experts) being no expert (an expert may be
+ * named twice for a token: two rows).  row_of and group_ws as there (both or
+ * neither).  Errors: as mxg_route. */
+mxg_status_t mxg_route_rows(const int32_t* expert, int64_t tokens, int experts, int k, int align,
+                            int64_t rows_capacity, int64_t last_dim, int32_t* counts,
+                            int32_t* row_of, int64_t* group_ws, void* workspace,
+                            size_t workspace_bytes, int32_t* dev_status, mxg_stream_t stream);
+
+/* The gradient of mxg_route with respect to the logits.
+ *   logits, expert : as given to and as written by mxg_route (a token's experts
+ *                    are distinct, or outside [0, experts) for none)
+ *   dweight : float [tokens, k], the gradient of the weights, or NULL: 0
+ *   slope   : float [experts] of mxg_route, with dloss float [1], the gradient
+ *             of the loss; both or neither (no loss)
+ *   dlogits : [tokens, experts] of dtype, ldd elements between rows (0: dense);
+ *             may be logits itself, with the same ld.  A token without any
+ *             expert gets zeros; an entry of dweight beside no expert counts
+ *             as 0, whatever it holds. */
+typedef struct {
+  mxg_dtype_t dtype;
+  int64_t tokens;
+  int32_t experts, k;
+  const void* logits;
+  int64_t ld;
+  const int32_t* expert;
+  mxg_score_t score;
+  int32_t normalize;
+  float scale;
+  const float* dweight;
+  const float* slope;
+  const float* dloss;
+  void* dlogits;
+  int64_t ldd;
+} mxg_route_grad_t;
+
+/* Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_ARCH, LAUNCH, as mxg_route. */
+mxg_status_t mxg_route_backward(const mxg_route_grad_t* desc, mxg_stream_t stream);
+
+/* Rows between the tokens' order and the experts'.  `tokens` is [n, cols] (ldt
+ * elements between rows, 0: dense), `rows` [rows_capacity, cols] (ldr), both of
+ * dtype; row_of int32 [n, k] as mxg_route writes it: distinct values, and one
+ * outside [0, rows_capacity) is no row.
+ *   mxg_dispatch : rows[row_of[t, j]] = tokens[t]
+ *   mxg_combine  : tokens[t] = sum_j weight[t, j] * rows[row_of[t, j]], summed in
+ *                  FP32 in the order of j and rounded once; a token without rows
+ *                  gets zeros.  weight float [n, k], or NULL for ones (the
+ *                  gradient of mxg_dispatch).
+ *   mxg_combine_backward : rows[row_of[t, j]] = weight[t, j] * tokens[t], with
+ *                  tokens the gradient of the sums and rows that of the rows; and,
+ *                  where dweight is given, dweight[t, j] = the sum over the
+ *                  columns of tokens[t] * y_rows[row_of[t, j]] in FP32 (0 where
+ *                  there is no row), y_rows [rows_capacity, cols] being what
+ *                  mxg_combine summed (ldy); y_rows may be rows itself, with the
+ *                  same ld.  rows may be NULL: only dweight.
+ * Rows that row_of does not name are not written, but for padding: where counts
+ * (int32 [experts]) and group_ws (as mxg_route writes them) are given to
+ * mxg_dispatch or mxg_combine_backward, the rows between an expert's count and
+ * its padded size are set to 0.  Where they are not, both are NULL and experts 0.
+ * n >= 0, k from 1 to 32, n * k and rows_capacity up to 2^31 - 128, 1 <= cols <=
+ * 2^20; without tokens (n = 0) or rows (rows_capacity = 0) their pointers may be
+ * NULL.  Any element alignment; rows on 32 or 16 bytes take accesses of that size.
+ * Apart from the one place named above, outputs do not overlap inputs. */
+typedef struct {
+  mxg_dtype_t dtype;
+  int64_t n, cols;
+  int32_t k, experts;
+  int64_t rows_capacity;
+  void* tokens;
+  int64_t ldt;
+  void* rows;
+  int64_t ldr;
+  const int32_t* row_of;
+  const float* weight;
+  const void* y_rows;
+  int64_t ldy;
+  float* dweight;
+  const int32_t* counts;
+  const int64_t* group_ws;
+} mxg_expert_rows_t;
+
+/* Errors of the three: INVALID_ARG (nulls, sizes, types, a leading dimension
+ * below cols, a field that the call does not take being set), ALIGNMENT (a
+ * pointer not aligned to its element), UNSUPPORTED_ARCH, LAUNCH. */
+mxg_status_t mxg_dispatch(const mxg_expert_rows_t* desc, mxg_stream_t stream);
+mxg_status_t mxg_combine(const mxg_expert_rows_t* desc, mxg_stream_t stream);
+mxg_status_t mxg_combine_backward(const mxg_expert_rows_t* desc, mxg_stream_t stream);
+
+/* The activations between an expert's products: x sigmoid(z(x)) with
+ *   MXG_ACT_SILU      : z = x
+ *   MXG_ACT_GELU_TANH : z = 2 sqrt(2 / pi) (x + 0.044715 x^3), which is
+ *                       x / 2 (1 + tanh(z / 2)) */
+typedef enum { MXG_ACT_SILU = 0, MXG_ACT_GELU_TANH = 1 } mxg_act_t;
+
+/* Forward (mxg_gated_act): h = act(gate) . up, all [rows, cols] of dtype
+ * (MXG_BF16 or MXG_F16), ld* elements between rows (0: dense); without up h =
+ * act(gate).  FP32 inside, h rounded once.  Where q and sf are given, the inputs
+ * are kept in 8 bits for the backward pass:
+ *   q  : E4M3 [rows, cols] of gate and, beside it in the same row from column
+ *        cols on, of up; ldq bytes between rows (0: cols, or 2 cols with up)
+ *   sf : E8M0 [rows, B] of gate and beside it of up, B = ceil(cols / 32), dense:
+ *        one byte for each 32 columns of a row (the last ones may be fewer)
+ * by the rule of mxg_group_quantize's 1x32 blocks (the scale the least power of two
+ * with amax <= 448 2^e; E4M3 to nearest even), the amax being taken over finite
+ * values; an infinity or NaN is kept as NaN and does not touch its neighbours (a
+ * bf16 value of more than 2^127 may be kept as 2^128, which is restored as
+ * infinity).
+ * Backward (mxg_gated_act_backward): from q, sf (gate and up being the values
+ * that they stand for) and dh, the gradient of h:
+ *   dgate = dh . up . act'(gate), dup = dh . act(gate), rounded once; and, where h
+ *   is given, h again from those values, for the weight gradient of the second
+ *   product.
+ * gated : 1, or 0 where there is no up (nor dup).
+ * group_ws : an offsets workspace of G groups, or NULL with G = 0.  Its first G
+ *   entries sum to the live rows (negative ones count as 0); rows at or beyond
+ *   them are neither read nor written.
+ * rows from 0 to 2^31 - 128, 1 <= cols <= 2^20, G <= 1024.  h may be gate or up,
+ * with the same ld, and dh dgate or dup.  Any element alignment; rows on 32 bytes
+ * (q: 16) take accesses of that size. */
+typedef struct {
+  mxg_dtype_t dtype;
+  mxg_act_t act;
+  int64_t rows, cols;
+  int32_t gated, G;
+  const int64_t* group_ws;
+  const void* gate;
+  int64_t ldg;
+  const void* up;
+  int64_t ldu;
+  void* h;
+  int64_t ldh;
+  uint8_t* q;
+  int64_t ldq;
+  uint8_t* sf;
+  const void* dh;
+  int64_t lddh;
+  void* dgate;
+  int64_t lddg;
+  void* dup;
+  int64_t lddu;
+} mxg_gated_act_t;
+
+/* Errors of both: INVALID_ARG (nulls, sizes, types, a leading dimension below its
+ * row, only one of q and sf, a field of the other direction being set),
+ * ALIGNMENT, UNSUPPORTED_ARCH, LAUNCH. */
+mxg_status_t mxg_gated_act(const mxg_gated_act_t* desc, mxg_stream_t stream);
+mxg_status_t mxg_gated_act_backward(const mxg_gated_act_t* desc, mxg_stream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* mxg_status_string(mxg_status_t status);
 

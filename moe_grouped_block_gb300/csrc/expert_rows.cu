@@ -1,0 +1,386 @@
+// expert_rows.cu -- rows between the tokens' order and the experts':
+//   dispatch         : rows[row_of[t, j]] = tokens[t]
+//   combine          : tokens[t] = sum_j weight[t, j] rows[row_of[t, j]]
+//   combine backward : rows[row_of[t, j]] = weight[t, j] tokens[t],
+//                      dweight[t, j] = sum over the columns of tokens[t] y_rows[row_of[t, j]]
+//
+// All three go by tokens, so that a token's row is read (or written) once and only the k
+// rows beside it are scattered; no row is shared, so nothing is atomic.  Memory is the
+// bound.
+#include <algorithm>
+
+#include "elem.cuh"
+#include "host16.h"
+
+namespace mxg {
+
+constexpr int kRowThreads = 256;
+
+// A lane's piece of a row: BYTES (32, 16, or one element) at a time, as fp32 and back.
+template <typename T, int BYTES>
+struct Piece {
+  static constexpr int kElems = BYTES / static_cast<int>(sizeof(T));
+  static constexpr int kWords = BYTES >= 4 ? BYTES / 4 : 1;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (BYTES == 32) {
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                     "=r"(w[6]), "=r"(w[7])
+                   : "l"(p)
+                   : "memory");
+    } else if constexpr (BYTES == 16) {
+      const uint4 q = *reinterpret_cast<const uint4*>(p);
+      w[0] = q.x;
+      w[1] = q.y;
+      w[2] = q.z;
+      w[3] = q.w;
+    } else if constexpr (sizeof(T) == 4) {
+      w[0] = __float_as_uint(*p);
+    } else {
+      w[0] = p->bits;
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (BYTES == 32) {
+      st_global_32B(p, w);
+    } else if constexpr (BYTES == 16) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if constexpr (sizeof(T) == 4) {
+      *p = __uint_as_float(w[0]);
+    } else {
+      p->bits = static_cast<uint16_t>(w[0]);
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[kElems]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < kElems; ++i) f[i] = __uint_as_float(w[i]);
+    } else if constexpr (kElems == 1) {
+      f[0] = to_f32(T{static_cast<uint16_t>(w[0])});
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) unpack2<T>(w[i], f[2 * i], f[2 * i + 1]);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&f)[kElems]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < kElems; ++i) w[i] = __float_as_uint(f[i]);
+    } else if constexpr (kElems == 1) {
+      w[0] = from_f32<T>(f[0]).bits;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = pack2<T>(f[2 * i], f[2 * i + 1]);
+    }
+  }
+};
+
+// Zeros in the rows between each expert's count and its padded size, by the warps
+// `warp`, `warp` + `warps` and so on: kPadWarps of them share an expert's.
+constexpr int kPadWarps = 16;
+
+template <typename T, int BYTES>
+__device__ __forceinline__ void zero_padding(const mxg_expert_rows_t& d, int64_t item) {
+  const int lane = threadIdx.x & 31;
+  const int e = static_cast<int>(item / kPadWarps), part = static_cast<int>(item % kPadWarps);
+  // the group's start: the sizes before it
+  int64_t start = 0;
+  for (int i = lane; i < e; i += 32) {
+    const int64_t s = d.group_ws[i];
+    start += s > 0 ? min(s, d.rows_capacity) : 0;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) start += __shfl_xor_sync(0xFFFFFFFFu, start, o);
+  const int64_t size = min(max(d.group_ws[e], static_cast<int64_t>(0)), d.rows_capacity);
+  const int64_t count = max(d.counts[e], 0);
+  const int64_t end = min(start + size, d.rows_capacity);
+  constexpr int kElems = Piece<T, BYTES>::kElems;
+  Piece<T, BYTES> none;
+  none.zero();
+  for (int64_t r = start + count + part; r < end; r += kPadWarps) {
+    T* row = static_cast<T*>(d.rows) + r * d.ldr;
+    for (int64_t c = lane * kElems; c < d.cols; c += 32 * kElems) {
+      if (c + kElems <= d.cols)
+        none.store(row + c);
+      else
+        for (int64_t i = c; i < d.cols; ++i) row[i] = T{};
+    }
+  }
+}
+
+// A warp's item: a token and `32 * UNROLL` pieces of its columns.
+template <typename T, int BYTES, int UNROLL>
+__global__ void __launch_bounds__(kRowThreads)
+    dispatch_kernel(const mxg_expert_rows_t d, int slices, int64_t pad_items) {
+  constexpr int kElems = Piece<T, BYTES>::kElems;
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kRowThreads / 32);
+  const int64_t items = pad_items + d.n * slices;
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+       item < items; item += warps) {
+    if (item < pad_items) {
+      zero_padding<T, BYTES>(d, item);
+      continue;
+    }
+    const int64_t t = (item - pad_items) / slices;
+    const int slice = static_cast<int>((item - pad_items) - t * slices);
+    int32_t at = -1;
+    if (lane < d.k) at = d.row_of[t * d.k + lane];
+    const T* from = static_cast<const T*>(d.tokens) + t * d.ldt;
+    const int c0 = (slice * UNROLL * 32 + lane) * kElems;
+    Piece<T, BYTES> x[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u)
+      if (c0 + (u * 32 + 1) * kElems <= d.cols) x[u].load(from + c0 + u * 32 * kElems);
+    for (int j = 0; j < d.k; ++j) {
+      const int64_t r = __shfl_sync(0xFFFFFFFFu, at, j);
+      if (r < 0 || r >= d.rows_capacity) continue;
+      T* to = static_cast<T*>(d.rows) + r * d.ldr;
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int c = c0 + u * 32 * kElems;
+        if (c + kElems <= d.cols)
+          x[u].store(to + c);
+        else
+          for (int i = c; i < d.cols; ++i) to[i] = from[i];
+      }
+    }
+  }
+}
+
+template <typename T, int BYTES>
+__global__ void __launch_bounds__(kRowThreads)
+    combine_kernel(const mxg_expert_rows_t d, int slices) {
+  constexpr int kElems = Piece<T, BYTES>::kElems;
+  constexpr int kAhead = 4;  // rows in flight
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kRowThreads / 32);
+  const int64_t items = d.n * slices;
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+       item < items; item += warps) {
+    const int64_t t = item / slices;
+    const int slice = static_cast<int>(item - t * slices);
+    int32_t at = -1;
+    float w = 1.0f;
+    if (lane < d.k) {
+      at = d.row_of[t * d.k + lane];
+      if (d.weight != nullptr) w = d.weight[t * d.k + lane];
+    }
+    const int c = (slice * 32 + lane) * kElems;
+    T* to = static_cast<T*>(d.tokens) + t * d.ldt;
+    const T* rows = static_cast<const T*>(d.rows);
+    const bool whole = c + kElems <= d.cols;
+    float acc[kElems];
+#pragma unroll
+    for (int i = 0; i < kElems; ++i) acc[i] = 0.0f;
+    for (int j0 = 0; j0 < d.k; j0 += kAhead) {
+      Piece<T, BYTES> x[kAhead];
+      float wj[kAhead];
+      bool in[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int64_t r = __shfl_sync(0xFFFFFFFFu, at, (j0 + j) & 31);
+        wj[j] = __shfl_sync(0xFFFFFFFFu, w, (j0 + j) & 31);
+        in[j] = j0 + j < d.k && r >= 0 && r < d.rows_capacity;
+        if (in[j] && whole) x[j].load(rows + r * d.ldr + c);
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (!in[j] || !whole) continue;
+        float f[kElems];
+        x[j].get(f);
+#pragma unroll
+        for (int i = 0; i < kElems; ++i) acc[i] = fmaf(wj[j], f[i], acc[i]);
+      }
+    }
+    if (whole) {
+      Piece<T, BYTES> y;
+      y.set(acc);
+      y.store(to + c);
+    }
+    // the last, shorter piece of a row
+    if (BYTES > static_cast<int>(sizeof(T)) && __any_sync(0xFFFFFFFFu, !whole && c < d.cols)) {
+      const int most = static_cast<int>(d.cols) - c;
+      for (int i = 0; i < kElems - 1; ++i) {
+        float sum = 0.0f;
+        for (int j = 0; j < d.k; ++j) {
+          const int64_t r = __shfl_sync(0xFFFFFFFFu, at, j);
+          const float wt = __shfl_sync(0xFFFFFFFFu, w, j);
+          if (r >= 0 && r < d.rows_capacity && !whole && i < most)
+            sum = fmaf(wt, to_f32(rows[r * d.ldr + c + i]), sum);
+        }
+        if (!whole && i < most) to[c + i] = from_f32<T>(sum);
+      }
+    }
+  }
+}
+
+// A team of `team` warps owns a token; sums over the columns are joined in shared memory.
+template <typename T, int BYTES>
+__global__ void __launch_bounds__(kRowThreads)
+    combine_backward_kernel(const mxg_expert_rows_t d, int team, int64_t pad_items) {
+  constexpr int kElems = Piece<T, BYTES>::kElems;
+  constexpr int kAhead = 4;  // experts at a time
+  constexpr int kWarps = kRowThreads / 32;
+  __shared__ float part[kWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, teams = kWarps / team;
+  const int place = warp % team;  // in the team
+  const int64_t pad_blocks = (pad_items + kWarps - 1) / kWarps;
+  const int64_t token_blocks = (d.n + teams - 1) / teams;
+  for (int64_t b = blockIdx.x; b < pad_blocks + token_blocks; b += gridDim.x) {
+    if (b < pad_blocks) {
+      if (b * kWarps + warp < pad_items) zero_padding<T, BYTES>(d, b * kWarps + warp);
+      continue;
+    }
+    const int64_t t = (b - pad_blocks) * teams + warp / team;
+    const bool on = t < d.n;
+    int32_t at = -1;
+    float w = 1.0f, dot_mine = 0.0f;
+    if (on && lane < d.k) {
+      at = d.row_of[t * d.k + lane];
+      if (d.weight != nullptr) w = d.weight[t * d.k + lane];
+    }
+    if (at >= d.rows_capacity) at = -1;
+    const T* dy = static_cast<const T*>(d.tokens) + (on ? t : 0) * d.ldt;
+    const T* y_rows = static_cast<const T*>(d.y_rows);
+    T* rows = static_cast<T*>(d.rows);
+    for (int j0 = 0; j0 < d.k; j0 += kAhead) {
+      float wj[kAhead], dot[kAhead];
+      int64_t r[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int from = j0 + j < d.k ? j0 + j : 31;
+        r[j] = __shfl_sync(0xFFFFFFFFu, at, from);
+        wj[j] = __shfl_sync(0xFFFFFFFFu, w, from);
+        if (j0 + j >= d.k) r[j] = -1;
+        dot[j] = 0.0f;
+      }
+      for (int64_t c = (place * 32 + lane) * kElems; on && c < d.cols; c += team * 32 * kElems) {
+        if (c + kElems <= d.cols) {
+          Piece<T, BYTES> x, y[kAhead];
+          x.load(dy + c);
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j)
+            if (r[j] >= 0 && d.dweight != nullptr) y[j].load(y_rows + r[j] * d.ldy + c);
+          float g[kElems];
+          x.get(g);
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            if (r[j] < 0) continue;
+            float f[kElems];
+            if (d.dweight != nullptr) {
+              y[j].get(f);
+#pragma unroll
+              for (int i = 0; i < kElems; ++i) dot[j] = fmaf(g[i], f[i], dot[j]);
+            }
+            if (rows != nullptr) {
+#pragma unroll
+              for (int i = 0; i < kElems; ++i) f[i] = wj[j] * g[i];
+              Piece<T, BYTES> o;
+              o.set(f);
+              o.store(rows + r[j] * d.ldr + c);
+            }
+          }
+        } else {
+          for (int64_t i = c; i < d.cols; ++i) {
+            const float g = to_f32(dy[i]);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+              if (r[j] < 0) continue;
+              if (d.dweight != nullptr) dot[j] = fmaf(g, to_f32(y_rows[r[j] * d.ldy + i]), dot[j]);
+              if (rows != nullptr) rows[r[j] * d.ldr + i] = from_f32<T>(wj[j] * g);
+            }
+          }
+        }
+      }
+      if (d.dweight != nullptr) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          float v = dot[j];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+          if (lane == j0 + j) dot_mine = v;
+        }
+      }
+    }
+    if (d.dweight != nullptr) {
+      if (team > 1) {
+        part[warp][lane] = dot_mine;
+        __syncthreads();
+        if (place == 0)
+          for (int i = 1; i < team; ++i) dot_mine += part[warp + i][lane];
+        __syncthreads();
+      }
+      if (on && place == 0 && lane < d.k) d.dweight[t * d.k + lane] = dot_mine;
+    }
+  }
+}
+
+namespace {
+
+// Bytes of the accesses that every row allows: 32, 16 or an element's.
+int piece_bytes(const mxg_expert_rows_t& d, size_t size) {
+  uintptr_t all = reinterpret_cast<uintptr_t>(d.tokens) | reinterpret_cast<uintptr_t>(d.rows) |
+                  reinterpret_cast<uintptr_t>(d.y_rows) | static_cast<uintptr_t>(d.ldt * size) |
+                  (d.rows != nullptr ? static_cast<uintptr_t>(d.ldr * size) : 0) |
+                  (d.y_rows != nullptr ? static_cast<uintptr_t>(d.ldy * size) : 0);
+  return (all & 31u) == 0 ? 32 : ((all & 15u) == 0 ? 16 : static_cast<int>(size));
+}
+
+unsigned grid_for(int64_t warps, int num_sms) {
+  const int64_t blocks = (warps + kRowThreads / 32 - 1) / (kRowThreads / 32);
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(blocks, num_sms * 64LL)));
+}
+
+int64_t slices_of(int64_t cols, int per) { return (cols + per - 1) / per; }
+
+template <typename T, int BYTES>
+cudaError_t run(const mxg_expert_rows_t& d, int op, int num_sms, cudaStream_t stream) {
+  constexpr int kSpan = 32 * Piece<T, BYTES>::kElems;
+  const int64_t pad = d.counts != nullptr && d.rows != nullptr
+                          ? static_cast<int64_t>(d.experts) * kPadWarps
+                          : 0;
+  if (op == 0) {
+    constexpr int kUnroll = BYTES >= 16 ? 2 : 4;
+    const int64_t slices = slices_of(d.cols, kSpan * kUnroll);
+    dispatch_kernel<T, BYTES, kUnroll>
+        <<<grid_for(pad + d.n * slices, num_sms), kRowThreads, 0, stream>>>(
+            d, static_cast<int>(slices), pad);
+  } else if (op == 1) {
+    const int64_t slices = slices_of(d.cols, kSpan);
+    combine_kernel<T, BYTES><<<grid_for(d.n * slices, num_sms), kRowThreads, 0, stream>>>(
+        d, static_cast<int>(slices));
+  } else {
+    // more warps a token where the tokens alone do not fill the device
+    int team = 1;
+    while (team < 8 && d.n * team < num_sms * 48LL && team * kSpan < d.cols) team *= 2;
+    combine_backward_kernel<T, BYTES>
+        <<<grid_for(pad + d.n * team, num_sms), kRowThreads, 0, stream>>>(d, team, pad);
+  }
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t typed(const mxg_expert_rows_t& d, int op, int num_sms, cudaStream_t stream) {
+  const int bytes = piece_bytes(d, sizeof(T));
+  if (bytes == 32) return run<T, 32>(d, op, num_sms, stream);
+  if (bytes == 16) return run<T, 16>(d, op, num_sms, stream);
+  return run<T, static_cast<int>(sizeof(T))>(d, op, num_sms, stream);
+}
+
+}  // namespace
+
+// op: 0 dispatch, 1 combine, 2 its gradients
+cudaError_t launch_expert_rows(const mxg_expert_rows_t& d, int op, int num_sms,
+                               cudaStream_t stream) {
+  if (d.dtype == MXG_F32) return typed<float>(d, op, num_sms, stream);
+  if (d.dtype == MXG_BF16) return typed<Bf16>(d, op, num_sms, stream);
+  return typed<F16>(d, op, num_sms, stream);
+}
+
+}  // namespace mxg

@@ -1,0 +1,315 @@
+// gated_act.cu -- the activation between an expert's two products, with its inputs kept
+// in 8 bits for the backward pass:
+//   h = act(gate) up,  act(x) = x sigmoid(z(x));  z = x, or 2 sqrt(2 / pi) (x + 0.044715 x^3)
+//   kept: E4M3 with one E8M0 scale for each 32 columns of a row (mx_exponent's rule)
+//   dgate = dh up act'(gate),  dup = dh act(gate),  act' = s + x s (1 - s) z'
+//
+// A thread owns 16 columns -- 32 bytes of a 16-bit tensor, 16 of the kept values -- and the
+// thread beside it the other half of the 32 that share a scale, so a block's largest
+// magnitude is one shuffle away.  Each input is read once and each output written once:
+// memory is the bound.
+#include <algorithm>
+
+#include "elem.cuh"
+#include "host16.h"
+
+namespace mxg {
+
+constexpr int kActThreads = 256;
+
+// 16 neighbouring values of a 16-bit type as packed pairs.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load16(const T* p, int n, uint32_t (&w)[8]) {
+  if constexpr (VEC) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                   "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t lo = 2 * i < n ? p[2 * i].bits : 0u;
+      const uint32_t hi = 2 * i + 1 < n ? p[2 * i + 1].bits : 0u;
+      w[i] = lo | (hi << 16);
+    }
+  }
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store16(T* p, int n, const float (&f)[16]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pack2<T>(f[2 * i], f[2 * i + 1]);
+  if constexpr (VEC) {
+    st_global_32B(p, w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) p[i].bits = static_cast<uint16_t>(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void unpack16(const uint32_t (&w)[8], float (&f)[16]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) unpack2<T>(w[i], f[2 * i], f[2 * i + 1]);
+}
+
+// Four E4M3 bytes -> fp32, exact.
+__device__ __forceinline__ void e4m3x4_values(uint32_t b, float* f) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(b));
+  f[0] = f16lo(lo);
+  f[1] = f16hi(lo);
+  f[2] = f16lo(hi);
+  f[3] = f16hi(hi);
+}
+
+// The value of a scale byte: 2^(b - 127), NaN for 255.
+__device__ __forceinline__ float e8m0_value(uint32_t b) {
+  const uint32_t bits = b == 0 ? 0x00400000u : (b == 255u ? 0x7FC00000u : b << 23);
+  return __uint_as_float(bits);
+}
+
+// sigmoid(z(x)), and z'(x).
+template <int ACT>
+__device__ __forceinline__ float act_z(float x) {
+  if constexpr (ACT == MXG_ACT_SILU) return x;
+  const float u = 1.59576912f * x;
+  return fmaf(0.0713548163f * x * x, x, u);
+}
+template <int ACT>
+__device__ __forceinline__ float act_dz(float x) {
+  if constexpr (ACT == MXG_ACT_SILU) return 1.0f;
+  // (bounded: it meets a slope of 0 there)
+  return fmaf(0.214064449f, fminf(x * x, 1e30f), 1.59576912f);
+}
+
+// Rows that take part: the sum of the group sizes, at most `rows`.
+__device__ __forceinline__ int64_t act_rows(const mxg_gated_act_t& d) {
+  if (d.group_ws == nullptr) return d.rows;
+  int64_t sum = 0;
+  for (int g = lane_id(); g < d.G; g += 32) {
+    const int64_t s = d.group_ws[g];
+    sum += s < 0 ? 0 : (s < d.rows ? s : d.rows);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  return sum < d.rows ? sum : d.rows;
+}
+
+// A thread's walk through the halves of blocks, `halves` (even) a row, a grid apart.
+struct HalfWalk {
+  int64_t row;
+  int half;
+  int64_t row_step;
+  int half_step, halves;
+  __device__ __forceinline__ HalfWalk(int halves) : halves(halves) {
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * kActThreads + threadIdx.x;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kActThreads;
+    row = at / halves;
+    half = static_cast<int>(at - row * halves);
+    row_step = step / halves;
+    half_step = static_cast<int>(step - row_step * halves);
+  }
+  __device__ __forceinline__ void next() {
+    row += row_step;
+    half += half_step;
+    if (half >= halves) {
+      half -= halves;
+      ++row;
+    }
+  }
+};
+
+// 16 of a block's values to E4M3 bytes and the block's scale byte, with the lane beside
+// this one; all lanes of the warp take part.
+template <bool VEC>
+__device__ __forceinline__ void keep16(const float (&v)[16], bool on, int n, uint8_t* q,
+                                       uint8_t* sf, bool first) {
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(v[i]));
+  float f[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] = v[i];
+  if (isinf(top)) {  // an infinity is kept as NaN
+    top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (isinf(f[i])) f[i] = __uint_as_float(0x7FC00000u);
+      top = fmaxf(top, fabsf(f[i]));
+    }
+  }
+  top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+  const int e = mx_exponent(top);
+  const float scale = pow2_neg(e);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = cvt_e4m3x2(f[4 * i] * scale, f[4 * i + 1] * scale) |
+           (cvt_e4m3x2(f[4 * i + 2] * scale, f[4 * i + 3] * scale) << 16);
+  if (!on) return;
+  if constexpr (VEC) {
+    if (n > 0) *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) q[i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
+  }
+  if (first) *sf = static_cast<uint8_t>(e + 127);
+}
+
+template <typename T, int ACT, bool GATED, bool VEC>
+__global__ void __launch_bounds__(kActThreads)
+    gated_act_kernel(const mxg_gated_act_t d, int blocks) {
+  const int cols = static_cast<int>(d.cols);
+  const int64_t live = act_rows(d);
+  const bool keep = d.q != nullptr;
+  HalfWalk at(2 * blocks);
+  const int64_t sf_row = (GATED ? 2 : 1) * static_cast<int64_t>(blocks);
+  // (a row ends with a warp's pair of lanes, so both of a pair go on or both stop)
+  while (__any_sync(0xFFFFFFFFu, at.row < live)) {
+    const bool on = at.row < live;
+    const int c = at.half * 16;
+    const int n = on ? min(cols - c, 16) : 0;  // 0 or less: the half is empty
+    uint32_t gw[8] = {}, uw[8] = {};
+    if (n > 0) {
+      load16<T, VEC>(static_cast<const T*>(d.gate) + at.row * d.ldg + c, n, gw);
+      if (GATED) load16<T, VEC>(static_cast<const T*>(d.up) + at.row * d.ldu + c, n, uw);
+    }
+    float g[16], u[16], h[16];
+    unpack16<T>(gw, g);
+    if (GATED) unpack16<T>(uw, u);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float e = __expf(-act_z<ACT>(g[i]));
+      h[i] = __fdividef(g[i], 1.0f + e);
+      if (GATED) h[i] *= u[i];
+    }
+    if (n > 0) store16<T, VEC>(static_cast<T*>(d.h) + at.row * d.ldh + c, n, h);
+    if (keep) {
+      uint8_t* q = d.q + at.row * d.ldq + c;
+      uint8_t* sf = d.sf + at.row * sf_row + (at.half >> 1);
+      const bool first = (at.half & 1) == 0;
+      keep16<VEC>(g, on, n, q, sf, first);
+      if (GATED) keep16<VEC>(u, on, n, q + cols, sf + blocks, first);
+    }
+    at.next();
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void restore16(const uint8_t* q, int n, uint32_t scale_byte,
+                                          float (&f)[16]) {
+  uint32_t w[4] = {};
+  if constexpr (VEC) {
+    const uint4 v = *reinterpret_cast<const uint4*>(q);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) w[i >> 2] |= static_cast<uint32_t>(q[i]) << (8 * (i & 3));
+  }
+  const float scale = e8m0_value(scale_byte);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) e4m3x4_values(w[i], f + 4 * i);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] *= scale;
+}
+
+template <typename T, int ACT, bool GATED, bool VEC>
+__global__ void __launch_bounds__(kActThreads)
+    gated_act_backward_kernel(const mxg_gated_act_t d, int blocks) {
+  const int cols = static_cast<int>(d.cols);
+  const int64_t live = act_rows(d);
+  const int64_t sf_row = (GATED ? 2 : 1) * static_cast<int64_t>(blocks);
+  for (HalfWalk at(2 * blocks); at.row < live; at.next()) {
+    const int c = at.half * 16;
+    const int n = min(cols - c, 16);
+    if (n <= 0) continue;
+    const uint8_t* q = d.q + at.row * d.ldq + c;
+    const uint8_t* sf = d.sf + at.row * sf_row + (at.half >> 1);
+    uint32_t dw[8];
+    load16<T, VEC>(static_cast<const T*>(d.dh) + at.row * d.lddh + c, n, dw);
+    float g[16], u[16], dh[16], dg[16];
+    restore16<VEC>(q, n, sf[0], g);
+    if (GATED) restore16<VEC>(q + cols, n, sf[blocks], u);
+    unpack16<T>(dw, dh);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float x = g[i];
+      const float s = __fdividef(1.0f, 1.0f + __expf(-act_z<ACT>(x)));
+      const float a = x * s;
+      const float slope = fmaf(a * (1.0f - s), act_dz<ACT>(x), s);
+      if (GATED) {
+        dg[i] = dh[i] * u[i] * slope;
+        dh[i] *= a;
+        u[i] *= a;
+      } else {
+        dg[i] = dh[i] * slope;
+        u[i] = a;
+      }
+    }
+    store16<T, VEC>(static_cast<T*>(d.dgate) + at.row * d.lddg + c, n, dg);
+    if (GATED) store16<T, VEC>(static_cast<T*>(d.dup) + at.row * d.lddu + c, n, dh);
+    if (d.h != nullptr) store16<T, VEC>(static_cast<T*>(d.h) + at.row * d.ldh + c, n, u);
+  }
+}
+
+namespace {
+
+// Whether every row that is given starts on `bytes` bytes.
+bool rows_on(const void* p, int64_t ld, size_t size, uintptr_t bytes) {
+  return p == nullptr || ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * size)) &
+                          (bytes - 1)) == 0;
+}
+
+template <typename T, int ACT, bool GATED>
+cudaError_t run(const mxg_gated_act_t& d, bool backward, int num_sms, cudaStream_t stream) {
+  const int blocks = static_cast<int>((d.cols + 31) / 32);
+  const bool vec = d.cols % 16 == 0 && rows_on(d.gate, d.ldg, 2, 32) && rows_on(d.up, d.ldu, 2, 32) &&
+                   rows_on(d.h, d.ldh, 2, 32) && rows_on(d.dh, d.lddh, 2, 32) &&
+                   rows_on(d.dgate, d.lddg, 2, 32) && rows_on(d.dup, d.lddu, 2, 32) &&
+                   rows_on(d.q, d.ldq, 1, 16);
+  const int64_t need = (d.rows * 2 * blocks + kActThreads - 1) / kActThreads;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(need, num_sms * 16LL));
+  if (backward) {
+    if (vec)
+      gated_act_backward_kernel<T, ACT, GATED, true><<<grid, kActThreads, 0, stream>>>(d, blocks);
+    else
+      gated_act_backward_kernel<T, ACT, GATED, false><<<grid, kActThreads, 0, stream>>>(d, blocks);
+  } else {
+    if (vec)
+      gated_act_kernel<T, ACT, GATED, true><<<grid, kActThreads, 0, stream>>>(d, blocks);
+    else
+      gated_act_kernel<T, ACT, GATED, false><<<grid, kActThreads, 0, stream>>>(d, blocks);
+  }
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t typed(const mxg_gated_act_t& d, bool backward, int num_sms, cudaStream_t stream) {
+  if (d.act == MXG_ACT_SILU)
+    return d.gated ? run<T, MXG_ACT_SILU, true>(d, backward, num_sms, stream)
+                   : run<T, MXG_ACT_SILU, false>(d, backward, num_sms, stream);
+  return d.gated ? run<T, MXG_ACT_GELU_TANH, true>(d, backward, num_sms, stream)
+                 : run<T, MXG_ACT_GELU_TANH, false>(d, backward, num_sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_gated_act(const mxg_gated_act_t& d, bool backward, int num_sms,
+                             cudaStream_t stream) {
+  return d.dtype == MXG_BF16 ? typed<Bf16>(d, backward, num_sms, stream)
+                             : typed<F16>(d, backward, num_sms, stream);
+}
+
+}  // namespace mxg

@@ -3,6 +3,7 @@
 // synchronisation.
 #include <atomic>
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
 
 #include "mxg_device.cuh"
@@ -48,6 +49,18 @@ size_t grad_ws_bytes();
 cudaError_t launch_grad_clip(const mxg_grad_t* grads, int n, bool clip, float max_norm,
                              float* norm, void* ws, int num_sms, cudaStream_t stream,
                              int* launches);
+size_t route_ws_bytes(int64_t tokens, int experts, int k);
+cudaError_t launch_route(const mxg_route_t& d, void* workspace, int32_t* status,
+                         cudaStream_t stream, int* launches);
+cudaError_t launch_route_rows(const int32_t* expert, int64_t tokens, int experts, int k, int align,
+                              int64_t capacity, int64_t last_dim, int32_t* counts, int32_t* row_of,
+                              int64_t* group_ws, void* workspace, int32_t* status,
+                              cudaStream_t stream, int* launches);
+cudaError_t launch_route_backward(const mxg_route_grad_t& d, int num_sms, cudaStream_t stream);
+cudaError_t launch_expert_rows(const mxg_expert_rows_t& d, int op, int num_sms,
+                               cudaStream_t stream);
+cudaError_t launch_gated_act(const mxg_gated_act_t& d, bool backward, int num_sms,
+                             cudaStream_t stream);
 constexpr uint64_t kDefaultWaitNs = 1000000000ull;
 }  // namespace mxg
 
@@ -190,6 +203,133 @@ mxg_status_t grad_impl(const mxg_grad_t* grads, int n, bool clip, float max_norm
       mxg::launch_grad_clip(grads, n, clip, max_norm, norm, workspace, sms,
                             reinterpret_cast<cudaStream_t>(stream), &launches);
   return launched(e, static_cast<uint64_t>(launches));
+}
+
+// Sizes of a routed batch.  The bounds keep every index of a choice or a row in 32 bits.
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxChosen = 32;
+constexpr int64_t kMaxRowCols = 1LL << 20;
+constexpr int64_t kMaxLd = 1LL << 36;  // elements between rows
+
+bool route_sizes_ok(int64_t tokens, int experts, int k) {
+  return tokens >= 0 && tokens <= kMaxRows && experts >= 1 && experts <= kMaxExperts && k >= 1 &&
+         k <= kMaxChosen && k <= experts && tokens * k <= kMaxRows;
+}
+
+// counts, and the rows where they are wanted.
+mxg_status_t route_rows_args(int64_t tokens, const int32_t* counts, const int32_t* row_of,
+                             const int64_t* group_ws, int align, int64_t rows_capacity,
+                             int64_t last_dim) {
+  if (counts == nullptr) return MXG_ERR_INVALID_ARG;
+  if (align < 1 || align > 1024 || rows_capacity < 0 || rows_capacity > kMaxRows || last_dim < 1 ||
+      (rows_capacity > 0 && last_dim > INT64_MAX / rows_capacity))
+    return MXG_ERR_INVALID_ARG;
+  if ((row_of != nullptr && group_ws == nullptr) ||
+      (group_ws != nullptr && row_of == nullptr && tokens != 0))
+    return MXG_ERR_INVALID_ARG;
+  if (!aligned_to(counts, 4) || !aligned_to(row_of, 4) || !aligned_to(group_ws, 8))
+    return MXG_ERR_ALIGNMENT;
+  return MXG_OK;
+}
+
+mxg_status_t route_workspace(int64_t tokens, int experts, int k, const void* workspace,
+                             size_t workspace_bytes) {
+  if (workspace == nullptr) return MXG_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return MXG_ERR_ALIGNMENT;
+  return workspace_bytes < mxg::route_ws_bytes(tokens, experts, k) ? MXG_ERR_WORKSPACE_TOO_SMALL
+                                                                   : MXG_OK;
+}
+
+// Checks a matrix's leading dimension, filling in a dense one.
+bool fill_ld(int64_t* ld, int64_t cols) {
+  if (*ld == 0) *ld = cols;
+  return *ld >= cols && *ld <= kMaxLd;
+}
+
+// op: 0 dispatch, 1 combine, 2 its gradients.
+mxg_status_t expert_rows_impl(const mxg_expert_rows_t* desc, int op, mxg_stream_t stream) {
+  if (desc == nullptr) return MXG_ERR_INVALID_ARG;
+  mxg_expert_rows_t d = *desc;
+  const size_t size = dtype_bytes(d.dtype);
+  if (size == 0 || d.n < 0 || d.n > kMaxRows || d.k < 1 || d.k > kMaxChosen ||
+      d.n * d.k > kMaxRows || d.cols < 1 || d.cols > kMaxRowCols || d.rows_capacity < 0 ||
+      d.rows_capacity > kMaxRows)
+    return MXG_ERR_INVALID_ARG;
+  const bool any = d.n != 0, rows = d.rows_capacity != 0;
+  if (any && (d.tokens == nullptr || d.row_of == nullptr)) return MXG_ERR_INVALID_ARG;
+  if (op != 2 && ((rows && d.rows == nullptr) || d.y_rows != nullptr || d.dweight != nullptr))
+    return MXG_ERR_INVALID_ARG;
+  if (op == 0 && d.weight != nullptr) return MXG_ERR_INVALID_ARG;
+  if (op == 2 && any && ((d.dweight != nullptr && rows && d.y_rows == nullptr) ||
+                         (d.dweight == nullptr && rows && d.rows == nullptr)))
+    return MXG_ERR_INVALID_ARG;
+  if (op == 2 && d.dweight == nullptr && d.y_rows != nullptr) return MXG_ERR_INVALID_ARG;
+  // padding: all three or none
+  const bool padded = d.counts != nullptr;
+  if (padded != (d.group_ws != nullptr) || padded != (d.experts != 0) ||
+      (padded && (op == 1 || d.experts < 1 || d.experts > kMaxExperts ||
+                  (rows && d.rows == nullptr))))
+    return MXG_ERR_INVALID_ARG;
+  if (!fill_ld(&d.ldt, d.cols) || !fill_ld(&d.ldr, d.cols) || !fill_ld(&d.ldy, d.cols) ||
+      (d.y_rows != nullptr && d.y_rows == d.rows && d.ldy != d.ldr))
+    return MXG_ERR_INVALID_ARG;
+  if (!aligned_to(d.tokens, size) || !aligned_to(d.rows, size) || !aligned_to(d.y_rows, size) ||
+      !aligned_to(d.row_of, 4) || !aligned_to(d.weight, 4) || !aligned_to(d.dweight, 4) ||
+      !aligned_to(d.counts, 4) || !aligned_to(d.group_ws, 8))
+    return MXG_ERR_ALIGNMENT;
+  int sms = 0;
+  const mxg_status_t st = current_device(&sms);
+  if (st != MXG_OK) return st;
+  if (!rows) {  // nothing lies there
+    d.rows = nullptr;
+    d.y_rows = nullptr;
+  }
+  if (op == 1 ? !any : !any && !(padded && rows)) return MXG_OK;
+  if (op == 0 && !rows) return MXG_OK;
+  return launched(mxg::launch_expert_rows(d, op, sms, reinterpret_cast<cudaStream_t>(stream)), 1);
+}
+
+mxg_status_t gated_act_impl(const mxg_gated_act_t* desc, bool backward, mxg_stream_t stream) {
+  if (desc == nullptr) return MXG_ERR_INVALID_ARG;
+  mxg_gated_act_t d = *desc;
+  if ((d.dtype != MXG_BF16 && d.dtype != MXG_F16) ||
+      (d.act != MXG_ACT_SILU && d.act != MXG_ACT_GELU_TANH) || d.rows < 0 || d.rows > kMaxRows ||
+      d.cols < 1 || d.cols > kMaxRowCols || (d.gated != 0 && d.gated != 1))
+    return MXG_ERR_INVALID_ARG;
+  if (d.G < 0 || d.G > kMaxExperts || (d.G != 0) != (d.group_ws != nullptr))
+    return MXG_ERR_INVALID_ARG;
+  const bool any = d.rows != 0;
+  if (backward ? d.gate != nullptr || d.up != nullptr
+               : d.dh != nullptr || d.dgate != nullptr || d.dup != nullptr)
+    return MXG_ERR_INVALID_ARG;
+  if (any) {
+    if (backward && (d.q == nullptr || d.sf == nullptr || d.dh == nullptr || d.dgate == nullptr ||
+                     (d.dup != nullptr) != (d.gated != 0)))
+      return MXG_ERR_INVALID_ARG;
+    if (!backward && (d.gate == nullptr || d.h == nullptr || (d.up != nullptr) != (d.gated != 0) ||
+                      (d.q != nullptr) != (d.sf != nullptr)))
+      return MXG_ERR_INVALID_ARG;
+  }
+  if (!fill_ld(&d.ldg, d.cols) || !fill_ld(&d.ldu, d.cols) || !fill_ld(&d.ldh, d.cols) ||
+      !fill_ld(&d.ldq, d.cols * (1 + d.gated)) || !fill_ld(&d.lddh, d.cols) ||
+      !fill_ld(&d.lddg, d.cols) || !fill_ld(&d.lddu, d.cols))
+    return MXG_ERR_INVALID_ARG;
+  // in place: the same element at the same time
+  if (d.h != nullptr && ((d.h == d.gate && d.ldh != d.ldg) || (d.h == d.up && d.ldh != d.ldu)))
+    return MXG_ERR_INVALID_ARG;
+  if (d.dh != nullptr &&
+      ((d.dh == d.dgate && d.lddh != d.lddg) || (d.dh == d.dup && d.lddh != d.lddu)))
+    return MXG_ERR_INVALID_ARG;
+  for (const void* p : {d.gate, d.up, static_cast<const void*>(d.h), d.dh,
+                        static_cast<const void*>(d.dgate), static_cast<const void*>(d.dup)})
+    if (!aligned_to(p, 2)) return MXG_ERR_ALIGNMENT;
+  if (!aligned_to(d.group_ws, 8)) return MXG_ERR_ALIGNMENT;
+  int sms = 0;
+  const mxg_status_t st = current_device(&sms);
+  if (st != MXG_OK) return st;
+  if (!any) return MXG_OK;
+  return launched(mxg::launch_gated_act(d, backward, sms, reinterpret_cast<cudaStream_t>(stream)),
+                  1);
 }
 
 }  // namespace
@@ -569,6 +709,102 @@ mxg_status_t mxg_grad_clip(const mxg_grad_t* grads, int n, float max_norm, float
                            void* workspace, size_t workspace_bytes, mxg_stream_t stream) {
   if (!(max_norm >= 0.0f)) return MXG_ERR_INVALID_ARG;
   return grad_impl(grads, n, true, max_norm, norm, workspace, workspace_bytes, stream);
+}
+
+size_t mxg_route_workspace_bytes(int64_t tokens, int experts, int k) {
+  return route_sizes_ok(tokens, experts, k) ? mxg::route_ws_bytes(tokens, experts, k) : 0;
+}
+
+mxg_status_t mxg_route(const mxg_route_t* desc, void* workspace, size_t workspace_bytes,
+                       int32_t* dev_status, mxg_stream_t stream) {
+  if (desc == nullptr) return MXG_ERR_INVALID_ARG;
+  mxg_route_t d = *desc;
+  const size_t size = dtype_bytes(d.dtype);
+  if (size == 0 || !route_sizes_ok(d.tokens, d.experts, d.k) ||
+      (d.score != MXG_SCORE_SOFTMAX && d.score != MXG_SCORE_SIGMOID) ||
+      !std::isfinite(d.scale) || !std::isfinite(d.balance))
+    return MXG_ERR_INVALID_ARG;
+  if (d.tokens != 0 && (d.logits == nullptr || d.expert == nullptr || d.weight == nullptr))
+    return MXG_ERR_INVALID_ARG;
+  if (!fill_ld(&d.ld, d.experts)) return MXG_ERR_INVALID_ARG;
+  mxg_status_t st = route_rows_args(d.tokens, d.counts, d.row_of, d.group_ws, d.align,
+                                    d.rows_capacity, d.last_dim);
+  if (st != MXG_OK) return st;
+  if (!aligned_to(d.logits, size) || !aligned_to(d.expert, 4) || !aligned_to(d.weight, 4) ||
+      !aligned_to(d.loss, 4) || !aligned_to(d.slope, 4))
+    return MXG_ERR_ALIGNMENT;
+  if ((st = route_workspace(d.tokens, d.experts, d.k, workspace, workspace_bytes)) != MXG_OK)
+    return st;
+  int sms = 0;
+  if ((st = current_device(&sms)) != MXG_OK) return st;
+  int launches = 0;
+  const cudaError_t e = mxg::launch_route(d, workspace, dev_status,
+                                          reinterpret_cast<cudaStream_t>(stream), &launches);
+  return launched(e, static_cast<uint64_t>(launches));
+}
+
+mxg_status_t mxg_route_rows(const int32_t* expert, int64_t tokens, int experts, int k, int align,
+                            int64_t rows_capacity, int64_t last_dim, int32_t* counts,
+                            int32_t* row_of, int64_t* group_ws, void* workspace,
+                            size_t workspace_bytes, int32_t* dev_status, mxg_stream_t stream) {
+  if (!route_sizes_ok(tokens, experts, k) || (tokens != 0 && expert == nullptr))
+    return MXG_ERR_INVALID_ARG;
+  mxg_status_t st =
+      route_rows_args(tokens, counts, row_of, group_ws, align, rows_capacity, last_dim);
+  if (st != MXG_OK) return st;
+  if (!aligned_to(expert, 4)) return MXG_ERR_ALIGNMENT;
+  if ((st = route_workspace(tokens, experts, k, workspace, workspace_bytes)) != MXG_OK) return st;
+  int sms = 0;
+  if ((st = current_device(&sms)) != MXG_OK) return st;
+  int launches = 0;
+  const cudaError_t e = mxg::launch_route_rows(
+      expert, tokens, experts, k, align, rows_capacity, last_dim, counts, row_of, group_ws,
+      workspace, dev_status, reinterpret_cast<cudaStream_t>(stream), &launches);
+  return launched(e, static_cast<uint64_t>(launches));
+}
+
+mxg_status_t mxg_route_backward(const mxg_route_grad_t* desc, mxg_stream_t stream) {
+  if (desc == nullptr) return MXG_ERR_INVALID_ARG;
+  mxg_route_grad_t d = *desc;
+  const size_t size = dtype_bytes(d.dtype);
+  if (size == 0 || !route_sizes_ok(d.tokens, d.experts, d.k) ||
+      (d.score != MXG_SCORE_SOFTMAX && d.score != MXG_SCORE_SIGMOID) || !std::isfinite(d.scale) ||
+      (d.slope != nullptr) != (d.dloss != nullptr))
+    return MXG_ERR_INVALID_ARG;
+  if (d.tokens != 0 && (d.logits == nullptr || d.expert == nullptr || d.dlogits == nullptr))
+    return MXG_ERR_INVALID_ARG;
+  if (!fill_ld(&d.ld, d.experts) || !fill_ld(&d.ldd, d.experts) ||
+      (d.dlogits != nullptr && d.dlogits == d.logits && d.ld != d.ldd))
+    return MXG_ERR_INVALID_ARG;
+  if (!aligned_to(d.logits, size) || !aligned_to(d.dlogits, size) || !aligned_to(d.expert, 4) ||
+      !aligned_to(d.dweight, 4) || !aligned_to(d.slope, 4) || !aligned_to(d.dloss, 4))
+    return MXG_ERR_ALIGNMENT;
+  int sms = 0;
+  const mxg_status_t st = current_device(&sms);
+  if (st != MXG_OK) return st;
+  if (d.tokens == 0) return MXG_OK;
+  return launched(
+      mxg::launch_route_backward(d, sms, reinterpret_cast<cudaStream_t>(stream)), 1);
+}
+
+mxg_status_t mxg_dispatch(const mxg_expert_rows_t* desc, mxg_stream_t stream) {
+  return expert_rows_impl(desc, 0, stream);
+}
+
+mxg_status_t mxg_combine(const mxg_expert_rows_t* desc, mxg_stream_t stream) {
+  return expert_rows_impl(desc, 1, stream);
+}
+
+mxg_status_t mxg_combine_backward(const mxg_expert_rows_t* desc, mxg_stream_t stream) {
+  return expert_rows_impl(desc, 2, stream);
+}
+
+mxg_status_t mxg_gated_act(const mxg_gated_act_t* desc, mxg_stream_t stream) {
+  return gated_act_impl(desc, false, stream);
+}
+
+mxg_status_t mxg_gated_act_backward(const mxg_gated_act_t* desc, mxg_stream_t stream) {
+  return gated_act_impl(desc, true, stream);
 }
 
 const char* mxg_status_string(mxg_status_t status) {

@@ -30,6 +30,8 @@ MXG_FPROP_TN, MXG_WGRAD_NT, MXG_DGRAD_NN = 0, 1, 2
 MXG_OUT_F32, MXG_OUT_BF16 = 0, 1
 MXG_F32, MXG_BF16, MXG_F16 = 0, 1, 2
 MXG_GATE_NONE, MXG_GATE_ROW, MXG_GATE_COL, MXG_GATE_FULL = 0, 1, 2, 3
+MXG_SCORE_SOFTMAX, MXG_SCORE_SIGMOID = 0, 1
+MXG_ACT_SILU, MXG_ACT_GELU_TANH = 0, 1
 MXG_DEV_NEG_SIZE, MXG_DEV_MISALIGNED, MXG_DEV_SUM_OVER_CAPACITY = 1, 2, 4
 MXG_DEV_BOUNDS, MXG_DEV_TIMEOUT = 8, 16
 STATUS_NAMES = {0: "MXG_OK", 1: "MXG_ERR_INVALID_ARG", 2: "MXG_ERR_ALIGNMENT",
@@ -78,6 +80,52 @@ class Grad(ctypes.Structure):
     """mxg_grad_t"""
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("numel", ctypes.c_int64),
                 ("src_type", ctypes.c_int), ("dst_type", ctypes.c_int)]
+
+
+class Route(ctypes.Structure):
+    """mxg_route_t"""
+    _fields_ = [("dtype", ctypes.c_int), ("tokens", ctypes.c_int64), ("experts", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("logits", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("mask", ctypes.c_void_p), ("score", ctypes.c_int), ("normalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("balance", ctypes.c_float),
+                ("expert", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("counts", ctypes.c_void_p), ("loss", ctypes.c_void_p), ("slope", ctypes.c_void_p),
+                ("row_of", ctypes.c_void_p), ("group_ws", ctypes.c_void_p),
+                ("align", ctypes.c_int32), ("rows_capacity", ctypes.c_int64),
+                ("last_dim", ctypes.c_int64)]
+
+
+class RouteGrad(ctypes.Structure):
+    """mxg_route_grad_t"""
+    _fields_ = [("dtype", ctypes.c_int), ("tokens", ctypes.c_int64), ("experts", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("logits", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("expert", ctypes.c_void_p), ("score", ctypes.c_int), ("normalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("dweight", ctypes.c_void_p),
+                ("slope", ctypes.c_void_p), ("dloss", ctypes.c_void_p),
+                ("dlogits", ctypes.c_void_p), ("ldd", ctypes.c_int64)]
+
+
+class ExpertRows(ctypes.Structure):
+    """mxg_expert_rows_t"""
+    _fields_ = [("dtype", ctypes.c_int), ("n", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("k", ctypes.c_int32), ("experts", ctypes.c_int32),
+                ("rows_capacity", ctypes.c_int64), ("tokens", ctypes.c_void_p),
+                ("ldt", ctypes.c_int64), ("rows", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("row_of", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("y_rows", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("dweight", ctypes.c_void_p),
+                ("counts", ctypes.c_void_p), ("group_ws", ctypes.c_void_p)]
+
+
+class GatedAct(ctypes.Structure):
+    """mxg_gated_act_t"""
+    _fields_ = [("dtype", ctypes.c_int), ("act", ctypes.c_int), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("gated", ctypes.c_int32), ("G", ctypes.c_int32),
+                ("group_ws", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64),
+                ("up", ctypes.c_void_p), ("ldu", ctypes.c_int64), ("h", ctypes.c_void_p),
+                ("ldh", ctypes.c_int64), ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64),
+                ("sf", ctypes.c_void_p), ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+                ("dgate", ctypes.c_void_p), ("lddg", ctypes.c_int64), ("dup", ctypes.c_void_p),
+                ("lddu", ctypes.c_int64)]
 
 
 def _operand(T, elems_per_byte: int) -> Operand:
@@ -155,6 +203,21 @@ def load() -> ctypes.CDLL:
         L.mxg_grad_norm.argtypes = [vp, c_int, vp, vp, sz, vp]
         L.mxg_grad_clip.restype = c_int
         L.mxg_grad_clip.argtypes = [vp, c_int, ctypes.c_float, vp, vp, sz, vp]
+        L.mxg_route_workspace_bytes.restype = sz
+        L.mxg_route_workspace_bytes.argtypes = [i64, c_int, c_int]
+        L.mxg_route.restype = c_int
+        L.mxg_route.argtypes = [ctypes.POINTER(Route), vp, sz, vp, vp]
+        L.mxg_route_rows.restype = c_int
+        L.mxg_route_rows.argtypes = [vp, i64, c_int, c_int, c_int, i64, i64, vp, vp, vp, vp, sz, vp,
+                                     vp]
+        L.mxg_route_backward.restype = c_int
+        L.mxg_route_backward.argtypes = [ctypes.POINTER(RouteGrad), vp]
+        for f in (L.mxg_dispatch, L.mxg_combine, L.mxg_combine_backward):
+            f.restype = c_int
+            f.argtypes = [ctypes.POINTER(ExpertRows), vp]
+        for f in (L.mxg_gated_act, L.mxg_gated_act_backward):
+            f.restype = c_int
+            f.argtypes = [ctypes.POINTER(GatedAct), vp]
         _lib = L
     return _lib
 
@@ -544,6 +607,235 @@ def mxg_grad_clip(grads: GradList, max_norm: float, norm: torch.Tensor, workspac
                                 workspace.nbytes, _s(stream)))
 
 
+# ------------------------------------------------ around the products of an expert block
+def _whole(t, dtypes, shape: tuple, name: str) -> None:
+    """A contiguous tensor of one of these types with as many elements as the shape, or none."""
+    if t is None:
+        return
+    if t.dtype not in dtypes or t.numel() != math.prod(shape) or not t.is_contiguous():
+        raise ValueError("%s: expected %s contiguous elements of %s: got %s of %s"
+                         % (name, shape, dtypes[0], tuple(t.shape), t.dtype))
+
+
+def _matrix(t, dtype, shape: tuple, name: str) -> int:
+    """_ld of a [rows, cols] matrix of this type and shape, or of none."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError("%s: expected %s of %s: got %s of %s"
+                         % (name, tuple(shape), dtype, tuple(t.shape), t.dtype))
+    return _ld(t)
+
+
+def _one_device(tensors) -> None:
+    """All on the device that the launch goes to."""
+    here = None
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            if here is None:
+                here = torch.cuda.current_device()
+            if t.get_device() != here:
+                raise ValueError("a tensor on %s: the current device is %d" % (t.device, here))
+
+
+_I32, _I64, _FP32 = (torch.int32,), (torch.int64,), (torch.float32,)
+_MASK, _BYTES = (torch.uint8, torch.bool), (torch.uint8, torch.float8_e4m3fn)
+
+
+def _choices(expert, name: str) -> tuple:
+    """(tokens, k) of a [tokens, k] tensor of choices."""
+    if expert.dim() != 2:
+        raise ValueError("%s: expected [tokens, k]: got %s" % (name, tuple(expert.shape)))
+    return expert.shape[0], expert.shape[1]
+
+
+def _rows_wanted(row_of, group_ws, tokens: int, k: int, experts: int, align: int,
+                 rows_capacity) -> int:
+    """Checks the plan's tensors; the rows that always suffice where none are given."""
+    if (row_of is None) != (group_ws is None):
+        raise ValueError("row_of and group_ws: both or neither")
+    _whole(row_of, _I32, (tokens, k), "row_of")
+    _whole(group_ws, _I64, (2 * experts + 1,), "group_ws")
+    return tokens * k + experts * (align - 1) if rows_capacity is None else rows_capacity
+
+
+def mxg_route_workspace_bytes(tokens: int, experts: int, k: int) -> int:
+    return load().mxg_route_workspace_bytes(tokens, experts, k)
+
+
+def mxg_route(logits: torch.Tensor, expert: torch.Tensor, weight: torch.Tensor,
+              counts: torch.Tensor, mask=None, score: int = MXG_SCORE_SOFTMAX,
+              normalize: bool = True, scale: float = 1.0, balance: float = 0.0, loss=None,
+              slope=None, row_of=None, group_ws=None, align: int = 1, rows_capacity=None,
+              last_dim: int = 1, workspace=None, dev_status=None, stream=None) -> None:
+    """logits: [tokens, experts] (rows may be strided); expert, weight, row_of: [tokens, k];
+    mask: uint8 or bool [tokens].  rows_capacity: by default the rows that always suffice,
+    tokens * k + experts * (align - 1)."""
+    tokens, k = _choices(expert, "expert")
+    if logits.dim() != 2 or logits.shape[0] != tokens or logits.dtype not in _DTYPES:
+        raise ValueError("logits: expected [%d, experts] of fp32, bf16 or fp16: got %s of %s"
+                         % (tokens, tuple(logits.shape), logits.dtype))
+    E = logits.shape[1]
+    _whole(expert, _I32, (tokens, k), "expert")
+    _whole(weight, _FP32, (tokens, k), "weight")
+    _whole(counts, _I32, (E,), "counts")
+    _whole(mask, _MASK, (tokens,), "mask")
+    _whole(loss, _FP32, (1,), "loss")
+    _whole(slope, _FP32, (E,), "slope")
+    capacity = _rows_wanted(row_of, group_ws, tokens, k, E, align, rows_capacity)
+    _one_device((logits, expert, weight, counts, mask, loss, slope, row_of, group_ws, workspace,
+                 dev_status))
+    d = Route(_DTYPES[logits.dtype], tokens, E, k, _p(logits), _ld(logits), _p(mask), score,
+              int(normalize), scale, balance, _p(expert), _p(weight), _p(counts), _p(loss),
+              _p(slope), _p(row_of), _p(group_ws), align, capacity, last_dim)
+    _check("mxg_route",
+           load().mxg_route(ctypes.byref(d), _p(workspace),
+                            0 if workspace is None else workspace.nbytes, _p(dev_status),
+                            _s(stream)))
+
+
+def mxg_route_rows(expert: torch.Tensor, counts: torch.Tensor, row_of=None, group_ws=None,
+                   align: int = 1, rows_capacity=None, last_dim: int = 1, workspace=None,
+                   dev_status=None, stream=None) -> None:
+    """expert: int32 [tokens, k]; counts: int32 [experts]."""
+    tokens, k = _choices(expert, "expert")
+    E = counts.numel()
+    _whole(expert, _I32, (tokens, k), "expert")
+    _whole(counts, _I32, (E,), "counts")
+    capacity = _rows_wanted(row_of, group_ws, tokens, k, E, align, rows_capacity)
+    _one_device((expert, counts, row_of, group_ws, workspace, dev_status))
+    _check("mxg_route_rows",
+           load().mxg_route_rows(_p(expert), tokens, E, k, align, capacity, last_dim, _p(counts),
+                                 _p(row_of), _p(group_ws), _p(workspace),
+                                 0 if workspace is None else workspace.nbytes, _p(dev_status),
+                                 _s(stream)))
+
+
+def mxg_route_backward(logits: torch.Tensor, expert: torch.Tensor, dlogits: torch.Tensor,
+                       dweight=None, score: int = MXG_SCORE_SOFTMAX, normalize: bool = True,
+                       scale: float = 1.0, slope=None, dloss=None, stream=None) -> None:
+    """logits, expert, slope: as mxg_route took and wrote them; dlogits: like logits."""
+    tokens, k = _choices(expert, "expert")
+    if logits.dim() != 2 or logits.shape[0] != tokens or logits.dtype not in _DTYPES:
+        raise ValueError("logits: expected [%d, experts] of fp32, bf16 or fp16: got %s of %s"
+                         % (tokens, tuple(logits.shape), logits.dtype))
+    E = logits.shape[1]
+    _whole(expert, _I32, (tokens, k), "expert")
+    _whole(dweight, _FP32, (tokens, k), "dweight")
+    _whole(slope, _FP32, (E,), "slope")
+    _whole(dloss, _FP32, (1,), "dloss")
+    ldd = _matrix(dlogits, logits.dtype, logits.shape, "dlogits")
+    _one_device((logits, expert, dlogits, dweight, slope, dloss))
+    d = RouteGrad(_DTYPES[logits.dtype], tokens, E, k, _p(logits), _ld(logits), _p(expert), score,
+                  int(normalize), scale, _p(dweight), _p(slope), _p(dloss), _p(dlogits), ldd)
+    _check("mxg_route_backward", load().mxg_route_backward(ctypes.byref(d), _s(stream)))
+
+
+def _expert_rows(fn: str, tokens, rows, row_of, weight=None, y_rows=None, dweight=None, counts=None,
+                 group_ws=None, stream=None) -> None:
+    n, k = _choices(row_of, "row_of")
+    if tokens.dim() != 2 or tokens.shape[0] != n or tokens.dtype not in _DTYPES:
+        raise ValueError("expected [%d, cols] of fp32, bf16 or fp16: got %s of %s"
+                         % (n, tuple(tokens.shape), tokens.dtype))
+    cols, like = tokens.shape[1], y_rows if rows is None else rows
+    capacity = 0 if like is None else like.shape[0]
+    _whole(row_of, _I32, (n, k), "row_of")
+    _whole(weight, _FP32, (n, k), "weight")
+    _whole(dweight, _FP32, (n, k), "dweight")
+    ldr = _matrix(rows, tokens.dtype, (capacity, cols), "rows")
+    ldy = _matrix(y_rows, tokens.dtype, (capacity, cols), "y_rows")
+    if (counts is None) != (group_ws is None):
+        raise ValueError("counts and group_ws: both or neither")
+    experts = 0 if counts is None else counts.numel()
+    _whole(counts, _I32, (experts,), "counts")
+    _whole(group_ws, _I64, (2 * experts + 1,), "group_ws")
+    _one_device((tokens, rows, row_of, weight, y_rows, dweight, counts, group_ws))
+    d = ExpertRows(_DTYPES[tokens.dtype], n, cols, k, experts, capacity, _p(tokens), _ld(tokens),
+                   _p(rows), ldr, _p(row_of), _p(weight), _p(y_rows), ldy, _p(dweight), _p(counts),
+                   _p(group_ws))
+    _check(fn, getattr(load(), fn)(ctypes.byref(d), _s(stream)))
+
+
+def mxg_dispatch(tokens: torch.Tensor, row_of: torch.Tensor, rows: torch.Tensor, counts=None,
+                 group_ws=None, stream=None) -> None:
+    """tokens [n, cols] to rows [rows_capacity, cols] (rows of both may be strided); counts and
+    group_ws: to set the groups' padding rows to 0."""
+    _expert_rows("mxg_dispatch", tokens, rows, row_of, counts=counts, group_ws=group_ws,
+                 stream=stream)
+
+
+def mxg_combine(rows: torch.Tensor, row_of: torch.Tensor, tokens: torch.Tensor, weight=None,
+                stream=None) -> None:
+    """tokens[t] = the sum of rows[row_of[t, j]], times weight[t, j] where that is given."""
+    _expert_rows("mxg_combine", tokens, rows, row_of, weight=weight, stream=stream)
+
+
+def mxg_combine_backward(dtokens: torch.Tensor, row_of: torch.Tensor, weight, drows, y_rows=None,
+                         dweight=None, counts=None, group_ws=None, stream=None) -> None:
+    """The gradients drows of the rows and dweight of the weights (either may be None); y_rows:
+    the rows that mxg_combine summed, for dweight."""
+    if drows is None and dweight is None:
+        raise ValueError("drows, dweight: one of them at least")
+    _expert_rows("mxg_combine_backward", dtokens, drows, row_of, weight=weight, y_rows=y_rows,
+                 dweight=dweight, counts=counts, group_ws=group_ws, stream=stream)
+
+
+def _act_blocks(cols: int) -> int:
+    return (cols + 31) // 32
+
+
+def _kept(q, sf, rows: int, cols: int, parts: int) -> int:
+    """Checks an 8-bit checkpoint of `parts` matrices; the bytes between its rows."""
+    if (q is None) != (sf is None):
+        raise ValueError("q and sf: both or neither")
+    if q is None:
+        return 0
+    if q.dtype not in _BYTES or q.shape != (rows, parts * cols):
+        raise ValueError("q: expected %s bytes: got %s of %s"
+                         % ((rows, parts * cols), tuple(q.shape), q.dtype))
+    _whole(sf, (torch.uint8,), (rows, parts * _act_blocks(cols)), "sf")
+    return _ld(q)
+
+
+def mxg_gated_act(gate: torch.Tensor, h: torch.Tensor, up=None, act: int = MXG_ACT_SILU, q=None,
+                  sf=None, group_ws=None, G: int = 0, stream=None) -> None:
+    """h = act(gate) * up, [rows, cols] (rows may be strided: gate and up are often the halves of
+    one product); q, sf: where the inputs are kept (alloc_act_checkpoint)."""
+    if gate.dim() != 2 or gate.dtype not in _DTYPES:
+        raise ValueError("gate: expected [rows, cols]: got %s of %s" % (tuple(gate.shape), gate.dtype))
+    rows, cols = gate.shape
+    parts = 1 if up is None else 2
+    ldu = _matrix(up, gate.dtype, gate.shape, "up")
+    ldh = _matrix(h, gate.dtype, gate.shape, "h")
+    ldq = _kept(q, sf, rows, cols, parts)
+    _whole(group_ws, _I64, (2 * G + 1,), "group_ws")
+    _one_device((gate, up, h, q, sf, group_ws))
+    d = GatedAct(dtype=_DTYPES[gate.dtype], act=act, rows=rows, cols=cols, gated=parts - 1, G=G,
+                 group_ws=_p(group_ws), gate=_p(gate), ldg=_ld(gate), up=_p(up), ldu=ldu, h=_p(h),
+                 ldh=ldh, q=_p(q), ldq=ldq, sf=_p(sf))
+    _check("mxg_gated_act", load().mxg_gated_act(ctypes.byref(d), _s(stream)))
+
+
+def mxg_gated_act_backward(q: torch.Tensor, sf: torch.Tensor, dh: torch.Tensor, dgate: torch.Tensor,
+                           dup=None, act: int = MXG_ACT_SILU, h=None, group_ws=None, G: int = 0,
+                           stream=None) -> None:
+    """The gradients of gate and up from the checkpoint, and h again where it is given."""
+    if dh.dim() != 2 or dh.dtype not in _DTYPES:
+        raise ValueError("dh: expected [rows, cols]: got %s of %s" % (tuple(dh.shape), dh.dtype))
+    rows, cols = dh.shape
+    parts = 1 if dup is None else 2
+    lddg = _matrix(dgate, dh.dtype, dh.shape, "dgate")
+    lddu = _matrix(dup, dh.dtype, dh.shape, "dup")
+    ldh = _matrix(h, dh.dtype, dh.shape, "h")
+    ldq = _kept(q, sf, rows, cols, parts)
+    _whole(group_ws, _I64, (2 * G + 1,), "group_ws")
+    _one_device((q, sf, dh, dgate, dup, h, group_ws))
+    d = GatedAct(dtype=_DTYPES[dh.dtype], act=act, rows=rows, cols=cols, gated=parts - 1, G=G,
+                 group_ws=_p(group_ws), h=_p(h), ldh=ldh, q=_p(q), ldq=ldq, sf=_p(sf), dh=_p(dh),
+                 lddh=_ld(dh), dgate=_p(dgate), lddg=lddg, dup=_p(dup), lddu=lddu)
+    _check("mxg_gated_act_backward", load().mxg_gated_act_backward(ctypes.byref(d), _s(stream)))
+
+
 def mxg_status_string(code: int) -> str:
     return load().mxg_status_string(code).decode()
 
@@ -608,3 +900,15 @@ def alloc_block_norm_workspace(rows: int, cols: int, device="cuda") -> torch.Ten
 
 def alloc_grad_workspace(device="cuda") -> torch.Tensor:
     return torch.empty(mxg_grad_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def alloc_route_workspace(tokens: int, experts: int, k: int, device="cuda") -> torch.Tensor:
+    return torch.empty(max(16, mxg_route_workspace_bytes(tokens, experts, k)), dtype=torch.uint8,
+                       device=device)
+
+
+def alloc_act_checkpoint(rows: int, cols: int, gated: bool = True, device="cuda") -> tuple:
+    """(q, sf) of mxg_gated_act: E4M3 bytes of gate and up side by side, and their scales."""
+    parts = 2 if gated else 1
+    return (torch.empty((rows, parts * cols), dtype=torch.uint8, device=device),
+            torch.empty((rows, parts * _act_blocks(cols)), dtype=torch.uint8, device=device))
