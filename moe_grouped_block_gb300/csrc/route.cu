@@ -23,18 +23,27 @@
 
 namespace mxg {
 
-constexpr int kRouteThreads = 512;
-constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kMaxExperts = 1024;
-constexpr int kMaxChunks = 304;
+constexpr int kMaxChunks = 152;
 constexpr uint32_t kNoLogit = 0x007FFFFFu;  // the key of -infinity: it and all below are not chosen
-constexpr int kBufWords = 4096;
+constexpr int kOneItems = 4096;  // choices of a batch that one CTA finishes
 
-// The workspace: chunk by chunk, tokens per expert, sums of p, tokens that take part.
+// Threads of a CTA: of the kernels that work on a whole batch alone, and of the others.  With
+// 16 or 32 columns a lane the choice needs the registers of two or four.
+constexpr int kOneThreads = 512;
+constexpr int kManyThreads = 1024;
+constexpr int threads_of(int vpl, bool one) {
+  const int most = vpl > 16 ? 256 : (vpl > 8 ? 512 : 1024);
+  return one && most > kOneThreads ? kOneThreads : most;
+}
+
+// The workspace: chunk by chunk, tokens per expert, sums of p, tokens that take part.  A
+// chunk's experts are padded to a multiple of 4, to be read 16 bytes at a time.
 struct RouteWs {
-  int32_t* hist;  // [chunks][experts]
-  float* psum;    // [chunks][experts]
+  int32_t* hist;  // [chunks][pitch]
+  float* psum;    // [chunks][pitch]
   int32_t* live;  // [chunks]
+  int32_t pitch;
 };
 
 // What the second half needs to know.
@@ -53,33 +62,38 @@ struct RowPlan {
   float balance;
 };
 
+constexpr int kBufWords = 8192;
+
+// BUF: words for sums by part or by warp, and for tokens per expert by warp.
+template <int BUF>
 struct RouteShared {
-  uint32_t buf[kBufWords];  // sums of p by warp, then tokens per expert by warp
+  uint4 buf[BUF / 4];
   int32_t hist[kMaxExperts];
   float psum[kMaxExperts];
-  uint32_t total[kMaxExperts], before[kMaxExperts], start[kMaxExperts];
-  uint32_t warp_sum[kRouteWarps];
-  float warp_f[kRouteWarps];
+  uint32_t start[kMaxExperts];
+  uint32_t warp_sum[32], warp_total[32];
+  float warp_f[32];
   int32_t live;
-  uint32_t sum;
 };
 
-// Logits as unsigned integers of the same order: -0 as 0, NaN above all.
+// Logits as unsigned integers of the same order: -0 as 0, NaN above all (an addition
+// gives the NaN of positive sign).
 __device__ __forceinline__ uint32_t logit_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);
-  if (v != v) return 0xFFFFFFFFu;
   return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_logit(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
 
-// sigmoid(l) e^-m, with m <= 0: shares of a token whose sigmoids all underflow are still
-// right (m the largest logit where that is negative).
+// sigmoid(l), and sigmoid(l) e^-m with m < 0: shares of a token whose sigmoids all underflow
+// are still right (m the largest logit where that is negative, so l <= m).
+__device__ __forceinline__ float sigmoid(float l) {
+  const float e = exp_approx(-fabsf(l));
+  return (l < 0.0f ? e : 1.0f) * rcp_approx(1.0f + e);
+}
 __device__ __forceinline__ float sigmoid_scaled(float l, float m) {
-  const float e = __expf(-fabsf(l));
-  const float num = l >= 0.0f ? 1.0f : (m < 0.0f ? __expf(l - m) : e);
-  return l != l ? l : __fdividef(num, 1.0f + e);
+  return m < 0.0f ? exp_approx(l - m) * rcp_approx(1.0f + exp_approx(l)) : sigmoid(l);
 }
 
 template <int LPT>
@@ -139,77 +153,130 @@ struct LogitRow {
 };
 
 // ---------------------------------------------------------------- rows
-// Everything that needs the whole batch's counts, by the CTA of chunk c.  `hist`, `psum`
-// and `live` are the chunks' (this CTA's own where there is one chunk).  The first CTA
-// writes counts and group_ws, the last one slope and loss.
-__device__ void finish_chunk(const RowPlan& p, RouteShared& sh, const int32_t* hist,
-                             const float* psum, const int32_t* live, int c) {
+// Sums over the chunks of `n` columns, `pitch` apart from one chunk to the next, into
+// parts of shared memory: part p, column c at [p * 4 * quads + c].  LOW: beside the sums, those
+// of the chunks below `low`, `kBufWords / 2` further on.  The parts are returned.
+template <int NT, bool LOW, typename V4, typename V>
+__device__ __forceinline__ int sum_chunks(V* to, const V* from, int pitch, int chunks, int low) {
+  const int quads = pitch / 4;
+  int wide = 1;
+  while (wide < quads) wide *= 2;
+  const int parts = min(min(NT / wide, 16), chunks);
+  const int q = threadIdx.x & (wide - 1), part = threadIdx.x / wide;
+  if (q < quads && part < parts) {
+    V4 all = {}, under = {};
+    const V4* at = reinterpret_cast<const V4*>(from) + q;
+    // ten loads at once: all of a part's where there are 16 parts
+    for (int h0 = part; h0 < chunks; h0 += 10 * parts) {
+      V4 v[10];
+#pragma unroll
+      for (int i = 0; i < 10; ++i) {
+        v[i] = V4{};
+        if (h0 + i * parts < chunks) v[i] = at[(h0 + i * parts) * quads];
+      }
+#pragma unroll
+      for (int i = 0; i < 10; ++i) {
+        all.x += v[i].x;
+        all.y += v[i].y;
+        all.z += v[i].z;
+        all.w += v[i].w;
+        if (LOW && h0 + i * parts < low) {
+          under.x += v[i].x;
+          under.y += v[i].y;
+          under.z += v[i].z;
+          under.w += v[i].w;
+        }
+      }
+    }
+    V4* out = reinterpret_cast<V4*>(to) + part * quads + q;
+    out[0] = all;
+    if (LOW) out[kBufWords / 8] = under;
+  }
+  return parts;
+}
+
+// Everything that needs the whole batch's counts, by the CTA of chunk c, of NT threads
+// (at least as many as experts, but for ONE).  ONE: this CTA has all tokens, whose counts and
+// sums are in `sh`.  The first CTA writes counts and group_ws; the last one, which has no
+// tokens where there are several, slope and loss.
+template <int NT, bool ONE, int BUF>
+__device__ __forceinline__ void finish_chunk(const RowPlan& p, RouteShared<BUF>& sh,
+                                             const RouteWs& ws, const int32_t* expert, int c) {
+  static_assert(ONE || BUF == kBufWords, "sums of chunks take two halves of a whole buffer");
+  constexpr int kPer = (kMaxExperts + NT - 1) / NT;  // experts a thread
+  constexpr int kWarps = NT / 32;
   const int tid = threadIdx.x, E = p.experts;
   const int lane = tid & 31, warp = tid >> 5;
-  int wide = 1;  // experts, as a power of two
-  while (wide < E) wide *= 2;
-  const int parts = max(1, min(min(kRouteThreads / wide, 16), p.chunks));
-  uint32_t* part_total = sh.buf;
-  uint32_t* part_before = sh.buf + kBufWords / 2;
-  // tokens of each expert, in all chunks and in those before this one
-  for (int i = tid; i < parts * wide; i += kRouteThreads) {
-    const int e = i & (wide - 1), part = i / wide;
-    uint32_t total = 0, before = 0;
-    if (e < E) {
-#pragma unroll 8
-      for (int h = part; h < p.chunks; h += parts) {
-        const uint32_t v = static_cast<uint32_t>(hist[static_cast<int64_t>(h) * E + e]);
-        total += v;
-        before += h < c ? v : 0u;
-      }
-    }
-    part_total[i] = total;
-    part_before[i] = before;
-  }
-  __syncthreads();
-  // starts of the padded groups: two experts a thread, a scan over the warp and the CTA
-  uint32_t size[2], total[2];
+  uint32_t* buf = reinterpret_cast<uint32_t*>(sh.buf);
+  // this chunk's choices: as many warps as the counts have room for, each a run of them, of which
+  // the first kHeld of a lane are asked for now
+  constexpr int kHeld = 4;
+  const int64_t begin = static_cast<int64_t>(c) * p.per;
+  const int64_t end = min(begin + p.per, p.tokens);
+  const int32_t items =
+      begin < end && p.row_of != nullptr ? static_cast<int32_t>((end - begin) * p.k) : 0;
+  const int warps = min(min(kWarps, BUF / E), (items + 31) / 32);
+  const int32_t run = warps == 0 ? 0 : ((items + warps - 1) / warps + 31) / 32 * 32;
+  const int32_t from = min(warp * run, items), to = warp < warps ? min(from + run, items) : from;
+  auto choice = [&](int i) {
+    const int32_t e = i < to ? expert[i] : -1;
+    return static_cast<uint32_t>(e) < static_cast<uint32_t>(E) ? e : -1;
+  };
+  int32_t held[kHeld];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int e = 2 * tid + i;
-    uint32_t t = 0, b = 0;
-    if (e < E) {
-      for (int part = 0; part < parts; ++part) {
-        t += part_total[part * wide + e];
-        b += part_before[part * wide + e];
-      }
-      sh.total[e] = t;
-      sh.before[e] = b;
-    }
-    total[i] = t;
-    const uint32_t a = static_cast<uint32_t>(p.align);
-    size[i] = a == 1 ? t : (t + a - 1) / a * a;
+  for (int i = 0; i < kHeld; ++i) held[i] = choice(from + 32 * i + lane);
+  // tokens of each expert, in all chunks and in those before this one
+  int parts = 1;
+  if (!ONE) {
+    parts = sum_chunks<NT, true, uint4>(buf, reinterpret_cast<const uint32_t*>(ws.hist), ws.pitch,
+                                        p.chunks, c);
+    __syncthreads();
   }
-  uint32_t incl = size[0] + size[1], sum = total[0] + total[1];
+  // starts of the padded groups: a scan over a thread's experts, the warp and the CTA
+  uint32_t size[kPer], total[kPer], before[kPer], incl = 0, sum = 0;
+  const uint32_t a = static_cast<uint32_t>(p.align);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = kPer * tid + i;
+    total[i] = before[i] = 0;
+    if (e < E) {
+      if (ONE) {
+        total[i] = static_cast<uint32_t>(sh.hist[e]);
+      } else {
+#pragma unroll
+        for (int part = 0; part < 16; ++part) {
+          if (part >= parts) break;
+          total[i] += buf[part * ws.pitch + e];
+          before[i] += buf[kBufWords / 2 + part * ws.pitch + e];
+        }
+      }
+    }
+    size[i] = a == 1 ? total[i] : (total[i] + a - 1) / a * a;
+    incl += size[i];
+    sum += total[i];
+  }
+  const uint32_t mine_size = incl;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
     if (lane >= d) incl += v;
   }
   sum = __reduce_add_sync(0xFFFFFFFFu, sum);
-  __syncthreads();  // part_total has been read
   if (lane == 31) {
     sh.warp_sum[warp] = incl;
-    sh.buf[warp] = sum;
+    sh.warp_total[warp] = sum;
   }
   __syncthreads();
-  uint32_t ahead = 0, all = 0;
+  const uint32_t w_size = lane < kWarps ? sh.warp_sum[lane] : 0u;
+  const uint32_t ahead = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w_size : 0u);
+  const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? sh.warp_total[lane] : 0u);
+  uint32_t start = ahead + incl - mine_size;
 #pragma unroll
-  for (int w = 0; w < kRouteWarps; ++w) {
-    if (w < warp) ahead += sh.warp_sum[w];
-    all += sh.buf[w];
-  }
-  uint32_t start = ahead + incl - size[0] - size[1];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int e = 2 * tid + i;
+  for (int i = 0; i < kPer; ++i) {
+    const int e = kPer * tid + i;
     if (e < E) {
-      sh.start[e] = start;
+      sh.start[e] = start + before[i];  // of this chunk's tokens
+      if (!ONE) sh.hist[e] = static_cast<int32_t>(total[i]);
       if (c == 0) {
         if (p.counts != nullptr) p.counts[e] = static_cast<int32_t>(total[i]);
         if (p.group_ws != nullptr) {
@@ -227,35 +294,31 @@ __device__ void finish_chunk(const RowPlan& p, RouteShared& sh, const int32_t* h
 
   if (c == static_cast<int>(gridDim.x) - 1 && (p.loss != nullptr || p.slope != nullptr)) {
     float* part_p = reinterpret_cast<float*>(sh.buf);
-    int n = 0;
-    for (int h = tid; h < p.chunks; h += kRouteThreads) n += live[h];
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    if (p.loss != nullptr) {
-      for (int i = tid; i < parts * wide; i += kRouteThreads) {
-        const int e = i & (wide - 1), part = i / wide;
-        float v = 0.0f;
-        if (e < E)
-#pragma unroll 8
-          for (int h = part; h < p.chunks; h += parts) v += psum[static_cast<int64_t>(h) * E + e];
-        part_p[i] = v;
-      }
+    int tokens = 0, p_parts = 1;
+    if (ONE) {
+      tokens = sh.live;
+    } else {
+      for (int h = lane; h < p.chunks; h += 32) tokens += ws.live[h];
+      tokens = __reduce_add_sync(0xFFFFFFFFu, tokens);
+      if (p.loss != nullptr)
+        p_parts = sum_chunks<NT, false, float4>(part_p, ws.psum, ws.pitch, p.chunks, 0);
+      __syncthreads();
     }
-    if (lane == 0) sh.warp_sum[warp] = static_cast<uint32_t>(n);
-    __syncthreads();
-    uint32_t tokens = 0;
-#pragma unroll
-    for (int w = 0; w < kRouteWarps; ++w) tokens += sh.warp_sum[w];
     // all and tokens are 0 together
-    const float unit = all == 0 ? 0.0f
-                                : p.balance * static_cast<float>(E) / static_cast<float>(tokens);
+    const float unit =
+        all == 0 ? 0.0f : p.balance * static_cast<float>(E) / static_cast<float>(tokens);
     float mine = 0.0f;
-    for (int e = tid; e < E; e += kRouteThreads) {
-      const float s = all == 0 ? 0.0f
-                               : unit * (static_cast<float>(sh.total[e]) / static_cast<float>(all));
+    for (int e = tid; e < E; e += NT) {
+      const float s =
+          all == 0 ? 0.0f : unit * (static_cast<float>(sh.hist[e]) / static_cast<float>(all));
       if (p.slope != nullptr) p.slope[e] = s;
       if (p.loss != nullptr) {
         float v = 0.0f;
-        for (int part = 0; part < parts; ++part) v += part_p[part * wide + e];
+        if (ONE) {
+          v = sh.psum[e];
+        } else {
+          for (int part = 0; part < p_parts; ++part) v += part_p[part * ws.pitch + e];
+        }
         mine += s * v;
       }
     }
@@ -263,178 +326,314 @@ __device__ void finish_chunk(const RowPlan& p, RouteShared& sh, const int32_t* h
       mine = team_add<32>(mine);
       if (lane == 0) sh.warp_f[warp] = mine;
       __syncthreads();
-      if (tid == 0) {
-        float v = 0.0f;
-        for (int w = 0; w < kRouteWarps; ++w) v += sh.warp_f[w];
-        *p.loss = v;
+      if (warp == 0) {
+        const float v = team_add<32>(lane < kWarps ? sh.warp_f[lane] : 0.0f);
+        if (lane == 0) *p.loss = v;
       }
     }
-    __syncthreads();
   }
-  if (p.row_of == nullptr) return;
 
-  // rows: as many warps as the counts have room for, each a run of the chunk's choices
-  const int warps = min(kRouteWarps, kBufWords / wide);
-  uint32_t* mine = sh.buf + warp * E;
-  const int64_t begin = static_cast<int64_t>(c) * p.per;
-  const int64_t end = min(begin + p.per, p.tokens);
-  const int32_t items = begin < end ? static_cast<int32_t>((end - begin) * p.k) : 0;
-  const int32_t run = ((items + warps - 1) / warps + 31) / 32 * 32;
-  const int32_t* expert = p.expert + begin * p.k;
+  if (items == 0) return;
+  // A choice's place among its expert's: those of earlier lanes, of earlier rounds of the
+  // warp (both now), then of earlier warps, chunks and experts.
+  uint32_t* mine = buf + warp * E;
   int32_t* row_of = p.row_of + begin * p.k;
-  const int32_t from = min(warp * run, items), to = warp < warps ? min(from + run, items) : from;
-  for (int i = tid; i < warps * E; i += kRouteThreads) sh.buf[i] = 0;
-  __syncthreads();
-  for (int i = from + lane; i < to; i += 32) {
-    const int32_t e = expert[i];
-    if (static_cast<uint32_t>(e) < static_cast<uint32_t>(E)) atomicAdd(&mine[e], 1u);
-  }
-  __syncthreads();
-  for (int e = tid; e < E; e += kRouteThreads) {
-    uint32_t at = sh.start[e] + sh.before[e];
-    for (int w = 0; w < warps; ++w) {
-      const uint32_t n = sh.buf[w * E + e];
-      sh.buf[w * E + e] = at;
-      at += n;
-    }
-  }
-  __syncthreads();
-  for (int base = from; base < to; base += 32) {
-    const int i = base + lane;
-    int32_t e = i < to ? expert[i] : -1;
-    if (static_cast<uint32_t>(e) >= static_cast<uint32_t>(E)) e = -1;
+  if (warp < warps)
+    for (int i = lane; i < E; i += 32) mine[i] = 0;
+  __syncwarp();
+  auto place = [&](int32_t e) {
     const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
     const uint32_t rank = __popc(same & ((1u << lane) - 1u));
-    uint32_t row = 0;
-    if (e >= 0) row = mine[e] + rank;
+    uint32_t at = rank;
+    if (e >= 0) at += mine[e];
     __syncwarp();
     if (e >= 0 && rank == 0) mine[e] += __popc(same);
     __syncwarp();
+    return at;
+  };
+  uint32_t at[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    at[i] = 0;
+    if (from + 32 * i < to) at[i] = place(held[i]);
+  }
+  for (int base = from + 32 * kHeld; base < to; base += 32) place(choice(base + lane));
+  __syncthreads();
+  for (int e = tid; e < E; e += NT) {
+    uint32_t first = sh.start[e];
+#pragma unroll 8
+    for (int w = 0; w < warps; ++w) {
+      const uint32_t n = buf[w * E + e];
+      buf[w * E + e] = first;
+      first += n;
+    }
+  }
+  __syncthreads();
+  auto write = [&](int i, int32_t e, uint32_t row) {
     if (i < to) row_of[i] = e >= 0 && row < p.capacity ? static_cast<int32_t>(row) : -1;
+  };
+  const bool more = to - from > 32 * kHeld;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (from + 32 * i < to)
+      write(from + 32 * i + lane, held[i], held[i] >= 0 ? mine[held[i]] + at[i] : 0u);
+  if (!more) return;
+  // the others' places are found again, after those of the held ones
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) place(held[i]);
+  for (int base = from + 32 * kHeld; base < to; base += 32) {
+    const int32_t e = choice(base + lane);
+    write(base + lane, e, place(e));
   }
 }
 
-__global__ void __launch_bounds__(kRouteThreads)
+__global__ void __launch_bounds__(kManyThreads)
     route_finish_kernel(const RowPlan p, const RouteWs ws) {
-  __shared__ RouteShared sh;
+  __shared__ RouteShared<kBufWords> sh;
   grid_wait_for_previous();
-  finish_chunk(p, sh, ws.hist, ws.psum, ws.live, blockIdx.x);
+  const int c = static_cast<int>(blockIdx.x);
+  finish_chunk<kManyThreads, false>(p, sh, ws, p.expert + c * p.per * p.k, c);
 }
 
 // Tokens per expert of a chunk, for experts chosen elsewhere.
-template <bool ONE>
-__global__ void __launch_bounds__(kRouteThreads)
-    route_count_kernel(const RowPlan p, const RouteWs ws) {
-  __shared__ RouteShared sh;
+template <int NT, bool ONE>
+__global__ void __launch_bounds__(NT) route_count_kernel(const RowPlan p, const RouteWs ws) {
+  __shared__ RouteShared<ONE ? kBufWords / 2 : kBufWords> sh;
   const int tid = threadIdx.x, c = blockIdx.x, E = p.experts;
   if (!ONE) grid_launch_dependents();
-  for (int e = tid; e < E; e += kRouteThreads) sh.hist[e] = 0;
+  for (int e = tid; e < E; e += NT) sh.hist[e] = 0;
   __syncthreads();
   const int64_t begin = c * p.per, end = min(begin + p.per, p.tokens);
   const int32_t items = begin < end ? static_cast<int32_t>((end - begin) * p.k) : 0;
-  for (int i = tid; i < items; i += kRouteThreads) {
-    const int32_t e = p.expert[begin * p.k + i];
+  const int32_t* expert = p.expert + begin * p.k;
+  for (int i = tid; i < items; i += NT) {
+    const int32_t e = expert[i];
     if (static_cast<uint32_t>(e) < static_cast<uint32_t>(E)) atomicAdd(&sh.hist[e], 1);
   }
   __syncthreads();
   if (ONE) {
-    finish_chunk(p, sh, sh.hist, nullptr, nullptr, 0);
+    finish_chunk<NT, true>(p, sh, ws, expert, 0);
   } else {
-    for (int e = tid; e < E; e += kRouteThreads) ws.hist[static_cast<int64_t>(c) * E + e] = sh.hist[e];
+    for (int e = tid; e < ws.pitch; e += NT)
+      ws.hist[static_cast<int64_t>(c) * ws.pitch + e] = e < E ? sh.hist[e] : 0;
   }
 }
 
 // ---------------------------------------------------------------- the choice
-template <typename T, int LPT, int VPL, bool ONE>
-__global__ void __launch_bounds__(kRouteThreads)
+// A team's k best keys: lane j keeps the j-th, with its column.
+struct Chosen {
+  uint32_t key;  // 0 where there is none
+  int expert;    // -1 there
+};
+
+// One after the other: the maximum over the team, and the lowest lane that holds it.  The keys
+// are used up.
+template <int LPT, int VPL>
+__device__ __forceinline__ Chosen choose_in_turn(uint32_t (&key)[VPL], int k, int gl) {
+  const int lane = threadIdx.x & 31, c0 = gl * VPL;
+  Chosen r = {0u, -1};
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) best = max(best, key[i]);
+    const uint32_t m = team_max<LPT>(best);
+    int slot = 0;
+#pragma unroll
+    for (int i = VPL - 1; i >= 0; --i)
+      if (key[i] == m) slot = i;
+    const uint32_t holds = __ballot_sync(0xFFFFFFFFu, best == m) >> (lane & ~(LPT - 1));
+    const int who = __ffs(holds) - 1;  // the team's lowest lane of them
+    const int e = __shfl_sync(0xFFFFFFFFu, c0 + slot, who, LPT);
+    if (gl == who)
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (i == slot) key[i] = 0u;
+    if (gl == j && m > kNoLogit) {
+      r.expert = e;
+      r.key = m;
+    }
+  }
+  return r;
+}
+
+// By counting, among the few keys that can be of the best.  The lanes form `groups` groups, at
+// least k of them, so none below the least of the groups' maxima is chosen (above 8, where that
+// leaves too many, none below the k-th largest of the lanes' maxima).  The others -- for 8 of
+// 64 some 15, for 8 of 256 some 17 -- are laid out in shared memory in the order of their
+// columns, and the lanes count those above each.  Where there are more than kMost, one after
+// the other after all.  `slots` has room for the warp's teams.
+constexpr int kMost = 31;  // (a stride that keeps the teams' slots on different banks)
+
+template <int LPT, int VPL>
+__device__ __forceinline__ Chosen choose_by_rank(uint32_t (&key)[VPL], int k, int gl, int groups,
+                                                 uint2* slots) {
+  constexpr int kRounds = (kMost + LPT - 1) / LPT;
+  const int lane = threadIdx.x & 31;
+  uint32_t bound = key[0];
+#pragma unroll
+  for (int i = 1; i < VPL; ++i) bound = max(bound, key[i]);
+  if (LPT == 32 && k > 8) {
+    uint32_t best = bound;
+    bound = __reduce_max_sync(0xFFFFFFFFu, best);
+    for (int j = 1; j < k; ++j) {
+      if (best == bound) best = 0u;  // all alike at once: the bound is only lower for it
+      bound = __reduce_max_sync(0xFFFFFFFFu, best);
+    }
+  } else {
+#pragma unroll
+    for (int d = LPT / 2; d > 0; d >>= 1) {
+      const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, bound, d);
+      bound = d >= groups ? max(bound, other) : min(bound, other);
+    }
+  }
+  bound = max(bound, kNoLogit + 1u);
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) n += key[i] >= bound ? 1 : 0;
+  int at = n;
+#pragma unroll
+  for (int d = 1; d < LPT; d <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, at, d, LPT);
+    if (gl >= d) at += v;
+  }
+  const int all = __shfl_sync(0xFFFFFFFFu, at, LPT - 1, LPT);
+  const int most = __reduce_max_sync(0xFFFFFFFFu, all);
+  if (most > kMost) return choose_in_turn<LPT, VPL>(key, k, gl);
+  uint2* team = slots + lane / LPT * kMost;
+  uint2* to = team + (at - n);
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (key[i] >= bound) *to++ = make_uint2(key[i], static_cast<uint32_t>(gl * VPL + i));
+  __syncwarp();
+  uint2 mine[kRounds];
+  int above[kRounds];
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    mine[r] = make_uint2(0xFFFFFFFFu, 0u);
+    if (r * LPT + gl < all) mine[r] = team[r * LPT + gl];
+    above[r] = 0;
+  }
+#pragma unroll 4
+  for (int j = 0; j < most; ++j) {
+    const uint32_t other = j < all ? team[j].x : 0u;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) above[r] += other > mine[r].x ? 1 : 0;
+  }
+  // without equal keys the counts are 0, 1, 2, ...
+  int sum = 0;
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) sum += above[r];
+#pragma unroll
+  for (int d = LPT / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+  if (__any_sync(0xFFFFFFFFu, 2 * sum != all * (all - 1))) {
+    for (int j = 0; j < all; ++j)
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r)
+        above[r] += team[j].x == mine[r].x && j < r * LPT + gl ? 1 : 0;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r)
+    if (r * LPT + gl < all && above[r] < k) team[above[r]] = mine[r];
+  __syncwarp();
+  Chosen c = {0u, -1};
+  if (gl < min(all, k)) {
+    const uint2 v = team[gl];
+    c.key = v.x;
+    c.expert = static_cast<int>(v.y);
+  }
+  __syncwarp();  // the slots are written again for the next token
+  return c;
+}
+
+template <typename T, int LPT, int VPL, int NT, bool ONE>
+__global__ void __launch_bounds__(NT)
     route_kernel(const mxg_route_t d, const RowPlan p, const RouteWs ws, int vec) {
-  __shared__ RouteShared sh;
+  constexpr int kTeams = NT / LPT, kWarps = NT / 32;
+  constexpr int kBuf = ONE ? kBufWords / 2 : kBufWords;
+  __shared__ RouteShared<kBuf> sh;
+  __shared__ int32_t choices[ONE ? kOneItems : 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
   const int gl = lane & (LPT - 1), c0 = gl * VPL, E = d.experts, k = d.k;
-  constexpr int kTeams = kRouteThreads / LPT;
   if (!ONE) grid_launch_dependents();
-  for (int e = tid; e < E; e += kRouteThreads) sh.hist[e] = 0;
+  for (int e = tid; e < E; e += NT) sh.hist[e] = 0;
   if (tid == 0) sh.live = 0;
   __syncthreads();
 
-  const int64_t begin = c * p.per, end = min(begin + p.per, d.tokens);
-  const T* logits = static_cast<const T*>(d.logits);
+  const int64_t begin = c * p.per;
+  const int count = static_cast<int>(max(min(begin + p.per, d.tokens) - begin, int64_t{0}));
+  const T* row = static_cast<const T*>(d.logits) + (begin + tid / LPT) * d.ld;
+  const uint8_t* mask = d.mask != nullptr ? d.mask + begin : nullptr;
+  int32_t* const expert = d.expert + begin * k;
+  float* const weight = d.weight + begin * k;
   const bool softmax = d.score == MXG_SCORE_SOFTMAX;
   const bool shares = d.loss != nullptr, whole = shares || (softmax && !d.normalize);
+  int groups = 1;
+  while (groups < k) groups *= 2;
+  // a few are found sooner in turn; and groups without columns have no maximum
+  const bool by_rank = LPT >= 8 && k > 3 && (LPT == 32 || k <= 8) && groups * VPL <= E;
   float acc[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
   int live = 0;
-  int64_t t = begin + tid / LPT;
+  int t = tid / LPT;  // in the chunk
   LogitRow<T, VPL> next;
   bool next_on = false;
-  auto fetch = [&](int64_t at) {
-    next_on = at < end && (d.mask == nullptr || d.mask[at] != 0);
-    if (at < end) next.load(logits + at * d.ld, c0, E, vec != 0);
+  auto fetch = [&](int at) {
+    next_on = at < count && (mask == nullptr || mask[at] != 0);
+    if (at < count) next.load(row, c0, E, vec != 0);
+    row += kTeams * d.ld;
   };
   fetch(t);
-  for (int64_t base = begin; base < end; base += kTeams, t += kTeams) {
+  for (int base = 0; base < count; base += kTeams, t += kTeams) {
     float v[VPL];
     next.values(v);
     const bool on = next_on;
     fetch(t + kTeams);
     uint32_t key[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = on && c0 + i < E ? logit_key(v[i]) : 0u;
-    // the k best: lane j of the team keeps the j-th
-    uint32_t my_key = 0, top = 0;
-    int my_e = -1;
-    for (int j = 0; j < k; ++j) {
-      uint32_t best = key[0];
-#pragma unroll
-      for (int i = 1; i < VPL; ++i) best = max(best, key[i]);
-      const uint32_t m = team_max<LPT>(best);
-      if (j == 0) top = m;
-      int slot = 0;
-#pragma unroll
-      for (int i = VPL - 1; i >= 0; --i)
-        if (key[i] == m) slot = i;
-      const uint32_t holds = __ballot_sync(0xFFFFFFFFu, best == m) >> (lane & ~(LPT - 1));
-      const int who = __ffs(holds) - 1;  // the team's lowest lane of them
-      const int e = __shfl_sync(0xFFFFFFFFu, c0 + slot, who, LPT);
-      if (gl == who)
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (i == slot) key[i] = 0u;
-      if (gl == j && m > kNoLogit) {
-        my_e = e;
-        my_key = m;
-      }
-    }
-    const bool taken = top > kNoLogit;
-    const float best = key_logit(top), mine = key_logit(my_key);
-    const float shift = softmax ? best : fminf(best, 0.0f);
+    for (int i = 0; i < VPL; ++i) key[i] = on ? logit_key(v[i]) : 0u;
+    Chosen best;
+    if (LPT >= 8 && by_rank)
+      best = choose_by_rank<LPT, VPL>(key, k, gl, groups, reinterpret_cast<uint2*>(sh.buf) +
+                                                              warp * (kMost * 32 / LPT));
+    else
+      best = choose_in_turn<LPT, VPL>(key, k, gl);
+    const float mine = key_logit(best.key);
+    const float top = __shfl_sync(0xFFFFFFFFu, mine, 0, LPT);
+    const bool taken = __shfl_sync(0xFFFFFFFFu, best.expert, 0, LPT) >= 0;
+    const float shift = softmax ? top : fminf(top, 0.0f);
     float sum = 0.0f, s[VPL];
     if (whole) {
+      if (softmax) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        s[i] = softmax ? __expf(v[i] - shift) : sigmoid_scaled(v[i], shift);
-        sum += s[i];
+        for (int i = 0; i < VPL; ++i) s[i] = exp_approx(v[i] - shift);
+      } else if (shift < 0.0f) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) s[i] = sigmoid_scaled(v[i], shift);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) s[i] = sigmoid(v[i]);
       }
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) sum += s[i];
       sum = team_add<LPT>(sum);
     }
     float w = 0.0f;
-    if (my_e >= 0) {
-      if (softmax)
-        w = __expf(mine - shift);
-      else
-        w = sigmoid_scaled(mine, d.normalize ? shift : 0.0f);
-    }
+    if (best.expert >= 0)
+      w = softmax ? exp_approx(mine - shift) : sigmoid_scaled(mine, d.normalize ? shift : 0.0f);
     const float chosen = d.normalize ? team_add<LPT>(w) : (softmax ? sum : 1.0f);
-    if (t < end && gl < k) {
-      d.expert[t * k + gl] = my_e;
-      d.weight[t * k + gl] = my_e >= 0 ? d.scale * (w / chosen) : 0.0f;
+    if (t < count && gl < k) {
+      expert[t * k + gl] = best.expert;
+      weight[t * k + gl] = best.expert >= 0 ? d.scale * (w / chosen) : 0.0f;
+      if (ONE) choices[t * k + gl] = best.expert;
     }
-    if (my_e >= 0) atomicAdd(&sh.hist[my_e], 1);
+    if (best.expert >= 0) atomicAdd(&sh.hist[best.expert], 1);
     if (taken) {
       if (gl == 0) ++live;
       if (shares) {
-        const float r = 1.0f / sum;
+        const float r = rcp_approx(sum);
 #pragma unroll
         for (int i = 0; i < VPL; ++i) acc[i] = fmaf(s[i], r, acc[i]);
       }
@@ -444,16 +643,15 @@ __global__ void __launch_bounds__(kRouteThreads)
   // the chunk's sums, in a fixed order: teams of a warp, then warps
   live = __reduce_add_sync(0xFFFFFFFFu, live);
   if (lane == 0 && live != 0) atomicAdd(&sh.live, live);
+  __syncthreads();  // the warps' slots give way to the sums
   if (shares) {
     float* rows = reinterpret_cast<float*>(sh.buf);
-    int wide = 1;
-    while (wide < E) wide *= 2;
-    const int fit = min(kRouteWarps, kBufWords / wide);
+    const int fit = min(kWarps, kBuf / E);
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
 #pragma unroll
       for (int o = LPT; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], o);
-    for (int w0 = 0; w0 < kRouteWarps; w0 += fit) {
+    for (int w0 = 0; w0 < kWarps; w0 += fit) {
       if (warp >= w0 && warp < w0 + fit && lane < LPT) {
         float* row = rows + (warp - w0) * E;
 #pragma unroll
@@ -462,20 +660,22 @@ __global__ void __launch_bounds__(kRouteThreads)
       }
       __syncthreads();
     }
-    for (int e = tid; e < E; e += kRouteThreads) {
+    for (int e = tid; e < E; e += NT) {
       float v = 0.0f;
+#pragma unroll 4
       for (int w = 0; w < fit; ++w) v += rows[w * E + e];
-      sh.psum[e] = v;
+      if (ONE)
+        sh.psum[e] = v;
+      else
+        ws.psum[static_cast<int64_t>(c) * ws.pitch + e] = v;
     }
   }
-  __syncthreads();
   if (ONE) {
-    finish_chunk(p, sh, sh.hist, sh.psum, &sh.live, 0);
+    __syncthreads();
+    finish_chunk<NT, true>(p, sh, ws, choices, 0);
   } else {
-    for (int e = tid; e < E; e += kRouteThreads) {
-      ws.hist[static_cast<int64_t>(c) * E + e] = sh.hist[e];
-      if (shares) ws.psum[static_cast<int64_t>(c) * E + e] = sh.psum[e];
-    }
+    for (int e = tid; e < ws.pitch; e += NT)
+      ws.hist[static_cast<int64_t>(c) * ws.pitch + e] = e < E ? sh.hist[e] : 0;
     if (tid == 0) ws.live[c] = sh.live;
   }
 }
@@ -535,9 +735,9 @@ __global__ void __launch_bounds__(kGradThreads)
     if (balance || joined) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        p[i] = softmax ? __expf(v[i] - shift) : sigmoid_scaled(v[i], shift);
+        p[i] = softmax ? exp_approx(v[i] - shift) : sigmoid_scaled(v[i], shift);
         // 1 - s, without its cancellation
-        rest[i] = softmax ? 1.0f : sigmoid_scaled(-v[i], 0.0f);
+        rest[i] = softmax ? 1.0f : sigmoid(-v[i]);
         sum += p[i];
         dot = fmaf(a[i], p[i], dot);
       }
@@ -545,8 +745,8 @@ __global__ void __launch_bounds__(kGradThreads)
     }
     // the chosen experts'
     float s = 0.0f, extra = 0.0f;
-    const float other = softmax ? 1.0f : sigmoid_scaled(-l, 0.0f);
-    if (e >= 0) s = softmax ? __expf(l - shift) : sigmoid_scaled(l, d.normalize ? shift : 0.0f);
+    const float other = softmax ? 1.0f : sigmoid(-l);
+    if (e >= 0) s = softmax ? exp_approx(l - shift) : sigmoid_scaled(l, d.normalize ? shift : 0.0f);
     if (d.normalize) {
       const float chosen = team_add<LPT>(s);
       const float q = e >= 0 ? s / chosen : 0.0f;
@@ -617,26 +817,36 @@ int lanes_per_token(int experts, int k) {
   return lanes;
 }
 
+// Columns a lane.
+int columns_per_lane(int experts) { return experts > 512 ? 32 : (experts > 256 ? 16 : 8); }
+
 struct Chunks {
   int n;
   int64_t per;  // tokens each
 };
 
-// At least a pass of a CTA's teams a chunk.
+// One CTA up to four passes of its teams (a second kernel costs more than three of them),
+// else a pass at least a CTA.
 Chunks chunks_of(int64_t tokens, int experts, int k) {
-  const int64_t pass = kRouteThreads / lanes_per_token(experts, k);
-  const int64_t n = std::max<int64_t>(1, std::min<int64_t>(kMaxChunks, (tokens + pass - 1) / pass));
+  const int lanes = lanes_per_token(experts, k), vpl = columns_per_lane(experts);
+  if (tokens <= 4 * (threads_of(vpl, true) / lanes) && tokens * k <= kOneItems)
+    return {1, std::max<int64_t>(1, tokens)};
+  const int64_t pass = threads_of(vpl, false) / lanes;
+  const int64_t n = std::min<int64_t>(kMaxChunks, (tokens + pass - 1) / pass);
   Chunks c;
-  c.per = std::max<int64_t>(1, (tokens + n - 1) / n);
-  c.n = static_cast<int>(std::max<int64_t>(1, (tokens + c.per - 1) / c.per));
+  c.per = (tokens + n - 1) / n;
+  c.n = static_cast<int>(std::max<int64_t>(2, (tokens + c.per - 1) / c.per));
   return c;
 }
 
+int pitch_of(int experts) { return (experts + 3) / 4 * 4; }
+
 RouteWs carve(void* ws, int chunks, int experts) {
   RouteWs w;
+  w.pitch = pitch_of(experts);
   w.hist = static_cast<int32_t*>(ws);
-  w.psum = reinterpret_cast<float*>(w.hist + static_cast<int64_t>(chunks) * experts);
-  w.live = reinterpret_cast<int32_t*>(w.psum + static_cast<int64_t>(chunks) * experts);
+  w.psum = reinterpret_cast<float*>(w.hist + static_cast<int64_t>(chunks) * w.pitch);
+  w.live = reinterpret_cast<int32_t*>(w.psum + static_cast<int64_t>(chunks) * w.pitch);
   return w;
 }
 
@@ -647,18 +857,19 @@ bool rows_of_16(const void* p, int64_t ld, size_t size) {
 cudaError_t launch_finish(const RowPlan& p, const RouteWs& ws, cudaStream_t stream, int* launches) {
   ++*launches;
   return launch_after(true, route_finish_kernel,
-                      static_cast<unsigned>(p.row_of != nullptr ? p.chunks : 1), kRouteThreads, 0,
-                      stream, p, ws);
+                      static_cast<unsigned>(p.row_of != nullptr ? p.chunks + 1 : 1), kManyThreads,
+                      0, stream, p, ws);
 }
 
 template <typename T, int LPT, int VPL>
 cudaError_t run_route(const mxg_route_t& d, const RowPlan& p, const RouteWs& ws, int vec,
                       cudaStream_t stream) {
+  constexpr int kThreads = threads_of(VPL, false), kOne = threads_of(VPL, true);
   if (p.chunks == 1)
-    route_kernel<T, LPT, VPL, true><<<1, kRouteThreads, 0, stream>>>(d, p, ws, vec);
+    route_kernel<T, LPT, VPL, kOne, true><<<1, kOne, 0, stream>>>(d, p, ws, vec);
   else
-    route_kernel<T, LPT, VPL, false>
-        <<<static_cast<unsigned>(p.chunks), kRouteThreads, 0, stream>>>(d, p, ws, vec);
+    route_kernel<T, LPT, VPL, kThreads, false>
+        <<<static_cast<unsigned>(p.chunks), kThreads, 0, stream>>>(d, p, ws, vec);
   return cudaGetLastError();
 }
 
@@ -681,8 +892,8 @@ cudaError_t run_backward(const mxg_route_grad_t& d, int vec, int num_sms, cudaSt
     case 8: return CALL(T, 8, 8);                 \
     case 16: return CALL(T, 16, 8);               \
   }                                               \
-  if (d.experts <= 256) return CALL(T, 32, 8);    \
-  if (d.experts <= 512) return CALL(T, 32, 16);   \
+  if (columns_per_lane(d.experts) == 8) return CALL(T, 32, 8);   \
+  if (columns_per_lane(d.experts) == 16) return CALL(T, 32, 16); \
   return CALL(T, 32, 32);
 
 template <typename T>
@@ -708,7 +919,7 @@ cudaError_t backward_typed(const mxg_route_grad_t& d, int num_sms, cudaStream_t 
 
 size_t route_ws_bytes(int64_t tokens, int experts, int k) {
   const int64_t n = chunks_of(tokens, experts, k).n;
-  return static_cast<size_t>((n * (2 * experts + 1) * 4 + 15) / 16 * 16);
+  return n == 1 ? 16 : static_cast<size_t>((n * (2 * pitch_of(experts) + 1) * 4 + 15) / 16 * 16);
 }
 
 cudaError_t launch_route(const mxg_route_t& d, void* workspace, int32_t* status,
@@ -762,10 +973,11 @@ cudaError_t launch_route_rows(const int32_t* expert, int64_t tokens, int experts
   const RouteWs ws = carve(workspace, c.n, experts);
   ++*launches;
   if (c.n == 1) {
-    route_count_kernel<true><<<1, kRouteThreads, 0, stream>>>(p, ws);
+    route_count_kernel<kOneThreads, true><<<1, kOneThreads, 0, stream>>>(p, ws);
     return cudaGetLastError();
   }
-  route_count_kernel<false><<<static_cast<unsigned>(c.n), kRouteThreads, 0, stream>>>(p, ws);
+  route_count_kernel<kManyThreads, false>
+      <<<static_cast<unsigned>(c.n), kManyThreads, 0, stream>>>(p, ws);
   const cudaError_t e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_finish(p, ws, stream, launches);
 }

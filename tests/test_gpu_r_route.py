@@ -452,7 +452,7 @@ def test_refusals():
         with pytest.raises(ValueError):
             mxg.mxg_route(**dict(ok, **kw))
     for kw, code in ((dict(scale=NAN), 1), (dict(balance=INF), 1), (dict(workspace=None), 1),
-                     (dict(workspace=ws[:16]), 5), (dict(score=2), 1), (dict(align=0), 1),
+                     (dict(workspace=ws[:8]), 5), (dict(score=2), 1), (dict(align=0), 1),
                      (dict(expert=i32(10, 9), weight=torch.zeros(10, 9, device=DEV)), 1)):
         with pytest.raises(mxg.MxgError) as err:
             mxg.mxg_route(**dict(ok, **kw))
