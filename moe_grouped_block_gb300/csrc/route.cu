@@ -6,9 +6,9 @@
 //   loss = sum_e slope_e sum_t p_te,  slope_e = balance * E / n * counts_e / sum(counts)
 //
 // A token is worked on by a team of 1 to 32 lanes that keep its logits in registers, 8 to
-// 32 neighbouring columns a lane.  Logits are compared as integers of the same order; an
-// expert is taken out by a maximum over the team and a ballot for the lowest lane that
-// holds it.
+// 32 columns a lane in runs of 8: few lanes with many columns for large batches, where
+// instructions are the bound and those between lanes cost most, and 8 columns a lane for
+// small ones.
 //
 // The tokens are cut into chunks, one for each CTA, which leaves its chunk's tokens per
 // expert and sums of p in the workspace.  A second kernel adds these up -- each CTA the
@@ -32,9 +32,8 @@ constexpr int kOneItems = 4096;  // choices of a batch that one CTA finishes
 // 16 or 32 columns a lane the choice needs the registers of two or four.
 constexpr int kOneThreads = 512;
 constexpr int kManyThreads = 1024;
-constexpr int threads_of(int vpl, bool one) {
-  const int most = vpl > 16 ? 256 : (vpl > 8 ? 512 : 1024);
-  return one && most > kOneThreads ? kOneThreads : most;
+constexpr int threads_of(int lpt, int vpl, bool one) {
+  return lpt == 32 && vpl == 32 ? 256 : (one || vpl > 8 || lpt == 1 ? 512 : 1024);
 }
 
 // The workspace: chunk by chunk, tokens per expert, sums of p, tokens that take part.  A
@@ -96,6 +95,17 @@ __device__ __forceinline__ float sigmoid_scaled(float l, float m) {
   return m < 0.0f ? exp_approx(l - m) * rcp_approx(1.0f + exp_approx(l)) : sigmoid(l);
 }
 
+// The same and 1 - sigmoid(l), without the subtraction's cancellation.
+__device__ __forceinline__ float sigmoid_scaled(float l, float m, float& rest) {
+  if (m < 0.0f) {
+    rest = rcp_approx(1.0f + exp_approx(l));
+    return exp_approx(l - m) * rest;
+  }
+  const float e = exp_approx(-fabsf(l)), r = rcp_approx(1.0f + e), er = e * r;
+  rest = l < 0.0f ? r : er;
+  return l < 0.0f ? er : r;
+}
+
 template <int LPT>
 __device__ __forceinline__ float team_add(float v) {
 #pragma unroll
@@ -110,14 +120,20 @@ __device__ __forceinline__ uint32_t team_max(uint32_t v) {
   return v;
 }
 
-// A lane's columns of a row, as they lie in memory; -infinity past the last expert.
-template <typename T, int VPL>
+// A lane's columns of a row: runs of 8, LPT of them from one to the next.
+template <int LPT>
+__device__ __forceinline__ int column(int i, int gl) {
+  return ((i >> 3) * LPT + gl) * 8 + (i & 7);
+}
+
+// As they lie in memory; -infinity past the last expert.
+template <typename T, int LPT, int VPL>
 struct LogitRow {
   Raw8<T> raw[VPL / 8];
-  __device__ __forceinline__ void load(const T* row, int c0, int experts, bool vec) {
+  __device__ __forceinline__ void load(const T* row, int gl, int experts, bool vec) {
 #pragma unroll
     for (int i = 0; i < VPL / 8; ++i) {
-      const int c = c0 + 8 * i;
+      const int c = column<LPT>(8 * i, gl);
       if (vec && c < experts) {
         raw[i] = load8<T>(row + c);
       } else {
@@ -148,6 +164,14 @@ struct LogitRow {
       unpack8<T>(raw[i], f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[8 * i + j] = f[j];
+    }
+  }
+  // asks for the lines of a row that is loaded later
+  static __device__ __forceinline__ void ahead(const T* row, int gl, int experts) {
+#pragma unroll
+    for (int i = 0; i < VPL / 8; ++i) {
+      const int c = column<LPT>(8 * i, gl);
+      if (c < experts) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
     }
   }
 };
@@ -208,23 +232,33 @@ __device__ __forceinline__ void finish_chunk(const RowPlan& p, RouteShared<BUF>&
   const int tid = threadIdx.x, E = p.experts;
   const int lane = tid & 31, warp = tid >> 5;
   uint32_t* buf = reinterpret_cast<uint32_t*>(sh.buf);
-  // this chunk's choices: as many warps as the counts have room for, each a run of them, of which
-  // the first kHeld of a lane are asked for now
-  constexpr int kHeld = 4;
+  // this chunk's choices, 32 tokens at most a warp and round (as many warps as the counts
+  // have room for); the first kHeld of a lane are asked for now
+  constexpr int kHeld = 8;
   const int64_t begin = static_cast<int64_t>(c) * p.per;
-  const int64_t end = min(begin + p.per, p.tokens);
-  const int32_t items =
-      begin < end && p.row_of != nullptr ? static_cast<int32_t>((end - begin) * p.k) : 0;
-  const int warps = min(min(kWarps, BUF / E), (items + 31) / 32);
-  const int32_t run = warps == 0 ? 0 : ((items + warps - 1) / warps + 31) / 32 * 32;
-  const int32_t from = min(warp * run, items), to = warp < warps ? min(from + run, items) : from;
+  const int tokens_here =
+      p.row_of == nullptr ? 0 : static_cast<int>(max(min(begin + p.per, p.tokens) - begin, int64_t{0}));
+  const int warps = min(kWarps, BUF / E);
+  const int rounds = (tokens_here + 32 * warps - 1) / (32 * warps);
+  const int each = rounds == 0 ? 0 : (tokens_here + rounds * warps - 1) / (rounds * warps);
+  const int inverse = (65536 + p.k - 1) / p.k;  // i / k for i below 1024
+  int from = 0, items = 0;                      // of this warp and round
+  auto take = [&](int round) {
+    const int first = warp < warps ? min((round * warps + warp) * each, tokens_here) : 0;
+    from = first * p.k;
+    items = warp < warps ? (min(first + each, tokens_here) - first) * p.k : 0;
+  };
   auto choice = [&](int i) {
-    const int32_t e = i < to ? expert[i] : -1;
+    const int32_t e = i < items ? expert[from + i] : -1;
     return static_cast<uint32_t>(e) < static_cast<uint32_t>(E) ? e : -1;
   };
   int32_t held[kHeld];
+  auto hold = [&] {
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) held[i] = choice(from + 32 * i + lane);
+    for (int i = 0; i < kHeld; ++i) held[i] = choice(32 * i + lane);
+  };
+  take(0);
+  hold();
   // tokens of each expert, in all chunks and in those before this one
   int parts = 1;
   if (!ONE) {
@@ -333,58 +367,59 @@ __device__ __forceinline__ void finish_chunk(const RowPlan& p, RouteShared<BUF>&
     }
   }
 
-  if (items == 0) return;
-  // A choice's place among its expert's: those of earlier lanes, of earlier rounds of the
-  // warp (both now), then of earlier warps, chunks and experts.
+  // A choice's place among its expert's: those of earlier tokens of the warp, then of earlier
+  // warps, chunks and experts.  The warp's tokens of an expert are bits of a word (a token
+  // names an expert once), so their order does not depend on that of the atomics.
   uint32_t* mine = buf + warp * E;
   int32_t* row_of = p.row_of + begin * p.k;
-  if (warp < warps)
-    for (int i = lane; i < E; i += 32) mine[i] = 0;
-  __syncwarp();
-  auto place = [&](int32_t e) {
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-    const uint32_t rank = __popc(same & ((1u << lane) - 1u));
-    uint32_t at = rank;
-    if (e >= 0) at += mine[e];
-    __syncwarp();
-    if (e >= 0 && rank == 0) mine[e] += __popc(same);
-    __syncwarp();
-    return at;
-  };
-  uint32_t at[kHeld];
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    at[i] = 0;
-    if (from + 32 * i < to) at[i] = place(held[i]);
-  }
-  for (int base = from + 32 * kHeld; base < to; base += 32) place(choice(base + lane));
-  __syncthreads();
-  for (int e = tid; e < E; e += NT) {
-    uint32_t first = sh.start[e];
-#pragma unroll 8
-    for (int w = 0; w < warps; ++w) {
-      const uint32_t n = buf[w * E + e];
-      buf[w * E + e] = first;
-      first += n;
+  for (int round = 0; round < rounds; ++round) {
+    if (round > 0) {
+      __syncthreads();  // the words of the round before have been read
+      take(round);
+      hold();
     }
-  }
-  __syncthreads();
-  auto write = [&](int i, int32_t e, uint32_t row) {
-    if (i < to) row_of[i] = e >= 0 && row < p.capacity ? static_cast<int32_t>(row) : -1;
-  };
-  const bool more = to - from > 32 * kHeld;
+    if (warp < warps)
+      for (int i = lane; i < E; i += 32) mine[i] = 0;
+    __syncwarp();
+    auto bit = [&](int i) { return 1u << ((i * inverse) >> 16); };
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i)
-    if (from + 32 * i < to)
-      write(from + 32 * i + lane, held[i], held[i] >= 0 ? mine[held[i]] + at[i] : 0u);
-  if (!more) return;
-  // the others' places are found again, after those of the held ones
-  __syncwarp();
+    for (int i = 0; i < kHeld; ++i)
+      if (held[i] >= 0) atomicOr(&mine[held[i]], bit(32 * i + lane));
+    for (int i = 32 * kHeld + lane; i < items; i += 32) {
+      const int32_t e = choice(i);
+      if (e >= 0) atomicOr(&mine[e], bit(i));
+    }
+    __syncwarp();
+    uint32_t at[kHeld];
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) place(held[i]);
-  for (int base = from + 32 * kHeld; base < to; base += 32) {
-    const int32_t e = choice(base + lane);
-    write(base + lane, e, place(e));
+    for (int i = 0; i < kHeld; ++i)
+      at[i] = held[i] < 0 ? 0u : __popc(mine[held[i]] & (bit(32 * i + lane) - 1u));
+    // (more than 8 choices a token: their places wait in row_of)
+    for (int i = 32 * kHeld + lane; i < items; i += 32) {
+      const int32_t e = choice(i);
+      row_of[from + i] = e < 0 ? 0 : __popc(mine[e] & (bit(i) - 1u));
+    }
+    __syncthreads();
+    for (int e = tid; e < E; e += NT) {
+      uint32_t first = sh.start[e];
+#pragma unroll 8
+      for (int w = 0; w < warps; ++w) {
+        const uint32_t n = __popc(buf[w * E + e]);
+        buf[w * E + e] = first;
+        first += n;
+      }
+      sh.start[e] = first;
+    }
+    __syncthreads();
+    auto write = [&](int i, int32_t e, uint32_t place) {
+      const uint32_t row = e >= 0 ? mine[e] + place : p.capacity;
+      row_of[from + i] = row < p.capacity ? static_cast<int32_t>(row) : -1;
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (32 * i + lane < items) write(32 * i + lane, held[i], at[i]);
+    for (int i = 32 * kHeld + lane; i < items; i += 32)
+      write(i, choice(i), static_cast<uint32_t>(row_of[from + i]));
   }
 }
 
@@ -421,18 +456,28 @@ __global__ void __launch_bounds__(NT) route_count_kernel(const RowPlan p, const 
 }
 
 // ---------------------------------------------------------------- the choice
-// A team's k best keys: lane j keeps the j-th, with its column.
+// A team's k best logits in falling order: lane j of the team keeps the j-th, the one LPT after it,
+// and so on, KPL of them.
+template <int KPL>
 struct Chosen {
-  uint32_t key;  // 0 where there is none
-  int expert;    // -1 there
+  uint32_t key[KPL];  // 0 where there is none
+  int expert[KPL];    // -1 there
 };
 
-// One after the other: the maximum over the team, and the lowest lane that holds it.  The keys
-// are used up.
-template <int LPT, int VPL>
-__device__ __forceinline__ Chosen choose_in_turn(uint32_t (&key)[VPL], int k, int gl) {
-  const int lane = threadIdx.x & 31, c0 = gl * VPL;
-  Chosen r = {0u, -1};
+// One after the other: the maximum over the team, and the lowest column that holds it.
+template <int LPT, int VPL, int KPL>
+__device__ __forceinline__ Chosen<KPL> choose_in_turn(const float (&v)[VPL], bool on, int k,
+                                                      int gl) {
+  const int lane = threadIdx.x & 31;
+  uint32_t key[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) key[i] = on ? logit_key(v[i]) : 0u;
+  Chosen<KPL> r;
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) {
+    r.key[i] = 0u;
+    r.expert[i] = -1;
+  }
   for (int j = 0; j < k; ++j) {
     uint32_t best = key[0];
 #pragma unroll
@@ -442,120 +487,166 @@ __device__ __forceinline__ Chosen choose_in_turn(uint32_t (&key)[VPL], int k, in
 #pragma unroll
     for (int i = VPL - 1; i >= 0; --i)
       if (key[i] == m) slot = i;
-    const uint32_t holds = __ballot_sync(0xFFFFFFFFu, best == m) >> (lane & ~(LPT - 1));
-    const int who = __ffs(holds) - 1;  // the team's lowest lane of them
-    const int e = __shfl_sync(0xFFFFFFFFu, c0 + slot, who, LPT);
-    if (gl == who)
+    int e = column<LPT>(slot, gl);
+    bool here = best == m;
+    if constexpr (VPL == 8) {  // the lanes are in the order of their columns
+      const uint32_t holds = __ballot_sync(0xFFFFFFFFu, here) >> (lane & ~(LPT - 1));
+      const int who = __ffs(holds) - 1;
+      e = __shfl_sync(0xFFFFFFFFu, e, who, LPT);
+      here = gl == who;
+    } else {
+      const uint32_t mine = here ? static_cast<uint32_t>(e) : 0xFFFFFFFFu;
+      e = static_cast<int>(~team_max<LPT>(~mine));
+      here = static_cast<uint32_t>(e) == mine;
+    }
+    if (here)
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
         if (i == slot) key[i] = 0u;
-    if (gl == j && m > kNoLogit) {
-      r.expert = e;
-      r.key = m;
+    if (gl == (j & (LPT - 1)) && m > kNoLogit) {
+#pragma unroll
+      for (int i = 0; i < KPL; ++i)
+        if (i == j / LPT) {
+          r.expert[i] = e;
+          r.key[i] = m;
+        }
     }
   }
   return r;
 }
 
-// By counting, among the few keys that can be of the best.  The lanes form `groups` groups, at
-// least k of them, so none below the least of the groups' maxima is chosen (above 8, where that
-// leaves too many, none below the k-th largest of the lanes' maxima).  The others -- for 8 of
-// 64 some 15, for 8 of 256 some 17 -- are laid out in shared memory in the order of their
-// columns, and the lanes count those above each.  Where there are more than kMost, one after
-// the other after all.  `slots` has room for the warp's teams.
+// By counting, among the few logits that can be of the best: the team's columns form 16 parts
+// (32, one a lane, where it is a whole warp), and nothing below the k-th largest of their maxima
+// is chosen.  The others -- for 8 of 64 some 10, for 8 of 256 some 11 -- are laid out in shared
+// memory, and the lanes count those above each.  Where there are more than kMost, one after
+// the other after all.  (The least maximum of 8 parts takes fewer steps to find, but leaves more
+// than kMost so often -- at 256 columns for 13 % of the tokens -- that all took longer.)
+// `slots` has room for the warp's teams.
 constexpr int kMost = 31;  // (a stride that keeps the teams' slots on different banks)
 
-template <int LPT, int VPL>
-__device__ __forceinline__ Chosen choose_by_rank(uint32_t (&key)[VPL], int k, int gl, int groups,
-                                                 uint2* slots) {
+template <int LPT, int VPL, int KPL>
+__device__ __forceinline__ Chosen<KPL> choose_by_rank(const float (&v)[VPL], bool on, int k, int gl,
+                                                      uint2* slots) {
   constexpr int kRounds = (kMost + LPT - 1) / LPT;
+  constexpr int kParts = LPT < 16 ? 16 / LPT : 1;    // of a lane
+  constexpr int kRun = kParts <= VPL / 8 ? 8 : 4;    // columns in a row of a part
   const int lane = threadIdx.x & 31;
-  uint32_t bound = key[0];
+  float part[kParts];
 #pragma unroll
-  for (int i = 1; i < VPL; ++i) bound = max(bound, key[i]);
-  if (LPT == 32 && k > 8) {
-    uint32_t best = bound;
-    bound = __reduce_max_sync(0xFFFFFFFFu, best);
-    for (int j = 1; j < k; ++j) {
-      if (best == bound) best = 0u;  // all alike at once: the bound is only lower for it
-      bound = __reduce_max_sync(0xFFFFFFFFu, best);
-    }
-  } else {
-#pragma unroll
-    for (int d = LPT / 2; d > 0; d >>= 1) {
-      const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, bound, d);
-      bound = d >= groups ? max(bound, other) : min(bound, other);
-    }
+  for (int i = 0; i < VPL; ++i) {
+    const int at = i / kRun % kParts;
+    part[at] = i < kRun * kParts && i % kRun == 0 ? v[i] : fmaxf(part[at], v[i]);
   }
-  bound = max(bound, kNoLogit + 1u);
+  float bound = INFINITY;
+  if constexpr (LPT == 32) {
+    uint32_t best = logit_key(part[0]), m = __reduce_max_sync(0xFFFFFFFFu, best);
+    for (int j = 1; j < k; ++j) {
+      if (best == m) best = 0u;  // all alike at once: the bound is only lower for it
+      m = __reduce_max_sync(0xFFFFFFFFu, best);
+    }
+    bound = key_logit(m);
+  } else {
+    int above[kParts] = {};
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+#pragma unroll
+      for (int o = 0; o < LPT; ++o) {
+        const float other = __shfl_sync(0xFFFFFFFFu, part[i], o, LPT);
+#pragma unroll
+        for (int j = 0; j < kParts; ++j) above[j] += other > part[j] ? 1 : 0;
+      }
+#pragma unroll
+    for (int j = 0; j < kParts; ++j)
+      if (above[j] < k) bound = fminf(bound, part[j]);
+#pragma unroll
+    for (int o = LPT / 2; o > 0; o >>= 1)
+      bound = fminf(bound, __shfl_xor_sync(0xFFFFFFFFu, bound, o));
+  }
+  bound = fmaxf(bound, -3.40282347e38f);  // -infinity is not chosen; NaN is not below anything
   int n = 0;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) n += key[i] >= bound ? 1 : 0;
+  for (int i = 0; i < VPL; ++i) n += !(v[i] < bound) ? 1 : 0;
+  if (!on) n = 0;
   int at = n;
 #pragma unroll
   for (int d = 1; d < LPT; d <<= 1) {
-    const int v = __shfl_up_sync(0xFFFFFFFFu, at, d, LPT);
-    if (gl >= d) at += v;
+    const int x = __shfl_up_sync(0xFFFFFFFFu, at, d, LPT);
+    if (gl >= d) at += x;
   }
   const int all = __shfl_sync(0xFFFFFFFFu, at, LPT - 1, LPT);
   const int most = __reduce_max_sync(0xFFFFFFFFu, all);
-  if (most > kMost) return choose_in_turn<LPT, VPL>(key, k, gl);
+  if (most > kMost) return choose_in_turn<LPT, VPL, KPL>(v, on, k, gl);
   uint2* team = slots + lane / LPT * kMost;
   uint2* to = team + (at - n);
+  if (n > 0)
 #pragma unroll
-  for (int i = 0; i < VPL; ++i)
-    if (key[i] >= bound) *to++ = make_uint2(key[i], static_cast<uint32_t>(gl * VPL + i));
+    for (int i = 0; i < VPL; ++i)
+      if (!(v[i] < bound))
+        *to++ = make_uint2(__float_as_uint(v[i]), static_cast<uint32_t>(column<LPT>(i, gl)));
   __syncwarp();
   uint2 mine[kRounds];
   int above[kRounds];
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
     mine[r] = make_uint2(0xFFFFFFFFu, 0u);
-    if (r * LPT + gl < all) mine[r] = team[r * LPT + gl];
     above[r] = 0;
+    if (r * LPT + gl < all) {
+      mine[r] = team[r * LPT + gl];
+      mine[r].x = logit_key(__uint_as_float(mine[r].x));
+      team[r * LPT + gl].x = mine[r].x;
+    }
   }
+  __syncwarp();
 #pragma unroll 4
   for (int j = 0; j < most; ++j) {
     const uint32_t other = j < all ? team[j].x : 0u;
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) above[r] += other > mine[r].x ? 1 : 0;
   }
-  // without equal keys the counts are 0, 1, 2, ...
+  // without equal keys the counts are 0, 1, 2, ...; else the lower column comes first
   int sum = 0;
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) sum += above[r];
 #pragma unroll
   for (int d = LPT / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
   if (__any_sync(0xFFFFFFFFu, 2 * sum != all * (all - 1))) {
-    for (int j = 0; j < all; ++j)
+    for (int j = 0; j < all; ++j) {
+      const uint2 other = team[j];
 #pragma unroll
       for (int r = 0; r < kRounds; ++r)
-        above[r] += team[j].x == mine[r].x && j < r * LPT + gl ? 1 : 0;
+        above[r] += r * LPT + gl < all && other.x == mine[r].x && other.y < mine[r].y ? 1 : 0;
+    }
   }
   __syncwarp();
 #pragma unroll
   for (int r = 0; r < kRounds; ++r)
     if (r * LPT + gl < all && above[r] < k) team[above[r]] = mine[r];
   __syncwarp();
-  Chosen c = {0u, -1};
-  if (gl < min(all, k)) {
-    const uint2 v = team[gl];
-    c.key = v.x;
-    c.expert = static_cast<int>(v.y);
+  Chosen<KPL> c;
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) {
+    uint2 x = make_uint2(0u, 0xFFFFFFFFu);
+    if (i * LPT + gl < min(all, k)) x = team[i * LPT + gl];
+    c.key[i] = x.x;
+    c.expert[i] = static_cast<int>(x.y);
   }
   __syncwarp();  // the slots are written again for the next token
   return c;
 }
 
-template <typename T, int LPT, int VPL, int NT, bool ONE>
+// KPL * LPT >= k; KPL > 1 in the kernels of few lanes a token.
+template <typename T, int LPT, int VPL, int KPL, int NT, bool ONE>
 __global__ void __launch_bounds__(NT)
     route_kernel(const mxg_route_t d, const RowPlan p, const RouteWs ws, int vec) {
   constexpr int kTeams = NT / LPT, kWarps = NT / 32;
   constexpr int kBuf = ONE ? kBufWords / 2 : kBufWords;
+  constexpr bool kRank = LPT >= 8 || (LPT == 4 && KPL > 1);  // room for the teams' slots
+  constexpr bool kAhead = VPL <= 16;  // registers for the next row
+  static_assert(!kRank || kWarps * kMost * (32 / LPT) * 2 <= kBuf, "slots of every team");
   __shared__ RouteShared<kBuf> sh;
   __shared__ int32_t choices[ONE ? kOneItems : 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
-  const int gl = lane & (LPT - 1), c0 = gl * VPL, E = d.experts, k = d.k;
+  const int gl = lane & (LPT - 1), E = d.experts, k = d.k;
   if (!ONE) grid_launch_dependents();
   for (int e = tid; e < E; e += NT) sh.hist[e] = 0;
   if (tid == 0) sh.live = 0;
@@ -569,73 +660,82 @@ __global__ void __launch_bounds__(NT)
   float* const weight = d.weight + begin * k;
   const bool softmax = d.score == MXG_SCORE_SOFTMAX;
   const bool shares = d.loss != nullptr, whole = shares || (softmax && !d.normalize);
-  int groups = 1;
-  while (groups < k) groups *= 2;
-  // a few are found sooner in turn; and groups without columns have no maximum
-  const bool by_rank = LPT >= 8 && k > 3 && (LPT == 32 || k <= 8) && groups * VPL <= E;
+  // a few are found sooner in turn, and of more than 8 the bound by 16 parts leaves too many
+  const bool by_rank = kRank && k > 3 && (LPT == 32 || k <= 8);
   float acc[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
   int live = 0;
   int t = tid / LPT;  // in the chunk
-  LogitRow<T, VPL> next;
+  LogitRow<T, LPT, VPL> next;
   bool next_on = false;
   auto fetch = [&](int at) {
     next_on = at < count && (mask == nullptr || mask[at] != 0);
-    if (at < count) next.load(row, c0, E, vec != 0);
+    if (at < count) next.load(row, gl, E, vec != 0);
     row += kTeams * d.ld;
   };
-  fetch(t);
+  if (kAhead) fetch(t);
   for (int base = 0; base < count; base += kTeams, t += kTeams) {
+    if (!kAhead) {
+      fetch(t);
+      if (t + kTeams < count) next.ahead(row, gl, E);
+    }
     float v[VPL];
     next.values(v);
     const bool on = next_on;
-    fetch(t + kTeams);
-    uint32_t key[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = on ? logit_key(v[i]) : 0u;
-    Chosen best;
-    if (LPT >= 8 && by_rank)
-      best = choose_by_rank<LPT, VPL>(key, k, gl, groups, reinterpret_cast<uint2*>(sh.buf) +
-                                                              warp * (kMost * 32 / LPT));
+    if (kAhead) fetch(t + kTeams);
+    Chosen<KPL> best;
+    if (kRank && by_rank)
+      best = choose_by_rank<LPT, VPL, KPL>(
+          v, on, k, gl, reinterpret_cast<uint2*>(sh.buf) + warp * (kMost * (32 / LPT)));
     else
-      best = choose_in_turn<LPT, VPL>(key, k, gl);
-    const float mine = key_logit(best.key);
-    const float top = __shfl_sync(0xFFFFFFFFu, mine, 0, LPT);
-    const bool taken = __shfl_sync(0xFFFFFFFFu, best.expert, 0, LPT) >= 0;
+      best = choose_in_turn<LPT, VPL, KPL>(v, on, k, gl);
+    const float top = __shfl_sync(0xFFFFFFFFu, key_logit(best.key[0]), 0, LPT);
+    const bool taken = __shfl_sync(0xFFFFFFFFu, best.expert[0], 0, LPT) >= 0;
     const float shift = softmax ? top : fminf(top, 0.0f);
-    float sum = 0.0f, s[VPL];
+    float w[KPL], chosen = 0.0f;
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) {
+      const float l = key_logit(best.key[i]);
+      w[i] = best.expert[i] < 0 ? 0.0f
+             : softmax          ? exp_approx(l - shift)
+                                : sigmoid_scaled(l, d.normalize ? shift : 0.0f);
+      chosen += w[i];
+    }
+    if (d.normalize) chosen = team_add<LPT>(chosen);
+    float sum = 0.0f;
     if (whole) {
       if (softmax) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) s[i] = exp_approx(v[i] - shift);
+        for (int i = 0; i < VPL; ++i) v[i] = exp_approx(v[i] - shift);
       } else if (shift < 0.0f) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) s[i] = sigmoid_scaled(v[i], shift);
+        for (int i = 0; i < VPL; ++i) v[i] = sigmoid_scaled(v[i], shift);
       } else {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) s[i] = sigmoid(v[i]);
+        for (int i = 0; i < VPL; ++i) v[i] = sigmoid(v[i]);
       }
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) sum += s[i];
+      for (int i = 0; i < VPL; ++i) sum += v[i];
       sum = team_add<LPT>(sum);
     }
-    float w = 0.0f;
-    if (best.expert >= 0)
-      w = softmax ? exp_approx(mine - shift) : sigmoid_scaled(mine, d.normalize ? shift : 0.0f);
-    const float chosen = d.normalize ? team_add<LPT>(w) : (softmax ? sum : 1.0f);
-    if (t < count && gl < k) {
-      expert[t * k + gl] = best.expert;
-      weight[t * k + gl] = best.expert >= 0 ? d.scale * (w / chosen) : 0.0f;
-      if (ONE) choices[t * k + gl] = best.expert;
+    if (!d.normalize) chosen = softmax ? sum : 1.0f;
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) {
+      const int j = i * LPT + gl, e = best.expert[i];
+      if (t < count && j < k) {
+        expert[t * k + j] = e;
+        weight[t * k + j] = e >= 0 ? d.scale * (w[i] / chosen) : 0.0f;
+        if (ONE) choices[t * k + j] = e;
+      }
+      if (e >= 0) atomicAdd(&sh.hist[e], 1);
     }
-    if (best.expert >= 0) atomicAdd(&sh.hist[best.expert], 1);
     if (taken) {
       if (gl == 0) ++live;
       if (shares) {
         const float r = rcp_approx(sum);
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) acc[i] = fmaf(s[i], r, acc[i]);
+        for (int i = 0; i < VPL; ++i) acc[i] = fmaf(v[i], r, acc[i]);
       }
     }
   }
@@ -653,21 +753,23 @@ __global__ void __launch_bounds__(NT)
       for (int o = LPT; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], o);
     for (int w0 = 0; w0 < kWarps; w0 += fit) {
       if (warp >= w0 && warp < w0 + fit && lane < LPT) {
-        float* row = rows + (warp - w0) * E;
+        float* to = rows + (warp - w0) * E;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (c0 + i < E) row[c0 + i] = w0 == 0 ? acc[i] : row[c0 + i] + acc[i];
+        for (int i = 0; i < VPL; ++i) {
+          const int e = column<LPT>(i, gl);
+          if (e < E) to[e] = w0 == 0 ? acc[i] : to[e] + acc[i];
+        }
       }
       __syncthreads();
     }
     for (int e = tid; e < E; e += NT) {
-      float v = 0.0f;
+      float x = 0.0f;
 #pragma unroll 4
-      for (int w = 0; w < fit; ++w) v += rows[w * E + e];
+      for (int w = 0; w < fit; ++w) x += rows[w * E + e];
       if (ONE)
-        sh.psum[e] = v;
+        sh.psum[e] = x;
       else
-        ws.psum[static_cast<int64_t>(c) * ws.pitch + e] = v;
+        ws.psum[static_cast<int64_t>(c) * ws.pitch + e] = x;
     }
   }
   if (ONE) {
@@ -687,42 +789,50 @@ __global__ void __launch_bounds__(NT)
 //             with q = s / sum of the chosen s, else p b, with sum b p joining sum a p
 //   sigmoid : dl = p (1 - s) (a - sum a p) + extra;  normalised: q (1 - s) (b - sum b q), else
 //             b s (1 - s)
+// The extras reach the lanes that own their columns through a row of shared memory a team.
 constexpr int kGradThreads = 256;
 
-template <typename T, int LPT, int VPL>
-__global__ void __launch_bounds__(kGradThreads)
+template <typename T, int LPT, int VPL, int KPL>
+__global__ void __launch_bounds__(kGradThreads, VPL == 32 && LPT < 32 ? 2 : 1)
     route_backward_kernel(const mxg_route_grad_t d, int vec) {
-  extern __shared__ float team_rows[];  // a row of LPT * VPL columns a team
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int gl = lane & (LPT - 1), c0 = gl * VPL, E = d.experts, k = d.k;
   constexpr int kTeams = kGradThreads / LPT;
-  float* mine = team_rows + tid / LPT * (LPT * VPL);
+  __shared__ float4 team_rows[kTeams][LPT * VPL / 4];
+  __shared__ float4 slopes[LPT * VPL / 4];
+  const int tid = threadIdx.x, gl = tid & (LPT - 1), E = d.experts, k = d.k;
+  float* const mine = reinterpret_cast<float*>(team_rows[tid / LPT]);
   const bool softmax = d.score == MXG_SCORE_SOFTMAX, balance = d.slope != nullptr;
-  const bool joined = softmax && !d.normalize;  // the weights' gradient goes through the shares
-  float a[VPL];
+  // the weights' gradient goes through the shares; whether any of it does
+  const bool joined = softmax && !d.normalize, shares = balance || joined;
   const float dloss = balance ? *d.dloss : 0.0f;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) a[i] = balance && c0 + i < E ? d.slope[c0 + i] * dloss : 0.0f;
-  const T* logits = static_cast<const T*>(d.logits);
+  for (int e = tid; e < LPT * VPL; e += kGradThreads)
+    reinterpret_cast<float*>(slopes)[e] = balance && e < E ? d.slope[e] * dloss : 0.0f;
+  __syncthreads();
   const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * kTeams; base < d.tokens; base += step) {
     const int64_t t = base + tid / LPT;
     const bool in = t < d.tokens;
-    const T* row = logits + (in ? t : 0) * d.ld;
-    LogitRow<T, VPL> raw;
-    float v[VPL];
-    raw.load(row, c0, in ? E : 0, vec != 0);
-    raw.values(v);
-    int e = -1;
-    float b = 0.0f, l = -INFINITY;
-    if (in && gl < k) e = d.expert[t * k + gl];
-    if (static_cast<uint32_t>(e) >= static_cast<uint32_t>(E)) e = -1;
-    if (e >= 0) {
-      l = to_f32(row[e]);
-      if (d.dweight != nullptr) b = d.scale * d.dweight[t * k + gl];
+    const T* row = static_cast<const T*>(d.logits) + (in ? t : 0) * d.ld;
+    int e[KPL];
+    float b[KPL], l[KPL];
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) {
+      e[i] = in && i * LPT + gl < k ? d.expert[t * k + i * LPT + gl] : -1;
+      if (static_cast<uint32_t>(e[i]) >= static_cast<uint32_t>(E)) e[i] = -1;
+      b[i] = e[i] >= 0 && d.dweight != nullptr ? d.scale * d.dweight[t * k + i * LPT + gl] : 0.0f;
     }
-    const uint32_t any = __ballot_sync(0xFFFFFFFFu, e >= 0) >> (lane & ~(LPT - 1));
-    const bool taken = (LPT == 32 ? any : any & ((1u << (LPT & 31)) - 1u)) != 0;
+    LogitRow<T, LPT, VPL> raw;
+    raw.load(row, gl, in ? E : 0, vec != 0);
+    if (t + step < d.tokens) raw.ahead(row + step * d.ld, gl, E);
+    float v[VPL];
+    raw.values(v);
+    int have = 0;
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) {
+      l[i] = e[i] >= 0 ? to_f32(row[e[i]]) : -INFINITY;
+      have |= e[i] >= 0 ? 1 : 0;
+    }
+#pragma unroll
+    for (int o = LPT / 2; o > 0; o >>= 1) have |= __shfl_xor_sync(0xFFFFFFFFu, have, o);
 
     float top = v[0];
 #pragma unroll
@@ -730,78 +840,92 @@ __global__ void __launch_bounds__(kGradThreads)
 #pragma unroll
     for (int o = LPT / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     const float shift = softmax ? top : fminf(top, 0.0f);
-    // the shares and their part of the sums
-    float p[VPL], rest[VPL], sum = 0.0f, dot = 0.0f;
-    if (balance || joined) {
+    // the shares (times 1 - s for sigmoids, once they are summed up) and their part of the sums
+    float sum = 0.0f, dot = 0.0f;
+    if (shares) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        p[i] = softmax ? exp_approx(v[i] - shift) : sigmoid_scaled(v[i], shift);
-        // 1 - s, without its cancellation
-        rest[i] = softmax ? 1.0f : sigmoid(-v[i]);
-        sum += p[i];
-        dot = fmaf(a[i], p[i], dot);
+      for (int i = 0; i < VPL; i += 4) {
+        const float4 a4 = slopes[column<LPT>(i, gl) / 4];
+        const float a[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float rest = 1.0f;
+          const float p = softmax ? exp_approx(v[i + j] - shift)
+                                  : sigmoid_scaled(v[i + j], shift, rest);
+          sum += p;
+          dot = fmaf(a[j], p, dot);
+          v[i + j] = softmax ? p : p * rest;
+        }
       }
       sum = team_add<LPT>(sum);
     }
     // the chosen experts'
-    float s = 0.0f, extra = 0.0f;
-    const float other = softmax ? 1.0f : sigmoid(-l);
-    if (e >= 0) s = softmax ? exp_approx(l - shift) : sigmoid_scaled(l, d.normalize ? shift : 0.0f);
+    float s[KPL], rest[KPL], chosen = 0.0f, bq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) {
+      rest[i] = 1.0f;
+      s[i] = 0.0f;
+      if (e[i] >= 0)
+        s[i] = softmax ? exp_approx(l[i] - shift)
+                       : sigmoid_scaled(l[i], d.normalize ? shift : 0.0f, rest[i]);
+      chosen += s[i];
+      bq = fmaf(b[i], s[i], bq);
+    }
     if (d.normalize) {
-      const float chosen = team_add<LPT>(s);
-      const float q = e >= 0 ? s / chosen : 0.0f;
-      const float bq = team_add<LPT>(b * q);
-      extra = q * other * (b - bq);
-    } else if (softmax) {
-      extra = b * s / sum;
-      dot = fmaf(b, s, dot);
+      chosen = team_add<LPT>(chosen);
+      bq = team_add<LPT>(bq) / chosen;
     } else {
-      extra = b * s * other;
+      if (joined) dot += bq;
+      chosen = joined ? sum : 1.0f;
+      bq = 0.0f;
     }
     float r = 0.0f;
-    if (balance || joined) {
-      dot = team_add<LPT>(dot);
-      r = 1.0f / sum;
-      dot *= r;
+    if (shares) {
+      r = rcp_approx(sum);
+      dot = -team_add<LPT>(dot) * r * r;
     }
 #pragma unroll
     for (int i = 0; i < VPL; i += 4)
-      *reinterpret_cast<float4*>(mine + c0 + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    __syncwarp();
-    if (e >= 0) atomicAdd(&mine[e], extra);
+      *reinterpret_cast<float4*>(mine + column<LPT>(i, gl)) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < VPL; i += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(mine + c0 + i);
-      v[i] = x.x;
-      v[i + 1] = x.y;
-      v[i + 2] = x.z;
-      v[i + 3] = x.w;
-    }
-    if (balance || joined)
+    for (int i = 0; i < KPL; ++i)
+      if (e[i] >= 0) atomicAdd(&mine[e[i]], s[i] / chosen * rest[i] * (b[i] - bq));
+    __syncwarp();
+    T* out = static_cast<T*>(d.dlogits) + (in ? t : 0) * d.ldd;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) v[i] = fmaf(p[i] * r * rest[i], a[i] - dot, v[i]);
-    if (in) {
-      T* out = static_cast<T*>(d.dlogits) + t * d.ldd;
+    for (int i = 0; i < VPL; i += 8) {
+      const int c = column<LPT>(i, gl);
+      float f[8];
 #pragma unroll
-      for (int i = 0; i < VPL; i += 8) {
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = taken ? v[i + j] : 0.0f;
-        if (vec && c0 + i < E) {
-          if constexpr (sizeof(T) == 4) {
-            reinterpret_cast<float4*>(out + c0 + i)[0] = make_float4(f[0], f[1], f[2], f[3]);
-            reinterpret_cast<float4*>(out + c0 + i)[1] = make_float4(f[4], f[5], f[6], f[7]);
-          } else {
-            *reinterpret_cast<uint4*>(out + c0 + i) =
-                make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]),
-                           pack2<T>(f[6], f[7]));
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (c0 + i + j < E) out[c0 + i + j] = from_f32<T>(f[j]);
+      for (int j = 0; j < 8; j += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(mine + c + j), a = slopes[(c + j) / 4];
+        f[j] = x.x;
+        f[j + 1] = x.y;
+        f[j + 2] = x.z;
+        f[j + 3] = x.w;
+        if (shares) {  // p / sum (a - dot / sum) + extra
+          f[j] = fmaf(v[i + j], fmaf(a.x, r, dot), f[j]);
+          f[j + 1] = fmaf(v[i + j + 1], fmaf(a.y, r, dot), f[j + 1]);
+          f[j + 2] = fmaf(v[i + j + 2], fmaf(a.z, r, dot), f[j + 2]);
+          f[j + 3] = fmaf(v[i + j + 3], fmaf(a.w, r, dot), f[j + 3]);
         }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = have ? f[j] : 0.0f;
+      if (!in) continue;
+      if (vec && c < E) {
+        if constexpr (sizeof(T) == 4) {
+          reinterpret_cast<float4*>(out + c)[0] = make_float4(f[0], f[1], f[2], f[3]);
+          reinterpret_cast<float4*>(out + c)[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+          *reinterpret_cast<uint4*>(out + c) = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]),
+                                                          pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j < E) out[c + j] = from_f32<T>(f[j]);
       }
     }
     __syncwarp();
@@ -810,33 +934,54 @@ __global__ void __launch_bounds__(kGradThreads)
 
 namespace {
 
-// Lanes a token: 8 columns each, and one for each of the k chosen.
-int lanes_per_token(int experts, int k) {
+// How a token is laid out over lanes: few lanes (kpl > 0 choices each) with many columns, where
+// k is at most 8 and there are at most 256 experts; else 8 columns a lane (up to 32 lanes), and a
+// lane for each of the k.
+struct Shape {
+  int lpt, vpl, kpl;
+};
+Shape few_lanes(int experts) {
+  if (experts <= 8) return {1, 8, 8};
+  if (experts <= 16) return {1, 16, 8};
+  if (experts <= 32) return {2, 16, 4};
+  if (experts <= 64) return {4, 16, 2};
+  if (experts <= 128) return {8, 16, 1};
+  return {8, 32, 1};
+}
+Shape many_lanes(int experts, int k) {
   int lanes = 1;
   while (lanes < 32 && (lanes * 8 < experts || lanes < k)) lanes *= 2;
-  return lanes;
+  return {lanes, experts > 512 ? 32 : (experts > 256 ? 16 : 8), 1};
 }
-
-// Columns a lane.
-int columns_per_lane(int experts) { return experts > 512 ? 32 : (experts > 256 ? 16 : 8); }
+bool few_serve(int experts, int k) { return k <= 8 && experts <= 256; }
 
 struct Chunks {
   int n;
   int64_t per;  // tokens each
 };
 
-// One CTA up to four passes of its teams (a second kernel costs more than three of them),
-// else a pass at least a CTA.
-Chunks chunks_of(int64_t tokens, int experts, int k) {
-  const int lanes = lanes_per_token(experts, k), vpl = columns_per_lane(experts);
-  if (tokens <= 4 * (threads_of(vpl, true) / lanes) && tokens * k <= kOneItems)
-    return {1, std::max<int64_t>(1, tokens)};
-  const int64_t pass = threads_of(vpl, false) / lanes;
+Chunks cut(int64_t tokens, int64_t pass) {
   const int64_t n = std::min<int64_t>(kMaxChunks, (tokens + pass - 1) / pass);
   Chunks c;
   c.per = (tokens + n - 1) / n;
   c.n = static_cast<int>(std::max<int64_t>(2, (tokens + c.per - 1) / c.per));
   return c;
+}
+
+// One CTA up to four passes of its teams (a second kernel costs more than three of them),
+// else a pass at least a CTA.
+Chunks chunks_of(int64_t tokens, int experts, int k) {
+  const Shape one = many_lanes(experts, k);
+  if (tokens <= 4 * (threads_of(one.lpt, one.vpl, true) / one.lpt) && tokens * k <= kOneItems)
+    return {1, std::max<int64_t>(1, tokens)};
+  const Shape s = few_serve(experts, k) ? few_lanes(experts) : one;
+  return cut(tokens, threads_of(s.lpt, s.vpl, false) / s.lpt);
+}
+
+// For choices made elsewhere, each counted as a token with one.
+Chunks chunks_of_choices(int64_t choices) {
+  if (choices <= 4 * kOneThreads) return {1, std::max<int64_t>(1, choices)};
+  return cut(choices, kManyThreads);
 }
 
 int pitch_of(int experts) { return (experts + 3) / 4 * 4; }
@@ -861,64 +1006,78 @@ cudaError_t launch_finish(const RowPlan& p, const RouteWs& ws, cudaStream_t stre
                       0, stream, p, ws);
 }
 
-template <typename T, int LPT, int VPL>
+template <typename T, int LPT, int VPL, int KPL, bool ONE>
 cudaError_t run_route(const mxg_route_t& d, const RowPlan& p, const RouteWs& ws, int vec,
                       cudaStream_t stream) {
-  constexpr int kThreads = threads_of(VPL, false), kOne = threads_of(VPL, true);
-  if (p.chunks == 1)
-    route_kernel<T, LPT, VPL, kOne, true><<<1, kOne, 0, stream>>>(d, p, ws, vec);
-  else
-    route_kernel<T, LPT, VPL, kThreads, false>
-        <<<static_cast<unsigned>(p.chunks), kThreads, 0, stream>>>(d, p, ws, vec);
+  constexpr int kThreads = threads_of(LPT, VPL, ONE);
+  route_kernel<T, LPT, VPL, KPL, kThreads, ONE>
+      <<<static_cast<unsigned>(p.chunks), kThreads, 0, stream>>>(d, p, ws, vec);
   return cudaGetLastError();
 }
-
-template <typename T, int LPT, int VPL>
-cudaError_t run_backward(const mxg_route_grad_t& d, int vec, int num_sms, cudaStream_t stream) {
-  constexpr int kTeams = kGradThreads / LPT;
-  const int64_t grid = std::min<int64_t>((d.tokens + kTeams - 1) / kTeams, num_sms * 8LL);
-  const size_t smem = static_cast<size_t>(kGradThreads) * VPL * sizeof(float);
-  route_backward_kernel<T, LPT, VPL>
-      <<<static_cast<unsigned>(grid), kGradThreads, smem, stream>>>(d, vec);
-  return cudaGetLastError();
-}
-
-// fn<T, LPT, VPL>() for a type, and the lanes and columns a lane that experts and k take.
-#define MXG_BY_LANES(T, CALL)                     \
-  switch (lanes_per_token(d.experts, d.k)) {      \
-    case 1: return CALL(T, 1, 8);                 \
-    case 2: return CALL(T, 2, 8);                 \
-    case 4: return CALL(T, 4, 8);                 \
-    case 8: return CALL(T, 8, 8);                 \
-    case 16: return CALL(T, 16, 8);               \
-  }                                               \
-  if (columns_per_lane(d.experts) == 8) return CALL(T, 32, 8);   \
-  if (columns_per_lane(d.experts) == 16) return CALL(T, 32, 16); \
-  return CALL(T, 32, 32);
 
 template <typename T>
 cudaError_t route_typed(const mxg_route_t& d, const RowPlan& p, const RouteWs& ws,
                         cudaStream_t stream) {
   const int vec = d.experts % 8 == 0 && rows_of_16(d.logits, d.ld, sizeof(T));
-#define MXG_CALL(T, L, V) (run_route<T, L, V>(d, p, ws, vec, stream))
-  MXG_BY_LANES(T, MXG_CALL)
-#undef MXG_CALL
+  if (p.chunks > 1 && few_serve(d.experts, d.k)) {
+    const Shape s = few_lanes(d.experts);
+    if (s.vpl == 8) return run_route<T, 1, 8, 8, false>(d, p, ws, vec, stream);
+    if (s.lpt == 1) return run_route<T, 1, 16, 8, false>(d, p, ws, vec, stream);
+    if (s.lpt == 2) return run_route<T, 2, 16, 4, false>(d, p, ws, vec, stream);
+    if (s.lpt == 4) return run_route<T, 4, 16, 2, false>(d, p, ws, vec, stream);
+    if (s.vpl == 16) return run_route<T, 8, 16, 1, false>(d, p, ws, vec, stream);
+    return run_route<T, 8, 32, 1, false>(d, p, ws, vec, stream);
+  }
+  const Shape s = many_lanes(d.experts, d.k);
+  if (p.chunks > 1) {  // (more than 8 of the experts, or more than 256 of them: 16 lanes at least)
+    if (s.lpt == 16) return run_route<T, 16, 8, 1, false>(d, p, ws, vec, stream);
+    if (s.vpl == 8) return run_route<T, 32, 8, 1, false>(d, p, ws, vec, stream);
+    if (s.vpl == 16) return run_route<T, 32, 16, 1, false>(d, p, ws, vec, stream);
+    return run_route<T, 32, 32, 1, false>(d, p, ws, vec, stream);
+  }
+  if (s.lpt == 1) return run_route<T, 1, 8, 1, true>(d, p, ws, vec, stream);
+  if (s.lpt == 2) return run_route<T, 2, 8, 1, true>(d, p, ws, vec, stream);
+  if (s.lpt == 4) return run_route<T, 4, 8, 1, true>(d, p, ws, vec, stream);
+  if (s.lpt == 8) return run_route<T, 8, 8, 1, true>(d, p, ws, vec, stream);
+  if (s.lpt == 16) return run_route<T, 16, 8, 1, true>(d, p, ws, vec, stream);
+  if (s.vpl == 8) return run_route<T, 32, 8, 1, true>(d, p, ws, vec, stream);
+  if (s.vpl == 16) return run_route<T, 32, 16, 1, true>(d, p, ws, vec, stream);
+  return run_route<T, 32, 32, 1, true>(d, p, ws, vec, stream);
+}
+
+template <typename T, int LPT, int VPL, int KPL>
+cudaError_t run_backward(const mxg_route_grad_t& d, int vec, int num_sms, cudaStream_t stream) {
+  constexpr int kTeams = kGradThreads / LPT;
+  const int64_t grid = std::min<int64_t>((d.tokens + kTeams - 1) / kTeams, num_sms * 8LL);
+  route_backward_kernel<T, LPT, VPL, KPL>
+      <<<static_cast<unsigned>(grid), kGradThreads, 0, stream>>>(d, vec);
+  return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t backward_typed(const mxg_route_grad_t& d, int num_sms, cudaStream_t stream) {
   const int vec = d.experts % 8 == 0 && rows_of_16(d.logits, d.ld, sizeof(T)) &&
                   rows_of_16(d.dlogits, d.ldd, sizeof(T));
-#define MXG_CALL(T, L, V) (run_backward<T, L, V>(d, vec, num_sms, stream))
-  MXG_BY_LANES(T, MXG_CALL)
-#undef MXG_CALL
+  if (few_serve(d.experts, d.k)) {
+    const Shape s = few_lanes(d.experts);
+    if (s.vpl == 8) return run_backward<T, 1, 8, 8>(d, vec, num_sms, stream);
+    if (s.lpt == 1) return run_backward<T, 1, 16, 8>(d, vec, num_sms, stream);
+    if (s.lpt == 2) return run_backward<T, 2, 16, 4>(d, vec, num_sms, stream);
+    if (s.lpt == 4) return run_backward<T, 4, 16, 2>(d, vec, num_sms, stream);
+    if (s.vpl == 16) return run_backward<T, 8, 16, 1>(d, vec, num_sms, stream);
+    return run_backward<T, 8, 32, 1>(d, vec, num_sms, stream);
+  }
+  const Shape s = many_lanes(d.experts, d.k);
+  if (s.lpt == 16) return run_backward<T, 16, 8, 1>(d, vec, num_sms, stream);
+  if (s.vpl == 8) return run_backward<T, 32, 8, 1>(d, vec, num_sms, stream);
+  if (s.vpl == 16) return run_backward<T, 32, 16, 1>(d, vec, num_sms, stream);
+  return run_backward<T, 32, 32, 1>(d, vec, num_sms, stream);
 }
-#undef MXG_BY_LANES
 
 }  // namespace
 
 size_t route_ws_bytes(int64_t tokens, int experts, int k) {
-  const int64_t n = chunks_of(tokens, experts, k).n;
+  const int64_t n = std::max(chunks_of(tokens, experts, k).n, chunks_of_choices(tokens * k).n);
   return n == 1 ? 16 : static_cast<size_t>((n * (2 * pitch_of(experts) + 1) * 4 + 15) / 16 * 16);
 }
 
@@ -955,19 +1114,20 @@ cudaError_t launch_route_rows(const int32_t* expert, int64_t tokens, int experts
                               int64_t capacity, int64_t last_dim, int32_t* counts, int32_t* row_of,
                               int64_t* group_ws, void* workspace, int32_t* status,
                               cudaStream_t stream, int* launches) {
-  const Chunks c = chunks_of(tokens, experts, k);
+  // an expert may be named twice for a token here: each choice is a token with one
+  const Chunks c = chunks_of_choices(tokens * k);
   RowPlan p = {};
   p.expert = expert;
   p.counts = counts;
   p.row_of = row_of;
   p.group_ws = group_ws;
   p.status = status;
-  p.tokens = tokens;
+  p.tokens = tokens * k;
   p.per = c.per;
   p.last_dim = last_dim;
   p.capacity = static_cast<uint32_t>(capacity / align * align);
   p.experts = experts;
-  p.k = k;
+  p.k = 1;
   p.align = align;
   p.chunks = c.n;
   const RouteWs ws = carve(workspace, c.n, experts);
