@@ -87,23 +87,19 @@ __device__ __forceinline__ float key_logit(uint32_t key) {
 
 // sigmoid(l), and sigmoid(l) e^-m with m < 0: shares of a token whose sigmoids all underflow
 // are still right (m the largest logit where that is negative, so l <= m).
-__device__ __forceinline__ float sigmoid(float l) {
-  const float e = exp_approx(-fabsf(l));
-  return (l < 0.0f ? e : 1.0f) * rcp_approx(1.0f + e);
-}
+__device__ __forceinline__ float sigmoid(float l) { return rcp_approx(1.0f + exp_approx(-l)); }
 __device__ __forceinline__ float sigmoid_scaled(float l, float m) {
   return m < 0.0f ? exp_approx(l - m) * rcp_approx(1.0f + exp_approx(l)) : sigmoid(l);
 }
-
 // The same and 1 - sigmoid(l), without the subtraction's cancellation.
 __device__ __forceinline__ float sigmoid_scaled(float l, float m, float& rest) {
   if (m < 0.0f) {
     rest = rcp_approx(1.0f + exp_approx(l));
     return exp_approx(l - m) * rest;
   }
-  const float e = exp_approx(-fabsf(l)), r = rcp_approx(1.0f + e), er = e * r;
-  rest = l < 0.0f ? r : er;
-  return l < 0.0f ? er : r;
+  const float e = exp_approx(-l), r = rcp_approx(1.0f + e);
+  rest = fminf(e * r, 1.0f);  // (infinity times 0 becomes 1)
+  return r;
 }
 
 template <int LPT>
@@ -171,7 +167,7 @@ struct LogitRow {
 #pragma unroll
     for (int i = 0; i < VPL / 8; ++i) {
       const int c = column<LPT>(8 * i, gl);
-      if (c < experts) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
+      if (c < experts) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + c));
     }
   }
 };
@@ -524,10 +520,9 @@ __device__ __forceinline__ Chosen<KPL> choose_in_turn(const float (&v)[VPL], boo
 // `slots` has room for the warp's teams.
 constexpr int kMost = 31;  // (a stride that keeps the teams' slots on different banks)
 
-template <int LPT, int VPL, int KPL>
-__device__ __forceinline__ Chosen<KPL> choose_by_rank(const float (&v)[VPL], bool on, int k, int gl,
-                                                      uint2* slots) {
-  constexpr int kRounds = (kMost + LPT - 1) / LPT;
+template <typename T, int LPT, int VPL, int KPL>
+__device__ __forceinline__ Chosen<KPL> choose_by_rank(const float (&v)[VPL], const T* row, bool on,
+                                                      int k, int gl, uint2* slots) {
   constexpr int kParts = LPT < 16 ? 16 / LPT : 1;    // of a lane
   constexpr int kRun = kParts <= VPL / 8 ? 8 : 4;    // columns in a row of a part
   const int lane = threadIdx.x & 31;
@@ -563,10 +558,11 @@ __device__ __forceinline__ Chosen<KPL> choose_by_rank(const float (&v)[VPL], boo
       bound = fminf(bound, __shfl_xor_sync(0xFFFFFFFFu, bound, o));
   }
   bound = fmaxf(bound, -3.40282347e38f);  // -infinity is not chosen; NaN is not below anything
-  int n = 0;
+  uint32_t among = 0;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) n += !(v[i] < bound) ? 1 : 0;
-  if (!on) n = 0;
+  for (int i = 0; i < VPL; ++i) among |= !(v[i] < bound) ? 1u << i : 0u;
+  if (!on) among = 0;
+  const int n = __popc(among);
   int at = n;
 #pragma unroll
   for (int d = 1; d < LPT; d <<= 1) {
@@ -577,50 +573,56 @@ __device__ __forceinline__ Chosen<KPL> choose_by_rank(const float (&v)[VPL], boo
   const int most = __reduce_max_sync(0xFFFFFFFFu, all);
   if (most > kMost) return choose_in_turn<LPT, VPL, KPL>(v, on, k, gl);
   uint2* team = slots + lane / LPT * kMost;
-  uint2* to = team + (at - n);
-  if (n > 0)
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (!(v[i] < bound))
-        *to++ = make_uint2(__float_as_uint(v[i]), static_cast<uint32_t>(column<LPT>(i, gl)));
-  __syncwarp();
-  uint2 mine[kRounds];
-  int above[kRounds];
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    mine[r] = make_uint2(0xFFFFFFFFu, 0u);
-    above[r] = 0;
-    if (r * LPT + gl < all) {
-      mine[r] = team[r * LPT + gl];
-      mine[r].x = logit_key(__uint_as_float(mine[r].x));
-      team[r * LPT + gl].x = mine[r].x;
-    }
+  for (uint2* to = team + (at - n); among != 0; among &= among - 1u) {
+    const int i = __ffs(static_cast<int>(among)) - 1;
+    const int e = ((i >> 3) * LPT + gl) * 8 + (i & 7);
+    // (read again: a register cannot be picked by a number)
+    *to++ = make_uint2(logit_key(to_f32(row[e])), static_cast<uint32_t>(e));
   }
+  // no key in the slots behind, up to those of the team that has most
+  for (int i = all + gl; i < most; i += LPT) team[i].x = 0u;
   __syncwarp();
-#pragma unroll 4
-  for (int j = 0; j < most; ++j) {
-    const uint32_t other = j < all ? team[j].x : 0u;
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r) above[r] += other > mine[r].x ? 1 : 0;
-  }
-  // without equal keys the counts are 0, 1, 2, ...; else the lower column comes first
+  // two a lane at once, as often as it takes: mostly once for 8 lanes, twice for 4
+  constexpr int kPairs = (kMost + 2 * LPT - 1) / (2 * LPT);
+  uint2 mine[2 * kPairs];
+  int above[2 * kPairs];
   int sum = 0;
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r) sum += above[r];
+  for (int r = 0; r < kPairs; ++r) {
+    const int i0 = 2 * r * LPT + gl, i1 = i0 + LPT;
+    above[2 * r] = above[2 * r + 1] = k;  // of a slot that is empty
+    if (2 * r * LPT < most) {
+      const uint2 a = i0 < all ? team[i0] : make_uint2(0xFFFFFFFFu, 0u);
+      const uint2 b = i1 < all ? team[i1] : make_uint2(0xFFFFFFFFu, 0u);
+      int x = 0, y = 0;
+#pragma unroll 4
+      for (int j = 0; j < most; ++j) {
+        const uint32_t other = team[j].x;
+        x += other > a.x ? 1 : 0;
+        y += other > b.x ? 1 : 0;
+      }
+      sum += x + y;
+      mine[2 * r] = a;
+      mine[2 * r + 1] = b;
+      if (i0 < all) above[2 * r] = x;
+      if (i1 < all) above[2 * r + 1] = y;
+    }
+  }
+  // without equal keys the counts are 0, 1, 2, ...; else the lower column comes first
 #pragma unroll
   for (int d = LPT / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
   if (__any_sync(0xFFFFFFFFu, 2 * sum != all * (all - 1))) {
     for (int j = 0; j < all; ++j) {
       const uint2 other = team[j];
 #pragma unroll
-      for (int r = 0; r < kRounds; ++r)
-        above[r] += r * LPT + gl < all && other.x == mine[r].x && other.y < mine[r].y ? 1 : 0;
+      for (int r = 0; r < 2 * kPairs; ++r)
+        if (r * LPT + gl < all && other.x == mine[r].x && other.y < mine[r].y) ++above[r];
     }
   }
   __syncwarp();
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r)
-    if (r * LPT + gl < all && above[r] < k) team[above[r]] = mine[r];
+  for (int r = 0; r < 2 * kPairs; ++r)
+    if (above[r] < k) team[above[r]] = mine[r];
   __syncwarp();
   Chosen<KPL> c;
 #pragma unroll
@@ -654,7 +656,8 @@ __global__ void __launch_bounds__(NT)
 
   const int64_t begin = c * p.per;
   const int count = static_cast<int>(max(min(begin + p.per, d.tokens) - begin, int64_t{0}));
-  const T* row = static_cast<const T*>(d.logits) + (begin + tid / LPT) * d.ld;
+  const T* const logits = static_cast<const T*>(d.logits) + begin * d.ld;
+  const T* row = logits + tid / LPT * d.ld;
   const uint8_t* mask = d.mask != nullptr ? d.mask + begin : nullptr;
   int32_t* const expert = d.expert + begin * k;
   float* const weight = d.weight + begin * k;
@@ -686,8 +689,8 @@ __global__ void __launch_bounds__(NT)
     if (kAhead) fetch(t + kTeams);
     Chosen<KPL> best;
     if (kRank && by_rank)
-      best = choose_by_rank<LPT, VPL, KPL>(
-          v, on, k, gl, reinterpret_cast<uint2*>(sh.buf) + warp * (kMost * (32 / LPT)));
+      best = choose_by_rank<T, LPT, VPL, KPL>(
+          v, logits + t * d.ld, on, k, gl, reinterpret_cast<uint2*>(sh.buf) + warp * (kMost * (32 / LPT)));
     else
       best = choose_in_turn<LPT, VPL, KPL>(v, on, k, gl);
     const float top = __shfl_sync(0xFFFFFFFFu, key_logit(best.key[0]), 0, LPT);
@@ -793,7 +796,7 @@ __global__ void __launch_bounds__(NT)
 constexpr int kGradThreads = 256;
 
 template <typename T, int LPT, int VPL, int KPL>
-__global__ void __launch_bounds__(kGradThreads, VPL == 32 && LPT < 32 ? 2 : 1)
+__global__ void __launch_bounds__(kGradThreads, VPL <= 16 ? 4 : 1)
     route_backward_kernel(const mxg_route_grad_t d, int vec) {
   constexpr int kTeams = kGradThreads / LPT;
   __shared__ float4 team_rows[kTeams][LPT * VPL / 4];
@@ -1065,7 +1068,8 @@ cudaError_t backward_typed(const mxg_route_grad_t& d, int num_sms, cudaStream_t 
     if (s.lpt == 2) return run_backward<T, 2, 16, 4>(d, vec, num_sms, stream);
     if (s.lpt == 4) return run_backward<T, 4, 16, 2>(d, vec, num_sms, stream);
     if (s.vpl == 16) return run_backward<T, 8, 16, 1>(d, vec, num_sms, stream);
-    return run_backward<T, 8, 32, 1>(d, vec, num_sms, stream);
+    // (more warps an SM than with 32 columns a lane: TIMING)
+    return run_backward<T, 16, 16, 1>(d, vec, num_sms, stream);
   }
   const Shape s = many_lanes(d.experts, d.k);
   if (s.lpt == 16) return run_backward<T, 16, 8, 1>(d, vec, num_sms, stream);
