@@ -31,14 +31,11 @@ struct Piece {
       asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                    : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
                      "=r"(w[6]), "=r"(w[7])
-                   : "l"(p)
-                   : "memory");
+                   : "l"(p));  // (volatile: in order with the stores)
     } else if constexpr (BYTES == 16) {
-      const uint4 q = *reinterpret_cast<const uint4*>(p);
-      w[0] = q.x;
-      w[1] = q.y;
-      w[2] = q.z;
-      w[3] = q.w;
+      asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "l"(p));
     } else if constexpr (sizeof(T) == 4) {
       w[0] = __float_as_uint(*p);
     } else {
@@ -153,49 +150,66 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
+// A warp's item: a token and 32 pieces of its columns.  A token's rows are all asked for
+// before the first is added, kAhead at a time, and the next token's places among the rows before
+// those.
 template <typename T, int BYTES>
 __global__ void __launch_bounds__(kRowThreads)
     combine_kernel(const mxg_expert_rows_t d, int slices) {
   constexpr int kElems = Piece<T, BYTES>::kElems;
-  constexpr int kAhead = 4;  // rows in flight
+  constexpr int kAhead = 8;
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kRowThreads / 32);
   const int64_t items = d.n * slices;
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
-       item < items; item += warps) {
-    const int64_t t = item / slices;
-    const int slice = static_cast<int>(item - t * slices);
-    int32_t at = -1;
-    float w = 1.0f;
-    if (lane < d.k) {
+  int64_t item = static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+  int64_t t = item / slices;
+  int slice = static_cast<int>(item - t * slices);
+  const int64_t t_step = warps / slices;
+  const int slice_step = static_cast<int>(warps - t_step * slices);
+  int32_t at = -1;
+  float w = 1.0f;
+  auto places = [&] {
+    at = -1;
+    if (t < d.n && lane < d.k) {
       at = d.row_of[t * d.k + lane];
       if (d.weight != nullptr) w = d.weight[t * d.k + lane];
     }
+  };
+  places();
+  for (; item < items; item += warps) {
+    const int32_t at_now = at < d.rows_capacity ? at : -1;
+    const float w_now = w;
     const int c = (slice * 32 + lane) * kElems;
     T* to = static_cast<T*>(d.tokens) + t * d.ldt;
-    const T* rows = static_cast<const T*>(d.rows);
+    const T* rows = static_cast<const T*>(d.rows) + c;
+    t += t_step;
+    slice += slice_step;
+    if (slice >= slices) {
+      slice -= slices;
+      ++t;
+    }
+    places();
     const bool whole = c + kElems <= d.cols;
     float acc[kElems];
 #pragma unroll
     for (int i = 0; i < kElems; ++i) acc[i] = 0.0f;
     for (int j0 = 0; j0 < d.k; j0 += kAhead) {
       Piece<T, BYTES> x[kAhead];
-      float wj[kAhead];
-      bool in[kAhead];
+      int32_t r[kAhead];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        const int64_t r = __shfl_sync(0xFFFFFFFFu, at, (j0 + j) & 31);
-        wj[j] = __shfl_sync(0xFFFFFFFFu, w, (j0 + j) & 31);
-        in[j] = j0 + j < d.k && r >= 0 && r < d.rows_capacity;
-        if (in[j] && whole) x[j].load(rows + r * d.ldr + c);
+        r[j] = __shfl_sync(0xFFFFFFFFu, at_now, (j0 + j) & 31);
+        if (j0 + j >= d.k) r[j] = -1;
+        if (r[j] >= 0 && whole) x[j].load(rows + r[j] * d.ldr);
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        if (!in[j] || !whole) continue;
+        const float wj = __shfl_sync(0xFFFFFFFFu, w_now, (j0 + j) & 31);
+        if (r[j] < 0 || !whole) continue;
         float f[kElems];
         x[j].get(f);
 #pragma unroll
-        for (int i = 0; i < kElems; ++i) acc[i] = fmaf(wj[j], f[i], acc[i]);
+        for (int i = 0; i < kElems; ++i) acc[i] = fmaf(wj, f[i], acc[i]);
       }
     }
     if (whole) {
@@ -204,15 +218,14 @@ __global__ void __launch_bounds__(kRowThreads)
       y.store(to + c);
     }
     // the last, shorter piece of a row
-    if (BYTES > static_cast<int>(sizeof(T)) && __any_sync(0xFFFFFFFFu, !whole && c < d.cols)) {
+    if (kElems > 1 && __any_sync(0xFFFFFFFFu, !whole && c < d.cols)) {
       const int most = static_cast<int>(d.cols) - c;
       for (int i = 0; i < kElems - 1; ++i) {
         float sum = 0.0f;
         for (int j = 0; j < d.k; ++j) {
-          const int64_t r = __shfl_sync(0xFFFFFFFFu, at, j);
-          const float wt = __shfl_sync(0xFFFFFFFFu, w, j);
-          if (r >= 0 && r < d.rows_capacity && !whole && i < most)
-            sum = fmaf(wt, to_f32(rows[r * d.ldr + c + i]), sum);
+          const int32_t r = __shfl_sync(0xFFFFFFFFu, at_now, j);
+          const float wj = __shfl_sync(0xFFFFFFFFu, w_now, j);
+          if (r >= 0 && !whole && i < most) sum = fmaf(wj, to_f32(rows[r * d.ldr + i]), sum);
         }
         if (!whole && i < most) to[c + i] = from_f32<T>(sum);
       }
@@ -220,18 +233,21 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-// A team of `team` warps owns a token; sums over the columns are joined in shared memory.
-template <typename T, int BYTES>
+// A team of `team` warps owns a token, KA of its rows at a time; a lane's next pieces are asked for
+// before it works on those it has.  Sums over the columns are joined in shared memory.
+template <typename T, int BYTES, int KA>
 __global__ void __launch_bounds__(kRowThreads)
     combine_backward_kernel(const mxg_expert_rows_t d, int team, int64_t pad_items) {
-  constexpr int kElems = Piece<T, BYTES>::kElems;
-  constexpr int kAhead = 4;  // experts at a time
+  using P = Piece<T, BYTES>;
+  constexpr int kElems = P::kElems;
   constexpr int kWarps = kRowThreads / 32;
   __shared__ float part[kWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, teams = kWarps / team;
   const int place = warp % team;  // in the team
+  const bool dots = d.dweight != nullptr, writes = d.rows != nullptr;
   const int64_t pad_blocks = (pad_items + kWarps - 1) / kWarps;
   const int64_t token_blocks = (d.n + teams - 1) / teams;
+  const int cols = static_cast<int>(d.cols), step = team * 32 * kElems;
   for (int64_t b = blockIdx.x; b < pad_blocks + token_blocks; b += gridDim.x) {
     if (b < pad_blocks) {
       if (b * kWarps + warp < pad_items) zero_padding<T, BYTES>(d, b * kWarps + warp);
@@ -249,58 +265,66 @@ __global__ void __launch_bounds__(kRowThreads)
     const T* dy = static_cast<const T*>(d.tokens) + (on ? t : 0) * d.ldt;
     const T* y_rows = static_cast<const T*>(d.y_rows);
     T* rows = static_cast<T*>(d.rows);
-    for (int j0 = 0; j0 < d.k; j0 += kAhead) {
-      float wj[kAhead], dot[kAhead];
-      int64_t r[kAhead];
+    for (int j0 = 0; j0 < d.k; j0 += KA) {
+      float wj[KA], dot[KA];
+      int32_t r[KA];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
+      for (int j = 0; j < KA; ++j) {
         const int from = j0 + j < d.k ? j0 + j : 31;
         r[j] = __shfl_sync(0xFFFFFFFFu, at, from);
         wj[j] = __shfl_sync(0xFFFFFFFFu, w, from);
         if (j0 + j >= d.k) r[j] = -1;
         dot[j] = 0.0f;
       }
-      for (int64_t c = (place * 32 + lane) * kElems; on && c < d.cols; c += team * 32 * kElems) {
-        if (c + kElems <= d.cols) {
-          Piece<T, BYTES> x, y[kAhead];
-          x.load(dy + c);
+      int c = (place * 32 + lane) * kElems;
+      P x, y[KA];
+      auto fetch = [&](P& a, P (&q)[KA], int at_c) {
+        if (!on || at_c + kElems > cols) return;
+        a.load(dy + at_c);
 #pragma unroll
-          for (int j = 0; j < kAhead; ++j)
-            if (r[j] >= 0 && d.dweight != nullptr) y[j].load(y_rows + r[j] * d.ldy + c);
-          float g[kElems];
-          x.get(g);
+        for (int j = 0; j < KA; ++j)
+          if (dots && r[j] >= 0) q[j].load(y_rows + r[j] * d.ldy + at_c);
+      };
+      fetch(x, y, c);
+      for (; on && c + kElems <= cols; c += step) {
+        P x2, y2[KA];
+        fetch(x2, y2, c + step);
+        float g[kElems];
+        x.get(g);
 #pragma unroll
-          for (int j = 0; j < kAhead; ++j) {
-            if (r[j] < 0) continue;
-            float f[kElems];
-            if (d.dweight != nullptr) {
-              y[j].get(f);
+        for (int j = 0; j < KA; ++j) {
+          if (r[j] < 0) continue;
+          float f[kElems];
+          if (dots) {
+            y[j].get(f);
 #pragma unroll
-              for (int i = 0; i < kElems; ++i) dot[j] = fmaf(g[i], f[i], dot[j]);
-            }
-            if (rows != nullptr) {
-#pragma unroll
-              for (int i = 0; i < kElems; ++i) f[i] = wj[j] * g[i];
-              Piece<T, BYTES> o;
-              o.set(f);
-              o.store(rows + r[j] * d.ldr + c);
-            }
+            for (int i = 0; i < kElems; ++i) dot[j] = fmaf(g[i], f[i], dot[j]);
           }
-        } else {
-          for (int64_t i = c; i < d.cols; ++i) {
-            const float g = to_f32(dy[i]);
+          if (writes) {
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-              if (r[j] < 0) continue;
-              if (d.dweight != nullptr) dot[j] = fmaf(g, to_f32(y_rows[r[j] * d.ldy + i]), dot[j]);
-              if (rows != nullptr) rows[r[j] * d.ldr + i] = from_f32<T>(wj[j] * g);
-            }
+            for (int i = 0; i < kElems; ++i) f[i] = wj[j] * g[i];
+            P o;
+            o.set(f);
+            o.store(rows + r[j] * d.ldr + c);
           }
         }
-      }
-      if (d.dweight != nullptr) {
+        x = x2;
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
+        for (int j = 0; j < KA; ++j) y[j] = y2[j];
+      }
+      // the last, shorter piece of a row
+      for (int i = c; on && i < cols && i < c + kElems; ++i) {
+        const float g = to_f32(dy[i]);
+#pragma unroll
+        for (int j = 0; j < KA; ++j) {
+          if (r[j] < 0) continue;
+          if (dots) dot[j] = fmaf(g, to_f32(y_rows[r[j] * d.ldy + i]), dot[j]);
+          if (writes) rows[r[j] * d.ldr + i] = from_f32<T>(wj[j] * g);
+        }
+      }
+      if (dots) {
+#pragma unroll
+        for (int j = 0; j < KA; ++j) {
           float v = dot[j];
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -308,7 +332,7 @@ __global__ void __launch_bounds__(kRowThreads)
         }
       }
     }
-    if (d.dweight != nullptr) {
+    if (dots) {
       if (team > 1) {
         part[warp][lane] = dot_mine;
         __syncthreads();
@@ -359,8 +383,11 @@ cudaError_t run(const mxg_expert_rows_t& d, int op, int num_sms, cudaStream_t st
     // more warps a token where the tokens alone do not fill the device
     int team = 1;
     while (team < 8 && d.n * team < num_sms * 48LL && team * kSpan < d.cols) team *= 2;
-    combine_backward_kernel<T, BYTES>
-        <<<grid_for(pad + d.n * team, num_sms), kRowThreads, 0, stream>>>(d, team, pad);
+    const unsigned grid = grid_for(pad + d.n * team, num_sms);
+    if (d.k <= 2)
+      combine_backward_kernel<T, BYTES, 2><<<grid, kRowThreads, 0, stream>>>(d, team, pad);
+    else
+      combine_backward_kernel<T, BYTES, 4><<<grid, kRowThreads, 0, stream>>>(d, team, pad);
   }
   return cudaGetLastError();
 }

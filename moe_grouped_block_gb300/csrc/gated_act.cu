@@ -24,8 +24,7 @@ __device__ __forceinline__ void load16(const T* p, int n, uint32_t (&w)[8]) {
     asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
                    "=r"(w[6]), "=r"(w[7])
-                 : "l"(p)
-                 : "memory");
+                 : "l"(p));  // (volatile: in order with the stores)
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -187,8 +186,7 @@ __global__ void __launch_bounds__(kActThreads)
     if (GATED) unpack16<T>(uw, u);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float e = __expf(-act_z<ACT>(g[i]));
-      h[i] = __fdividef(g[i], 1.0f + e);
+      h[i] = g[i] * rcp_approx(1.0f + exp_approx(-act_z<ACT>(g[i])));
       if (GATED) h[i] *= u[i];
     }
     if (n > 0) store16<T, VEC>(static_cast<T*>(d.h) + at.row * d.ldh + c, n, h);
@@ -203,64 +201,95 @@ __global__ void __launch_bounds__(kActThreads)
   }
 }
 
+// 16 kept bytes as words, and the values that they stand for.
 template <bool VEC>
-__device__ __forceinline__ void restore16(const uint8_t* q, int n, uint32_t scale_byte,
-                                          float (&f)[16]) {
-  uint32_t w[4] = {};
+__device__ __forceinline__ void load_kept(const uint8_t* q, int n, uint32_t (&w)[4]) {
   if constexpr (VEC) {
-    const uint4 v = *reinterpret_cast<const uint4*>(q);
-    w[0] = v.x;
-    w[1] = v.y;
-    w[2] = v.z;
-    w[3] = v.w;
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "l"(q));
   } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       if (i < n) w[i >> 2] |= static_cast<uint32_t>(q[i]) << (8 * (i & 3));
   }
-  const float scale = e8m0_value(scale_byte);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) e4m3x4_values(w[i], f + 4 * i);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) f[i] *= scale;
 }
 
+// What a thread reads for 16 columns.
+template <typename T, bool GATED, bool VEC>
+struct KeptHalf {
+  uint32_t dh[8], g[4], u[4];
+  uint32_t sf_g, sf_u;
+  __device__ __forceinline__ void load(const mxg_gated_act_t& d, const HalfWalk& at, int64_t live,
+                                       int blocks) {
+    const int c = at.half * 16, cols = static_cast<int>(d.cols);
+    const int n = min(cols - c, 16);
+    if (at.row >= live || n <= 0) return;
+    const uint8_t* q = d.q + at.row * d.ldq + c;
+    const uint8_t* sf =
+        d.sf + at.row * ((GATED ? 2 : 1) * static_cast<int64_t>(blocks)) + (at.half >> 1);
+    load_kept<VEC>(q, n, g);
+    sf_g = sf[0];
+    if (GATED) {
+      load_kept<VEC>(q + cols, n, u);
+      sf_u = sf[blocks];
+    }
+    load16<T, VEC>(static_cast<const T*>(d.dh) + at.row * d.lddh + c, n, dh);
+  }
+};
+
 template <typename T, int ACT, bool GATED, bool VEC>
-__global__ void __launch_bounds__(kActThreads)
+__global__ void __launch_bounds__(kActThreads, 3)
     gated_act_backward_kernel(const mxg_gated_act_t d, int blocks) {
   const int cols = static_cast<int>(d.cols);
   const int64_t live = act_rows(d);
-  const int64_t sf_row = (GATED ? 2 : 1) * static_cast<int64_t>(blocks);
-  for (HalfWalk at(2 * blocks); at.row < live; at.next()) {
+  HalfWalk at(2 * blocks), then = at;
+  KeptHalf<T, GATED, VEC> in;
+  in.load(d, at, live, blocks);
+  for (; at.row < live; at = then) {
+    // the next ones are asked for before these are worked on
+    then.next();
+    KeptHalf<T, GATED, VEC> in2;
+    in2.load(d, then, live, blocks);
     const int c = at.half * 16;
     const int n = min(cols - c, 16);
-    if (n <= 0) continue;
-    const uint8_t* q = d.q + at.row * d.ldq + c;
-    const uint8_t* sf = d.sf + at.row * sf_row + (at.half >> 1);
-    uint32_t dw[8];
-    load16<T, VEC>(static_cast<const T*>(d.dh) + at.row * d.lddh + c, n, dw);
-    float g[16], u[16], dh[16], dg[16];
-    restore16<VEC>(q, n, sf[0], g);
-    if (GATED) restore16<VEC>(q + cols, n, sf[blocks], u);
-    unpack16<T>(dw, dh);
+    if (n > 0) {
+      T* dgate = static_cast<T*>(d.dgate) + at.row * d.lddg + c;
+      T* dup = GATED ? static_cast<T*>(d.dup) + at.row * d.lddu + c : nullptr;
+      T* h = d.h != nullptr ? static_cast<T*>(d.h) + at.row * d.ldh + c : nullptr;
+      const float scale_g = e8m0_value(in.sf_g), scale_u = GATED ? e8m0_value(in.sf_u) : 0.0f;
+      float dg[16], du[16], again[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float x = g[i];
-      const float s = __fdividef(1.0f, 1.0f + __expf(-act_z<ACT>(x)));
-      const float a = x * s;
-      const float slope = fmaf(a * (1.0f - s), act_dz<ACT>(x), s);
-      if (GATED) {
-        dg[i] = dh[i] * u[i] * slope;
-        dh[i] *= a;
-        u[i] *= a;
-      } else {
-        dg[i] = dh[i] * slope;
-        u[i] = a;
+      for (int i = 0; i < 4; ++i) {
+        float g[4], u[4], dh[4];
+        e4m3x4_values(in.g[i], g);
+        if (GATED) e4m3x4_values(in.u[i], u);
+        unpack2<T>(in.dh[2 * i], dh[0], dh[1]);
+        unpack2<T>(in.dh[2 * i + 1], dh[2], dh[3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x = g[j] * scale_g;
+          const float s = rcp_approx(1.0f + exp_approx(-act_z<ACT>(x)));
+          const float a = x * s;
+          const float slope = fmaf(a * (1.0f - s), act_dz<ACT>(x), s);
+          if (GATED) {
+            const float y = u[j] * scale_u;
+            dg[4 * i + j] = dh[j] * y * slope;
+            du[4 * i + j] = dh[j] * a;
+            again[4 * i + j] = y * a;
+          } else {
+            dg[4 * i + j] = dh[j] * slope;
+            again[4 * i + j] = a;
+          }
+        }
       }
+      store16<T, VEC>(dgate, n, dg);
+      if (GATED) store16<T, VEC>(dup, n, du);
+      if (h != nullptr) store16<T, VEC>(h, n, again);
     }
-    store16<T, VEC>(static_cast<T*>(d.dgate) + at.row * d.lddg + c, n, dg);
-    if (GATED) store16<T, VEC>(static_cast<T*>(d.dup) + at.row * d.lddu + c, n, dh);
-    if (d.h != nullptr) store16<T, VEC>(static_cast<T*>(d.h) + at.row * d.ldh + c, n, u);
+    in = in2;
   }
 }
 
