@@ -10,8 +10,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "elem.cuh"
-#include "host16.h"
+#include "rows.cuh"
 
 namespace mxg {
 
@@ -151,13 +150,14 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-// A lane's place in a walk through (token, slice of its columns), `warps` apart.
+// A warp's walk through (token, slice of its columns), all warps of the grid apart.
+template <int NT>
 struct TokenWalk {
   int64_t t, t_step;
   int slice, slice_step, slices;
   __device__ __forceinline__ TokenWalk(int slices) : slices(slices) {
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kRowThreads / 32);
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (NT / 32);
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * (NT / 32) + (threadIdx.x >> 5);
     t = item / slices;
     slice = static_cast<int>(item - t * slices);
     t_step = warps / slices;
@@ -173,121 +173,143 @@ struct TokenWalk {
   }
 };
 
-// A lane's row of its token (lane j: the j-th), or -1, and its weight: 0 where there is none.
-struct Place {
-  int32_t at;
-  float w;
-};
-__device__ __forceinline__ Place place_of(const mxg_expert_rows_t& d, int64_t t) {
+// Where a lane's row of its token starts (lane j: the j-th), in elements, or -1; and its weight, 0
+// where there is none.
+__device__ __forceinline__ int64_t row_start(const mxg_expert_rows_t& d, int64_t t) {
   const int lane = threadIdx.x & 31;
-  Place p = {-1, 0.0f};
-  if (t < d.n && lane < d.k) {
-    const int32_t at = d.row_of[t * d.k + lane];
-    if (at >= 0 && at < d.rows_capacity) {
-      p.at = at;
-      p.w = d.weight != nullptr ? d.weight[t * d.k + lane] : 1.0f;
-    }
-  }
-  return p;
+  int32_t at = -1;
+  if (t < d.n && lane < d.k) at = d.row_of[t * d.k + lane];
+  return at >= 0 && at < d.rows_capacity ? at * d.ldr : -1;
+}
+__device__ __forceinline__ float row_weight(const mxg_expert_rows_t& d, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  if (t >= d.n || lane >= d.k) return 0.0f;
+  const int32_t at = d.row_of[t * d.k + lane];
+  if (at < 0 || at >= d.rows_capacity) return 0.0f;
+  return d.weight != nullptr ? d.weight[t * d.k + lane] : 1.0f;
 }
 
-// Sums of rows that come in pieces of 16 bytes.  A warp's item is a token and 32 pieces of its
-// columns; a lane's pieces of `per` (at most 8) rows are a unit, and every thread has a ring of
-// `depth` units in shared memory that asynchronous copies fill ahead of the sums: with the rows
-// in registers 4 at a time -- as many as leave room for enough warps -- 4096 tokens of 8 rows of
-// 2048 in fp16 took 38.6 us.  No thread reads another's pieces, so there is no barrier.
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads)
-    combine_ring_kernel(const mxg_expert_rows_t d, int slices, int per, int depth) {
+// 16 bytes into shared memory past L1; zeros where `in` is not set (`src` is not read).
+__device__ __forceinline__ void cp_async_16_or_zeros(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
+               : "memory");
+}
+
+// Sums of rows that start on 16 bytes.  A warp's item is a token and 1 KB of its columns, twice 16
+// bytes a lane; a lane's pieces of PER rows are a unit, and every thread has a ring of kDepth units in
+// shared memory that asynchronous copies fill ahead of the sums.  No thread reads another's
+// pieces, so there is no barrier.  4096 tokens of 8 rows of 2048 in fp16: TIMING; with the rows in
+// registers, 4 at a time to leave room for enough warps, 38.6 us; with 16 bytes a lane the
+// instructions for a row's place were the bound, at 33.5 us.
+constexpr int kRingThreads = 128, kDepth = 4;
+
+template <typename T, int PER>
+__global__ void __launch_bounds__(kRingThreads)
+    combine_ring_kernel(const mxg_expert_rows_t d, int slices) {
   extern __shared__ __align__(16) uint8_t ring[];
-  using P = Piece<T, 16>;
-  constexpr int kElems = P::kElems;
-  constexpr uint32_t kPitch = kRowThreads * 16;  // from one row's piece to the next one's
-  const int lane = threadIdx.x & 31;
-  const uint32_t mine = smem_u32(ring) + threadIdx.x * 16, unit = per * kPitch, end = mine + depth * unit;
+  constexpr int kHalf = 16 / static_cast<int>(sizeof(T));  // elements of 16 bytes
+  constexpr uint32_t kPitch = kRingThreads * 16;           // from one half piece to the next one's
+  constexpr uint32_t kUnit = 2 * PER * kPitch;
+  const int lane = threadIdx.x & 31, cols = static_cast<int>(d.cols);
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * 16, end = mine + kDepth * kUnit;
   const T* const rows = static_cast<const T*>(d.rows);
 
-  TokenWalk fill(slices), work = fill;
-  Place fill_now = place_of(d, fill.t), work_now = fill_now;
-  TokenWalk fill_next = fill;
+  TokenWalk<kRingThreads> fill(slices), work = fill, fill_next = fill;
   fill_next.next();
-  Place fill_then = place_of(d, fill_next.t);
+  int64_t fill_row = row_start(d, fill.t), fill_then = row_start(d, fill_next.t);
+  float work_w = row_weight(d, work.t);
   int fill_j = 0;
   uint32_t fill_at = mine;
   auto fill_unit = [&] {
     if (fill.t < d.n) {
-      const int c = (fill.slice * 32 + lane) * kElems;
-      for (int j = 0; j < per; ++j) {
-        const int64_t r = __shfl_sync(0xFFFFFFFFu, fill_now.at, (fill_j + j) & 31);
-        const uint32_t to = fill_at + j * kPitch;
-        if (fill_j + j < d.k && r >= 0) {
-          if (c + kElems <= d.cols) cp_async_16_l2(to, rows + r * d.ldr + c);
-        } else {
-          st_shared_v4(to, 0, 0, 0, 0);
-        }
+      const int c = (fill.slice * 64 + lane) * kHalf;
+      const bool in0 = c + kHalf <= cols, in1 = c + 33 * kHalf <= cols;
+      const T* const from = rows + c;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        // (lanes behind the k-th have no row; past 32 there is none to ask)
+        const int64_t r = __shfl_sync(0xFFFFFFFFu, fill_row, (fill_j + j) & 31);
+        const T* const src = r < 0 ? rows : from + r;
+        cp_async_16_or_zeros(fill_at + 2 * j * kPitch, in0 ? src : rows, in0 && r >= 0);
+        cp_async_16_or_zeros(fill_at + (2 * j + 1) * kPitch, in1 ? src + 32 * kHalf : rows, in1 && r >= 0);
       }
-      fill_j += per;
+      fill_j += PER;
       if (fill_j >= d.k) {
         fill_j = 0;
         fill = fill_next;
-        fill_now = fill_then;
+        fill_row = fill_then;
         fill_next.next();
-        fill_then = place_of(d, fill_next.t);
+        fill_then = row_start(d, fill_next.t);
       }
     }
     cp_async_commit();
-    if ((fill_at += unit) == end) fill_at = mine;
+    if ((fill_at += kUnit) == end) fill_at = mine;
   };
-  for (int i = 0; i < depth - 1; ++i) fill_unit();
+#pragma unroll
+  for (int i = 0; i < kDepth - 1; ++i) fill_unit();
   uint32_t at = mine;
-  for (; work.t < d.n; work.next()) {
-    const Place now = work_now;
-    TokenWalk then = work;
+  TokenWalk<kRingThreads> then = work;
+  for (; work.t < d.n; work = then) {
+    const float w_now = work_w;
     then.next();
-    work_now = place_of(d, then.t);
-    const int c = (work.slice * 32 + lane) * kElems;
-    float acc[kElems];
+    work_w = row_weight(d, then.t);
+    const int c = (work.slice * 64 + lane) * kHalf;
+    F2 acc[kHalf];
 #pragma unroll
-    for (int i = 0; i < kElems; ++i) acc[i] = 0.0f;
-    for (int j0 = 0; j0 < d.k; j0 += per) {
+    for (int i = 0; i < kHalf; ++i) acc[i] = 0;
+    for (int j0 = 0; j0 < d.k; j0 += PER) {
       fill_unit();
-      if (depth > 2)
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
-      else
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-#pragma unroll 4
-      for (int j = 0; j < per; ++j) {
-        const float w = __shfl_sync(0xFFFFFFFFu, now.w, (j0 + j) & 31);
-        P x;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3])
-                     : "r"(at + j * kPitch)
-                     : "memory");
-        float f[kElems];
-        x.get(f);
-        // (a lane past 32 is one of the first again: what lies behind the k-th row is 0)
+      cp_async_wait(kDepth - 1);
 #pragma unroll
-        for (int i = 0; i < kElems; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+      for (int j = 0; j < PER; ++j) {
+        const F2 w = f2(__shfl_sync(0xFFFFFFFFu, w_now, (j0 + j) & 31));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 q = lds16(at + (2 * j + h) * kPitch);
+          const uint32_t word[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int i = 0; i < kHalf / 2; ++i) {
+            float lo, hi;
+            if constexpr (sizeof(T) == 4) {
+              lo = __uint_as_float(word[2 * i]);
+              hi = __uint_as_float(word[2 * i + 1]);
+            } else {
+              unpack2<T>(word[i], lo, hi);
+            }
+            acc[h * kHalf / 2 + i] = fma2(w, f2(lo, hi), acc[h * kHalf / 2 + i]);
+          }
+        }
       }
-      if ((at += unit) == end) at = mine;
+      if ((at += kUnit) == end) at = mine;
     }
-    T* to = static_cast<T*>(d.tokens) + work.t * d.ldt;
-    if (c + kElems <= d.cols) {
-      P y;
-      y.set(acc);
-      y.store(to + c);
-    }
-    // the last, shorter piece of a row
-    if (__any_sync(0xFFFFFFFFu, c < d.cols && c + kElems > d.cols)) {
-      for (int i = 0; i < kElems - 1; ++i) {
-        const bool in = c < d.cols && c + kElems > d.cols && c + i < d.cols;
+    T* const to = static_cast<T*>(d.tokens) + work.t * d.ldt;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (c + (32 * h + 1) * kHalf <= cols) {
+        uint32_t word[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (sizeof(T) == 4)
+            word[i] = __float_as_uint(i & 1 ? f2_hi(acc[h * 2 + i / 2]) : f2_lo(acc[h * 2 + i / 2]));
+          else
+            word[i] = pack2<T>(f2_lo(acc[h * 4 + i]), f2_hi(acc[h * 4 + i]));
+        }
+        *reinterpret_cast<uint4*>(to + c + 32 * h * kHalf) =
+            make_uint4(word[0], word[1], word[2], word[3]);
+      }
+    // what is left of a row whose columns do not end on 16 bytes
+    if (cols % kHalf != 0) {
+      const int64_t row = row_start(d, work.t);
+      const int first = cols / kHalf * kHalf;
+      const bool last = first == c || first == c + 32 * kHalf;
+      for (int i = first; i < cols; ++i) {
         float sum = 0.0f;
         for (int j = 0; j < d.k; ++j) {
-          const int64_t r = __shfl_sync(0xFFFFFFFFu, now.at, j);
-          const float w = __shfl_sync(0xFFFFFFFFu, now.w, j);
-          if (r >= 0 && in) sum = fmaf(w, to_f32(rows[r * d.ldr + c + i]), sum);
+          const int64_t r = __shfl_sync(0xFFFFFFFFu, row, j);
+          const float w = __shfl_sync(0xFFFFFFFFu, w_now, j);
+          if (r >= 0 && last) sum = fmaf(w, to_f32(rows[r + i]), sum);
         }
-        if (in) to[c + i] = from_f32<T>(sum);
+        if (last) to[i] = from_f32<T>(sum);
       }
     }
   }
@@ -300,26 +322,29 @@ __global__ void __launch_bounds__(kRowThreads)
   constexpr int kAhead = 8;
   const int lane = threadIdx.x & 31;
   const T* const rows = static_cast<const T*>(d.rows);
-  TokenWalk at(slices), then = at;
-  Place next = place_of(d, at.t);
+  TokenWalk<kRowThreads> at(slices), then = at;
+  int64_t row = row_start(d, at.t);
+  float weight = row_weight(d, at.t);
   for (; at.t < d.n; at = then) {
-    const Place now = next;
+    const int64_t row_now = row;
+    const float w_now = weight;
     then.next();
-    next = place_of(d, then.t);
+    row = row_start(d, then.t);
+    weight = row_weight(d, then.t);
     const int c = at.slice * 32 + lane;
     float sum = 0.0f;
     for (int j0 = 0; j0 < d.k; j0 += kAhead) {
       T x[kAhead];
-      int32_t r[kAhead];
+      int64_t r[kAhead];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        r[j] = __shfl_sync(0xFFFFFFFFu, now.at, (j0 + j) & 31);
-        if (j0 + j >= d.k || c >= d.cols) r[j] = -1;
-        if (r[j] >= 0) x[j] = rows[r[j] * d.ldr + c];
+        r[j] = __shfl_sync(0xFFFFFFFFu, row_now, (j0 + j) & 31);
+        if (c >= d.cols) r[j] = -1;
+        if (r[j] >= 0) x[j] = rows[r[j] + c];
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        const float w = __shfl_sync(0xFFFFFFFFu, now.w, (j0 + j) & 31);
+        const float w = __shfl_sync(0xFFFFFFFFu, w_now, (j0 + j) & 31);
         if (r[j] >= 0) sum = fmaf(w, to_f32(x[j]), sum);
       }
     }
@@ -457,29 +482,27 @@ unsigned grid_for(int64_t warps, int num_sms) {
 
 int64_t slices_of(int64_t cols, int per) { return (cols + per - 1) / per; }
 
-// Rings of 200 KB an SM at most: units of up to 8 rows, 4 or 3 deep, in as many CTAs as fit.  The
-// shared memory that a kernel may be launched with is set once per device, to the most that any
-// call takes.
-template <typename T>
+// Units of 1, 2 or 4 rows, whichever holds k in fewest; as many CTAs as an SM has room for.  The
+// shared memory that a kernel may be launched with is set once per device.
+template <typename T, int PER>
 cudaError_t run_combine_ring(const mxg_expert_rows_t& d, int num_sms, cudaStream_t stream) {
-  constexpr int kMost = 200 * 1024, kPitch = kRowThreads * 16, kMaxDev = 64;
+  constexpr int kSmem = kDepth * 2 * PER * kRingThreads * 16, kMaxDev = 64;
+  constexpr int kCtas = std::min(8, 220 * 1024 / (kSmem + 1024));
   static std::atomic<bool> ready[kMaxDev];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
   if (!ready[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(combine_ring_kernel<T>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMost / 2);
+    const cudaError_t e = cudaFuncSetAttribute(combine_ring_kernel<T, PER>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     ready[dev].store(true, std::memory_order_release);
   }
-  const int per = std::min<int>(d.k, 8), depth = 3;
-  const int smem = per * depth * kPitch;
-  const int ctas = std::min(6, kMost / smem);
-  const int64_t slices = slices_of(d.cols, 32 * Piece<T, 16>::kElems);
-  const int64_t blocks = (d.n * slices + kRowThreads / 32 - 1) / (kRowThreads / 32);
+  const int64_t slices = slices_of(d.cols, 32 * 32 / static_cast<int>(sizeof(T)));
+  const int64_t blocks = (d.n * slices + kRingThreads / 32 - 1) / (kRingThreads / 32);
   const unsigned grid =
-      static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * ctas));
-  combine_ring_kernel<T><<<grid, kRowThreads, smem, stream>>>(d, static_cast<int>(slices), per, depth);
+      static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * kCtas));
+  combine_ring_kernel<T, PER>
+      <<<grid, kRingThreads, kSmem, stream>>>(d, static_cast<int>(slices));
   return cudaGetLastError();
 }
 
@@ -497,7 +520,9 @@ cudaError_t run(const mxg_expert_rows_t& d, int op, int num_sms, cudaStream_t st
             d, static_cast<int>(slices), pad);
   } else if (op == 1) {
     if constexpr (BYTES >= 16) {
-      return run_combine_ring<T>(d, num_sms, stream);
+      if (d.k == 1) return run_combine_ring<T, 1>(d, num_sms, stream);
+      if (d.k == 2) return run_combine_ring<T, 2>(d, num_sms, stream);
+      return run_combine_ring<T, 4>(d, num_sms, stream);
     } else {
       const int64_t slices = slices_of(d.cols, 32);
       combine_kernel<T><<<grid_for(d.n * slices, num_sms), kRowThreads, 0, stream>>>(
