@@ -15,6 +15,7 @@ import ctypes
 import math
 import os
 import re
+import struct
 
 import torch
 
@@ -206,18 +207,18 @@ def load() -> ctypes.CDLL:
         L.mxg_route_workspace_bytes.restype = sz
         L.mxg_route_workspace_bytes.argtypes = [i64, c_int, c_int]
         L.mxg_route.restype = c_int
-        L.mxg_route.argtypes = [ctypes.POINTER(Route), vp, sz, vp, vp]
+        L.mxg_route.argtypes = [vp, vp, sz, vp, vp]
         L.mxg_route_rows.restype = c_int
         L.mxg_route_rows.argtypes = [vp, i64, c_int, c_int, c_int, i64, i64, vp, vp, vp, vp, sz, vp,
                                      vp]
         L.mxg_route_backward.restype = c_int
-        L.mxg_route_backward.argtypes = [ctypes.POINTER(RouteGrad), vp]
+        L.mxg_route_backward.argtypes = [vp, vp]
         for f in (L.mxg_dispatch, L.mxg_combine, L.mxg_combine_backward):
             f.restype = c_int
-            f.argtypes = [ctypes.POINTER(ExpertRows), vp]
+            f.argtypes = [vp, vp]
         for f in (L.mxg_gated_act, L.mxg_gated_act_backward):
             f.restype = c_int
-            f.argtypes = [ctypes.POINTER(GatedAct), vp]
+            f.argtypes = [vp, vp]
         _lib = L
     return _lib
 
@@ -608,55 +609,96 @@ def mxg_grad_clip(grads: GradList, max_norm: float, norm: torch.Tensor, workspac
 
 
 # ------------------------------------------------ around the products of an expert block
-def _whole(t, dtypes, shape: tuple, name: str) -> None:
-    """A contiguous tensor of one of these types with as many elements as the shape, or none."""
-    if t is None:
-        return
-    if t.dtype not in dtypes or t.numel() != math.prod(shape) or not t.is_contiguous():
-        raise ValueError("%s: expected %s contiguous elements of %s: got %s of %s"
-                         % (name, shape, dtypes[0], tuple(t.shape), t.dtype))
+# A call of these takes 6 to 10 us of the host's time, of which every tensor's checks are some:
+# they are made in one place, on the way to its address, and a descriptor is packed into bytes at
+# once (a ctypes structure of 20 fields takes 2.5 us to fill).
+_PACK = {ctypes.c_int: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_void_p: "P"}
 
 
-def _matrix(t, dtype, shape: tuple, name: str) -> int:
-    """_ld of a [rows, cols] matrix of this type and shape, or of none."""
-    if t is None:
-        return 0
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError("%s: expected %s of %s: got %s of %s"
-                         % (name, tuple(shape), dtype, tuple(t.shape), t.dtype))
-    return _ld(t)
+def _packer(desc):
+    """A function that packs a descriptor's fields, in their order, as C lays them out."""
+    return struct.Struct("@" + "".join(_PACK[kind] for _, kind in desc._fields_)).pack
 
 
-def _one_device(tensors) -> None:
-    """All on the device that the launch goes to."""
-    here = None
-    for t in tensors:
-        if t is not None and t.is_cuda:
-            if here is None:
-                here = torch.cuda.current_device()
-            if t.get_device() != here:
-                raise ValueError("a tensor on %s: the current device is %d" % (t.device, here))
-
-
+_pack_route, _pack_route_grad = _packer(Route), _packer(RouteGrad)
+_pack_expert_rows, _pack_gated_act = _packer(ExpertRows), _packer(GatedAct)
 _I32, _I64, _FP32 = (torch.int32,), (torch.int64,), (torch.float32,)
 _MASK, _BYTES = (torch.uint8, torch.bool), (torch.uint8, torch.float8_e4m3fn)
 
 
+def _here() -> int:
+    """The device that launches go to."""
+    return torch.cuda.current_device()
+
+
+def _on(t, here: int) -> int:
+    """The address of a tensor on the current device."""
+    if t.get_device() != here:
+        if not t.is_cuda:
+            raise ValueError("libmxg takes device tensors; got a %s tensor" % t.device)
+        raise ValueError("a tensor on %s: the current device is %d" % (t.device, here))
+    return t.data_ptr()
+
+
+def _whole(t, dtypes: tuple, n: int, name: str, here: int) -> int:
+    """The address of a contiguous tensor of n elements of one of these types; 0 of none."""
+    if t is None:
+        return 0
+    if t.dtype not in dtypes or t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s: expected %d contiguous elements of %s: got %s of %s"
+                         % (name, n, dtypes[0], tuple(t.shape), t.dtype))
+    return _on(t, here)
+
+
+def _matrix(t, dtype, shape, name: str, here: int) -> tuple:
+    """(address, elements between the rows) of a [rows, cols] matrix of this type; zeros of none."""
+    if t is None:
+        return 0, 0
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError("%s: expected %s of %s: got %s of %s"
+                         % (name, tuple(shape), dtype, tuple(t.shape), t.dtype))
+    return _on(t, here), _ld(t)
+
+
+def _any(t, here: int) -> int:
+    """The address of a device tensor (or the number that is given for one); 0 of none."""
+    if t is None or isinstance(t, int):
+        return t or 0
+    return _on(t, here)
+
+
+def _stream_on(stream, here: int):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(here)
+    return _s(stream)
+
+
 def _choices(expert, name: str) -> tuple:
     """(tokens, k) of a [tokens, k] tensor of choices."""
-    if expert.dim() != 2:
-        raise ValueError("%s: expected [tokens, k]: got %s" % (name, tuple(expert.shape)))
-    return expert.shape[0], expert.shape[1]
+    shape = expert.shape
+    if len(shape) != 2:
+        raise ValueError("%s: expected [tokens, k]: got %s" % (name, tuple(shape)))
+    return shape
 
 
-def _rows_wanted(row_of, group_ws, tokens: int, k: int, experts: int, align: int,
-                 rows_capacity) -> int:
-    """Checks the plan's tensors; the rows that always suffice where none are given."""
+def _logits(t, tokens: int) -> tuple:
+    """(type, experts) of the router's logits."""
+    shape, kind = t.shape, _DTYPES.get(t.dtype)
+    if len(shape) != 2 or shape[0] != tokens or kind is None:
+        raise ValueError("logits: expected [%d, experts] of fp32, bf16 or fp16: got %s of %s"
+                         % (tokens, tuple(shape), t.dtype))
+    return kind, shape[1]
+
+
+def _rows_wanted(row_of, group_ws, choices: int, experts: int, align: int, rows_capacity,
+                 here: int) -> tuple:
+    """(row_of, group_ws, capacity); the rows that always suffice where none are given."""
     if (row_of is None) != (group_ws is None):
         raise ValueError("row_of and group_ws: both or neither")
-    _whole(row_of, _I32, (tokens, k), "row_of")
-    _whole(group_ws, _I64, (2 * experts + 1,), "group_ws")
-    return tokens * k + experts * (align - 1) if rows_capacity is None else rows_capacity
+    if rows_capacity is None:
+        rows_capacity = choices + experts * (align - 1)
+    return (_whole(row_of, _I32, choices, "row_of", here),
+            _whole(group_ws, _I64, 2 * experts + 1, "group_ws", here), rows_capacity)
 
 
 def mxg_route_workspace_bytes(tokens: int, experts: int, k: int) -> int:
@@ -671,103 +713,90 @@ def mxg_route(logits: torch.Tensor, expert: torch.Tensor, weight: torch.Tensor,
     """logits: [tokens, experts] (rows may be strided); expert, weight, row_of: [tokens, k];
     mask: uint8 or bool [tokens].  rows_capacity: by default the rows that always suffice,
     tokens * k + experts * (align - 1)."""
+    here = _here()
     tokens, k = _choices(expert, "expert")
-    if logits.dim() != 2 or logits.shape[0] != tokens or logits.dtype not in _DTYPES:
-        raise ValueError("logits: expected [%d, experts] of fp32, bf16 or fp16: got %s of %s"
-                         % (tokens, tuple(logits.shape), logits.dtype))
-    E = logits.shape[1]
-    _whole(expert, _I32, (tokens, k), "expert")
-    _whole(weight, _FP32, (tokens, k), "weight")
-    _whole(counts, _I32, (E,), "counts")
-    _whole(mask, _MASK, (tokens,), "mask")
-    _whole(loss, _FP32, (1,), "loss")
-    _whole(slope, _FP32, (E,), "slope")
-    capacity = _rows_wanted(row_of, group_ws, tokens, k, E, align, rows_capacity)
-    _one_device((logits, expert, weight, counts, mask, loss, slope, row_of, group_ws, workspace,
-                 dev_status))
-    d = Route(_DTYPES[logits.dtype], tokens, E, k, _p(logits), _ld(logits), _p(mask), score,
-              int(normalize), scale, balance, _p(expert), _p(weight), _p(counts), _p(loss),
-              _p(slope), _p(row_of), _p(group_ws), align, capacity, last_dim)
+    kind, E = _logits(logits, tokens)
+    n = tokens * k
+    row, groups, capacity = _rows_wanted(row_of, group_ws, n, E, align, rows_capacity, here)
+    d = _pack_route(kind, tokens, E, k, _on(logits, here), _ld(logits),
+                    _whole(mask, _MASK, tokens, "mask", here), score, normalize, scale, balance,
+                    _whole(expert, _I32, n, "expert", here), _whole(weight, _FP32, n, "weight", here),
+                    _whole(counts, _I32, E, "counts", here), _whole(loss, _FP32, 1, "loss", here),
+                    _whole(slope, _FP32, E, "slope", here), row, groups, align, capacity, last_dim)
     _check("mxg_route",
-           load().mxg_route(ctypes.byref(d), _p(workspace),
-                            0 if workspace is None else workspace.nbytes, _p(dev_status),
-                            _s(stream)))
+           load().mxg_route(d, _any(workspace, here), 0 if workspace is None else workspace.nbytes,
+                            _any(dev_status, here), _stream_on(stream, here)))
 
 
 def mxg_route_rows(expert: torch.Tensor, counts: torch.Tensor, row_of=None, group_ws=None,
                    align: int = 1, rows_capacity=None, last_dim: int = 1, workspace=None,
                    dev_status=None, stream=None) -> None:
     """expert: int32 [tokens, k]; counts: int32 [experts]."""
+    here = _here()
     tokens, k = _choices(expert, "expert")
-    E = counts.numel()
-    _whole(expert, _I32, (tokens, k), "expert")
-    _whole(counts, _I32, (E,), "counts")
-    capacity = _rows_wanted(row_of, group_ws, tokens, k, E, align, rows_capacity)
-    _one_device((expert, counts, row_of, group_ws, workspace, dev_status))
+    E, n = counts.numel(), tokens * k
+    row, groups, capacity = _rows_wanted(row_of, group_ws, n, E, align, rows_capacity, here)
     _check("mxg_route_rows",
-           load().mxg_route_rows(_p(expert), tokens, E, k, align, capacity, last_dim, _p(counts),
-                                 _p(row_of), _p(group_ws), _p(workspace),
-                                 0 if workspace is None else workspace.nbytes, _p(dev_status),
-                                 _s(stream)))
+           load().mxg_route_rows(_whole(expert, _I32, n, "expert", here), tokens, E, k, align,
+                                 capacity, last_dim, _whole(counts, _I32, E, "counts", here), row,
+                                 groups, _any(workspace, here),
+                                 0 if workspace is None else workspace.nbytes,
+                                 _any(dev_status, here), _stream_on(stream, here)))
 
 
 def mxg_route_backward(logits: torch.Tensor, expert: torch.Tensor, dlogits: torch.Tensor,
                        dweight=None, score: int = MXG_SCORE_SOFTMAX, normalize: bool = True,
                        scale: float = 1.0, slope=None, dloss=None, stream=None) -> None:
     """logits, expert, slope: as mxg_route took and wrote them; dlogits: like logits."""
+    here = _here()
     tokens, k = _choices(expert, "expert")
-    if logits.dim() != 2 or logits.shape[0] != tokens or logits.dtype not in _DTYPES:
-        raise ValueError("logits: expected [%d, experts] of fp32, bf16 or fp16: got %s of %s"
-                         % (tokens, tuple(logits.shape), logits.dtype))
-    E = logits.shape[1]
-    _whole(expert, _I32, (tokens, k), "expert")
-    _whole(dweight, _FP32, (tokens, k), "dweight")
-    _whole(slope, _FP32, (E,), "slope")
-    _whole(dloss, _FP32, (1,), "dloss")
-    ldd = _matrix(dlogits, logits.dtype, logits.shape, "dlogits")
-    _one_device((logits, expert, dlogits, dweight, slope, dloss))
-    d = RouteGrad(_DTYPES[logits.dtype], tokens, E, k, _p(logits), _ld(logits), _p(expert), score,
-                  int(normalize), scale, _p(dweight), _p(slope), _p(dloss), _p(dlogits), ldd)
-    _check("mxg_route_backward", load().mxg_route_backward(ctypes.byref(d), _s(stream)))
+    kind, E = _logits(logits, tokens)
+    n = tokens * k
+    d_at, ldd = _matrix(dlogits, logits.dtype, logits.shape, "dlogits", here)
+    d = _pack_route_grad(kind, tokens, E, k, _on(logits, here), _ld(logits),
+                         _whole(expert, _I32, n, "expert", here), score, normalize, scale,
+                         _whole(dweight, _FP32, n, "dweight", here),
+                         _whole(slope, _FP32, E, "slope", here),
+                         _whole(dloss, _FP32, 1, "dloss", here), d_at, ldd)
+    _check("mxg_route_backward", load().mxg_route_backward(d, _stream_on(stream, here)))
 
 
-def _expert_rows(fn: str, tokens, rows, row_of, weight=None, y_rows=None, dweight=None, counts=None,
-                 group_ws=None, stream=None) -> None:
+def _expert_rows(fn: str, tokens, rows, row_of, weight, y_rows, dweight, counts, group_ws,
+                 stream) -> None:
+    here = _here()
     n, k = _choices(row_of, "row_of")
-    if tokens.dim() != 2 or tokens.shape[0] != n or tokens.dtype not in _DTYPES:
+    shape, dtype = tokens.shape, tokens.dtype
+    kind = _DTYPES.get(dtype)
+    if len(shape) != 2 or shape[0] != n or kind is None:
         raise ValueError("expected [%d, cols] of fp32, bf16 or fp16: got %s of %s"
-                         % (n, tuple(tokens.shape), tokens.dtype))
-    cols, like = tokens.shape[1], y_rows if rows is None else rows
+                         % (n, tuple(shape), dtype))
+    cols, like = shape[1], y_rows if rows is None else rows
     capacity = 0 if like is None else like.shape[0]
-    _whole(row_of, _I32, (n, k), "row_of")
-    _whole(weight, _FP32, (n, k), "weight")
-    _whole(dweight, _FP32, (n, k), "dweight")
-    ldr = _matrix(rows, tokens.dtype, (capacity, cols), "rows")
-    ldy = _matrix(y_rows, tokens.dtype, (capacity, cols), "y_rows")
+    rows_at, ldr = _matrix(rows, dtype, (capacity, cols), "rows", here)
+    y_at, ldy = _matrix(y_rows, dtype, (capacity, cols), "y_rows", here)
     if (counts is None) != (group_ws is None):
         raise ValueError("counts and group_ws: both or neither")
     experts = 0 if counts is None else counts.numel()
-    _whole(counts, _I32, (experts,), "counts")
-    _whole(group_ws, _I64, (2 * experts + 1,), "group_ws")
-    _one_device((tokens, rows, row_of, weight, y_rows, dweight, counts, group_ws))
-    d = ExpertRows(_DTYPES[tokens.dtype], n, cols, k, experts, capacity, _p(tokens), _ld(tokens),
-                   _p(rows), ldr, _p(row_of), _p(weight), _p(y_rows), ldy, _p(dweight), _p(counts),
-                   _p(group_ws))
-    _check(fn, getattr(load(), fn)(ctypes.byref(d), _s(stream)))
+    d = _pack_expert_rows(kind, n, cols, k, experts, capacity, _on(tokens, here), _ld(tokens), rows_at,
+                          ldr, _whole(row_of, _I32, n * k, "row_of", here),
+                          _whole(weight, _FP32, n * k, "weight", here), y_at, ldy,
+                          _whole(dweight, _FP32, n * k, "dweight", here),
+                          _whole(counts, _I32, experts, "counts", here),
+                          _whole(group_ws, _I64, 2 * experts + 1, "group_ws", here))
+    _check(fn, getattr(load(), fn)(d, _stream_on(stream, here)))
 
 
 def mxg_dispatch(tokens: torch.Tensor, row_of: torch.Tensor, rows: torch.Tensor, counts=None,
                  group_ws=None, stream=None) -> None:
     """tokens [n, cols] to rows [rows_capacity, cols] (rows of both may be strided); counts and
     group_ws: to set the groups' padding rows to 0."""
-    _expert_rows("mxg_dispatch", tokens, rows, row_of, counts=counts, group_ws=group_ws,
-                 stream=stream)
+    _expert_rows("mxg_dispatch", tokens, rows, row_of, None, None, None, counts, group_ws, stream)
 
 
 def mxg_combine(rows: torch.Tensor, row_of: torch.Tensor, tokens: torch.Tensor, weight=None,
                 stream=None) -> None:
     """tokens[t] = the sum of rows[row_of[t, j]], times weight[t, j] where that is given."""
-    _expert_rows("mxg_combine", tokens, rows, row_of, weight=weight, stream=stream)
+    _expert_rows("mxg_combine", tokens, rows, row_of, weight, None, None, None, None, stream)
 
 
 def mxg_combine_backward(dtokens: torch.Tensor, row_of: torch.Tensor, weight, drows, y_rows=None,
@@ -776,64 +805,65 @@ def mxg_combine_backward(dtokens: torch.Tensor, row_of: torch.Tensor, weight, dr
     the rows that mxg_combine summed, for dweight."""
     if drows is None and dweight is None:
         raise ValueError("drows, dweight: one of them at least")
-    _expert_rows("mxg_combine_backward", dtokens, drows, row_of, weight=weight, y_rows=y_rows,
-                 dweight=dweight, counts=counts, group_ws=group_ws, stream=stream)
+    _expert_rows("mxg_combine_backward", dtokens, drows, row_of, weight, y_rows, dweight, counts,
+                 group_ws, stream)
 
 
 def _act_blocks(cols: int) -> int:
     return (cols + 31) // 32
 
 
-def _kept(q, sf, rows: int, cols: int, parts: int) -> int:
-    """Checks an 8-bit checkpoint of `parts` matrices; the bytes between its rows."""
+def _kept(q, sf, rows: int, cols: int, parts: int, here: int) -> tuple:
+    """(q, bytes between its rows, sf) of an 8-bit checkpoint of `parts` matrices, or zeros."""
     if (q is None) != (sf is None):
         raise ValueError("q and sf: both or neither")
     if q is None:
-        return 0
+        return 0, 0, 0
     if q.dtype not in _BYTES or q.shape != (rows, parts * cols):
         raise ValueError("q: expected %s bytes: got %s of %s"
                          % ((rows, parts * cols), tuple(q.shape), q.dtype))
-    _whole(sf, (torch.uint8,), (rows, parts * _act_blocks(cols)), "sf")
-    return _ld(q)
+    return _on(q, here), _ld(q), _whole(sf, _BYTES[:1], rows * parts * _act_blocks(cols), "sf", here)
+
+
+def _act_shape(t, name: str) -> tuple:
+    """(type, rows, cols)"""
+    shape, kind = t.shape, _DTYPES.get(t.dtype)
+    if len(shape) != 2 or kind is None:
+        raise ValueError("%s: expected [rows, cols]: got %s of %s" % (name, tuple(shape), t.dtype))
+    return kind, shape[0], shape[1]
 
 
 def mxg_gated_act(gate: torch.Tensor, h: torch.Tensor, up=None, act: int = MXG_ACT_SILU, q=None,
                   sf=None, group_ws=None, G: int = 0, stream=None) -> None:
     """h = act(gate) * up, [rows, cols] (rows may be strided: gate and up are often the halves of
     one product); q, sf: where the inputs are kept (alloc_act_checkpoint)."""
-    if gate.dim() != 2 or gate.dtype not in _DTYPES:
-        raise ValueError("gate: expected [rows, cols]: got %s of %s" % (tuple(gate.shape), gate.dtype))
-    rows, cols = gate.shape
+    here = _here()
+    kind, rows, cols = _act_shape(gate, "gate")
     parts = 1 if up is None else 2
-    ldu = _matrix(up, gate.dtype, gate.shape, "up")
-    ldh = _matrix(h, gate.dtype, gate.shape, "h")
-    ldq = _kept(q, sf, rows, cols, parts)
-    _whole(group_ws, _I64, (2 * G + 1,), "group_ws")
-    _one_device((gate, up, h, q, sf, group_ws))
-    d = GatedAct(dtype=_DTYPES[gate.dtype], act=act, rows=rows, cols=cols, gated=parts - 1, G=G,
-                 group_ws=_p(group_ws), gate=_p(gate), ldg=_ld(gate), up=_p(up), ldu=ldu, h=_p(h),
-                 ldh=ldh, q=_p(q), ldq=ldq, sf=_p(sf))
-    _check("mxg_gated_act", load().mxg_gated_act(ctypes.byref(d), _s(stream)))
+    up_at, ldu = _matrix(up, gate.dtype, gate.shape, "up", here)
+    h_at, ldh = _matrix(h, gate.dtype, gate.shape, "h", here)
+    q_at, ldq, sf_at = _kept(q, sf, rows, cols, parts, here)
+    d = _pack_gated_act(kind, act, rows, cols, parts - 1, G,
+                        _whole(group_ws, _I64, 2 * G + 1, "group_ws", here), _on(gate, here), _ld(gate),
+                        up_at, ldu, h_at, ldh, q_at, ldq, sf_at, 0, 0, 0, 0, 0, 0)
+    _check("mxg_gated_act", load().mxg_gated_act(d, _stream_on(stream, here)))
 
 
 def mxg_gated_act_backward(q: torch.Tensor, sf: torch.Tensor, dh: torch.Tensor, dgate: torch.Tensor,
                            dup=None, act: int = MXG_ACT_SILU, h=None, group_ws=None, G: int = 0,
                            stream=None) -> None:
     """The gradients of gate and up from the checkpoint, and h again where it is given."""
-    if dh.dim() != 2 or dh.dtype not in _DTYPES:
-        raise ValueError("dh: expected [rows, cols]: got %s of %s" % (tuple(dh.shape), dh.dtype))
-    rows, cols = dh.shape
+    here = _here()
+    kind, rows, cols = _act_shape(dh, "dh")
     parts = 1 if dup is None else 2
-    lddg = _matrix(dgate, dh.dtype, dh.shape, "dgate")
-    lddu = _matrix(dup, dh.dtype, dh.shape, "dup")
-    ldh = _matrix(h, dh.dtype, dh.shape, "h")
-    ldq = _kept(q, sf, rows, cols, parts)
-    _whole(group_ws, _I64, (2 * G + 1,), "group_ws")
-    _one_device((q, sf, dh, dgate, dup, h, group_ws))
-    d = GatedAct(dtype=_DTYPES[dh.dtype], act=act, rows=rows, cols=cols, gated=parts - 1, G=G,
-                 group_ws=_p(group_ws), h=_p(h), ldh=ldh, q=_p(q), ldq=ldq, sf=_p(sf), dh=_p(dh),
-                 lddh=_ld(dh), dgate=_p(dgate), lddg=lddg, dup=_p(dup), lddu=lddu)
-    _check("mxg_gated_act_backward", load().mxg_gated_act_backward(ctypes.byref(d), _s(stream)))
+    dgate_at, lddg = _matrix(dgate, dh.dtype, dh.shape, "dgate", here)
+    dup_at, lddu = _matrix(dup, dh.dtype, dh.shape, "dup", here)
+    h_at, ldh = _matrix(h, dh.dtype, dh.shape, "h", here)
+    q_at, ldq, sf_at = _kept(q, sf, rows, cols, parts, here)
+    d = _pack_gated_act(kind, act, rows, cols, parts - 1, G,
+                        _whole(group_ws, _I64, 2 * G + 1, "group_ws", here), 0, 0, 0, 0, h_at, ldh, q_at,
+                        ldq, sf_at, _on(dh, here), _ld(dh), dgate_at, lddg, dup_at, lddu)
+    _check("mxg_gated_act_backward", load().mxg_gated_act_backward(d, _stream_on(stream, here)))
 
 
 def mxg_status_string(code: int) -> str:
