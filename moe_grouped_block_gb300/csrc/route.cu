@@ -217,8 +217,8 @@ __device__ __forceinline__ int sum_chunks(V* to, const V* from, int pitch, int c
 
 // Everything that needs the whole batch's counts, by the CTA of chunk c, of NT threads
 // (at least as many as experts, but for ONE).  ONE: this CTA has all tokens, whose counts and
-// sums are in `sh`.  The first CTA writes counts and group_ws; the last one, which has no
-// tokens where there are several, slope and loss.
+// sums are in `sh`.  Else the CTA behind the last chunk's, which has no tokens, writes counts,
+// group_ws, slope and loss.
 template <int NT, bool ONE, int BUF>
 __device__ __forceinline__ void finish_chunk(const RowPlan& p, RouteShared<BUF>& sh,
                                              const RouteWs& ws, const int32_t* expert, int c) {
@@ -234,7 +234,8 @@ __device__ __forceinline__ void finish_chunk(const RowPlan& p, RouteShared<BUF>&
   const int64_t begin = static_cast<int64_t>(c) * p.per;
   const int tokens_here =
       p.row_of == nullptr ? 0 : static_cast<int>(max(min(begin + p.per, p.tokens) - begin, int64_t{0}));
-  const int warps = min(kWarps, BUF / E);
+  const int pitch = E | 1;  // of a warp's words: a column of them lies on different banks
+  const int warps = min(kWarps, BUF / pitch);
   const int rounds = (tokens_here + 32 * warps - 1) / (32 * warps);
   const int each = rounds == 0 ? 0 : (tokens_here + rounds * warps - 1) / (rounds * warps);
   const int inverse = (65536 + p.k - 1) / p.k;  // i / k for i below 1024
@@ -257,9 +258,17 @@ __device__ __forceinline__ void finish_chunk(const RowPlan& p, RouteShared<BUF>&
   hold();
   // tokens of each expert, in all chunks and in those before this one
   int parts = 1;
+  const bool losses = (ONE || c == p.chunks) && (p.loss != nullptr || p.slope != nullptr);
   if (!ONE) {
-    parts = sum_chunks<NT, true, uint4>(buf, reinterpret_cast<const uint32_t*>(ws.hist), ws.pitch,
-                                        p.chunks, c);
+    const uint32_t* hist = reinterpret_cast<const uint32_t*>(ws.hist);
+    if (c == p.chunks) {  // no tokens: the sums of p in the place of those before them
+      parts = sum_chunks<NT, false, uint4>(buf, hist, ws.pitch, p.chunks, 0);
+      if (losses && p.loss != nullptr)
+        sum_chunks<NT, false, float4>(reinterpret_cast<float*>(buf) + kBufWords / 2, ws.psum, ws.pitch,
+                                      p.chunks, 0);
+    } else {
+      parts = sum_chunks<NT, true, uint4>(buf, hist, ws.pitch, p.chunks, c);
+    }
     __syncthreads();
   }
   // starts of the padded groups: a scan over a thread's experts, the warp and the CTA
@@ -307,7 +316,7 @@ __device__ __forceinline__ void finish_chunk(const RowPlan& p, RouteShared<BUF>&
     if (e < E) {
       sh.start[e] = start + before[i];  // of this chunk's tokens
       if (!ONE) sh.hist[e] = static_cast<int32_t>(total[i]);
-      if (c == 0) {
+      if (ONE || c == p.chunks) {
         if (p.counts != nullptr) p.counts[e] = static_cast<int32_t>(total[i]);
         if (p.group_ws != nullptr) {
           const uint32_t from = min(start, p.capacity), to = min(start + size[i], p.capacity);
@@ -322,17 +331,14 @@ __device__ __forceinline__ void finish_chunk(const RowPlan& p, RouteShared<BUF>&
   }
   __syncthreads();
 
-  if (c == static_cast<int>(gridDim.x) - 1 && (p.loss != nullptr || p.slope != nullptr)) {
-    float* part_p = reinterpret_cast<float*>(sh.buf);
-    int tokens = 0, p_parts = 1;
+  if (losses) {
+    const float* part_p = reinterpret_cast<const float*>(buf) + kBufWords / 2;
+    int tokens = 0;
     if (ONE) {
       tokens = sh.live;
     } else {
       for (int h = lane; h < p.chunks; h += 32) tokens += ws.live[h];
       tokens = __reduce_add_sync(0xFFFFFFFFu, tokens);
-      if (p.loss != nullptr)
-        p_parts = sum_chunks<NT, false, float4>(part_p, ws.psum, ws.pitch, p.chunks, 0);
-      __syncthreads();
     }
     // all and tokens are 0 together
     const float unit =
@@ -347,7 +353,7 @@ __device__ __forceinline__ void finish_chunk(const RowPlan& p, RouteShared<BUF>&
         if (ONE) {
           v = sh.psum[e];
         } else {
-          for (int part = 0; part < p_parts; ++part) v += part_p[part * ws.pitch + e];
+          for (int part = 0; part < parts; ++part) v += part_p[part * ws.pitch + e];
         }
         mine += s * v;
       }
@@ -366,7 +372,7 @@ __device__ __forceinline__ void finish_chunk(const RowPlan& p, RouteShared<BUF>&
   // A choice's place among its expert's: those of earlier tokens of the warp, then of earlier
   // warps, chunks and experts.  The warp's tokens of an expert are bits of a word (a token
   // names an expert once), so their order does not depend on that of the atomics.
-  uint32_t* mine = buf + warp * E;
+  uint32_t* mine = buf + warp * pitch;
   int32_t* row_of = p.row_of + begin * p.k;
   for (int round = 0; round < rounds; ++round) {
     if (round > 0) {
@@ -396,15 +402,19 @@ __device__ __forceinline__ void finish_chunk(const RowPlan& p, RouteShared<BUF>&
       row_of[from + i] = e < 0 ? 0 : __popc(mine[e] & (bit(i) - 1u));
     }
     __syncthreads();
-    for (int e = tid; e < E; e += NT) {
-      uint32_t first = sh.start[e];
-#pragma unroll 8
-      for (int w = 0; w < warps; ++w) {
-        const uint32_t n = __popc(buf[w * E + e]);
-        buf[w * E + e] = first;
-        first += n;
+    // an expert's tokens in the warps before, a lane a warp
+    for (int e = warp; e < E; e += kWarps) {
+      const uint32_t first = sh.start[e];
+      const uint32_t n = lane < warps ? __popc(buf[lane * pitch + e]) : 0u;
+      uint32_t upto = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        if (lane >= d) upto += v;
       }
-      sh.start[e] = first;
+      if (lane < warps) buf[lane * pitch + e] = first + upto - n;
+      __syncwarp();
+      if (lane == 31) sh.start[e] = first + upto;
     }
     __syncthreads();
     auto write = [&](int i, int32_t e, uint32_t place) {
@@ -420,10 +430,10 @@ __device__ __forceinline__ void finish_chunk(const RowPlan& p, RouteShared<BUF>&
 }
 
 __global__ void __launch_bounds__(kManyThreads)
-    route_finish_kernel(const RowPlan p, const RouteWs ws) {
+    route_finish_kernel(const RowPlan p, const RouteWs ws, int first) {
   __shared__ RouteShared<kBufWords> sh;
   grid_wait_for_previous();
-  const int c = static_cast<int>(blockIdx.x);
+  const int c = first + static_cast<int>(blockIdx.x);
   finish_chunk<kManyThreads, false>(p, sh, ws, p.expert + c * p.per * p.k, c);
 }
 
@@ -795,45 +805,60 @@ __global__ void __launch_bounds__(NT)
 // The extras reach the lanes that own their columns through a row of shared memory a team.
 constexpr int kGradThreads = 256;
 
+// A row of n columns in shared memory: the first halves of its runs of 8, then the second ones, so
+// that neighbouring lanes read neighbouring 16 bytes.
+__device__ __forceinline__ int halves_at(int c, int n) {
+  return (c >> 3) * 4 + (c & 3) + ((c & 4) != 0 ? n / 2 : 0);
+}
+
 template <typename T, int LPT, int VPL, int KPL>
 __global__ void __launch_bounds__(kGradThreads, VPL <= 16 ? 4 : 1)
     route_backward_kernel(const mxg_route_grad_t d, int vec) {
-  constexpr int kTeams = kGradThreads / LPT;
-  __shared__ float4 team_rows[kTeams][LPT * VPL / 4];
-  __shared__ float4 slopes[LPT * VPL / 4];
+  constexpr int kTeams = kGradThreads / LPT, kCols = LPT * VPL;
+  __shared__ float4 team_rows[kTeams][kCols / 4];
+  __shared__ float4 slopes[kCols / 4];
   const int tid = threadIdx.x, gl = tid & (LPT - 1), E = d.experts, k = d.k;
-  float* const mine = reinterpret_cast<float*>(team_rows[tid / LPT]);
+  float4* const mine = team_rows[tid / LPT];
   const bool softmax = d.score == MXG_SCORE_SOFTMAX, balance = d.slope != nullptr;
   // the weights' gradient goes through the shares; whether any of it does
   const bool joined = softmax && !d.normalize, shares = balance || joined;
   const float dloss = balance ? *d.dloss : 0.0f;
-  for (int e = tid; e < LPT * VPL; e += kGradThreads)
-    reinterpret_cast<float*>(slopes)[e] = balance && e < E ? d.slope[e] * dloss : 0.0f;
+  for (int e = tid; e < kCols; e += kGradThreads)
+    reinterpret_cast<float*>(slopes)[halves_at(e, kCols)] = balance && e < E ? d.slope[e] * dloss : 0.0f;
   __syncthreads();
   const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kTeams; base < d.tokens; base += step) {
-    const int64_t t = base + tid / LPT;
-    const bool in = t < d.tokens;
-    const T* row = static_cast<const T*>(d.logits) + (in ? t : 0) * d.ld;
-    int e[KPL];
-    float b[KPL], l[KPL];
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + tid / LPT;
+  // the chosen experts and their weights' gradients are asked for a token ahead
+  int e[KPL];
+  float b[KPL];
+  auto choices = [&](int64_t at) {
 #pragma unroll
     for (int i = 0; i < KPL; ++i) {
-      e[i] = in && i * LPT + gl < k ? d.expert[t * k + i * LPT + gl] : -1;
-      if (static_cast<uint32_t>(e[i]) >= static_cast<uint32_t>(E)) e[i] = -1;
-      b[i] = e[i] >= 0 && d.dweight != nullptr ? d.scale * d.dweight[t * k + i * LPT + gl] : 0.0f;
+      const int j = i * LPT + gl;
+      e[i] = at < d.tokens && j < k ? d.expert[at * k + j] : -1;
+      b[i] = at < d.tokens && j < k && d.dweight != nullptr ? d.dweight[at * k + j] : 0.0f;
     }
+  };
+  choices(t);
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kTeams; base < d.tokens;
+       base += step, t += step) {
+    const bool in = t < d.tokens;
+    const T* row = static_cast<const T*>(d.logits) + (in ? t : 0) * d.ld;
     LogitRow<T, LPT, VPL> raw;
     raw.load(row, gl, in ? E : 0, vec != 0);
     if (t + step < d.tokens) raw.ahead(row + step * d.ld, gl, E);
-    float v[VPL];
-    raw.values(v);
-    int have = 0;
+    int at[KPL], have = 0;
+    float l[KPL], db[KPL];
 #pragma unroll
     for (int i = 0; i < KPL; ++i) {
-      l[i] = e[i] >= 0 ? to_f32(row[e[i]]) : -INFINITY;
-      have |= e[i] >= 0 ? 1 : 0;
+      at[i] = static_cast<uint32_t>(e[i]) < static_cast<uint32_t>(E) ? e[i] : -1;
+      l[i] = at[i] >= 0 ? to_f32(row[at[i]]) : -INFINITY;
+      db[i] = at[i] >= 0 ? d.scale * b[i] : 0.0f;
+      have |= at[i] >= 0 ? 1 : 0;
     }
+    choices(t + step);
+    float v[VPL];
+    raw.values(v);
 #pragma unroll
     for (int o = LPT / 2; o > 0; o >>= 1) have |= __shfl_xor_sync(0xFFFFFFFFu, have, o);
 
@@ -848,7 +873,7 @@ __global__ void __launch_bounds__(kGradThreads, VPL <= 16 ? 4 : 1)
     if (shares) {
 #pragma unroll
       for (int i = 0; i < VPL; i += 4) {
-        const float4 a4 = slopes[column<LPT>(i, gl) / 4];
+        const float4 a4 = slopes[halves_at(column<LPT>(i, gl), kCols) / 4];
         const float a[4] = {a4.x, a4.y, a4.z, a4.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -868,11 +893,11 @@ __global__ void __launch_bounds__(kGradThreads, VPL <= 16 ? 4 : 1)
     for (int i = 0; i < KPL; ++i) {
       rest[i] = 1.0f;
       s[i] = 0.0f;
-      if (e[i] >= 0)
+      if (at[i] >= 0)
         s[i] = softmax ? exp_approx(l[i] - shift)
                        : sigmoid_scaled(l[i], d.normalize ? shift : 0.0f, rest[i]);
       chosen += s[i];
-      bq = fmaf(b[i], s[i], bq);
+      bq = fmaf(db[i], s[i], bq);
     }
     if (d.normalize) {
       chosen = team_add<LPT>(chosen);
@@ -889,11 +914,13 @@ __global__ void __launch_bounds__(kGradThreads, VPL <= 16 ? 4 : 1)
     }
 #pragma unroll
     for (int i = 0; i < VPL; i += 4)
-      *reinterpret_cast<float4*>(mine + column<LPT>(i, gl)) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      mine[halves_at(column<LPT>(i, gl), kCols) / 4] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < KPL; ++i)
-      if (e[i] >= 0) atomicAdd(&mine[e[i]], s[i] / chosen * rest[i] * (b[i] - bq));
+      if (at[i] >= 0)
+        atomicAdd(reinterpret_cast<float*>(mine) + halves_at(at[i], kCols),
+                  s[i] / chosen * rest[i] * (db[i] - bq));
     __syncwarp();
     T* out = static_cast<T*>(d.dlogits) + (in ? t : 0) * d.ldd;
 #pragma unroll
@@ -902,7 +929,8 @@ __global__ void __launch_bounds__(kGradThreads, VPL <= 16 ? 4 : 1)
       float f[8];
 #pragma unroll
       for (int j = 0; j < 8; j += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(mine + c + j), a = slopes[(c + j) / 4];
+        const int q = halves_at(c + j, kCols) / 4;
+        const float4 x = mine[q], a = slopes[q];
         f[j] = x.x;
         f[j + 1] = x.y;
         f[j + 2] = x.z;
@@ -1006,7 +1034,7 @@ cudaError_t launch_finish(const RowPlan& p, const RouteWs& ws, cudaStream_t stre
   ++*launches;
   return launch_after(true, route_finish_kernel,
                       static_cast<unsigned>(p.row_of != nullptr ? p.chunks + 1 : 1), kManyThreads,
-                      0, stream, p, ws);
+                      0, stream, p, ws, p.row_of != nullptr ? 0 : p.chunks);
 }
 
 template <typename T, int LPT, int VPL, int KPL, bool ONE>
