@@ -59,6 +59,12 @@ struct RowPlan {
   uint32_t capacity;  // a multiple of align
   int32_t experts, k, align, chunks;
   float balance;
+  // how the second half is cut, found on the host: a division takes a kernel 150 cycles
+  int32_t warps, rounds, each;  // a chunk's tokens over warps and rounds, 32 at most each
+  int32_t inverse;              // 65536 / k, rounded up
+  int32_t pitch;                // of a warp's words: odd, a column of them lies on different banks
+  int32_t share_bits, each_share;  // neighbouring lanes that take an expert's words, words of each
+  int32_t quad_bits, parts;        // threads that read a chunk's experts, chunks read at once
 };
 
 constexpr int kBufWords = 8192;
@@ -175,14 +181,12 @@ struct LogitRow {
 // ---------------------------------------------------------------- rows
 // Sums over the chunks of `n` columns, `pitch` apart from one chunk to the next, into
 // parts of shared memory: part p, column c at [p * 4 * quads + c].  LOW: beside the sums, those
-// of the chunks below `low`, `kBufWords / 2` further on.  The parts are returned.
-template <int NT, bool LOW, typename V4, typename V>
-__device__ __forceinline__ int sum_chunks(V* to, const V* from, int pitch, int chunks, int low) {
-  const int quads = pitch / 4;
-  int wide = 1;
-  while (wide < quads) wide *= 2;
-  const int parts = min(min(NT / wide, 16), chunks);
-  const int q = threadIdx.x & (wide - 1), part = threadIdx.x / wide;
+// of the chunks below `low`, `kBufWords / 2` further on.
+template <bool LOW, typename V4, typename V>
+__device__ __forceinline__ void sum_chunks(V* to, const V* from, int pitch, int chunks, int low,
+                                           int quad_bits, int parts) {
+  const int quads = pitch >> 2;
+  const int q = threadIdx.x & ((1 << quad_bits) - 1), part = threadIdx.x >> quad_bits;
   if (q < quads && part < parts) {
     V4 all = {}, under = {};
     const V4* at = reinterpret_cast<const V4*>(from) + q;
@@ -212,7 +216,6 @@ __device__ __forceinline__ int sum_chunks(V* to, const V* from, int pitch, int c
     out[0] = all;
     if (LOW) out[kBufWords / 8] = under;
   }
-  return parts;
 }
 
 // Everything that needs the whole batch's counts, by the CTA of chunk c, of NT threads
@@ -230,16 +233,13 @@ __device__ __forceinline__ void finish_chunk(const RowPlan& p, RouteShared<BUF>&
   uint32_t* buf = reinterpret_cast<uint32_t*>(sh.buf);
   // this chunk's choices, 32 tokens at most a warp and round (as many warps as the counts
   // have room for); the first kHeld of a lane are asked for now
-  constexpr int kHeld = 8;
+  constexpr int kHeld = 4;
   const int64_t begin = static_cast<int64_t>(c) * p.per;
   const int tokens_here =
       p.row_of == nullptr ? 0 : static_cast<int>(max(min(begin + p.per, p.tokens) - begin, int64_t{0}));
-  const int pitch = E | 1;  // of a warp's words: a column of them lies on different banks
-  const int warps = min(kWarps, BUF / pitch);
-  const int rounds = (tokens_here + 32 * warps - 1) / (32 * warps);
-  const int each = rounds == 0 ? 0 : (tokens_here + rounds * warps - 1) / (rounds * warps);
-  const int inverse = (65536 + p.k - 1) / p.k;  // i / k for i below 1024
-  int from = 0, items = 0;                      // of this warp and round
+  const int warps = p.warps, each = p.each, pitch = p.pitch, inverse = p.inverse;
+  const int rounds = tokens_here == 0 ? 0 : p.rounds;
+  int from = 0, items = 0;  // of this warp and round
   auto take = [&](int round) {
     const int first = warp < warps ? min((round * warps + warp) * each, tokens_here) : 0;
     from = first * p.k;
@@ -257,17 +257,17 @@ __device__ __forceinline__ void finish_chunk(const RowPlan& p, RouteShared<BUF>&
   take(0);
   hold();
   // tokens of each expert, in all chunks and in those before this one
-  int parts = 1;
+  const int parts = p.parts;
   const bool losses = (ONE || c == p.chunks) && (p.loss != nullptr || p.slope != nullptr);
   if (!ONE) {
     const uint32_t* hist = reinterpret_cast<const uint32_t*>(ws.hist);
     if (c == p.chunks) {  // no tokens: the sums of p in the place of those before them
-      parts = sum_chunks<NT, false, uint4>(buf, hist, ws.pitch, p.chunks, 0);
+      sum_chunks<false, uint4>(buf, hist, ws.pitch, p.chunks, 0, p.quad_bits, p.parts);
       if (losses && p.loss != nullptr)
-        sum_chunks<NT, false, float4>(reinterpret_cast<float*>(buf) + kBufWords / 2, ws.psum, ws.pitch,
-                                      p.chunks, 0);
+        sum_chunks<false, float4>(reinterpret_cast<float*>(buf) + kBufWords / 2, ws.psum, ws.pitch,
+                                  p.chunks, 0, p.quad_bits, p.parts);
     } else {
-      parts = sum_chunks<NT, true, uint4>(buf, hist, ws.pitch, p.chunks, c);
+      sum_chunks<true, uint4>(buf, hist, ws.pitch, p.chunks, c, p.quad_bits, p.parts);
     }
     __syncthreads();
   }
@@ -374,6 +374,7 @@ __device__ __forceinline__ void finish_chunk(const RowPlan& p, RouteShared<BUF>&
   // names an expert once), so their order does not depend on that of the atomics.
   uint32_t* mine = buf + warp * pitch;
   int32_t* row_of = p.row_of + begin * p.k;
+  const int shares = 1 << p.share_bits;
   for (int round = 0; round < rounds; ++round) {
     if (round > 0) {
       __syncthreads();  // the words of the round before have been read
@@ -396,25 +397,36 @@ __device__ __forceinline__ void finish_chunk(const RowPlan& p, RouteShared<BUF>&
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
       at[i] = held[i] < 0 ? 0u : __popc(mine[held[i]] & (bit(32 * i + lane) - 1u));
-    // (more than 8 choices a token: their places wait in row_of)
+    // (more than a lane holds: their places wait in row_of)
     for (int i = 32 * kHeld + lane; i < items; i += 32) {
       const int32_t e = choice(i);
       row_of[from + i] = e < 0 ? 0 : __popc(mine[e] & (bit(i) - 1u));
     }
     __syncthreads();
-    // an expert's tokens in the warps before, a lane a warp
-    for (int e = warp; e < E; e += kWarps) {
-      const uint32_t first = sh.start[e];
-      const uint32_t n = lane < warps ? __popc(buf[lane * pitch + e]) : 0u;
+    // an expert's tokens in the warps before: neighbouring lanes take a part of the warps each
+    for (int i = tid; (i & ~31) < E << p.share_bits; i += NT) {
+      const int e = i >> p.share_bits, share = i & (shares - 1);
+      const int w0 = share * p.each_share, w1 = min(w0 + p.each_share, warps);
+      uint32_t n = 0;
+      if (e < E)
+#pragma unroll 4
+        for (int w = w0; w < w1; ++w) n += __popc(buf[w * pitch + e]);
       uint32_t upto = n;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
+      for (int d = 1; d < shares; d <<= 1) {
         const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-        if (lane >= d) upto += v;
+        if (share >= d) upto += v;
       }
-      if (lane < warps) buf[lane * pitch + e] = first + upto - n;
-      __syncwarp();
-      if (lane == 31) sh.start[e] = first + upto;
+      uint32_t first = e < E ? sh.start[e] + upto - n : 0u;
+      __syncwarp();  // an expert's lanes have all read its start
+      if (e < E) {
+#pragma unroll 4
+        for (int w = w0; w < w1; ++w) {
+          n = __popc(buf[w * pitch + e]);
+          buf[w * pitch + e] = first;
+          first += n;
+        }
+        if (share == shares - 1) sh.start[e] = first;
+      }
     }
     __syncthreads();
     auto write = [&](int i, int32_t e, uint32_t place) {
@@ -1030,6 +1042,27 @@ bool rows_of_16(const void* p, int64_t ld, size_t size) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * static_cast<int64_t>(size)) % 16 == 0;
 }
 
+// How finish_chunk cuts its work, in a CTA of `threads`.
+void cut_finish(RowPlan* p, int threads) {
+  const int words = p->chunks == 1 ? kBufWords / 2 : kBufWords;
+  p->pitch = p->experts | 1;
+  p->warps = std::min(threads / 32, words / p->pitch);
+  p->rounds = static_cast<int>(std::max<int64_t>(1, (p->per + 32 * p->warps - 1) / (32 * p->warps)));
+  p->each = static_cast<int>((p->per + p->rounds * p->warps - 1) / (p->rounds * p->warps));
+  p->inverse = (65536 + p->k - 1) / p->k;
+  int wide = 1, quads = 1;
+  while (wide < p->experts) wide *= 2;
+  p->share_bits = 0;
+  while (p->share_bits < 5 && (wide << (p->share_bits + 1)) <= threads) ++p->share_bits;
+  p->each_share = (p->warps + (1 << p->share_bits) - 1) >> p->share_bits;
+  p->quad_bits = 0;
+  while (quads < (p->experts + 3) / 4) {
+    quads *= 2;
+    ++p->quad_bits;
+  }
+  p->parts = std::max(1, std::min({threads / quads, 16, p->chunks}));
+}
+
 cudaError_t launch_finish(const RowPlan& p, const RouteWs& ws, cudaStream_t stream, int* launches) {
   ++*launches;
   return launch_after(true, route_finish_kernel,
@@ -1133,6 +1166,8 @@ cudaError_t launch_route(const mxg_route_t& d, void* workspace, int32_t* status,
   p.align = d.align;
   p.chunks = c.n;
   p.balance = d.balance;
+  const Shape one = many_lanes(d.experts, d.k);
+  cut_finish(&p, c.n == 1 ? threads_of(one.lpt, one.vpl, true) : kManyThreads);
   const RouteWs ws = carve(workspace, c.n, d.experts);
   const cudaError_t e = d.dtype == MXG_F32    ? route_typed<float>(d, p, ws, stream)
                         : d.dtype == MXG_BF16 ? route_typed<Bf16>(d, p, ws, stream)
@@ -1162,6 +1197,7 @@ cudaError_t launch_route_rows(const int32_t* expert, int64_t tokens, int experts
   p.k = 1;
   p.align = align;
   p.chunks = c.n;
+  cut_finish(&p, c.n == 1 ? kOneThreads : kManyThreads);
   const RouteWs ws = carve(workspace, c.n, experts);
   ++*launches;
   if (c.n == 1) {
