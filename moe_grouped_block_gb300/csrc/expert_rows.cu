@@ -315,13 +315,14 @@ __global__ void __launch_bounds__(kRingThreads)
   }
 }
 
-// Rows of any alignment, an element a lane.
+// Rows of any alignment: kAcross elements a lane, 32 columns apart.
+constexpr int kAcross = 4;
+
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads)
     combine_kernel(const mxg_expert_rows_t d, int slices) {
-  constexpr int kAhead = 8;
-  const int lane = threadIdx.x & 31;
-  const T* const rows = static_cast<const T*>(d.rows);
+  constexpr int kAhead = 4;
+  const int lane = threadIdx.x & 31, cols = static_cast<int>(d.cols);
   TokenWalk<kRowThreads> at(slices), then = at;
   int64_t row = row_start(d, at.t);
   float weight = row_weight(d, at.t);
@@ -331,34 +332,45 @@ __global__ void __launch_bounds__(kRowThreads)
     then.next();
     row = row_start(d, then.t);
     weight = row_weight(d, then.t);
-    const int c = at.slice * 32 + lane;
-    float sum = 0.0f;
+    const int c = at.slice * 32 * kAcross + lane;
+    const T* const from = static_cast<const T*>(d.rows) + c;
+    float sum[kAcross];
+#pragma unroll
+    for (int i = 0; i < kAcross; ++i) sum[i] = 0.0f;
     for (int j0 = 0; j0 < d.k; j0 += kAhead) {
-      T x[kAhead];
+      T x[kAhead][kAcross];
       int64_t r[kAhead];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         r[j] = __shfl_sync(0xFFFFFFFFu, row_now, (j0 + j) & 31);
-        if (c >= d.cols) r[j] = -1;
-        if (r[j] >= 0) x[j] = rows[r[j] + c];
+#pragma unroll
+        for (int i = 0; i < kAcross; ++i)
+          if (r[j] >= 0 && c + 32 * i < cols) x[j][i] = from[r[j] + 32 * i];
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         const float w = __shfl_sync(0xFFFFFFFFu, w_now, (j0 + j) & 31);
-        if (r[j] >= 0) sum = fmaf(w, to_f32(x[j]), sum);
+        if (r[j] < 0) continue;
+#pragma unroll
+        for (int i = 0; i < kAcross; ++i)
+          if (c + 32 * i < cols) sum[i] = fmaf(w, to_f32(x[j][i]), sum[i]);
       }
     }
-    if (c < d.cols) static_cast<T*>(d.tokens)[at.t * d.ldt + c] = from_f32<T>(sum);
+    T* const to = static_cast<T*>(d.tokens) + at.t * d.ldt + c;
+#pragma unroll
+    for (int i = 0; i < kAcross; ++i)
+      if (c + 32 * i < cols) to[32 * i] = from_f32<T>(sum[i]);
   }
 }
 
-// A team of `team` warps owns a token, KA of its rows at a time; a lane's next pieces are asked for
-// before it works on those it has.  Sums over the columns are joined in shared memory.
-template <typename T, int BYTES, int KA>
+// A team of `team` warps owns a token, KA of its rows at a time and ACROSS pieces of each row a
+// lane; a lane's next pieces are asked for before it works on those it has.  Sums over the columns
+// are joined in shared memory.
+template <typename T, int BYTES, int KA, int ACROSS>
 __global__ void __launch_bounds__(kRowThreads)
     combine_backward_kernel(const mxg_expert_rows_t d, int team, int64_t pad_items) {
   using P = Piece<T, BYTES>;
-  constexpr int kElems = P::kElems;
+  constexpr int kElems = P::kElems, kSpan = 32 * kElems;
   constexpr int kWarps = kRowThreads / 32;
   __shared__ float part[kWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, teams = kWarps / team;
@@ -366,7 +378,7 @@ __global__ void __launch_bounds__(kRowThreads)
   const bool dots = d.dweight != nullptr, writes = d.rows != nullptr;
   const int64_t pad_blocks = (pad_items + kWarps - 1) / kWarps;
   const int64_t token_blocks = (d.n + teams - 1) / teams;
-  const int cols = static_cast<int>(d.cols), step = team * 32 * kElems;
+  const int cols = static_cast<int>(d.cols), step = team * kSpan * ACROSS;
   for (int64_t b = blockIdx.x; b < pad_blocks + token_blocks; b += gridDim.x) {
     if (b < pad_blocks) {
       if (b * kWarps + warp < pad_items) zero_padding<T, BYTES>(d, b * kWarps + warp);
@@ -395,50 +407,59 @@ __global__ void __launch_bounds__(kRowThreads)
         if (j0 + j >= d.k) r[j] = -1;
         dot[j] = 0.0f;
       }
-      int c = (place * 32 + lane) * kElems;
-      P x, y[KA];
-      auto fetch = [&](P& a, P (&q)[KA], int at_c) {
-        if (!on || at_c + kElems > cols) return;
-        a.load(dy + at_c);
-#pragma unroll
-        for (int j = 0; j < KA; ++j)
-          if (dots && r[j] >= 0) q[j].load(y_rows + r[j] * d.ldy + at_c);
+      struct Pieces {
+        P x[ACROSS], y[ACROSS][KA];
       };
-      fetch(x, y, c);
+      auto fetch = [&](Pieces& p, int c) {
+#pragma unroll
+        for (int i = 0; i < ACROSS; ++i) {
+          if (!on || c + i * kSpan + kElems > cols) continue;
+          p.x[i].load(dy + c + i * kSpan);
+#pragma unroll
+          for (int j = 0; j < KA; ++j)
+            if (dots && r[j] >= 0) p.y[i][j].load(y_rows + r[j] * d.ldy + c + i * kSpan);
+        }
+      };
+      int c = place * kSpan * ACROSS + lane * kElems;
+      Pieces now;
+      fetch(now, c);
       for (; on && c + kElems <= cols; c += step) {
-        P x2, y2[KA];
-        fetch(x2, y2, c + step);
-        float g[kElems];
-        x.get(g);
+        Pieces next;
+        fetch(next, c + step);
 #pragma unroll
-        for (int j = 0; j < KA; ++j) {
-          if (r[j] < 0) continue;
-          float f[kElems];
-          if (dots) {
-            y[j].get(f);
+        for (int i = 0; i < ACROSS; ++i) {
+          if (c + i * kSpan + kElems > cols) continue;
+          float g[kElems];
+          now.x[i].get(g);
 #pragma unroll
-            for (int i = 0; i < kElems; ++i) dot[j] = fmaf(g[i], f[i], dot[j]);
-          }
-          if (writes) {
+          for (int j = 0; j < KA; ++j) {
+            if (r[j] < 0) continue;
+            float f[kElems];
+            if (dots) {
+              now.y[i][j].get(f);
 #pragma unroll
-            for (int i = 0; i < kElems; ++i) f[i] = wj[j] * g[i];
-            P o;
-            o.set(f);
-            o.store(rows + r[j] * d.ldr + c);
+              for (int e = 0; e < kElems; ++e) dot[j] = fmaf(g[e], f[e], dot[j]);
+            }
+            if (writes) {
+#pragma unroll
+              for (int e = 0; e < kElems; ++e) f[e] = wj[j] * g[e];
+              P o;
+              o.set(f);
+              o.store(rows + r[j] * d.ldr + c + i * kSpan);
+            }
           }
         }
-        x = x2;
-#pragma unroll
-        for (int j = 0; j < KA; ++j) y[j] = y2[j];
+        now = next;
       }
-      // the last, shorter piece of a row
-      for (int i = c; on && i < cols && i < c + kElems; ++i) {
-        const float g = to_f32(dy[i]);
+      // what is left of a row whose columns do not end on a piece: an element a lane
+      if (kElems > 1 && on && place == 0 && lane < cols % kElems) {
+        const int e = cols / kElems * kElems + lane;
+        const float g = to_f32(dy[e]);
 #pragma unroll
         for (int j = 0; j < KA; ++j) {
           if (r[j] < 0) continue;
-          if (dots) dot[j] = fmaf(g, to_f32(y_rows[r[j] * d.ldy + i]), dot[j]);
-          if (writes) rows[r[j] * d.ldr + i] = from_f32<T>(wj[j] * g);
+          if (dots) dot[j] = fmaf(g, to_f32(y_rows[r[j] * d.ldy + e]), dot[j]);
+          if (writes) rows[r[j] * d.ldr + e] = from_f32<T>(wj[j] * g);
         }
       }
       if (dots) {
@@ -513,7 +534,7 @@ cudaError_t run(const mxg_expert_rows_t& d, int op, int num_sms, cudaStream_t st
                           ? static_cast<int64_t>(d.experts) * kPadWarps
                           : 0;
   if (op == 0) {
-    constexpr int kUnroll = BYTES >= 16 ? 2 : 4;
+    constexpr int kUnroll = BYTES >= 16 ? 2 : 8;
     const int64_t slices = slices_of(d.cols, kSpan * kUnroll);
     dispatch_kernel<T, BYTES, kUnroll>
         <<<grid_for(pad + d.n * slices, num_sms, 64), kRowThreads, 0, stream>>>(
@@ -524,7 +545,7 @@ cudaError_t run(const mxg_expert_rows_t& d, int op, int num_sms, cudaStream_t st
       if (d.k == 2) return run_combine_ring<T, 2>(d, num_sms, stream);
       return run_combine_ring<T, 4>(d, num_sms, stream);
     } else {
-      const int64_t slices = slices_of(d.cols, 32);
+      const int64_t slices = slices_of(d.cols, 32 * kAcross);
       combine_kernel<T><<<grid_for(d.n * slices, num_sms, 64), kRowThreads, 0, stream>>>(
           d, static_cast<int>(slices));
     }
@@ -534,10 +555,15 @@ cudaError_t run(const mxg_expert_rows_t& d, int op, int num_sms, cudaStream_t st
     while (team < 8 && d.n * team < num_sms * 48LL && team * kSpan < d.cols) team *= 2;
     // (two waves: 8192 tokens of 2 rows of 4096 in bf16 take 56 us, 58 us with a CTA for each 8)
     const unsigned grid = grid_for(pad + d.n * team, num_sms, 4);
+    constexpr int kAcrossOf2 = BYTES < 16 ? 4 : 1, kAcrossOf4 = BYTES < 16 ? 2 : 1;
+    // pieces of 16 bytes where a lane has more than two rows' at once
+    constexpr int kBytes = BYTES == 32 ? 16 : BYTES;
     if (d.k <= 2)
-      combine_backward_kernel<T, BYTES, 2><<<grid, kRowThreads, 0, stream>>>(d, team, pad);
+      combine_backward_kernel<T, BYTES, 2, kAcrossOf2><<<grid, kRowThreads, 0, stream>>>(d, team, pad);
+    else if (d.k <= 4)
+      combine_backward_kernel<T, kBytes, 4, kAcrossOf4><<<grid, kRowThreads, 0, stream>>>(d, team, pad);
     else
-      combine_backward_kernel<T, BYTES, 4><<<grid, kRowThreads, 0, stream>>>(d, team, pad);
+      combine_backward_kernel<T, kBytes, 8, 1><<<grid, kRowThreads, 0, stream>>>(d, team, pad);
   }
   return cudaGetLastError();
 }

@@ -6,7 +6,8 @@
 //
 // A thread owns 16 columns -- 32 bytes of a 16-bit tensor, 16 of the kept values -- and the
 // thread beside it the other half of the 32 that share a scale, so a block's largest
-// magnitude is one shuffle away.  Each input is read once and each output written once:
+// magnitude is one shuffle away.  Rows that do not start on 16 bytes, or whose columns are no
+// multiple of 8, have a lane for each column and a warp for each block.  Each input is read once and each output written once:
 // memory is the bound.
 #include <algorithm>
 
@@ -17,34 +18,37 @@ namespace mxg {
 
 constexpr int kActThreads = 256;
 
-// 16 neighbouring values of a 16-bit type as packed pairs.
-template <typename T, bool VEC>
+// 16 neighbouring values of a 16-bit type as packed pairs, by accesses of ALIGN = 32 or 16 bytes;
+// of the latter only the first where n is 8.
+template <typename T, int ALIGN>
 __device__ __forceinline__ void load16(const T* p, int n, uint32_t (&w)[8]) {
-  if constexpr (VEC) {
+  // (volatile: in order with the stores)
+  if constexpr (ALIGN == 32) {
     asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
                    "=r"(w[6]), "=r"(w[7])
-                 : "l"(p));  // (volatile: in order with the stores)
+                 : "l"(p));
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t lo = 2 * i < n ? p[2 * i].bits : 0u;
-      const uint32_t hi = 2 * i + 1 < n ? p[2 * i + 1].bits : 0u;
-      w[i] = lo | (hi << 16);
-    }
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "l"(p));
+    w[4] = w[5] = w[6] = w[7] = 0;
+    if (n > 8)
+      asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                   : "l"(p + 8));
   }
 }
-template <typename T, bool VEC>
+template <typename T, int ALIGN>
 __device__ __forceinline__ void store16(T* p, int n, const float (&f)[16]) {
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = pack2<T>(f[2 * i], f[2 * i + 1]);
-  if constexpr (VEC) {
+  if constexpr (ALIGN == 32) {
     st_global_32B(p, w);
   } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) p[i].bits = static_cast<uint16_t>(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu);
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (n > 8) reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 template <typename T>
@@ -127,7 +131,7 @@ struct HalfWalk {
 
 // 16 of a block's values to E4M3 bytes and the block's scale byte, with the lane beside
 // this one; all lanes of the warp take part.
-template <bool VEC>
+template <int ALIGN>
 __device__ __forceinline__ void keep16(const float (&v)[16], bool on, int n, uint8_t* q,
                                        uint8_t* sf, bool first) {
   float top = 0.0f;
@@ -153,17 +157,16 @@ __device__ __forceinline__ void keep16(const float (&v)[16], bool on, int n, uin
     w[i] = cvt_e4m3x2(f[4 * i] * scale, f[4 * i + 1] * scale) |
            (cvt_e4m3x2(f[4 * i + 2] * scale, f[4 * i + 3] * scale) << 16);
   if (!on) return;
-  if constexpr (VEC) {
+  if constexpr (ALIGN == 32) {
     if (n > 0) *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) q[i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
+  } else {  // (kept rows on 8 bytes)
+    if (n > 0) reinterpret_cast<uint2*>(q)[0] = make_uint2(w[0], w[1]);
+    if (n > 8) reinterpret_cast<uint2*>(q)[1] = make_uint2(w[2], w[3]);
   }
   if (first) *sf = static_cast<uint8_t>(e + 127);
 }
 
-template <typename T, int ACT, bool GATED, bool VEC>
+template <typename T, int ACT, bool GATED, int ALIGN>
 __global__ void __launch_bounds__(kActThreads)
     gated_act_kernel(const mxg_gated_act_t d, int blocks) {
   const int cols = static_cast<int>(d.cols);
@@ -178,8 +181,8 @@ __global__ void __launch_bounds__(kActThreads)
     const int n = on ? min(cols - c, 16) : 0;  // 0 or less: the half is empty
     uint32_t gw[8] = {}, uw[8] = {};
     if (n > 0) {
-      load16<T, VEC>(static_cast<const T*>(d.gate) + at.row * d.ldg + c, n, gw);
-      if (GATED) load16<T, VEC>(static_cast<const T*>(d.up) + at.row * d.ldu + c, n, uw);
+      load16<T, ALIGN>(static_cast<const T*>(d.gate) + at.row * d.ldg + c, n, gw);
+      if (GATED) load16<T, ALIGN>(static_cast<const T*>(d.up) + at.row * d.ldu + c, n, uw);
     }
     float g[16], u[16], h[16];
     unpack16<T>(gw, g);
@@ -189,36 +192,34 @@ __global__ void __launch_bounds__(kActThreads)
       h[i] = g[i] * rcp_approx(1.0f + exp_approx(-act_z<ACT>(g[i])));
       if (GATED) h[i] *= u[i];
     }
-    if (n > 0) store16<T, VEC>(static_cast<T*>(d.h) + at.row * d.ldh + c, n, h);
+    if (n > 0) store16<T, ALIGN>(static_cast<T*>(d.h) + at.row * d.ldh + c, n, h);
     if (keep) {
       uint8_t* q = d.q + at.row * d.ldq + c;
       uint8_t* sf = d.sf + at.row * sf_row + (at.half >> 1);
       const bool first = (at.half & 1) == 0;
-      keep16<VEC>(g, on, n, q, sf, first);
-      if (GATED) keep16<VEC>(u, on, n, q + cols, sf + blocks, first);
+      keep16<ALIGN>(g, on, n, q, sf, first);
+      if (GATED) keep16<ALIGN>(u, on, n, q + cols, sf + blocks, first);
     }
     at.next();
   }
 }
 
 // 16 kept bytes as words, and the values that they stand for.
-template <bool VEC>
+template <int ALIGN>
 __device__ __forceinline__ void load_kept(const uint8_t* q, int n, uint32_t (&w)[4]) {
-  if constexpr (VEC) {
+  if constexpr (ALIGN == 32) {
     asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                  : "l"(q));
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) w[i >> 2] |= static_cast<uint32_t>(q[i]) << (8 * (i & 3));
+    asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(q));
+    w[2] = w[3] = 0;
+    if (n > 8) asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(w[2]), "=r"(w[3]) : "l"(q + 8));
   }
 }
 
 // What a thread reads for 16 columns.
-template <typename T, bool GATED, bool VEC>
+template <typename T, bool GATED, int ALIGN>
 struct KeptHalf {
   uint32_t dh[8], g[4], u[4];
   uint32_t sf_g, sf_u;
@@ -230,28 +231,28 @@ struct KeptHalf {
     const uint8_t* q = d.q + at.row * d.ldq + c;
     const uint8_t* sf =
         d.sf + at.row * ((GATED ? 2 : 1) * static_cast<int64_t>(blocks)) + (at.half >> 1);
-    load_kept<VEC>(q, n, g);
+    load_kept<ALIGN>(q, n, g);
     sf_g = sf[0];
     if (GATED) {
-      load_kept<VEC>(q + cols, n, u);
+      load_kept<ALIGN>(q + cols, n, u);
       sf_u = sf[blocks];
     }
-    load16<T, VEC>(static_cast<const T*>(d.dh) + at.row * d.lddh + c, n, dh);
+    load16<T, ALIGN>(static_cast<const T*>(d.dh) + at.row * d.lddh + c, n, dh);
   }
 };
 
-template <typename T, int ACT, bool GATED, bool VEC>
+template <typename T, int ACT, bool GATED, int ALIGN>
 __global__ void __launch_bounds__(kActThreads, 3)
     gated_act_backward_kernel(const mxg_gated_act_t d, int blocks) {
   const int cols = static_cast<int>(d.cols);
   const int64_t live = act_rows(d);
   HalfWalk at(2 * blocks), then = at;
-  KeptHalf<T, GATED, VEC> in;
+  KeptHalf<T, GATED, ALIGN> in;
   in.load(d, at, live, blocks);
   for (; at.row < live; at = then) {
     // the next ones are asked for before these are worked on
     then.next();
-    KeptHalf<T, GATED, VEC> in2;
+    KeptHalf<T, GATED, ALIGN> in2;
     in2.load(d, then, live, blocks);
     const int c = at.half * 16;
     const int n = min(cols - c, 16);
@@ -285,41 +286,176 @@ __global__ void __launch_bounds__(kActThreads, 3)
           }
         }
       }
-      store16<T, VEC>(dgate, n, dg);
-      if (GATED) store16<T, VEC>(dup, n, du);
-      if (h != nullptr) store16<T, VEC>(h, n, again);
+      store16<T, ALIGN>(dgate, n, dg);
+      if (GATED) store16<T, ALIGN>(dup, n, du);
+      if (h != nullptr) store16<T, ALIGN>(h, n, again);
     }
     in = in2;
   }
 }
 
+// ---------------------------------------------------------------- rows of any alignment
+// A warp's item: kAcross blocks of a row side by side, a lane a column of each.
+constexpr int kAcross = 4;
+
+struct BlockWalk {
+  int64_t row, row_step;
+  int group, group_step, groups;
+  __device__ __forceinline__ BlockWalk(int blocks) : groups((blocks + kAcross - 1) / kAcross) {
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * (kActThreads / 32) + (threadIdx.x >> 5);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kActThreads / 32);
+    row = at / groups;
+    group = static_cast<int>(at - row * groups);
+    row_step = step / groups;
+    group_step = static_cast<int>(step - row_step * groups);
+  }
+  __device__ __forceinline__ void next() {
+    row += row_step;
+    group += group_step;
+    if (group >= groups) {
+      group -= groups;
+      ++row;
+    }
+  }
+};
+
+// A column's value to its E4M3 byte, and the block's scale byte; by a whole warp.
+__device__ __forceinline__ void keep_column(float v, uint32_t& byte, uint32_t& scale_byte) {
+  if (isinf(v)) v = __uint_as_float(0x7FC00000u);  // an infinity is kept as NaN
+  // magnitudes are in the order of their bits; NaN is none
+  const uint32_t size = v != v ? 0u : __float_as_uint(fabsf(v));
+  const int e = mx_exponent(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, size)));
+  byte = cvt_e4m3x2(v * pow2_neg(e), 0.0f) & 0xFFu;
+  scale_byte = static_cast<uint32_t>(e + 127);
+}
+
+template <typename T, int ACT, bool GATED>
+__global__ void __launch_bounds__(kActThreads)
+    gated_act_columns_kernel(const mxg_gated_act_t d, int blocks) {
+  const int cols = static_cast<int>(d.cols), lane = threadIdx.x & 31;
+  const int64_t live = act_rows(d), sf_row = (GATED ? 2 : 1) * static_cast<int64_t>(blocks);
+  for (BlockWalk at(blocks); at.row < live; at.next()) {
+    const T* gate = static_cast<const T*>(d.gate) + at.row * d.ldg;
+    const T* up = GATED ? static_cast<const T*>(d.up) + at.row * d.ldu : nullptr;
+    T* h = static_cast<T*>(d.h) + at.row * d.ldh;
+    const int b0 = at.group * kAcross;
+    float g[kAcross], u[kAcross];
+#pragma unroll
+    for (int i = 0; i < kAcross; ++i) {
+      const int c = (b0 + i) * 32 + lane;
+      g[i] = c < cols ? to_f32(gate[c]) : 0.0f;
+      u[i] = GATED && c < cols ? to_f32(up[c]) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kAcross; ++i) {
+      const int c = (b0 + i) * 32 + lane;
+      float v = g[i] * rcp_approx(1.0f + exp_approx(-act_z<ACT>(g[i])));
+      if (GATED) v *= u[i];
+      if (c < cols) h[c] = from_f32<T>(v);
+    }
+    if (d.q == nullptr) continue;
+    uint8_t* q = d.q + at.row * d.ldq;
+    uint8_t* sf = d.sf + at.row * sf_row;
+#pragma unroll
+    for (int i = 0; i < kAcross; ++i) {
+      const int b = b0 + i, c = b * 32 + lane;
+      uint32_t byte, scale;
+      keep_column(g[i], byte, scale);
+      if (c < cols) q[c] = static_cast<uint8_t>(byte);
+      if (lane == 0 && b < blocks) sf[b] = static_cast<uint8_t>(scale);
+      if (GATED) {
+        keep_column(u[i], byte, scale);
+        if (c < cols) q[cols + c] = static_cast<uint8_t>(byte);
+        if (lane == 0 && b < blocks) sf[blocks + b] = static_cast<uint8_t>(scale);
+      }
+    }
+  }
+}
+
+template <typename T, int ACT, bool GATED>
+__global__ void __launch_bounds__(kActThreads)
+    gated_act_backward_columns_kernel(const mxg_gated_act_t d, int blocks) {
+  const int cols = static_cast<int>(d.cols), lane = threadIdx.x & 31;
+  const int64_t live = act_rows(d), sf_row = (GATED ? 2 : 1) * static_cast<int64_t>(blocks);
+  for (BlockWalk at(blocks); at.row < live; at.next()) {
+    const T* dh = static_cast<const T*>(d.dh) + at.row * d.lddh;
+    T* dgate = static_cast<T*>(d.dgate) + at.row * d.lddg;
+    T* dup = GATED ? static_cast<T*>(d.dup) + at.row * d.lddu : nullptr;
+    T* h = d.h != nullptr ? static_cast<T*>(d.h) + at.row * d.ldh : nullptr;
+    const uint8_t* q = d.q + at.row * d.ldq;
+    const uint8_t* sf = d.sf + at.row * sf_row;
+    const int b0 = at.group * kAcross;
+    uint32_t qg[kAcross], qu[kAcross], sg[kAcross], su[kAcross];
+    float y[kAcross];
+#pragma unroll
+    for (int i = 0; i < kAcross; ++i) {
+      const int b = b0 + i, c = b * 32 + lane;
+      const bool in = c < cols;
+      qg[i] = in ? q[c] : 0u;
+      qu[i] = GATED && in ? q[cols + c] : 0u;
+      sg[i] = in ? sf[b] : 0u;
+      su[i] = GATED && in ? sf[blocks + b] : 0u;
+      y[i] = in ? to_f32(dh[c]) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kAcross; ++i) {
+      const int c = (b0 + i) * 32 + lane;
+      float f[4];
+      e4m3x4_values(qg[i] | (qu[i] << 8), f);
+      const float x = f[0] * e8m0_value(sg[i]), u = f[1] * e8m0_value(su[i]);
+      const float s = rcp_approx(1.0f + exp_approx(-act_z<ACT>(x))), a = x * s;
+      const float slope = fmaf(a * (1.0f - s), act_dz<ACT>(x), s);
+      if (c < cols) {
+        dgate[c] = from_f32<T>(GATED ? y[i] * u * slope : y[i] * slope);
+        if (GATED) dup[c] = from_f32<T>(y[i] * a);
+        if (h != nullptr) h[c] = from_f32<T>(GATED ? u * a : a);
+      }
+    }
+  }
+}
+
 namespace {
 
-// Whether every row that is given starts on `bytes` bytes.
-bool rows_on(const void* p, int64_t ld, size_t size, uintptr_t bytes) {
-  return p == nullptr || ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * size)) &
-                          (bytes - 1)) == 0;
+// The widest accesses that every row allows: 32 or 16 bytes (of the kept values half as many), or
+// 2, an element's.
+int act_align(const mxg_gated_act_t& d) {
+  const uintptr_t kept = reinterpret_cast<uintptr_t>(d.q) |
+                         (d.q != nullptr ? static_cast<uintptr_t>(d.ldq | d.cols) : 0);
+  uintptr_t all = 2 * kept | static_cast<uintptr_t>(2 * d.cols);
+  auto add = [&](const void* p, int64_t ld) {
+    if (p != nullptr) all |= reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(2 * ld);
+  };
+  add(d.gate, d.ldg);
+  add(d.up, d.ldu);
+  add(d.h, d.ldh);
+  add(d.dh, d.lddh);
+  add(d.dgate, d.lddg);
+  add(d.dup, d.lddu);
+  return (all & 31u) == 0 ? 32 : ((all & 15u) == 0 ? 16 : 2);
 }
 
 template <typename T, int ACT, bool GATED>
 cudaError_t run(const mxg_gated_act_t& d, bool backward, int num_sms, cudaStream_t stream) {
-  const int blocks = static_cast<int>((d.cols + 31) / 32);
-  const bool vec = d.cols % 16 == 0 && rows_on(d.gate, d.ldg, 2, 32) && rows_on(d.up, d.ldu, 2, 32) &&
-                   rows_on(d.h, d.ldh, 2, 32) && rows_on(d.dh, d.lddh, 2, 32) &&
-                   rows_on(d.dgate, d.lddg, 2, 32) && rows_on(d.dup, d.lddu, 2, 32) &&
-                   rows_on(d.q, d.ldq, 1, 16);
-  const int64_t need = (d.rows * 2 * blocks + kActThreads - 1) / kActThreads;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(need, num_sms * 16LL));
+  const int blocks = static_cast<int>((d.cols + 31) / 32), align = act_align(d);
+  const int64_t threads = align == 2 ? d.rows * ((blocks + kAcross - 1) / kAcross) * 32
+                                     : d.rows * 2 * blocks;
+  const unsigned grid = static_cast<unsigned>(
+      std::min<int64_t>((threads + kActThreads - 1) / kActThreads, num_sms * 16LL));
   if (backward) {
-    if (vec)
-      gated_act_backward_kernel<T, ACT, GATED, true><<<grid, kActThreads, 0, stream>>>(d, blocks);
+    if (align == 32)
+      gated_act_backward_kernel<T, ACT, GATED, 32><<<grid, kActThreads, 0, stream>>>(d, blocks);
+    else if (align == 16)
+      gated_act_backward_kernel<T, ACT, GATED, 16><<<grid, kActThreads, 0, stream>>>(d, blocks);
     else
-      gated_act_backward_kernel<T, ACT, GATED, false><<<grid, kActThreads, 0, stream>>>(d, blocks);
+      gated_act_backward_columns_kernel<T, ACT, GATED>
+          <<<grid, kActThreads, 0, stream>>>(d, blocks);
   } else {
-    if (vec)
-      gated_act_kernel<T, ACT, GATED, true><<<grid, kActThreads, 0, stream>>>(d, blocks);
+    if (align == 32)
+      gated_act_kernel<T, ACT, GATED, 32><<<grid, kActThreads, 0, stream>>>(d, blocks);
+    else if (align == 16)
+      gated_act_kernel<T, ACT, GATED, 16><<<grid, kActThreads, 0, stream>>>(d, blocks);
     else
-      gated_act_kernel<T, ACT, GATED, false><<<grid, kActThreads, 0, stream>>>(d, blocks);
+      gated_act_columns_kernel<T, ACT, GATED><<<grid, kActThreads, 0, stream>>>(d, blocks);
   }
   return cudaGetLastError();
 }

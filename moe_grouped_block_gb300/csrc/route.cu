@@ -17,6 +17,7 @@
 // the warp's lanes.  One chunk alone is finished by the first kernel.  No floating-point
 // atomics and no counters kept between calls.
 #include <algorithm>
+#include <type_traits>
 
 #include "elem.cuh"
 #include "host16.h"
@@ -89,6 +90,25 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
 }
 __device__ __forceinline__ float key_logit(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
+// A key that orders a token's logits, and among equal ones the lower column first: of 16-bit
+// types, whose order fits into 16 bits, the rest of the word is the column.  kUnique: no two of
+// a token are equal.
+template <typename T>
+constexpr bool kUnique = sizeof(T) == 2;
+template <typename T>
+__device__ __forceinline__ uint32_t order_key(T v, int column) {
+  if constexpr (sizeof(T) == 4) {
+    return logit_key(v);
+  } else {
+    constexpr uint32_t kInf = std::is_same<T, Bf16>::value ? 0x7F80u : 0x7C00u;
+    uint32_t u = v.bits;
+    if ((u & 0x7FFFu) > kInf) u = 0x7FFFu;  // NaN, of either sign
+    if (u == 0x8000u) u = 0u;
+    u ^= u & 0x8000u ? 0xFFFFu : 0x8000u;
+    return (u << 16) | (0xFFFFu - static_cast<uint32_t>(column));
+  }
 }
 
 // sigmoid(l), and sigmoid(l) e^-m with m < 0: shares of a token whose sigmoids all underflow
@@ -478,8 +498,8 @@ __global__ void __launch_bounds__(NT) route_count_kernel(const RowPlan p, const 
 // and so on, KPL of them.
 template <int KPL>
 struct Chosen {
-  uint32_t key[KPL];  // 0 where there is none
-  int expert[KPL];    // -1 there
+  float logit[KPL];  // -infinity where there is none
+  int expert[KPL];   // -1 there
 };
 
 // One after the other: the maximum over the team, and the lowest column that holds it.
@@ -493,7 +513,7 @@ __device__ __forceinline__ Chosen<KPL> choose_in_turn(const float (&v)[VPL], boo
   Chosen<KPL> r;
 #pragma unroll
   for (int i = 0; i < KPL; ++i) {
-    r.key[i] = 0u;
+    r.logit[i] = -INFINITY;
     r.expert[i] = -1;
   }
   for (int j = 0; j < k; ++j) {
@@ -526,7 +546,7 @@ __device__ __forceinline__ Chosen<KPL> choose_in_turn(const float (&v)[VPL], boo
       for (int i = 0; i < KPL; ++i)
         if (i == j / LPT) {
           r.expert[i] = e;
-          r.key[i] = m;
+          r.logit[i] = key_logit(m);
         }
     }
   }
@@ -599,7 +619,7 @@ __device__ __forceinline__ Chosen<KPL> choose_by_rank(const float (&v)[VPL], con
     const int i = __ffs(static_cast<int>(among)) - 1;
     const int e = ((i >> 3) * LPT + gl) * 8 + (i & 7);
     // (read again: a register cannot be picked by a number)
-    *to++ = make_uint2(logit_key(to_f32(row[e])), static_cast<uint32_t>(e));
+    *to++ = make_uint2(order_key<T>(row[e], e), static_cast<uint32_t>(e));
   }
   // no key in the slots behind, up to those of the team that has most
   for (int i = all + gl; i < most; i += LPT) team[i].x = 0u;
@@ -631,14 +651,16 @@ __device__ __forceinline__ Chosen<KPL> choose_by_rank(const float (&v)[VPL], con
     }
   }
   // without equal keys the counts are 0, 1, 2, ...; else the lower column comes first
+  if constexpr (!kUnique<T>) {
 #pragma unroll
-  for (int d = LPT / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-  if (__any_sync(0xFFFFFFFFu, 2 * sum != all * (all - 1))) {
-    for (int j = 0; j < all; ++j) {
-      const uint2 other = team[j];
+    for (int d = LPT / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    if (__any_sync(0xFFFFFFFFu, 2 * sum != all * (all - 1))) {
+      for (int j = 0; j < all; ++j) {
+        const uint2 other = team[j];
 #pragma unroll
-      for (int r = 0; r < 2 * kPairs; ++r)
-        if (r * LPT + gl < all && other.x == mine[r].x && other.y < mine[r].y) ++above[r];
+        for (int r = 0; r < 2 * kPairs; ++r)
+          if (r * LPT + gl < all && other.x == mine[r].x && other.y < mine[r].y) ++above[r];
+      }
     }
   }
   __syncwarp();
@@ -651,8 +673,8 @@ __device__ __forceinline__ Chosen<KPL> choose_by_rank(const float (&v)[VPL], con
   for (int i = 0; i < KPL; ++i) {
     uint2 x = make_uint2(0u, 0xFFFFFFFFu);
     if (i * LPT + gl < min(all, k)) x = team[i * LPT + gl];
-    c.key[i] = x.x;
     c.expert[i] = static_cast<int>(x.y);
+    c.logit[i] = c.expert[i] >= 0 ? to_f32(row[c.expert[i]]) : -INFINITY;
   }
   __syncwarp();  // the slots are written again for the next token
   return c;
@@ -715,13 +737,13 @@ __global__ void __launch_bounds__(NT)
           v, logits + t * d.ld, on, k, gl, reinterpret_cast<uint2*>(sh.buf) + warp * (kMost * (32 / LPT)));
     else
       best = choose_in_turn<LPT, VPL, KPL>(v, on, k, gl);
-    const float top = __shfl_sync(0xFFFFFFFFu, key_logit(best.key[0]), 0, LPT);
+    const float top = __shfl_sync(0xFFFFFFFFu, best.logit[0], 0, LPT);
     const bool taken = __shfl_sync(0xFFFFFFFFu, best.expert[0], 0, LPT) >= 0;
     const float shift = softmax ? top : fminf(top, 0.0f);
     float w[KPL], chosen = 0.0f;
 #pragma unroll
     for (int i = 0; i < KPL; ++i) {
-      const float l = key_logit(best.key[i]);
+      const float l = best.logit[i];
       w[i] = best.expert[i] < 0 ? 0.0f
              : softmax          ? exp_approx(l - shift)
                                 : sigmoid_scaled(l, d.normalize ? shift : 0.0f);
@@ -978,7 +1000,7 @@ __global__ void __launch_bounds__(kGradThreads, VPL <= 16 ? 4 : 1)
 namespace {
 
 // How a token is laid out over lanes: few lanes (kpl > 0 choices each) with many columns, where
-// k is at most 8 and there are at most 256 experts; else 8 columns a lane (up to 32 lanes), and a
+// k is at most 8 and there are at most 512 experts; else 8 columns a lane (up to 32 lanes), and a
 // lane for each of the k.
 struct Shape {
   int lpt, vpl, kpl;
@@ -988,15 +1010,16 @@ Shape few_lanes(int experts) {
   if (experts <= 16) return {1, 16, 8};
   if (experts <= 32) return {2, 16, 4};
   if (experts <= 64) return {4, 16, 2};
-  if (experts <= 128) return {8, 16, 1};
-  return {8, 32, 1};
+  if (experts <= 128) return {4, 32, 2};
+  if (experts <= 256) return {8, 32, 1};
+  return {16, 32, 1};
 }
 Shape many_lanes(int experts, int k) {
   int lanes = 1;
   while (lanes < 32 && (lanes * 8 < experts || lanes < k)) lanes *= 2;
   return {lanes, experts > 512 ? 32 : (experts > 256 ? 16 : 8), 1};
 }
-bool few_serve(int experts, int k) { return k <= 8 && experts <= 256; }
+bool few_serve(int experts, int k) { return k <= 8 && experts <= 512; }
 
 struct Chunks {
   int n;
@@ -1011,11 +1034,11 @@ Chunks cut(int64_t tokens, int64_t pass) {
   return c;
 }
 
-// One CTA up to four passes of its teams (a second kernel costs more than three of them),
-// else a pass at least a CTA.
+// One CTA up to two passes of its teams, else a pass at least a CTA: 256 tokens of 64 experts, four
+// passes, took 13.6 us in one CTA and 10.6 in four.
 Chunks chunks_of(int64_t tokens, int experts, int k) {
   const Shape one = many_lanes(experts, k);
-  if (tokens <= 4 * (threads_of(one.lpt, one.vpl, true) / one.lpt) && tokens * k <= kOneItems)
+  if (tokens <= 2 * (threads_of(one.lpt, one.vpl, true) / one.lpt) && tokens * k <= kOneItems)
     return {1, std::max<int64_t>(1, tokens)};
   const Shape s = few_serve(experts, k) ? few_lanes(experts) : one;
   return cut(tokens, threads_of(s.lpt, s.vpl, false) / s.lpt);
@@ -1088,12 +1111,13 @@ cudaError_t route_typed(const mxg_route_t& d, const RowPlan& p, const RouteWs& w
     if (s.vpl == 8) return run_route<T, 1, 8, 8, false>(d, p, ws, vec, stream);
     if (s.lpt == 1) return run_route<T, 1, 16, 8, false>(d, p, ws, vec, stream);
     if (s.lpt == 2) return run_route<T, 2, 16, 4, false>(d, p, ws, vec, stream);
-    if (s.lpt == 4) return run_route<T, 4, 16, 2, false>(d, p, ws, vec, stream);
-    if (s.vpl == 16) return run_route<T, 8, 16, 1, false>(d, p, ws, vec, stream);
-    return run_route<T, 8, 32, 1, false>(d, p, ws, vec, stream);
+    if (d.experts <= 64) return run_route<T, 4, 16, 2, false>(d, p, ws, vec, stream);
+    if (s.lpt == 4) return run_route<T, 4, 32, 2, false>(d, p, ws, vec, stream);
+    if (s.lpt == 8) return run_route<T, 8, 32, 1, false>(d, p, ws, vec, stream);
+    return run_route<T, 16, 32, 1, false>(d, p, ws, vec, stream);
   }
   const Shape s = many_lanes(d.experts, d.k);
-  if (p.chunks > 1) {  // (more than 8 of the experts, or more than 256 of them: 16 lanes at least)
+  if (p.chunks > 1) {  // (more than 8 of the experts, or more than 512 of them: 16 lanes at least)
     if (s.lpt == 16) return run_route<T, 16, 8, 1, false>(d, p, ws, vec, stream);
     if (s.vpl == 8) return run_route<T, 32, 8, 1, false>(d, p, ws, vec, stream);
     if (s.vpl == 16) return run_route<T, 32, 16, 1, false>(d, p, ws, vec, stream);
@@ -1122,14 +1146,13 @@ template <typename T>
 cudaError_t backward_typed(const mxg_route_grad_t& d, int num_sms, cudaStream_t stream) {
   const int vec = d.experts % 8 == 0 && rows_of_16(d.logits, d.ld, sizeof(T)) &&
                   rows_of_16(d.dlogits, d.ldd, sizeof(T));
-  if (few_serve(d.experts, d.k)) {
-    const Shape s = few_lanes(d.experts);
-    if (s.vpl == 8) return run_backward<T, 1, 8, 8>(d, vec, num_sms, stream);
-    if (s.lpt == 1) return run_backward<T, 1, 16, 8>(d, vec, num_sms, stream);
-    if (s.lpt == 2) return run_backward<T, 2, 16, 4>(d, vec, num_sms, stream);
-    if (s.lpt == 4) return run_backward<T, 4, 16, 2>(d, vec, num_sms, stream);
-    if (s.vpl == 16) return run_backward<T, 8, 16, 1>(d, vec, num_sms, stream);
-    // (more warps an SM than with 32 columns a lane, 36 against 45 us for 65536 x 256 in fp32)
+  if (d.k <= 8 && d.experts <= 256) {
+    // (16 columns a lane: more warps an SM than with 32, 36 against 45 us for 65536 x 256 in fp32)
+    if (d.experts <= 8) return run_backward<T, 1, 8, 8>(d, vec, num_sms, stream);
+    if (d.experts <= 16) return run_backward<T, 1, 16, 8>(d, vec, num_sms, stream);
+    if (d.experts <= 32) return run_backward<T, 2, 16, 4>(d, vec, num_sms, stream);
+    if (d.experts <= 64) return run_backward<T, 4, 16, 2>(d, vec, num_sms, stream);
+    if (d.experts <= 128) return run_backward<T, 8, 16, 1>(d, vec, num_sms, stream);
     return run_backward<T, 16, 16, 1>(d, vec, num_sms, stream);
   }
   const Shape s = many_lanes(d.experts, d.k);
