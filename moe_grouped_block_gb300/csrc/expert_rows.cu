@@ -20,6 +20,7 @@ constexpr int kRowThreads = 256;
 template <typename T, int BYTES>
 struct Piece {
   static constexpr int kElems = BYTES / static_cast<int>(sizeof(T));
+  static_assert(BYTES == 32 || BYTES == 16 || kElems == 1, "pieces of three sizes");
   static constexpr int kWords = BYTES >= 4 ? BYTES / 4 : 1;
   uint32_t w[kWords];
   __device__ __forceinline__ void zero() {
@@ -36,10 +37,27 @@ struct Piece {
       asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                    : "l"(p));
-    } else if constexpr (sizeof(T) == 4) {
-      w[0] = __float_as_uint(*p);
     } else {
-      w[0] = p->bits;
+      load_if(p, true);
+    }
+  }
+  // An element, or 0 where `in` is not set; without a branch, so that many can be asked for at once.
+  __device__ __forceinline__ void load_if(const T* p, bool in) {
+    static_assert(kElems == 1, "of single elements");
+    if constexpr (sizeof(T) == 4) {
+      asm volatile(
+          "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b32 %0, 0;\n\t"
+          "@q ld.global.b32 %0, [%1];\n\t}"
+          : "=r"(w[0])
+          : "l"(p), "r"(static_cast<int>(in)));
+    } else {
+      uint16_t v;
+      asm volatile(
+          "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b16 %0, 0;\n\t"
+          "@q ld.global.b16 %0, [%1];\n\t}"
+          : "=h"(v)
+          : "l"(p), "r"(static_cast<int>(in)));
+      w[0] = v;
     }
   }
   __device__ __forceinline__ void store(T* p) const {
@@ -338,22 +356,24 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
     for (int i = 0; i < kAcross; ++i) sum[i] = 0.0f;
     for (int j0 = 0; j0 < d.k; j0 += kAhead) {
-      T x[kAhead][kAcross];
-      int64_t r[kAhead];
+      Piece<T, static_cast<int>(sizeof(T))> x[kAhead][kAcross];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        r[j] = __shfl_sync(0xFFFFFFFFu, row_now, (j0 + j) & 31);
+        // (lanes behind the k-th have no row)
+        const int64_t r = __shfl_sync(0xFFFFFFFFu, row_now, (j0 + j) & 31);
 #pragma unroll
         for (int i = 0; i < kAcross; ++i)
-          if (r[j] >= 0 && c + 32 * i < cols) x[j][i] = from[r[j] + 32 * i];
+          x[j][i].load_if(from + r + 32 * i, r >= 0 && c + 32 * i < cols);
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         const float w = __shfl_sync(0xFFFFFFFFu, w_now, (j0 + j) & 31);
-        if (r[j] < 0) continue;
 #pragma unroll
-        for (int i = 0; i < kAcross; ++i)
-          if (c + 32 * i < cols) sum[i] = fmaf(w, to_f32(x[j][i]), sum[i]);
+        for (int i = 0; i < kAcross; ++i) {
+          float f[1];
+          x[j][i].get(f);
+          sum[i] = fmaf(w, f[0], sum[i]);
+        }
       }
     }
     T* const to = static_cast<T*>(d.tokens) + at.t * d.ldt + c;
@@ -413,11 +433,19 @@ __global__ void __launch_bounds__(kRowThreads)
       auto fetch = [&](Pieces& p, int c) {
 #pragma unroll
         for (int i = 0; i < ACROSS; ++i) {
-          if (!on || c + i * kSpan + kElems > cols) continue;
-          p.x[i].load(dy + c + i * kSpan);
+          const int at_c = c + i * kSpan;
+          const bool in = on && at_c + kElems <= cols;
+          if constexpr (kElems == 1) {
+            p.x[i].load_if(dy + at_c, in);
 #pragma unroll
-          for (int j = 0; j < KA; ++j)
-            if (dots && r[j] >= 0) p.y[i][j].load(y_rows + r[j] * d.ldy + c + i * kSpan);
+            for (int j = 0; j < KA; ++j)
+              p.y[i][j].load_if(y_rows + r[j] * d.ldy + at_c, in && dots && r[j] >= 0);
+          } else if (in) {
+            p.x[i].load(dy + at_c);
+#pragma unroll
+            for (int j = 0; j < KA; ++j)
+              if (dots && r[j] >= 0) p.y[i][j].load(y_rows + r[j] * d.ldy + at_c);
+          }
         }
       };
       int c = place * kSpan * ACROSS + lane * kElems;
@@ -560,10 +588,8 @@ cudaError_t run(const mxg_expert_rows_t& d, int op, int num_sms, cudaStream_t st
     constexpr int kBytes = BYTES == 32 ? 16 : BYTES;
     if (d.k <= 2)
       combine_backward_kernel<T, BYTES, 2, kAcrossOf2><<<grid, kRowThreads, 0, stream>>>(d, team, pad);
-    else if (d.k <= 4)
-      combine_backward_kernel<T, kBytes, 4, kAcrossOf4><<<grid, kRowThreads, 0, stream>>>(d, team, pad);
     else
-      combine_backward_kernel<T, kBytes, 8, 1><<<grid, kRowThreads, 0, stream>>>(d, team, pad);
+      combine_backward_kernel<T, kBytes, 4, kAcrossOf4><<<grid, kRowThreads, 0, stream>>>(d, team, pad);
   }
   return cudaGetLastError();
 }
