@@ -6,7 +6,9 @@
 //
 // All three go by tokens, so that a token's row is read (or written) once and only the k
 // rows beside it are scattered; no row is shared, so nothing is atomic.  Memory is the
-// bound.
+// bound: dispatching 8192 tokens of 4096 in bf16 to 2 experts each takes 33.3 us, 6.2 TB/s of the
+// 6.78 that a copy reaches.  Rows that do not start on 16 bytes move element by element, at
+// 30 to 55 % of that.
 #include <algorithm>
 #include <atomic>
 
@@ -216,8 +218,8 @@ __device__ __forceinline__ void cp_async_16_or_zeros(uint32_t dst, const void* s
 // Sums of rows that start on 16 bytes.  A warp's item is a token and 1 KB of its columns, twice 16
 // bytes a lane; a lane's pieces of PER rows are a unit, and every thread has a ring of kDepth units in
 // shared memory that asynchronous copies fill ahead of the sums.  No thread reads another's
-// pieces, so there is no barrier.  4096 tokens of 8 rows of 2048 in fp16: TIMING; with the rows in
-// registers, 4 at a time to leave room for enough warps, 38.6 us; with 16 bytes a lane the
+// pieces, so there is no barrier.  4096 tokens of 8 rows of 2048 in fp16: 26.3 us, 5.7 TB/s; with the
+// rows in registers, 4 at a time to leave room for enough warps, 38.6 us; with 16 bytes a lane the
 // instructions for a row's place were the bound, at 33.5 us.
 constexpr int kRingThreads = 128, kDepth = 4;
 
@@ -383,9 +385,10 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-// A team of `team` warps owns a token, KA of its rows at a time and ACROSS pieces of each row a
-// lane; a lane's next pieces are asked for before it works on those it has.  Sums over the columns
-// are joined in shared memory.
+// The gradients of sums without the weights' among them, or of rows of any alignment (8192 tokens of
+// 2 rows of 4095 in bf16: 91 us).  A team of `team` warps owns a token, KA of its rows at a time and
+// ACROSS pieces of each row a lane; a lane's next pieces are asked for before it works on those it
+// has.  Sums over the columns are joined in shared memory.
 template <typename T, int BYTES, int KA, int ACROSS>
 __global__ void __launch_bounds__(kRowThreads)
     combine_backward_kernel(const mxg_expert_rows_t d, int team, int64_t pad_items) {
@@ -513,6 +516,177 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
+// The gradients of sums of rows that start on 16 bytes, with the weights' among them: as the sums,
+// through rings, a unit being 1 KB of a token's gradient and of PER of its rows.  A team of `team`
+// warps owns a token.  4096 tokens of 8 rows of 2048 in bf16: 53 us, 5.3 TB/s, through registers 62
+// us; 8192 tokens of 2 rows of 4096: 56 us, 5.8 TB/s, either way.
+constexpr int ring_depth(int per) { return per == 8 ? 3 : 4; }
+
+// A unit's halves for a thread, as pairs.
+template <typename T>
+__device__ __forceinline__ void ring_values(uint32_t at, uint32_t pitch,
+                                            F2 (&f)[16 / sizeof(T)]) {
+  constexpr int kPairs = 8 / static_cast<int>(sizeof(T));  // of a half
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint4 q = lds16(at + h * pitch);
+    const uint32_t word[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      float lo, hi;
+      if constexpr (sizeof(T) == 4) {
+        lo = __uint_as_float(word[2 * i]);
+        hi = __uint_as_float(word[2 * i + 1]);
+      } else {
+        unpack2<T>(word[i], lo, hi);
+      }
+      f[h * kPairs + i] = f2(lo, hi);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 half_of(const F2* f) {
+  uint32_t word[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4)
+      word[i] = __float_as_uint(i & 1 ? f2_hi(f[i / 2]) : f2_lo(f[i / 2]));
+    else
+      word[i] = pack2<T>(f2_lo(f[i]), f2_hi(f[i]));
+  }
+  return make_uint4(word[0], word[1], word[2], word[3]);
+}
+
+template <typename T, int PER>
+__global__ void __launch_bounds__(kRingThreads)
+    combine_backward_ring_kernel(const mxg_expert_rows_t d, int team, int slices, int64_t pad_items) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  constexpr int kWarps = kRingThreads / 32, kDeep = ring_depth(PER);
+  constexpr int kHalf = 16 / static_cast<int>(sizeof(T)), kPairs = kHalf;  // pairs of both halves
+  constexpr uint32_t kPitch = kRingThreads * 16, kUnit = 2 * (1 + PER) * kPitch;
+  __shared__ float part[kWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cols = static_cast<int>(d.cols);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + warp; i < pad_items;
+       i += static_cast<int64_t>(gridDim.x) * kWarps)
+    zero_padding<T, 16>(d, i);
+  const int teams = kWarps / team, place = warp % team;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * teams + warp / team;
+  const T* const dy = static_cast<const T*>(d.tokens);
+  const T* const y_rows = static_cast<const T*>(d.y_rows);
+  T* const rows = static_cast<T*>(d.rows);
+  auto row_at = [&](int64_t t) {
+    const int32_t at = t < d.n && lane < d.k ? d.row_of[t * d.k + lane] : -1;
+    return at < d.rows_capacity ? at : -1;
+  };
+  auto weight_at = [&](int64_t t) {
+    return t < d.n && lane < d.k && d.weight != nullptr ? d.weight[t * d.k + lane] : 1.0f;
+  };
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * 16, end = mine + kDeep * kUnit;
+  int64_t fill_t = first;
+  int fill_j = 0, fill_s = place;
+  int32_t fill_row = row_at(first), fill_then = row_at(first + step);
+  uint32_t fill_at = mine;
+  auto fill_unit = [&] {
+    if (fill_t < d.n) {
+      const int c = (fill_s * 64 + lane) * kHalf;
+      const bool in0 = c + kHalf <= cols, in1 = c + 33 * kHalf <= cols;
+      const T* const from = dy + fill_t * d.ldt + c;
+      cp_async_16_or_zeros(fill_at, in0 ? from : dy, in0);
+      cp_async_16_or_zeros(fill_at + kPitch, in1 ? from + 32 * kHalf : dy, in1);
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        // (lanes behind the k-th have no row)
+        const int32_t r = __shfl_sync(0xFFFFFFFFu, fill_row, (fill_j + j) & 31);
+        const T* const src = y_rows + r * d.ldy + c;
+        cp_async_16_or_zeros(fill_at + (2 + 2 * j) * kPitch, in0 && r >= 0 ? src : dy, in0 && r >= 0);
+        cp_async_16_or_zeros(fill_at + (3 + 2 * j) * kPitch, in1 && r >= 0 ? src + 32 * kHalf : dy,
+                             in1 && r >= 0);
+      }
+      if ((fill_s += team) >= slices) {
+        fill_s = place;
+        if ((fill_j += PER) >= d.k) {
+          fill_j = 0;
+          fill_t += step;
+          fill_row = fill_then;
+          fill_then = row_at(fill_t + step);
+        }
+      }
+    }
+    cp_async_commit();
+    if ((fill_at += kUnit) == end) fill_at = mine;
+  };
+#pragma unroll
+  for (int i = 0; i < kDeep - 1; ++i) fill_unit();
+  uint32_t at = mine;
+  int32_t next_row = row_at(first);
+  float next_w = weight_at(first);
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * teams, t = first; base < d.n;
+       base += step, t += step) {
+    const bool on = t < d.n;
+    const int32_t row = next_row;
+    const float w = next_w;
+    next_row = row_at(t + step);
+    next_w = weight_at(t + step);
+    float dot_mine = 0.0f;
+    for (int j0 = 0; on && j0 < d.k; j0 += PER) {
+      int32_t r[PER];
+      F2 wj[PER], dot[PER];
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        r[j] = __shfl_sync(0xFFFFFFFFu, row, (j0 + j) & 31);
+        wj[j] = f2(__shfl_sync(0xFFFFFFFFu, w, (j0 + j) & 31));
+        dot[j] = 0;
+      }
+      for (int s = place; s < slices; s += team) {
+        fill_unit();
+        cp_async_wait(kDeep - 1);
+        const int c = (s * 64 + lane) * kHalf;
+        const bool in0 = c + kHalf <= cols, in1 = c + 33 * kHalf <= cols;
+        F2 g[kPairs];
+        ring_values<T>(at, kPitch, g);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          F2 f[kPairs];
+          ring_values<T>(at + (2 + 2 * j) * kPitch, kPitch, f);
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) dot[j] = fma2(g[i], f[i], dot[j]);
+          if (rows != nullptr && r[j] >= 0) {
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) f[i] = mul2(wj[j], g[i]);
+            T* const to = rows + r[j] * d.ldr + c;
+            if (in0) *reinterpret_cast<uint4*>(to) = half_of<T>(f);
+            if (in1) *reinterpret_cast<uint4*>(to + 32 * kHalf) = half_of<T>(f + kPairs / 2);
+          }
+        }
+        if ((at += kUnit) == end) at = mine;
+      }
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        float v = r[j] < 0 ? 0.0f : sum2(dot[j]);
+        // what is left of a row whose columns do not end on 16 bytes: an element a lane
+        if (place == 0 && r[j] >= 0 && lane < cols % kHalf) {
+          const int e = cols / kHalf * kHalf + lane;
+          const float g = to_f32(dy[t * d.ldt + e]);
+          v = fmaf(g, to_f32(y_rows[r[j] * d.ldy + e]), v);
+          if (rows != nullptr) rows[r[j] * d.ldr + e] = from_f32<T>(f2_lo(wj[j]) * g);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        if (lane == j0 + j) dot_mine = v;
+      }
+    }
+    if (team > 1) {
+      part[warp][lane] = dot_mine;
+      __syncthreads();
+      if (place == 0)
+        for (int i = 1; i < team; ++i) dot_mine += part[warp + i][lane];
+      __syncthreads();
+    }
+    if (on && place == 0 && lane < d.k) d.dweight[t * d.k + lane] = dot_mine;
+  }
+}
+
 namespace {
 
 // Bytes of the accesses that every row allows: 32, 16 or an element's.
@@ -531,27 +705,55 @@ unsigned grid_for(int64_t warps, int num_sms, int64_t most) {
 
 int64_t slices_of(int64_t cols, int per) { return (cols + per - 1) / per; }
 
-// Units of 1, 2 or 4 rows, whichever holds k in fewest; as many CTAs as an SM has room for.  The
-// shared memory that a kernel may be launched with is set once per device.
-template <typename T, int PER>
-cudaError_t run_combine_ring(const mxg_expert_rows_t& d, int num_sms, cudaStream_t stream) {
-  constexpr int kSmem = kDepth * 2 * PER * kRingThreads * 16, kMaxDev = 64;
-  constexpr int kCtas = std::min(8, 220 * 1024 / (kSmem + 1024));
+constexpr int kRingSmem = 220 * 1024;  // of an SM's 227 KB
+
+// Allows KERN `smem` bytes, once per device: the limit belongs to the kernel, for all host threads.
+template <auto KERN>
+cudaError_t allow_smem(int smem) {
+  constexpr int kMaxDev = 64;
   static std::atomic<bool> ready[kMaxDev];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
-  if (!ready[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(combine_ring_kernel<T, PER>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    ready[dev].store(true, std::memory_order_release);
-  }
+  if (ready[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) ready[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+// Units of 1, 2 or 4 rows, whichever holds k in fewest; as many CTAs as an SM has room for.
+template <typename T, int PER>
+cudaError_t run_combine_ring(const mxg_expert_rows_t& d, int num_sms, cudaStream_t stream) {
+  constexpr int kSmem = kDepth * 2 * PER * kRingThreads * 16;
+  constexpr int kCtas = std::min(8, kRingSmem / (kSmem + 1024));
+  const cudaError_t e = allow_smem<combine_ring_kernel<T, PER>>(kSmem);
+  if (e != cudaSuccess) return e;
   const int64_t slices = slices_of(d.cols, 32 * 32 / static_cast<int>(sizeof(T)));
   const int64_t blocks = (d.n * slices + kRingThreads / 32 - 1) / (kRingThreads / 32);
   const unsigned grid =
       static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * kCtas));
   combine_ring_kernel<T, PER>
       <<<grid, kRingThreads, kSmem, stream>>>(d, static_cast<int>(slices));
+  return cudaGetLastError();
+}
+
+template <typename T, int PER>
+cudaError_t run_backward_ring(const mxg_expert_rows_t& d, int64_t pad, int num_sms,
+                              cudaStream_t stream) {
+  constexpr int kSmem = ring_depth(PER) * 2 * (1 + PER) * kRingThreads * 16;
+  constexpr int kCtas = std::min(4, kRingSmem / (kSmem + 2048)), kWarps = kRingThreads / 32;
+  const cudaError_t e = allow_smem<combine_backward_ring_kernel<T, PER>>(kSmem);
+  if (e != cudaSuccess) return e;
+  const int slices = static_cast<int>(slices_of(d.cols, 32 * 32 / static_cast<int>(sizeof(T))));
+  // more warps a token where the tokens alone do not fill the device
+  const int64_t most = static_cast<int64_t>(num_sms) * kCtas;
+  int team = 1;
+  while (team < kWarps && 2 * team <= slices && d.n * team < most * kWarps) team *= 2;
+  const int64_t warps = std::max(pad, d.n * team);
+  const unsigned grid =
+      static_cast<unsigned>(std::min<int64_t>((warps + kWarps - 1) / kWarps, most));
+  combine_backward_ring_kernel<T, PER>
+      <<<grid, kRingThreads, kSmem, stream>>>(d, team, slices, pad);
   return cudaGetLastError();
 }
 
@@ -578,18 +780,23 @@ cudaError_t run(const mxg_expert_rows_t& d, int op, int num_sms, cudaStream_t st
           d, static_cast<int>(slices));
     }
   } else {
+    if constexpr (BYTES >= 16) {
+      if (d.dweight != nullptr) {
+        if (d.k <= 2) return run_backward_ring<T, 2>(d, pad, num_sms, stream);
+        if (d.k <= 4) return run_backward_ring<T, 4>(d, pad, num_sms, stream);
+        return run_backward_ring<T, 8>(d, pad, num_sms, stream);
+      }
+    }
     // more warps a token where the tokens alone do not fill the device
     int team = 1;
     while (team < 8 && d.n * team < num_sms * 48LL && team * kSpan < d.cols) team *= 2;
-    // (two waves: 8192 tokens of 2 rows of 4096 in bf16 take 56 us, 58 us with a CTA for each 8)
+    // (two waves of them: 56 us for 8192 tokens of 2 rows of 4096 in bf16, 58 with a CTA for each 8)
     const unsigned grid = grid_for(pad + d.n * team, num_sms, 4);
     constexpr int kAcrossOf2 = BYTES < 16 ? 4 : 1, kAcrossOf4 = BYTES < 16 ? 2 : 1;
-    // pieces of 16 bytes where a lane has more than two rows' at once
-    constexpr int kBytes = BYTES == 32 ? 16 : BYTES;
     if (d.k <= 2)
       combine_backward_kernel<T, BYTES, 2, kAcrossOf2><<<grid, kRowThreads, 0, stream>>>(d, team, pad);
     else
-      combine_backward_kernel<T, kBytes, 4, kAcrossOf4><<<grid, kRowThreads, 0, stream>>>(d, team, pad);
+      combine_backward_kernel<T, BYTES, 4, kAcrossOf4><<<grid, kRowThreads, 0, stream>>>(d, team, pad);
   }
   return cudaGetLastError();
 }
