@@ -733,8 +733,8 @@ typedef enum { MXG_ACT_SILU = 0, MXG_ACT_GELU_TANH = 1 } mxg_act_t;
  *   entries sum to the live rows (negative ones count as 0); rows at or beyond
  *   them are neither read nor written.
  * rows from 0 to 2^31 - 128, 1 <= cols <= 2^20, G <= 1024.  h may be gate or up,
- * with the same ld, and dh dgate or dup.  Any element alignment; rows on 32 bytes
- * (q: 16) take accesses of that size. */
+ * with the same ld, and dh dgate or dup.  Any element alignment; rows on 32 or 16
+ * bytes (q: 16 or 8) with cols a multiple of 16 or 8 take accesses of that size. */
 typedef struct {
   mxg_dtype_t dtype;
   mxg_act_t act;

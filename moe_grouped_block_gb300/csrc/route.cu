@@ -14,8 +14,14 @@
 // expert and sums of p in the workspace.  A second kernel adds these up -- each CTA the
 // same ones in the same order -- and gives its chunk's tokens their rows: the expert's
 // start, the tokens of it in earlier chunks, those of earlier warps, and the rank among
-// the warp's lanes.  One chunk alone is finished by the first kernel.  No floating-point
+// the warp's tokens.  One chunk alone is finished by the first kernel.  No floating-point
 // atomics and no counters kept between calls.
+//
+// Instructions and the latency of dependent steps are the bound, not memory: 65536 tokens
+// to 8 of 256 experts (fp32, sigmoids, with the loss and the rows) take 40 us, 1.8 TB/s: 29 in the
+// first kernel, 286 instructions a token, and 6 in the second.  16384 tokens to 8 of 64: 11.7
+// us, half of it the second kernel and the step between the two.  8 tokens to 2 of 8: 6.3 us, one CTA.
+// The gradient of the former: 31.4 us, 4.4 TB/s of the 6.78 that a copy reaches.
 #include <algorithm>
 #include <type_traits>
 

@@ -83,7 +83,7 @@ def exact(layer, x, dy, kept):
     (dl,) = torch.autograd.grad((weight * dweight).sum() + loss, logits)
     dl = torch.where(live[:, None], dl, 0.0)
     grads["wr"] = dl.t() @ x
-    return y, float(loss), dx + dl @ w["wr"], grads
+    return y, float(loss.detach()), dx + dl @ w["wr"], grads
 
 
 def off(got, want):
