@@ -650,6 +650,17 @@ def _whole(t, dtypes: tuple, n: int, name: str, here: int) -> int:
     return _on(t, here)
 
 
+def _pitch(t, shape) -> int:
+    """_ld of a [rows, cols] matrix, in a third of its time."""
+    if t.is_contiguous():
+        return 0
+    rows, cols = shape
+    between, within = t.stride()
+    if (within != 1 and cols > 1) or (rows > 1 and between < cols):
+        return _ld(t)  # which says what is wrong
+    return between if rows > 1 else max(between, cols)
+
+
 def _matrix(t, dtype, shape, name: str, here: int) -> tuple:
     """(address, elements between the rows) of a [rows, cols] matrix of this type; zeros of none."""
     if t is None:
@@ -657,7 +668,7 @@ def _matrix(t, dtype, shape, name: str, here: int) -> tuple:
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError("%s: expected %s of %s: got %s of %s"
                          % (name, tuple(shape), dtype, tuple(t.shape), t.dtype))
-    return _on(t, here), _ld(t)
+    return _on(t, here), _pitch(t, shape)
 
 
 def _any(t, here: int) -> int:
@@ -718,7 +729,7 @@ def mxg_route(logits: torch.Tensor, expert: torch.Tensor, weight: torch.Tensor,
     kind, E = _logits(logits, tokens)
     n = tokens * k
     row, groups, capacity = _rows_wanted(row_of, group_ws, n, E, align, rows_capacity, here)
-    d = _pack_route(kind, tokens, E, k, _on(logits, here), _ld(logits),
+    d = _pack_route(kind, tokens, E, k, _on(logits, here), _pitch(logits, (tokens, E)),
                     _whole(mask, _MASK, tokens, "mask", here), score, normalize, scale, balance,
                     _whole(expert, _I32, n, "expert", here), _whole(weight, _FP32, n, "weight", here),
                     _whole(counts, _I32, E, "counts", here), _whole(loss, _FP32, 1, "loss", here),
@@ -753,7 +764,7 @@ def mxg_route_backward(logits: torch.Tensor, expert: torch.Tensor, dlogits: torc
     kind, E = _logits(logits, tokens)
     n = tokens * k
     d_at, ldd = _matrix(dlogits, logits.dtype, logits.shape, "dlogits", here)
-    d = _pack_route_grad(kind, tokens, E, k, _on(logits, here), _ld(logits),
+    d = _pack_route_grad(kind, tokens, E, k, _on(logits, here), _pitch(logits, (tokens, E)),
                          _whole(expert, _I32, n, "expert", here), score, normalize, scale,
                          _whole(dweight, _FP32, n, "dweight", here),
                          _whole(slope, _FP32, E, "slope", here),
@@ -777,7 +788,7 @@ def _expert_rows(fn: str, tokens, rows, row_of, weight, y_rows, dweight, counts,
     if (counts is None) != (group_ws is None):
         raise ValueError("counts and group_ws: both or neither")
     experts = 0 if counts is None else counts.numel()
-    d = _pack_expert_rows(kind, n, cols, k, experts, capacity, _on(tokens, here), _ld(tokens), rows_at,
+    d = _pack_expert_rows(kind, n, cols, k, experts, capacity, _on(tokens, here), _pitch(tokens, shape), rows_at,
                           ldr, _whole(row_of, _I32, n * k, "row_of", here),
                           _whole(weight, _FP32, n * k, "weight", here), y_at, ldy,
                           _whole(dweight, _FP32, n * k, "dweight", here),
@@ -822,7 +833,7 @@ def _kept(q, sf, rows: int, cols: int, parts: int, here: int) -> tuple:
     if q.dtype not in _BYTES or q.shape != (rows, parts * cols):
         raise ValueError("q: expected %s bytes: got %s of %s"
                          % ((rows, parts * cols), tuple(q.shape), q.dtype))
-    return _on(q, here), _ld(q), _whole(sf, _BYTES[:1], rows * parts * _act_blocks(cols), "sf", here)
+    return _on(q, here), _pitch(q, (rows, parts * cols)), _whole(sf, _BYTES[:1], rows * parts * _act_blocks(cols), "sf", here)
 
 
 def _act_shape(t, name: str) -> tuple:
@@ -844,7 +855,7 @@ def mxg_gated_act(gate: torch.Tensor, h: torch.Tensor, up=None, act: int = MXG_A
     h_at, ldh = _matrix(h, gate.dtype, gate.shape, "h", here)
     q_at, ldq, sf_at = _kept(q, sf, rows, cols, parts, here)
     d = _pack_gated_act(kind, act, rows, cols, parts - 1, G,
-                        _whole(group_ws, _I64, 2 * G + 1, "group_ws", here), _on(gate, here), _ld(gate),
+                        _whole(group_ws, _I64, 2 * G + 1, "group_ws", here), _on(gate, here), _pitch(gate, (rows, cols)),
                         up_at, ldu, h_at, ldh, q_at, ldq, sf_at, 0, 0, 0, 0, 0, 0)
     _check("mxg_gated_act", load().mxg_gated_act(d, _stream_on(stream, here)))
 
@@ -862,7 +873,7 @@ def mxg_gated_act_backward(q: torch.Tensor, sf: torch.Tensor, dh: torch.Tensor, 
     q_at, ldq, sf_at = _kept(q, sf, rows, cols, parts, here)
     d = _pack_gated_act(kind, act, rows, cols, parts - 1, G,
                         _whole(group_ws, _I64, 2 * G + 1, "group_ws", here), 0, 0, 0, 0, h_at, ldh, q_at,
-                        ldq, sf_at, _on(dh, here), _ld(dh), dgate_at, lddg, dup_at, lddu)
+                        ldq, sf_at, _on(dh, here), _pitch(dh, (rows, cols)), dgate_at, lddg, dup_at, lddu)
     _check("mxg_gated_act_backward", load().mxg_gated_act_backward(d, _stream_on(stream, here)))
 
 

@@ -271,3 +271,40 @@ def test_refusals():
         with pytest.raises(mxg.MxgError) as err:
             call()
         assert err.value.code == 1
+
+
+def test_calls_from_several_threads():
+    """Each thread on a stream of its own, with its own k and so its own kernel and shared memory."""
+    import threading
+    want, wrong = {}, []
+
+    def call(k):
+        row_of, _, _, cap = plan(64, 16, k, 20 + k)
+        rows, x = normal((cap, 256), BF, k), normal((64, 256), BF, 30 + k)
+        w = normal((64, k), F32, 50 + k)
+
+        def once():
+            y, d, dw = torch.empty_like(x), torch.zeros_like(rows), torch.empty(64, k, device=DEV)
+            mxg.mxg_combine(rows, row_of, y, weight=w)
+            mxg.mxg_combine_backward(x, row_of, w, d, y_rows=rows, dweight=dw)
+            return y, d, dw
+        return once
+    calls = {k: call(k) for k in (1, 2, 3, 8)}
+    for k, once in calls.items():
+        want[k] = once()
+    torch.cuda.synchronize()
+
+    def work(k):
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            for _ in range(100):
+                got = calls[k]()
+                side.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[k])):
+                    wrong.append(k)
+    threads = [threading.Thread(target=work, args=(k,)) for k in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == []
