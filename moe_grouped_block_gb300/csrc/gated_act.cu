@@ -324,13 +324,17 @@ struct BlockWalk {
 };
 
 // A column's value to its E4M3 byte, and the block's scale byte; by a whole warp.
-__device__ __forceinline__ void keep_column(float v, uint32_t& byte, uint32_t& scale_byte) {
-  if (isinf(v)) v = __uint_as_float(0x7FC00000u);  // an infinity is kept as NaN
-  // magnitudes are in the order of their bits; NaN is none
-  const uint32_t size = v != v ? 0u : __float_as_uint(fabsf(v));
-  const int e = mx_exponent(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, size)));
-  byte = cvt_e4m3x2(v * pow2_neg(e), 0.0f) & 0xFFu;
-  scale_byte = static_cast<uint32_t>(e + 127);
+__device__ __forceinline__ uint32_t keep_column(float v, uint32_t& byte) {
+  // magnitudes are in the order of their bits
+  uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(v)));
+  if (top >= 0x7F800000u) {  // infinities are kept as NaN, and neither is among the magnitudes
+    const bool fine = fabsf(v) < INFINITY;
+    top = __reduce_max_sync(0xFFFFFFFFu, fine ? __float_as_uint(fabsf(v)) : 0u);
+    if (!fine) v = __uint_as_float(0x7FC00000u);
+  }
+  const int e = mx_exponent(__uint_as_float(top));
+  byte = cvt_e4m3x2(v * pow2_neg(e), 0.0f);
+  return static_cast<uint32_t>(e + 127);
 }
 
 template <typename T, int ACT, bool GATED>
@@ -360,18 +364,23 @@ __global__ void __launch_bounds__(kActThreads)
     if (d.q == nullptr) continue;
     uint8_t* q = d.q + at.row * d.ldq;
     uint8_t* sf = d.sf + at.row * sf_row;
+    uint32_t mine_g = 0, mine_u = 0;  // lane i keeps the scale of block i
 #pragma unroll
     for (int i = 0; i < kAcross; ++i) {
-      const int b = b0 + i, c = b * 32 + lane;
-      uint32_t byte, scale;
-      keep_column(g[i], byte, scale);
+      const int c = (b0 + i) * 32 + lane;
+      uint32_t byte;
+      const uint32_t scale = keep_column(g[i], byte);
       if (c < cols) q[c] = static_cast<uint8_t>(byte);
-      if (lane == 0 && b < blocks) sf[b] = static_cast<uint8_t>(scale);
+      if (lane == i) mine_g = scale;
       if (GATED) {
-        keep_column(u[i], byte, scale);
+        const uint32_t scale_u = keep_column(u[i], byte);
         if (c < cols) q[cols + c] = static_cast<uint8_t>(byte);
-        if (lane == 0 && b < blocks) sf[blocks + b] = static_cast<uint8_t>(scale);
+        if (lane == i) mine_u = scale_u;
       }
+    }
+    if (lane < kAcross && b0 + lane < blocks) {
+      sf[b0 + lane] = static_cast<uint8_t>(mine_g);
+      if (GATED) sf[blocks + b0 + lane] = static_cast<uint8_t>(mine_u);
     }
   }
 }
