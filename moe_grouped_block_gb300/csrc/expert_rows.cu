@@ -48,15 +48,15 @@ struct Piece {
     static_assert(kElems == 1, "of single elements");
     if constexpr (sizeof(T) == 4) {
       asm volatile(
-          "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b32 %0, 0;\n\t"
-          "@q ld.global.b32 %0, [%1];\n\t}"
+          "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+          "@q ld.global.b32 %0, [%1];\n\t@!q mov.b32 %0, 0;\n\t}"
           : "=r"(w[0])
           : "l"(p), "r"(static_cast<int>(in)));
     } else {
       uint16_t v;
       asm volatile(
-          "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b16 %0, 0;\n\t"
-          "@q ld.global.b16 %0, [%1];\n\t}"
+          "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+          "@q ld.global.b16 %0, [%1];\n\t@!q mov.b16 %0, 0;\n\t}"
           : "=h"(v)
           : "l"(p), "r"(static_cast<int>(in)));
       w[0] = v;
@@ -97,8 +97,8 @@ struct Piece {
   }
 };
 
-// Zeros in the rows between each expert's count and its padded size, by the warps
-// `warp`, `warp` + `warps` and so on: kPadWarps of them share an expert's.
+// Zeros in the rows between an expert's count and its padded size: item kPadWarps e + i is a warp's
+// share of expert e's.
 constexpr int kPadWarps = 16;
 
 template <typename T, int BYTES>

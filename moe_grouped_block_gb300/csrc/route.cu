@@ -19,7 +19,7 @@
 //
 // Instructions and the latency of dependent steps are the bound, not memory: 65536 tokens
 // to 8 of 256 experts (fp32, sigmoids, with the loss and the rows) take 40 us, 1.8 TB/s: 29 in the
-// first kernel, 286 instructions a token, and 6 in the second.  16384 tokens to 8 of 64: 11.7
+// first kernel, 280 instructions a token, and 6 in the second.  16384 tokens to 8 of 64: 11.7
 // us, half of it the second kernel and the step between the two.  8 tokens to 2 of 8: 6.3 us, one CTA.
 // The gradient of the former: 31.4 us, 4.4 TB/s of the 6.78 that a copy reaches.
 #include <algorithm>
@@ -31,7 +31,7 @@
 namespace mxg {
 
 constexpr int kMaxExperts = 1024;
-constexpr int kMaxChunks = 152;
+constexpr int kMaxChunks = 152;  // a CTA an SM
 constexpr uint32_t kNoLogit = 0x007FFFFFu;  // the key of -infinity: it and all below are not chosen
 constexpr int kOneItems = 4096;  // choices of a batch that one CTA finishes
 
@@ -205,8 +205,8 @@ struct LogitRow {
 };
 
 // ---------------------------------------------------------------- rows
-// Sums over the chunks of `n` columns, `pitch` apart from one chunk to the next, into
-// parts of shared memory: part p, column c at [p * 4 * quads + c].  LOW: beside the sums, those
+// Sums over the chunks, `pitch` columns each, into parts of shared memory: part p, column c at
+// [p * pitch + c].  LOW: beside the sums, those
 // of the chunks below `low`, `kBufWords / 2` further on.
 template <bool LOW, typename V4, typename V>
 __device__ __forceinline__ void sum_chunks(V* to, const V* from, int pitch, int chunks, int low,

@@ -20,7 +20,8 @@ NAN = float("nan")
 
 # tokens, columns, experts, k
 SHAPES = [(1, 8, 4, 1), (1, 4096, 8, 2), (5, 1, 3, 3), (37, 100, 8, 4), (300, 512, 16, 8),
-          (64, 1000, 8, 5), (2000, 136, 64, 6), (130, 4100, 4, 2), (513, 257, 40, 32), (16, 7168, 64, 8)]
+          (64, 1000, 8, 5), (2000, 136, 64, 6), (130, 4100, 4, 2), (513, 257, 40, 32), (16, 7168, 64, 8),
+          (50, 264, 40, 32), (70, 128, 32, 11), (3, 521, 9, 3), (1, 1033, 16, 9)]
 
 
 @pytest.fixture(autouse=True)
@@ -55,7 +56,9 @@ def buffers(shape, dtype, ld, offset, fill):
     return whole, whole[offset:offset + rows * ld].view(rows, ld)[:, :cols]
 
 
-LAYOUTS = [(0, 0), (8, 0), (3, 1)]  # elements more in a row, elements before the first
+# elements more in a row, elements before the first; (7, 0) brings rows of 8 n + 1 columns, whose
+# last element is no whole piece, to 16 bytes and more
+LAYOUTS = [(0, 0), (8, 0), (7, 0), (3, 1)]
 
 
 @pytest.mark.parametrize("n,cols,E,k", SHAPES)
