@@ -136,6 +136,8 @@ __global__ void __launch_bounds__(kRowThreads)
     dispatch_kernel(const mxg_expert_rows_t d, int slices, int64_t pad_items) {
   constexpr int kElems = Piece<T, BYTES>::kElems;
   const int lane = threadIdx.x & 31;
+  grid_wait_for_previous();
+  grid_launch_dependents();
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kRowThreads / 32);
   const int64_t items = pad_items + d.n * slices;
   for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
@@ -233,6 +235,8 @@ __global__ void __launch_bounds__(kRingThreads)
   const int lane = threadIdx.x & 31, cols = static_cast<int>(d.cols);
   const uint32_t mine = smem_u32(ring) + threadIdx.x * 16, end = mine + kDepth * kUnit;
   const T* const rows = static_cast<const T*>(d.rows);
+  grid_wait_for_previous();
+  grid_launch_dependents();
 
   TokenWalk<kRingThreads> fill(slices), work = fill, fill_next = fill;
   fill_next.next();
@@ -343,6 +347,8 @@ __global__ void __launch_bounds__(kRowThreads)
     combine_kernel(const mxg_expert_rows_t d, int slices) {
   constexpr int kAhead = 4;
   const int lane = threadIdx.x & 31, cols = static_cast<int>(d.cols);
+  grid_wait_for_previous();
+  grid_launch_dependents();
   TokenWalk<kRowThreads> at(slices), then = at;
   int64_t row = row_start(d, at.t);
   float weight = row_weight(d, at.t);
@@ -399,6 +405,8 @@ __global__ void __launch_bounds__(kRowThreads)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, teams = kWarps / team;
   const int place = warp % team;  // in the team
   const bool dots = d.dweight != nullptr, writes = d.rows != nullptr;
+  grid_wait_for_previous();
+  grid_launch_dependents();
   const int64_t pad_blocks = (pad_items + kWarps - 1) / kWarps;
   const int64_t token_blocks = (d.n + teams - 1) / teams;
   const int cols = static_cast<int>(d.cols), step = team * kSpan * ACROSS;
@@ -566,6 +574,8 @@ __global__ void __launch_bounds__(kRingThreads)
   constexpr uint32_t kPitch = kRingThreads * 16, kUnit = 2 * (1 + PER) * kPitch;
   __shared__ float part[kWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cols = static_cast<int>(d.cols);
+  grid_wait_for_previous();
+  grid_launch_dependents();
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + warp; i < pad_items;
        i += static_cast<int64_t>(gridDim.x) * kWarps)
     zero_padding<T, 16>(d, i);
@@ -732,9 +742,8 @@ cudaError_t run_combine_ring(const mxg_expert_rows_t& d, int num_sms, cudaStream
   const int64_t blocks = (d.n * slices + kRingThreads / 32 - 1) / (kRingThreads / 32);
   const unsigned grid =
       static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * kCtas));
-  combine_ring_kernel<T, PER>
-      <<<grid, kRingThreads, kSmem, stream>>>(d, static_cast<int>(slices));
-  return cudaGetLastError();
+  return launch_after(true, combine_ring_kernel<T, PER>, grid, kRingThreads, kSmem, stream, d,
+                      static_cast<int>(slices));
 }
 
 template <typename T, int PER>
@@ -752,9 +761,8 @@ cudaError_t run_backward_ring(const mxg_expert_rows_t& d, int64_t pad, int num_s
   const int64_t warps = std::max(pad, d.n * team);
   const unsigned grid =
       static_cast<unsigned>(std::min<int64_t>((warps + kWarps - 1) / kWarps, most));
-  combine_backward_ring_kernel<T, PER>
-      <<<grid, kRingThreads, kSmem, stream>>>(d, team, slices, pad);
-  return cudaGetLastError();
+  return launch_after(true, combine_backward_ring_kernel<T, PER>, grid, kRingThreads, kSmem, stream,
+                      d, team, slices, pad);
 }
 
 template <typename T, int BYTES>
@@ -766,9 +774,9 @@ cudaError_t run(const mxg_expert_rows_t& d, int op, int num_sms, cudaStream_t st
   if (op == 0) {
     constexpr int kUnroll = BYTES >= 16 ? 2 : 8;
     const int64_t slices = slices_of(d.cols, kSpan * kUnroll);
-    dispatch_kernel<T, BYTES, kUnroll>
-        <<<grid_for(pad + d.n * slices, num_sms, 64), kRowThreads, 0, stream>>>(
-            d, static_cast<int>(slices), pad);
+    return launch_after(true, dispatch_kernel<T, BYTES, kUnroll>,
+                        grid_for(pad + d.n * slices, num_sms, 64), kRowThreads, 0, stream, d,
+                        static_cast<int>(slices), pad);
   } else if (op == 1) {
     if constexpr (BYTES >= 16) {
       if (d.k == 1) return run_combine_ring<T, 1>(d, num_sms, stream);
@@ -776,8 +784,8 @@ cudaError_t run(const mxg_expert_rows_t& d, int op, int num_sms, cudaStream_t st
       return run_combine_ring<T, 4>(d, num_sms, stream);
     } else {
       const int64_t slices = slices_of(d.cols, 32 * kAcross);
-      combine_kernel<T><<<grid_for(d.n * slices, num_sms, 64), kRowThreads, 0, stream>>>(
-          d, static_cast<int>(slices));
+      return launch_after(true, combine_kernel<T>, grid_for(d.n * slices, num_sms, 64), kRowThreads, 0,
+                          stream, d, static_cast<int>(slices));
     }
   } else {
     if constexpr (BYTES >= 16) {
@@ -794,11 +802,11 @@ cudaError_t run(const mxg_expert_rows_t& d, int op, int num_sms, cudaStream_t st
     const unsigned grid = grid_for(pad + d.n * team, num_sms, 4);
     constexpr int kAcrossOf2 = BYTES < 16 ? 4 : 1, kAcrossOf4 = BYTES < 16 ? 2 : 1;
     if (d.k <= 2)
-      combine_backward_kernel<T, BYTES, 2, kAcrossOf2><<<grid, kRowThreads, 0, stream>>>(d, team, pad);
-    else
-      combine_backward_kernel<T, BYTES, 4, kAcrossOf4><<<grid, kRowThreads, 0, stream>>>(d, team, pad);
+      return launch_after(true, combine_backward_kernel<T, BYTES, 2, kAcrossOf2>, grid, kRowThreads, 0,
+                          stream, d, team, pad);
+    return launch_after(true, combine_backward_kernel<T, BYTES, 4, kAcrossOf4>, grid, kRowThreads, 0,
+                        stream, d, team, pad);
   }
-  return cudaGetLastError();
 }
 
 template <typename T>

@@ -174,6 +174,8 @@ template <typename T, int ACT, bool GATED, int ALIGN>
 __global__ void __launch_bounds__(kActThreads)
     gated_act_kernel(const mxg_gated_act_t d, int blocks) {
   const int cols = static_cast<int>(d.cols);
+  grid_wait_for_previous();
+  grid_launch_dependents();
   const int64_t live = act_rows(d);
   const bool keep = d.q != nullptr;
   HalfWalk at(2 * blocks);
@@ -249,6 +251,8 @@ template <typename T, int ACT, bool GATED, int ALIGN>
 __global__ void __launch_bounds__(kActThreads, 3)
     gated_act_backward_kernel(const mxg_gated_act_t d, int blocks) {
   const int cols = static_cast<int>(d.cols);
+  grid_wait_for_previous();
+  grid_launch_dependents();
   const int64_t live = act_rows(d);
   HalfWalk at(2 * blocks), then = at;
   KeptHalf<T, GATED, ALIGN> in;
@@ -341,6 +345,8 @@ template <typename T, int ACT, bool GATED>
 __global__ void __launch_bounds__(kActThreads)
     gated_act_columns_kernel(const mxg_gated_act_t d, int blocks) {
   const int cols = static_cast<int>(d.cols), lane = threadIdx.x & 31;
+  grid_wait_for_previous();
+  grid_launch_dependents();
   const int64_t live = act_rows(d), sf_row = (GATED ? 2 : 1) * static_cast<int64_t>(blocks);
   for (BlockWalk at(blocks); at.row < live; at.next()) {
     const T* gate = static_cast<const T*>(d.gate) + at.row * d.ldg;
@@ -389,6 +395,8 @@ template <typename T, int ACT, bool GATED>
 __global__ void __launch_bounds__(kActThreads)
     gated_act_backward_columns_kernel(const mxg_gated_act_t d, int blocks) {
   const int cols = static_cast<int>(d.cols), lane = threadIdx.x & 31;
+  grid_wait_for_previous();
+  grid_launch_dependents();
   const int64_t live = act_rows(d), sf_row = (GATED ? 2 : 1) * static_cast<int64_t>(blocks);
   for (BlockWalk at(blocks); at.row < live; at.next()) {
     const T* dh = static_cast<const T*>(d.dh) + at.row * d.lddh;
@@ -454,23 +462,16 @@ cudaError_t run(const mxg_gated_act_t& d, bool backward, int num_sms, cudaStream
                                      : d.rows * 2 * blocks;
   const unsigned grid = static_cast<unsigned>(
       std::min<int64_t>((threads + kActThreads - 1) / kActThreads, num_sms * 16LL));
-  if (backward) {
-    if (align == 32)
-      gated_act_backward_kernel<T, ACT, GATED, 32><<<grid, kActThreads, 0, stream>>>(d, blocks);
-    else if (align == 16)
-      gated_act_backward_kernel<T, ACT, GATED, 16><<<grid, kActThreads, 0, stream>>>(d, blocks);
-    else
-      gated_act_backward_columns_kernel<T, ACT, GATED>
-          <<<grid, kActThreads, 0, stream>>>(d, blocks);
-  } else {
-    if (align == 32)
-      gated_act_kernel<T, ACT, GATED, 32><<<grid, kActThreads, 0, stream>>>(d, blocks);
-    else if (align == 16)
-      gated_act_kernel<T, ACT, GATED, 16><<<grid, kActThreads, 0, stream>>>(d, blocks);
-    else
-      gated_act_columns_kernel<T, ACT, GATED><<<grid, kActThreads, 0, stream>>>(d, blocks);
-  }
-  return cudaGetLastError();
+  auto launch = [&](auto kern) {
+    return launch_after(true, kern, grid, kActThreads, 0, stream, d, blocks);
+  };
+  if (backward)
+    return align == 32   ? launch(gated_act_backward_kernel<T, ACT, GATED, 32>)
+           : align == 16 ? launch(gated_act_backward_kernel<T, ACT, GATED, 16>)
+                         : launch(gated_act_backward_columns_kernel<T, ACT, GATED>);
+  return align == 32   ? launch(gated_act_kernel<T, ACT, GATED, 32>)
+         : align == 16 ? launch(gated_act_kernel<T, ACT, GATED, 16>)
+                       : launch(gated_act_columns_kernel<T, ACT, GATED>);
 }
 
 template <typename T>

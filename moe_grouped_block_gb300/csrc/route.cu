@@ -471,6 +471,7 @@ __global__ void __launch_bounds__(kManyThreads)
     route_finish_kernel(const RowPlan p, const RouteWs ws, int first) {
   __shared__ RouteShared<kBufWords> sh;
   grid_wait_for_previous();
+  grid_launch_dependents();
   const int c = first + static_cast<int>(blockIdx.x);
   finish_chunk<kManyThreads, false>(p, sh, ws, p.expert + c * p.per * p.k, c);
 }
@@ -480,7 +481,8 @@ template <int NT, bool ONE>
 __global__ void __launch_bounds__(NT) route_count_kernel(const RowPlan p, const RouteWs ws) {
   __shared__ RouteShared<ONE ? kBufWords / 2 : kBufWords> sh;
   const int tid = threadIdx.x, c = blockIdx.x, E = p.experts;
-  if (!ONE) grid_launch_dependents();
+  grid_wait_for_previous();
+  grid_launch_dependents();
   for (int e = tid; e < E; e += NT) sh.hist[e] = 0;
   __syncthreads();
   const int64_t begin = c * p.per, end = min(begin + p.per, p.tokens);
@@ -699,10 +701,11 @@ __global__ void __launch_bounds__(NT)
   __shared__ int32_t choices[ONE ? kOneItems : 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
   const int gl = lane & (LPT - 1), E = d.experts, k = d.k;
-  if (!ONE) grid_launch_dependents();
   for (int e = tid; e < E; e += NT) sh.hist[e] = 0;
   if (tid == 0) sh.live = 0;
   __syncthreads();
+  grid_wait_for_previous();
+  grid_launch_dependents();
 
   const int64_t begin = c * p.per;
   const int count = static_cast<int>(max(min(begin + p.per, d.tokens) - begin, int64_t{0}));
@@ -862,6 +865,8 @@ __global__ void __launch_bounds__(kGradThreads, VPL <= 16 ? 4 : 1)
   const bool softmax = d.score == MXG_SCORE_SOFTMAX, balance = d.slope != nullptr;
   // the weights' gradient goes through the shares; whether any of it does
   const bool joined = softmax && !d.normalize, shares = balance || joined;
+  grid_wait_for_previous();
+  grid_launch_dependents();
   const float dloss = balance ? *d.dloss : 0.0f;
   for (int e = tid; e < kCols; e += kGradThreads)
     reinterpret_cast<float*>(slopes)[halves_at(e, kCols)] = balance && e < E ? d.slope[e] * dloss : 0.0f;
@@ -1103,9 +1108,8 @@ template <typename T, int LPT, int VPL, int KPL, bool ONE>
 cudaError_t run_route(const mxg_route_t& d, const RowPlan& p, const RouteWs& ws, int vec,
                       cudaStream_t stream) {
   constexpr int kThreads = threads_of(LPT, VPL, ONE);
-  route_kernel<T, LPT, VPL, KPL, kThreads, ONE>
-      <<<static_cast<unsigned>(p.chunks), kThreads, 0, stream>>>(d, p, ws, vec);
-  return cudaGetLastError();
+  return launch_after(true, route_kernel<T, LPT, VPL, KPL, kThreads, ONE>,
+                      static_cast<unsigned>(p.chunks), kThreads, 0, stream, d, p, ws, vec);
 }
 
 template <typename T>
@@ -1142,10 +1146,10 @@ cudaError_t route_typed(const mxg_route_t& d, const RowPlan& p, const RouteWs& w
 template <typename T, int LPT, int VPL, int KPL>
 cudaError_t run_backward(const mxg_route_grad_t& d, int vec, int num_sms, cudaStream_t stream) {
   constexpr int kTeams = kGradThreads / LPT;
-  const int64_t grid = std::min<int64_t>((d.tokens + kTeams - 1) / kTeams, num_sms * 8LL);
-  route_backward_kernel<T, LPT, VPL, KPL>
-      <<<static_cast<unsigned>(grid), kGradThreads, 0, stream>>>(d, vec);
-  return cudaGetLastError();
+  // as many CTAs as the device holds: 29.4 us for 65536 x 256 in fp32, 31.1 with two waves of them
+  const int64_t grid = std::min<int64_t>((d.tokens + kTeams - 1) / kTeams, num_sms * 4LL);
+  return launch_after(true, route_backward_kernel<T, LPT, VPL, KPL>, static_cast<unsigned>(grid),
+                      kGradThreads, 0, stream, d, vec);
 }
 
 template <typename T>
@@ -1229,13 +1233,10 @@ cudaError_t launch_route_rows(const int32_t* expert, int64_t tokens, int experts
   cut_finish(&p, c.n == 1 ? kOneThreads : kManyThreads);
   const RouteWs ws = carve(workspace, c.n, experts);
   ++*launches;
-  if (c.n == 1) {
-    route_count_kernel<kOneThreads, true><<<1, kOneThreads, 0, stream>>>(p, ws);
-    return cudaGetLastError();
-  }
-  route_count_kernel<kManyThreads, false>
-      <<<static_cast<unsigned>(c.n), kManyThreads, 0, stream>>>(p, ws);
-  const cudaError_t e = cudaGetLastError();
+  if (c.n == 1)
+    return launch_after(true, route_count_kernel<kOneThreads, true>, 1, kOneThreads, 0, stream, p, ws);
+  const cudaError_t e = launch_after(true, route_count_kernel<kManyThreads, false>,
+                                     static_cast<unsigned>(c.n), kManyThreads, 0, stream, p, ws);
   return e != cudaSuccess ? e : launch_finish(p, ws, stream, launches);
 }
 

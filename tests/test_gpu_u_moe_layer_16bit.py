@@ -172,3 +172,51 @@ def test_padded_groups_feed_the_quantized_products():
     # each operand is off by half a step of E4M3 at most, 2^-4 of the value: independent, so well
     # within twice that in the 2-norm
     assert off(y, want) <= 2 * 2.0 ** -4
+
+
+@pytest.mark.parametrize("tokens", [5, 300, 4000])
+def test_calls_one_after_the_other(example, tokens):
+    """Each kernel is set up while the one before it ends: calls that read what the last one wrote,
+    into the same buffers over and over, give the same bits as calls that are waited for."""
+    from gpu_util import DEV
+    from moe_grouped_block_gb300 import mxg
+    D, F, E, k = 128, 96, 16, 4
+
+    def run(wait):
+        layer = example.Layer(tokens, D, F, E, k, balance=0.3)
+        x, dy, mask = example.batch(tokens, D)
+        names = [n for n in dir(mxg) if n in (
+            "mxg_route", "mxg_dispatch", "mxg_gated_act", "mxg_combine", "mxg_combine_backward",
+            "mxg_gated_act_backward", "mxg_route_backward", "mxg_grouped_gemm_16bit")]
+        kept = {n: getattr(mxg, n) for n in names}
+
+        def waited(fn):
+            def call(*a, **kw):
+                fn(*a, **kw)
+                if wait:
+                    torch.cuda.synchronize()
+            return call
+        try:
+            for n in names:
+                setattr(mxg, n, waited(kept[n]))
+            for _ in range(20):
+                y = layer.forward(x, mask)
+                dx = layer.backward(x, dy)
+                x = (x.float() + 0.1 * y.float() - 0.1 * dx.float()).to(torch.bfloat16)
+        finally:
+            for n in names:
+                setattr(mxg, n, kept[n])
+        torch.cuda.synchronize()
+        return [x, y, dx, layer.expert, layer.weight, layer.loss] + list(layer.grads.values())
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)
+    # and each operator on what it wrote itself a moment ago
+    rows = torch.zeros(tokens, D, device=DEV)
+    t = torch.arange(tokens, dtype=torch.int32, device=DEV)[:, None]
+    back = tokens - 1 - t
+    a = torch.randn(tokens, D, generator=torch.Generator(device=DEV).manual_seed(5), device=DEV)
+    want = a.clone()
+    for i in range(60):  # an odd number of reversals in each round
+        mxg.mxg_dispatch(a, back.contiguous(), rows)
+        mxg.mxg_combine(rows, t, a)
+    assert torch.equal(a, want)
