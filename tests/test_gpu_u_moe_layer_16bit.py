@@ -185,6 +185,7 @@ def test_calls_one_after_the_other(example, tokens):
     def run(wait):
         layer = example.Layer(tokens, D, F, E, k, balance=0.3)
         x, dy, mask = example.batch(tokens, D)
+        seen = []
         names = [n for n in dir(mxg) if n in (
             "mxg_route", "mxg_dispatch", "mxg_gated_act", "mxg_combine", "mxg_combine_backward",
             "mxg_gated_act_backward", "mxg_route_backward", "mxg_grouped_gemm_16bit")]
@@ -202,14 +203,17 @@ def test_calls_one_after_the_other(example, tokens):
             for _ in range(20):
                 y = layer.forward(x, mask)
                 dx = layer.backward(x, dy)
+                seen += [y.clone(), dx.clone(), layer.expert.clone(), layer.dlogits.clone()]
                 x = (x.float() + 0.1 * y.float() - 0.1 * dx.float()).to(torch.bfloat16)
         finally:
             for n in names:
                 setattr(mxg, n, kept[n])
         torch.cuda.synchronize()
-        return [x, y, dx, layer.expert, layer.weight, layer.loss] + list(layer.grads.values())
+        return seen + [x, layer.weight, layer.loss] + list(layer.grads.values())
+    # (x grows until, after some 14 rounds, it is past bf16's range: NaN is the same as NaN here)
     for a, b in zip(run(True), run(False)):
-        assert torch.equal(a, b)
+        assert torch.equal(torch.isnan(a), torch.isnan(b))
+        assert torch.equal(a.nan_to_num(), b.nan_to_num())
     # and each operator on what it wrote itself a moment ago
     rows = torch.zeros(tokens, D, device=DEV)
     t = torch.arange(tokens, dtype=torch.int32, device=DEV)[:, None]
