@@ -626,9 +626,13 @@ _I32, _I64, _FP32 = (torch.int32,), (torch.int64,), (torch.float32,)
 _MASK, _BYTES = (torch.uint8, torch.bool), (torch.uint8, torch.float8_e4m3fn)
 
 
+# (the public torch.cuda.current_device takes twice the time)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _here() -> int:
     """The device that launches go to."""
-    return torch.cuda.current_device()
+    return _device()
 
 
 def _on(t, here: int) -> int:
@@ -641,9 +645,7 @@ def _on(t, here: int) -> int:
 
 
 def _whole(t, dtypes: tuple, n: int, name: str, here: int) -> int:
-    """The address of a contiguous tensor of n elements of one of these types; 0 of none."""
-    if t is None:
-        return 0
+    """The address of a contiguous tensor of n elements of one of these types."""
     if t.dtype not in dtypes or t.numel() != n or not t.is_contiguous():
         raise ValueError("%s: expected %d contiguous elements of %s: got %s of %s"
                          % (name, n, dtypes[0], tuple(t.shape), t.dtype))
@@ -708,6 +710,8 @@ def _rows_wanted(row_of, group_ws, choices: int, experts: int, align: int, rows_
         raise ValueError("row_of and group_ws: both or neither")
     if rows_capacity is None:
         rows_capacity = choices + experts * (align - 1)
+    if row_of is None:
+        return 0, 0, rows_capacity
     return (_whole(row_of, _I32, choices, "row_of", here),
             _whole(group_ws, _I64, 2 * experts + 1, "group_ws", here), rows_capacity)
 
@@ -730,10 +734,12 @@ def mxg_route(logits: torch.Tensor, expert: torch.Tensor, weight: torch.Tensor,
     n = tokens * k
     row, groups, capacity = _rows_wanted(row_of, group_ws, n, E, align, rows_capacity, here)
     d = _pack_route(kind, tokens, E, k, _on(logits, here), _pitch(logits, (tokens, E)),
-                    _whole(mask, _MASK, tokens, "mask", here), score, normalize, scale, balance,
-                    _whole(expert, _I32, n, "expert", here), _whole(weight, _FP32, n, "weight", here),
-                    _whole(counts, _I32, E, "counts", here), _whole(loss, _FP32, 1, "loss", here),
-                    _whole(slope, _FP32, E, "slope", here), row, groups, align, capacity, last_dim)
+                    0 if mask is None else _whole(mask, _MASK, tokens, "mask", here), score,
+                    normalize, scale, balance, _whole(expert, _I32, n, "expert", here),
+                    _whole(weight, _FP32, n, "weight", here), _whole(counts, _I32, E, "counts", here),
+                    0 if loss is None else _whole(loss, _FP32, 1, "loss", here),
+                    0 if slope is None else _whole(slope, _FP32, E, "slope", here), row, groups,
+                    align, capacity, last_dim)
     _check("mxg_route",
            load().mxg_route(d, _any(workspace, here), 0 if workspace is None else workspace.nbytes,
                             _any(dev_status, here), _stream_on(stream, here)))
@@ -766,9 +772,9 @@ def mxg_route_backward(logits: torch.Tensor, expert: torch.Tensor, dlogits: torc
     d_at, ldd = _matrix(dlogits, logits.dtype, logits.shape, "dlogits", here)
     d = _pack_route_grad(kind, tokens, E, k, _on(logits, here), _pitch(logits, (tokens, E)),
                          _whole(expert, _I32, n, "expert", here), score, normalize, scale,
-                         _whole(dweight, _FP32, n, "dweight", here),
-                         _whole(slope, _FP32, E, "slope", here),
-                         _whole(dloss, _FP32, 1, "dloss", here), d_at, ldd)
+                         0 if dweight is None else _whole(dweight, _FP32, n, "dweight", here),
+                         0 if slope is None else _whole(slope, _FP32, E, "slope", here),
+                         0 if dloss is None else _whole(dloss, _FP32, 1, "dloss", here), d_at, ldd)
     _check("mxg_route_backward", load().mxg_route_backward(d, _stream_on(stream, here)))
 
 
@@ -788,12 +794,15 @@ def _expert_rows(fn: str, tokens, rows, row_of, weight, y_rows, dweight, counts,
     if (counts is None) != (group_ws is None):
         raise ValueError("counts and group_ws: both or neither")
     experts = 0 if counts is None else counts.numel()
-    d = _pack_expert_rows(kind, n, cols, k, experts, capacity, _on(tokens, here), _pitch(tokens, shape), rows_at,
-                          ldr, _whole(row_of, _I32, n * k, "row_of", here),
-                          _whole(weight, _FP32, n * k, "weight", here), y_at, ldy,
-                          _whole(dweight, _FP32, n * k, "dweight", here),
-                          _whole(counts, _I32, experts, "counts", here),
-                          _whole(group_ws, _I64, 2 * experts + 1, "group_ws", here))
+    at = _whole(row_of, _I32, n * k, "row_of", here)
+    w_at = 0 if weight is None else _whole(weight, _FP32, n * k, "weight", here)
+    dw_at = 0 if dweight is None else _whole(dweight, _FP32, n * k, "dweight", here)
+    c_at = g_at = 0
+    if counts is not None:
+        c_at = _whole(counts, _I32, experts, "counts", here)
+        g_at = _whole(group_ws, _I64, 2 * experts + 1, "group_ws", here)
+    d = _pack_expert_rows(kind, n, cols, k, experts, capacity, _on(tokens, here),
+                          _pitch(tokens, shape), rows_at, ldr, at, w_at, y_at, ldy, dw_at, c_at, g_at)
     _check(fn, getattr(load(), fn)(d, _stream_on(stream, here)))
 
 
@@ -833,7 +842,8 @@ def _kept(q, sf, rows: int, cols: int, parts: int, here: int) -> tuple:
     if q.dtype not in _BYTES or q.shape != (rows, parts * cols):
         raise ValueError("q: expected %s bytes: got %s of %s"
                          % ((rows, parts * cols), tuple(q.shape), q.dtype))
-    return _on(q, here), _pitch(q, (rows, parts * cols)), _whole(sf, _BYTES[:1], rows * parts * _act_blocks(cols), "sf", here)
+    return (_on(q, here), _pitch(q, (rows, parts * cols)),
+            _whole(sf, _BYTES[:1], rows * parts * _act_blocks(cols), "sf", here))
 
 
 def _act_shape(t, name: str) -> tuple:
@@ -855,7 +865,8 @@ def mxg_gated_act(gate: torch.Tensor, h: torch.Tensor, up=None, act: int = MXG_A
     h_at, ldh = _matrix(h, gate.dtype, gate.shape, "h", here)
     q_at, ldq, sf_at = _kept(q, sf, rows, cols, parts, here)
     d = _pack_gated_act(kind, act, rows, cols, parts - 1, G,
-                        _whole(group_ws, _I64, 2 * G + 1, "group_ws", here), _on(gate, here), _pitch(gate, (rows, cols)),
+                        0 if group_ws is None else _whole(group_ws, _I64, 2 * G + 1, "group_ws", here),
+                        _on(gate, here), _pitch(gate, (rows, cols)),
                         up_at, ldu, h_at, ldh, q_at, ldq, sf_at, 0, 0, 0, 0, 0, 0)
     _check("mxg_gated_act", load().mxg_gated_act(d, _stream_on(stream, here)))
 
@@ -872,7 +883,8 @@ def mxg_gated_act_backward(q: torch.Tensor, sf: torch.Tensor, dh: torch.Tensor, 
     h_at, ldh = _matrix(h, dh.dtype, dh.shape, "h", here)
     q_at, ldq, sf_at = _kept(q, sf, rows, cols, parts, here)
     d = _pack_gated_act(kind, act, rows, cols, parts - 1, G,
-                        _whole(group_ws, _I64, 2 * G + 1, "group_ws", here), 0, 0, 0, 0, h_at, ldh, q_at,
+                        0 if group_ws is None else _whole(group_ws, _I64, 2 * G + 1, "group_ws", here),
+                        0, 0, 0, 0, h_at, ldh, q_at,
                         ldq, sf_at, _on(dh, here), _pitch(dh, (rows, cols)), dgate_at, lddg, dup_at, lddu)
     _check("mxg_gated_act_backward", load().mxg_gated_act_backward(d, _stream_on(stream, here)))
 
