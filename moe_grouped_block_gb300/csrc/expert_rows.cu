@@ -46,18 +46,18 @@ struct Piece {
   // An element, or 0 where `in` is not set; without a branch, so that many can be asked for at once.
   __device__ __forceinline__ void load_if(const T* p, bool in) {
     static_assert(kElems == 1, "of single elements");
+    // (the 0 comes before the load: put behind it, it would wait for it)
     if constexpr (sizeof(T) == 4) {
+      w[0] = 0;
       asm volatile(
-          "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-          "@q ld.global.b32 %0, [%1];\n\t@!q mov.b32 %0, 0;\n\t}"
-          : "=r"(w[0])
+          "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q ld.global.b32 %0, [%1];\n\t}"
+          : "+r"(w[0])
           : "l"(p), "r"(static_cast<int>(in)));
     } else {
-      uint16_t v;
+      uint16_t v = 0;
       asm volatile(
-          "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-          "@q ld.global.b16 %0, [%1];\n\t@!q mov.b16 %0, 0;\n\t}"
-          : "=h"(v)
+          "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q ld.global.b16 %0, [%1];\n\t}"
+          : "+h"(v)
           : "l"(p), "r"(static_cast<int>(in)));
       w[0] = v;
     }
