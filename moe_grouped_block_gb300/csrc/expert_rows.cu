@@ -6,7 +6,7 @@
 //
 // All three go by tokens, so that a token's row is read (or written) once and only the k
 // rows beside it are scattered; no row is shared, so nothing is atomic.  Memory is the
-// bound: dispatching 8192 tokens of 4096 in bf16 to 2 experts each takes 33.3 us, 6.2 TB/s of the
+// bound: dispatching 8192 tokens of 4096 in bf16 to 2 experts each takes 31.8 us, 6.5 TB/s of the
 // 6.78 that a copy reaches.  Rows that do not start on 16 bytes move element by element, at
 // 30 to 55 % of that.
 #include <algorithm>
@@ -220,7 +220,7 @@ __device__ __forceinline__ void cp_async_16_or_zeros(uint32_t dst, const void* s
 // Sums of rows that start on 16 bytes.  A warp's item is a token and 1 KB of its columns, twice 16
 // bytes a lane; a lane's pieces of PER rows are a unit, and every thread has a ring of kDepth units in
 // shared memory that asynchronous copies fill ahead of the sums.  No thread reads another's
-// pieces, so there is no barrier.  4096 tokens of 8 rows of 2048 in fp16: 26.3 us, 5.7 TB/s; with the
+// pieces, so there is no barrier.  4096 tokens of 8 rows of 2048 in fp16: 25.8 us, 5.9 TB/s; with the
 // rows in registers, 4 at a time to leave room for enough warps, 38.6 us; with 16 bytes a lane the
 // instructions for a row's place were the bound, at 33.5 us.
 constexpr int kRingThreads = 128, kDepth = 4;
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 // The gradients of sums without the weights' among them, or of rows of any alignment (8192 tokens of
-// 2 rows of 4095 in bf16: 91 us).  A team of `team` warps owns a token, KA of its rows at a time and
+// 2 rows of 4095 in bf16: 88 us).  A team of `team` warps owns a token, KA of its rows at a time and
 // ACROSS pieces of each row a lane; a lane's next pieces are asked for before it works on those it
 // has.  Sums over the columns are joined in shared memory.
 template <typename T, int BYTES, int KA, int ACROSS>
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kRowThreads)
 // The gradients of sums of rows that start on 16 bytes, with the weights' among them: as the sums,
 // through rings, a unit being 1 KB of a token's gradient and of PER of its rows.  A team of `team`
 // warps owns a token.  4096 tokens of 8 rows of 2048 in bf16: 53 us, 5.3 TB/s, through registers 62
-// us; 8192 tokens of 2 rows of 4096: 56 us, 5.8 TB/s, either way.
+// us; 8192 tokens of 2 rows of 4096: 54 us, 6.1 TB/s.
 constexpr int ring_depth(int per) { return per == 8 ? 3 : 4; }
 
 // A unit's halves for a thread, as pairs.

@@ -10,9 +10,10 @@
 // multiple of 8, have a lane for each column and a warp for each block.  Each input is read once
 // and each output written once: memory is the bound.
 //
-// Forward, 16384 x 14336 in bf16 with the checkpoint: 291 us, 6.5 TB/s of the 6.78 that a copy
-// reaches (14328 columns, rows on 16 bytes: 301 us; 14335, a lane a column: 685 us).  Backward,
-// 32768 x 1408 in fp16 with h again: 73.6 us, 6.3 TB/s; 78 us without the next half's loads ahead.
+// Forward, 16384 x 14336 in bf16 with the checkpoint: 289 us, 6.55 TB/s of the 6.78 that a copy
+// reaches (14328 columns, rows on 16 bytes: 301 us; 14335, a lane a column: 683 us).  Backward,
+// 32768 x 1408 in fp16 with h again: 70.5 us, 6.6 TB/s; 5 us more without the next half's loads
+// ahead.
 #include <algorithm>
 
 #include "elem.cuh"

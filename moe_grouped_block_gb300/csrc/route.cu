@@ -19,9 +19,9 @@
 //
 // Instructions and the latency of dependent steps are the bound, not memory: 65536 tokens
 // to 8 of 256 experts (fp32, sigmoids, with the loss and the rows) take 40 us, 1.8 TB/s: 29 in the
-// first kernel, 280 instructions a token, and 6 in the second.  16384 tokens to 8 of 64: 11.7
-// us, half of it the second kernel and the step between the two.  8 tokens to 2 of 8: 6.3 us, one CTA.
-// The gradient of the former: 31.4 us, 4.4 TB/s of the 6.78 that a copy reaches.
+// first kernel, 280 instructions a token, and 6 in the second.  16384 tokens to 8 of 64: 11.3
+// us, half of it the second kernel and the step between the two.  8 tokens to 2 of 8: 6.0 us, one CTA.
+// The gradient of the first: 29 us, 4.8 TB/s of the 6.78 that a copy reaches.
 #include <algorithm>
 #include <type_traits>
 
