@@ -436,6 +436,36 @@ def test_large_batch():
     check_gradient(x[:100000], k, balance=0.1)
 
 
+def test_past_32_bits_of_logits():
+    T, E, k = (1 << 21) + 77, 1024, 2
+    x = torch.empty(T, E, dtype=BF, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(19)
+    for part in x.split(1 << 19):
+        part.normal_(generator=gen)
+    got = route(x, k, balance=0.1)
+    order = got["row_of"].view(-1).long().argsort()
+    assert torch.equal(got["row_of"].view(-1).long().sort().values, torch.arange(T * k, device=DEV))
+    flat = got["expert"].view(-1)[order]
+    assert (flat[1:] >= flat[:-1]).all()  # sorted by expert, and within one by token
+    same = flat[1:] == flat[:-1]
+    assert (order[1:][same] > order[:-1][same]).all()
+    d = torch.empty_like(x)
+    dw = torch.randn(T, k, generator=gen, device=DEV)
+    mxg.mxg_route_backward(x, got["expert"], d, dweight=dw, normalize=False)
+    for rows in (slice(0, 50), slice(T // 2, T // 2 + 50), slice(T - 50, T)):
+        want = exact(x[rows], k)
+        assert torch.equal(got["expert"][rows].cpu().long(), want["expert"])
+        p = torch.softmax(x[rows].double(), 1)
+        at, g = got["expert"][rows].long(), dw[rows].double()
+        chosen = p.gather(1, at)
+        ref = -p * (g * chosen).sum(1, keepdim=True)
+        ref = ref.scatter_add(1, at, g * chosen)
+        size = p * (g.abs() * chosen).sum(1, keepdim=True)
+        size = size.scatter_add(1, at, g.abs() * chosen)
+        tol = 3 * want["rel"] * size + U[BF] * ref.abs() + TINY * 8
+        assert not ((d[rows].double() - ref).abs() > tol).any()
+
+
 def test_refusals():
     x = draw(10, 8, F32, 18)
     i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device=DEV)  # noqa: E731

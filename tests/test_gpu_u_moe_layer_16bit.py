@@ -224,3 +224,32 @@ def test_calls_one_after_the_other(example, tokens):
         mxg.mxg_dispatch(a, back.contiguous(), rows)
         mxg.mxg_combine(rows, t, a)
     assert torch.equal(a, want)
+
+
+def test_captured_behind_copies_and_other_streams():
+    """In a graph, a call behind a copy, behind a fill, and behind two streams that meet."""
+    from gpu_util import DEV
+    from moe_grouped_block_gb300 import mxg
+    n, D = 3000, 512
+    at = torch.randperm(n, generator=torch.Generator().manual_seed(6)).to(torch.int32)[:, None].to(DEV)
+    src = torch.randn(n, D, generator=torch.Generator(device=DEV).manual_seed(7), device=DEV)
+    x, rows, y = torch.zeros(n, D, device=DEV), torch.zeros(n, D, device=DEV), torch.zeros(n, D, device=DEV)
+    other, z = torch.zeros(n, D, device=DEV), torch.zeros(n, D, device=DEV)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        x.copy_(src)
+        mxg.mxg_dispatch(x, at, rows)  # behind a copy
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            other.zero_()
+            mxg.mxg_dispatch(src, at, other)  # behind a fill
+        mxg.mxg_combine(rows, at, y)
+        here.wait_stream(side)
+        mxg.mxg_combine(other, at, z)  # behind both streams
+        x.zero_()
+    for i in range(5):
+        src.mul_(1.5)
+        rows.fill_(7.0), y.fill_(7.0), z.fill_(7.0)
+        graph.replay()
+        assert torch.equal(y, src) and torch.equal(z, src) and (x == 0).all()
