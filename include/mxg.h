@@ -612,7 +612,8 @@ size_t mxg_route_workspace_bytes(int64_t tokens, int experts, int k);
 
 /* Errors: INVALID_ARG (nulls, sizes, types, ld < experts, last_dim < 1, or
  * rows_capacity * last_dim beyond int64), ALIGNMENT (a pointer not aligned to
- * its element, workspace), WORKSPACE_TOO_SMALL, UNSUPPORTED_ARCH, LAUNCH. */
+ * its element, workspace, dev_status), WORKSPACE_TOO_SMALL, UNSUPPORTED_ARCH,
+ * LAUNCH. */
 mxg_status_t mxg_route(const mxg_route_t* desc, void* workspace, size_t workspace_bytes,
                        int32_t* dev_status, mxg_stream_t stream);
 

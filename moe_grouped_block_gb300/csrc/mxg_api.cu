@@ -232,10 +232,11 @@ mxg_status_t route_rows_args(int64_t tokens, const int32_t* counts, const int32_
   return MXG_OK;
 }
 
-mxg_status_t route_workspace(int64_t tokens, int experts, int k, const void* workspace,
-                             size_t workspace_bytes) {
+// The workspace, and the word that a kernel's atomics may write.
+mxg_status_t route_memory(int64_t tokens, int experts, int k, const void* workspace,
+                          size_t workspace_bytes, const int32_t* dev_status) {
   if (workspace == nullptr) return MXG_ERR_INVALID_ARG;
-  if (!aligned16(workspace)) return MXG_ERR_ALIGNMENT;
+  if (!aligned16(workspace) || !aligned_to(dev_status, 4)) return MXG_ERR_ALIGNMENT;
   return workspace_bytes < mxg::route_ws_bytes(tokens, experts, k) ? MXG_ERR_WORKSPACE_TOO_SMALL
                                                                    : MXG_OK;
 }
@@ -733,8 +734,8 @@ mxg_status_t mxg_route(const mxg_route_t* desc, void* workspace, size_t workspac
   if (!aligned_to(d.logits, size) || !aligned_to(d.expert, 4) || !aligned_to(d.weight, 4) ||
       !aligned_to(d.loss, 4) || !aligned_to(d.slope, 4))
     return MXG_ERR_ALIGNMENT;
-  if ((st = route_workspace(d.tokens, d.experts, d.k, workspace, workspace_bytes)) != MXG_OK)
-    return st;
+  st = route_memory(d.tokens, d.experts, d.k, workspace, workspace_bytes, dev_status);
+  if (st != MXG_OK) return st;
   int sms = 0;
   if ((st = current_device(&sms)) != MXG_OK) return st;
   int launches = 0;
@@ -753,7 +754,8 @@ mxg_status_t mxg_route_rows(const int32_t* expert, int64_t tokens, int experts, 
       route_rows_args(tokens, counts, row_of, group_ws, align, rows_capacity, last_dim);
   if (st != MXG_OK) return st;
   if (!aligned_to(expert, 4)) return MXG_ERR_ALIGNMENT;
-  if ((st = route_workspace(tokens, experts, k, workspace, workspace_bytes)) != MXG_OK) return st;
+  st = route_memory(tokens, experts, k, workspace, workspace_bytes, dev_status);
+  if (st != MXG_OK) return st;
   int sms = 0;
   if ((st = current_device(&sms)) != MXG_OK) return st;
   int launches = 0;
