@@ -673,10 +673,22 @@ def _matrix(t, dtype, shape, name: str, here: int) -> tuple:
     return _on(t, here), _pitch(t, shape)
 
 
-def _any(t, here: int) -> int:
-    """The address of a device tensor (or the number that is given for one); 0 of none."""
+def _workspace(t, here: int) -> tuple:
+    """(address, bytes) of a workspace; zeros of none."""
+    if t is None:
+        return 0, 0
+    if not t.is_contiguous():  # its bytes are not those from its address on
+        raise ValueError("a workspace must be contiguous: got strides %s" % (t.stride(),))
+    return _on(t, here), t.nbytes
+
+
+def _status(t, here: int) -> int:
+    """The address of a status word (or the number that is given for one); 0 of none."""
     if t is None or isinstance(t, int):
         return t or 0
+    if t.dtype is not torch.int32 or t.numel() < 1:
+        raise ValueError("dev_status: expected an int32 word: got %s of %s"
+                         % (tuple(t.shape), t.dtype))
     return _on(t, here)
 
 
@@ -740,9 +752,9 @@ def mxg_route(logits: torch.Tensor, expert: torch.Tensor, weight: torch.Tensor,
                     0 if loss is None else _whole(loss, _FP32, 1, "loss", here),
                     0 if slope is None else _whole(slope, _FP32, E, "slope", here), row, groups,
                     align, capacity, last_dim)
+    ws, ws_bytes = _workspace(workspace, here)
     _check("mxg_route",
-           load().mxg_route(d, _any(workspace, here), 0 if workspace is None else workspace.nbytes,
-                            _any(dev_status, here), _stream_on(stream, here)))
+           load().mxg_route(d, ws, ws_bytes, _status(dev_status, here), _stream_on(stream, here)))
 
 
 def mxg_route_rows(expert: torch.Tensor, counts: torch.Tensor, row_of=None, group_ws=None,
@@ -753,12 +765,12 @@ def mxg_route_rows(expert: torch.Tensor, counts: torch.Tensor, row_of=None, grou
     tokens, k = _choices(expert, "expert")
     E, n = counts.numel(), tokens * k
     row, groups, capacity = _rows_wanted(row_of, group_ws, n, E, align, rows_capacity, here)
+    ws, ws_bytes = _workspace(workspace, here)
     _check("mxg_route_rows",
            load().mxg_route_rows(_whole(expert, _I32, n, "expert", here), tokens, E, k, align,
                                  capacity, last_dim, _whole(counts, _I32, E, "counts", here), row,
-                                 groups, _any(workspace, here),
-                                 0 if workspace is None else workspace.nbytes,
-                                 _any(dev_status, here), _stream_on(stream, here)))
+                                 groups, ws, ws_bytes, _status(dev_status, here),
+                                 _stream_on(stream, here)))
 
 
 def mxg_route_backward(logits: torch.Tensor, expert: torch.Tensor, dlogits: torch.Tensor,
