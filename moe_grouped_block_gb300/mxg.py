@@ -240,6 +240,21 @@ def _p(t) -> int | None:
     return t.data_ptr()
 
 
+def _word(t) -> int | None:
+    """A status word: kernels write four bytes on a boundary of four."""
+    if isinstance(t, torch.Tensor) and (t.itemsize < 4 or t.numel() < 1):
+        raise ValueError("dev_status: expected an int32 word: got %s of %s"
+                         % (tuple(t.shape), t.dtype))
+    return _p(t)
+
+
+def _dense(workspace):
+    """A workspace whose bytes are those from its address on."""
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("a workspace must be contiguous: got strides %s" % (workspace.stride(),))
+    return workspace
+
+
 # the handle alone of the current stream of a device: making the Stream object
 # costs 6 us, as much as the rest of a call
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -268,7 +283,7 @@ def mxg_group_offsets(sizes: torch.Tensor, multiplier: int, last_dim: int, rows_
     assert sizes.dtype in (torch.int32, torch.int64) and ws.dtype == torch.int64
     _check("mxg_group_offsets",
            load().mxg_group_offsets(_p(sizes), 1 if sizes.dtype == torch.int64 else 0, sizes.numel(),
-                                    multiplier, last_dim, rows_capacity, _p(ws), _p(dev_status),
+                                    multiplier, last_dim, rows_capacity, _p(ws), _word(dev_status),
                                     _s(stream)))
 
 
@@ -280,7 +295,7 @@ def mxg_group_quantize(fmt: int, layout: int, x: torch.Tensor, rows_capacity: in
     _check("mxg_group_quantize",
            load().mxg_group_quantize(fmt, layout, _p(x), rows_capacity, cols, _p(group_ws), G,
                                      _p(q_row), _p(sf_row), _p(q_col), _p(sf_col), _p(outer_row),
-                                     _p(outer_col), _p(dev_status), _s(stream)))
+                                     _p(outer_col), _word(dev_status), _s(stream)))
 
 
 def mxg_grouped_gemm(fmt: int, mode: int, A: tuple, B: tuple, group_ws: torch.Tensor, G: int,
@@ -294,7 +309,7 @@ def mxg_grouped_gemm(fmt: int, mode: int, A: tuple, B: tuple, group_ws: torch.Te
            load().mxg_grouped_gemm(fmt, mode, ctypes.byref(a), ctypes.byref(b), _p(group_ws), G,
                                    M_cap, N, K, _p(alpha), _p(beta), _p(bias), _p(C), out_type,
                                    _p(workspace),
-                                   workspace_bytes, _p(dev_status), _s(stream)))
+                                   workspace_bytes, _word(dev_status), _s(stream)))
 
 
 def mxg_grouped_gemm_debug(fmt: int, mode: int, A: tuple, B: tuple, group_ws, G: int, M_cap: int,
@@ -307,7 +322,7 @@ def mxg_grouped_gemm_debug(fmt: int, mode: int, A: tuple, B: tuple, group_ws, G:
     _check("mxg_grouped_gemm_debug",
            load().mxg_grouped_gemm_debug(fmt, mode, ctypes.byref(a), ctypes.byref(b), _p(group_ws),
                                          G, M_cap, N, K, _p(alpha), _p(beta), _p(bias), _p(C),
-                                         out_type, _p(dev_status), tile_n, stage_bytes,
+                                         out_type, _word(dev_status), tile_n, stage_bytes,
                                          inject_flags, wait_timeout_ns, _s(stream)))
 
 
@@ -333,7 +348,7 @@ def mxg_group_offsets_unaligned(sizes: torch.Tensor, multiplier: int, last_dim: 
     _check("mxg_group_offsets_unaligned",
            load().mxg_group_offsets_unaligned(_p(sizes), 1 if sizes.dtype == torch.int64 else 0,
                                               sizes.numel(), multiplier, last_dim, rows_capacity,
-                                              _p(ws), _p(dev_status), _s(stream)))
+                                              _p(ws), _word(dev_status), _s(stream)))
 
 
 def mxg_group_quantize_unaligned(layout: int, x: torch.Tensor, rows_capacity: int, cols: int,
@@ -343,7 +358,7 @@ def mxg_group_quantize_unaligned(layout: int, x: torch.Tensor, rows_capacity: in
     _check("mxg_group_quantize_unaligned",
            load().mxg_group_quantize_unaligned(layout, _p(x), rows_capacity, cols, _p(group_ws), G,
                                                _p(q_row), _p(sf_row), _p(q_col), _p(sf_col),
-                                               _p(dev_status), _s(stream)))
+                                               _word(dev_status), _s(stream)))
 
 
 def mxg_grouped_gemm_unaligned(mode: int, A: tuple, B: tuple, group_ws: torch.Tensor, G: int,
@@ -355,7 +370,7 @@ def mxg_grouped_gemm_unaligned(mode: int, A: tuple, B: tuple, group_ws: torch.Te
     _check("mxg_grouped_gemm_unaligned",
            load().mxg_grouped_gemm_unaligned(mode, ctypes.byref(a), ctypes.byref(b), _p(group_ws),
                                              G, M_cap, N, K, _p(alpha), _p(beta), _p(bias), _p(C),
-                                             out_type, _p(dev_status), _s(stream)))
+                                             out_type, _word(dev_status), _s(stream)))
 
 
 # ------------------------------------------------ 16-bit operators of an expert block
@@ -470,7 +485,7 @@ def mxg_grouped_gemm_16bit(mode: int, A: torch.Tensor, B: torch.Tensor, group_ws
     _check("mxg_grouped_gemm_16bit",
            load().mxg_grouped_gemm_16bit(kind, mode, _p(A), lda, _p(B), ldb, _p(group_ws), G,
                                          M_cap, N, K, _p(alpha), _p(beta), _p(C), ldc, out,
-                                         _p(dev_status), _s(stream)))
+                                         _word(dev_status), _s(stream)))
 
 
 def _same_type(tensors) -> int:
@@ -559,7 +574,7 @@ def mxg_block_norm_backward(x: torch.Tensor, y=None, w_post=None, gate=None,
                       _ld(dx_out), _p(dn), _ld(dn), _p(dx), _ld(dx), _p(dy), _ld(dy), _p(dw_post),
                       _p(dw_pre), _p(dgate), _ld(dgate) if full else 0)
     _check("mxg_block_norm_backward",
-           load().mxg_block_norm_backward(ctypes.byref(d), _p(workspace),
+           load().mxg_block_norm_backward(ctypes.byref(d), _p(_dense(workspace)),
                                           0 if workspace is None else workspace.nbytes, _s(stream)))
 
 
@@ -596,7 +611,7 @@ def mxg_grad_norm(grads: GradList, norm: torch.Tensor, workspace: torch.Tensor,
                   stream=None) -> None:
     assert norm.dtype == torch.float32
     _check("mxg_grad_norm",
-           load().mxg_grad_norm(grads.address, grads.n, _p(norm), _p(workspace),
+           load().mxg_grad_norm(grads.address, grads.n, _p(norm), _p(_dense(workspace)),
                                 workspace.nbytes, _s(stream)))
 
 
@@ -604,7 +619,7 @@ def mxg_grad_clip(grads: GradList, max_norm: float, norm: torch.Tensor, workspac
                   stream=None) -> None:
     assert norm.dtype == torch.float32
     _check("mxg_grad_clip",
-           load().mxg_grad_clip(grads.address, grads.n, max_norm, _p(norm), _p(workspace),
+           load().mxg_grad_clip(grads.address, grads.n, max_norm, _p(norm), _p(_dense(workspace)),
                                 workspace.nbytes, _s(stream)))
 
 
@@ -677,9 +692,7 @@ def _workspace(t, here: int) -> tuple:
     """(address, bytes) of a workspace; zeros of none."""
     if t is None:
         return 0, 0
-    if not t.is_contiguous():  # its bytes are not those from its address on
-        raise ValueError("a workspace must be contiguous: got strides %s" % (t.stride(),))
-    return _on(t, here), t.nbytes
+    return _on(_dense(t), here), t.nbytes
 
 
 def _status(t, here: int) -> int:
