@@ -813,7 +813,9 @@ def _expert_rows(fn: str, tokens, rows, row_of, weight, y_rows, dweight, counts,
         raise ValueError("expected [%d, cols] of fp32, bf16 or fp16: got %s of %s"
                          % (n, tuple(shape), dtype))
     cols, like = shape[1], y_rows if rows is None else rows
-    capacity = 0 if like is None else like.shape[0]
+    if like is None:
+        raise ValueError("%s: no rows are given" % fn)
+    capacity = like.shape[0]
     rows_at, ldr = _matrix(rows, dtype, (capacity, cols), "rows", here)
     y_at, ldy = _matrix(y_rows, dtype, (capacity, cols), "y_rows", here)
     if (counts is None) != (group_ws is None):
