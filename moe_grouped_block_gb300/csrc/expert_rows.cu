@@ -391,20 +391,22 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-// The gradients of sums without the weights' among them, or of rows of any alignment (8192 tokens of
-// 2 rows of 4095 in bf16: 88 us).  A team of `team` warps owns a token, KA of its rows at a time and
-// ACROSS pieces of each row a lane; a lane's next pieces are asked for before it works on those it
-// has.  Sums over the columns are joined in shared memory.
-template <typename T, int BYTES, int KA, int ACROSS>
+// The gradients of sums of rows, without the weights' or (DOTS, rows of any alignment alone) with them.
+// 8192 tokens of 2 rows of 4096 in bf16, rows alone: 37 us, 5.4 TB/s; of 4095, both: 90 us.  A team of
+// `team` warps owns a token, KA of its rows at a time and ACROSS pieces of each row a lane; a lane's next
+// pieces are asked for before it works on those it has.  Sums over the columns are joined in shared
+// memory.  (With the sums tested for when run, registers of both: 41 us for the rows alone.)
+template <typename T, int BYTES, int KA, int ACROSS, bool DOTS>
 __global__ void __launch_bounds__(kRowThreads)
     combine_backward_kernel(const mxg_expert_rows_t d, int team, int64_t pad_items) {
   using P = Piece<T, BYTES>;
   constexpr int kElems = P::kElems, kSpan = 32 * kElems;
   constexpr int kWarps = kRowThreads / 32;
-  __shared__ float part[kWarps][32];
+  static_assert(!DOTS || kElems == 1, "rows on 16 bytes and their weights: by rings");
+  __shared__ float part[DOTS ? kWarps : 1][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, teams = kWarps / team;
   const int place = warp % team;  // in the team
-  const bool dots = d.dweight != nullptr, writes = d.rows != nullptr;
+  const bool writes = !DOTS || d.rows != nullptr;
   grid_wait_for_previous();
   grid_launch_dependents();
   const int64_t pad_blocks = (pad_items + kWarps - 1) / kWarps;
@@ -439,7 +441,7 @@ __global__ void __launch_bounds__(kRowThreads)
         dot[j] = 0.0f;
       }
       struct Pieces {
-        P x[ACROSS], y[ACROSS][KA];
+        P x[ACROSS], y[DOTS ? ACROSS : 1][DOTS ? KA : 1];
       };
       auto fetch = [&](Pieces& p, int c) {
 #pragma unroll
@@ -448,14 +450,13 @@ __global__ void __launch_bounds__(kRowThreads)
           const bool in = on && at_c + kElems <= cols;
           if constexpr (kElems == 1) {
             p.x[i].load_if(dy + at_c, in);
+            if constexpr (DOTS) {
 #pragma unroll
-            for (int j = 0; j < KA; ++j)
-              p.y[i][j].load_if(y_rows + r[j] * d.ldy + at_c, in && dots && r[j] >= 0);
+              for (int j = 0; j < KA; ++j)
+                p.y[i][j].load_if(y_rows + r[j] * d.ldy + at_c, in && r[j] >= 0);
+            }
           } else if (in) {
             p.x[i].load(dy + at_c);
-#pragma unroll
-            for (int j = 0; j < KA; ++j)
-              if (dots && r[j] >= 0) p.y[i][j].load(y_rows + r[j] * d.ldy + at_c);
           }
         }
       };
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(kRowThreads)
           for (int j = 0; j < KA; ++j) {
             if (r[j] < 0) continue;
             float f[kElems];
-            if (dots) {
+            if constexpr (DOTS) {
               now.y[i][j].get(f);
 #pragma unroll
               for (int e = 0; e < kElems; ++e) dot[j] = fmaf(g[e], f[e], dot[j]);
@@ -497,11 +498,10 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
         for (int j = 0; j < KA; ++j) {
           if (r[j] < 0) continue;
-          if (dots) dot[j] = fmaf(g, to_f32(y_rows[r[j] * d.ldy + e]), dot[j]);
-          if (writes) rows[r[j] * d.ldr + e] = from_f32<T>(wj[j] * g);
+          rows[r[j] * d.ldr + e] = from_f32<T>(wj[j] * g);
         }
       }
-      if (dots) {
+      if constexpr (DOTS) {
 #pragma unroll
         for (int j = 0; j < KA; ++j) {
           float v = dot[j];
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kRowThreads)
         }
       }
     }
-    if (dots) {
+    if constexpr (DOTS) {
       if (team > 1) {
         part[warp][lane] = dot_mine;
         __syncthreads();
@@ -798,14 +798,20 @@ cudaError_t run(const mxg_expert_rows_t& d, int op, int num_sms, cudaStream_t st
     // more warps a token where the tokens alone do not fill the device
     int team = 1;
     while (team < 8 && d.n * team < num_sms * 48LL && team * kSpan < d.cols) team *= 2;
-    // (two waves of them: 56 us for 8192 tokens of 2 rows of 4096 in bf16, 58 with a CTA for each 8)
-    const unsigned grid = grid_for(pad + d.n * team, num_sms, 4);
+    // CTAs an SM: without the weights 8 (4096 tokens of 8 rows of 2048 in fp32: 54 us, 61 with 4; in
+    // bf16 28.5 and 28.3), with them 4 (8192 tokens of 2 rows of 4095 in bf16: 90 us, 91.5 with 8)
+    const unsigned grid = grid_for(pad + d.n * team, num_sms, d.dweight != nullptr ? 4 : 8);
     constexpr int kAcrossOf2 = BYTES < 16 ? 4 : 1, kAcrossOf4 = BYTES < 16 ? 2 : 1;
-    if (d.k <= 2)
-      return launch_after(true, combine_backward_kernel<T, BYTES, 2, kAcrossOf2>, grid, kRowThreads, 0,
-                          stream, d, team, pad);
-    return launch_after(true, combine_backward_kernel<T, BYTES, 4, kAcrossOf4>, grid, kRowThreads, 0,
-                        stream, d, team, pad);
+    auto launch = [&](auto kern) {
+      return launch_after(true, kern, grid, kRowThreads, 0, stream, d, team, pad);
+    };
+    if constexpr (BYTES < 16) {
+      if (d.dweight != nullptr)
+        return d.k <= 2 ? launch(combine_backward_kernel<T, BYTES, 2, kAcrossOf2, true>)
+                        : launch(combine_backward_kernel<T, BYTES, 4, kAcrossOf4, true>);
+    }
+    return d.k <= 2 ? launch(combine_backward_kernel<T, BYTES, 2, kAcrossOf2, false>)
+                    : launch(combine_backward_kernel<T, BYTES, 4, kAcrossOf4, false>);
   }
 }
 
