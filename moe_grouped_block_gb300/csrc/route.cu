@@ -694,7 +694,8 @@ __global__ void __launch_bounds__(NT)
     route_kernel(const mxg_route_t d, const RowPlan p, const RouteWs ws, int vec) {
   constexpr int kTeams = NT / LPT, kWarps = NT / 32;
   constexpr int kBuf = ONE ? kBufWords / 2 : kBufWords;
-  constexpr bool kRank = LPT >= 8 || (LPT == 4 && KPL > 1);  // room for the teams' slots
+  // room for the teams' slots; many CTAs take 8 columns by 16 lanes for more than 8 of the experts alone
+  constexpr bool kRank = (LPT >= 8 && (ONE || LPT != 16 || VPL != 8)) || (LPT == 4 && KPL > 1);
   constexpr bool kAhead = VPL <= 16;  // registers for the next row
   static_assert(!kRank || kWarps * kMost * (32 / LPT) * 2 <= kBuf, "slots of every team");
   __shared__ RouteShared<kBuf> sh;
