@@ -555,7 +555,9 @@ typedef enum { MXG_SCORE_SOFTMAX = 0, MXG_SCORE_SIGMOID = 1 } mxg_score_t;
  *   mask   : uint8 [tokens], 0 for a token that takes no part (padding), or NULL
  * For each token the k experts of the largest logits, in falling order; the
  * lower expert first where logits are equal (-0 equals 0), NaN above infinity.
- * A logit of -infinity is never chosen.
+ * A logit of -infinity is never chosen.  The logits alone decide: a router that
+ * chooses by them and a bias per expert, and weighs without it, chooses elsewhere
+ * and takes mxg_route_rows.
  *   expert : int32 [tokens, k]; -1 where there is none: a masked token, a
  *            token whose logits are all -infinity (it counts as masked), or
  *            less than k logits above -infinity
@@ -582,8 +584,12 @@ typedef enum { MXG_SCORE_SOFTMAX = 0, MXG_SCORE_SIGMOID = 1 } mxg_score_t;
  * experts * (align - 1) rows always suffice.
  * 1 <= experts <= 1024, 1 <= k <= min(experts, 32), tokens >= 0 and tokens * k
  * and rows_capacity up to 2^31 - 128; scale and balance finite.  Sums are FP32
- * and of a fixed order.  Any element alignment; logits whose rows start on 16
- * bytes with experts a multiple of 8 take 16-byte accesses. */
+ * and of a fixed order; the loss's adds no more than tokens / 1216 + 256 terms
+ * one after the other.  Exponentials, of the differences of logits (sigmoid: of
+ * logits), are off by at most 2 + 1.7 |difference| units of 2^-23, a score by
+ * about twice that; a score, weight or share below 2^-126 may be 0.  Any element
+ * alignment; logits whose rows start on 16 bytes with experts a multiple of 8
+ * take 16-byte accesses. */
 typedef struct {
   mxg_dtype_t dtype;
   int64_t tokens;
@@ -713,7 +719,9 @@ typedef enum { MXG_ACT_SILU = 0, MXG_ACT_GELU_TANH = 1 } mxg_act_t;
 
 /* Forward (mxg_gated_act): h = act(gate) . up, all [rows, cols] of dtype
  * (MXG_BF16 or MXG_F16), ld* elements between rows (0: dense); without up h =
- * act(gate).  FP32 inside, h rounded once.  Where q and sf are given, the inputs
+ * act(gate).  FP32 inside, h rounded once; the exponential is off by at most 2 +
+ * 1.2 |z| units of 2^-23, and where sigmoid(z) is below 2^-126 (z below about
+ * -87.3) it counts as 0, in both directions.  Where q and sf are given, the inputs
  * are kept in 8 bits for the backward pass:
  *   q  : E4M3 [rows, cols] of gate and, beside it in the same row from column
  *        cols on, of up; ldq bytes between rows (0: cols, or 2 cols with up)

@@ -18,10 +18,12 @@
 // atomics and no counters kept between calls.
 //
 // Instructions and the latency of dependent steps are the bound, not memory: 65536 tokens
-// to 8 of 256 experts (fp32, sigmoids, with the loss and the rows) take 40 us, 1.8 TB/s: 29 in the
-// first kernel, 280 instructions a token, and 6 in the second.  16384 tokens to 8 of 64: 11.3
-// us, half of it the second kernel and the step between the two.  8 tokens to 2 of 8: 6.0 us, one CTA.
-// The gradient of the first: 29 us, 4.8 TB/s of the 6.78 that a copy reaches.
+// to 8 of 256 experts (fp32, sigmoids, with the loss and the rows) take 39.5 us, 1.9 TB/s: 30 in the
+// first kernel (alone), 281 instructions a token, and the rest in the second.  4 of those are a second
+// wave: with 152 chunks its 153 CTAs, of an SM's whole register file each, do not fit 152 SMs at once,
+// and the last one starts when another has ended (35.1 us with 151 chunks).  16384 tokens to 8 of 64:
+// 11.3 us, 128 chunks, half of it the second kernel and the step between the two.  8 tokens to 2 of 8:
+// 5.9 us, one CTA.  The gradient of the first: 29 us, 4.8 TB/s of the 6.78 that a copy reaches.
 #include <algorithm>
 #include <type_traits>
 
@@ -31,7 +33,7 @@
 namespace mxg {
 
 constexpr int kMaxExperts = 1024;
-constexpr int kMaxChunks = 152;  // a CTA an SM
+constexpr int kMaxChunks = 152;  // a CTA an SM (of the first kernel; the second has one more)
 constexpr uint32_t kNoLogit = 0x007FFFFFu;  // the key of -infinity: it and all below are not chosen
 constexpr int kOneItems = 4096;  // choices of a batch that one CTA finishes
 
@@ -688,7 +690,9 @@ __device__ __forceinline__ Chosen<KPL> choose_by_rank(const float (&v)[VPL], con
   return c;
 }
 
-// KPL * LPT >= k; KPL > 1 in the kernels of few lanes a token.
+// KPL * LPT >= k; KPL > 1 in the kernels of few lanes a token.  With 32 columns a lane the 128
+// registers of 512 threads are just too few: 4 lanes a token put 28 to 136 bytes a thread on the stack,
+// 8 and 16 lanes 12 to 88 (16-bit logits alone).
 template <typename T, int LPT, int VPL, int KPL, int NT, bool ONE>
 __global__ void __launch_bounds__(NT)
     route_kernel(const mxg_route_t d, const RowPlan p, const RouteWs ws, int vec) {
@@ -855,6 +859,9 @@ __device__ __forceinline__ int halves_at(int c, int n) {
   return (c >> 3) * 4 + (c & 3) + ((c & 4) != 0 ? n / 2 : 0);
 }
 
+// CTAs an SM: four, which 64 registers a thread allow.  Lanes of 8 or 4 choices put 44 to 164 bytes of
+// theirs on the stack for it (32 experts or fewer); with two CTAs and 12 bytes there at most, 65536
+// tokens took 3.0 and not 3.6 us (2 of 8, bf16), 4.3 and not 5.5 (4 of 16), but 8.4 and not 7.7 (8 of 32).
 template <typename T, int LPT, int VPL, int KPL>
 __global__ void __launch_bounds__(kGradThreads, VPL <= 16 ? 4 : 1)
     route_backward_kernel(const mxg_route_grad_t d, int vec) {
@@ -1158,7 +1165,7 @@ cudaError_t backward_typed(const mxg_route_grad_t& d, int num_sms, cudaStream_t 
   const int vec = d.experts % 8 == 0 && rows_of_16(d.logits, d.ld, sizeof(T)) &&
                   rows_of_16(d.dlogits, d.ldd, sizeof(T));
   if (d.k <= 8 && d.experts <= 256) {
-    // (16 columns a lane: more warps an SM than with 32, 36 against 45 us for 65536 x 256 in fp32)
+    // (16 columns a lane: more warps an SM than with 32, 29.3 against 32.3 us for 65536 x 256 in fp32)
     if (d.experts <= 8) return run_backward<T, 1, 8, 8>(d, vec, num_sms, stream);
     if (d.experts <= 16) return run_backward<T, 1, 16, 8>(d, vec, num_sms, stream);
     if (d.experts <= 32) return run_backward<T, 2, 16, 4>(d, vec, num_sms, stream);
