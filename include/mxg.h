@@ -612,8 +612,9 @@ typedef struct {
 } mxg_route_t;
 
 /* Bytes of the workspace of mxg_route and mxg_route_rows (0 for sizes that they
- * refuse); 16-byte aligned device memory whose contents mean nothing before or
- * after the call. */
+ * refuse), which grow with the tokens: that of the largest batch serves smaller
+ * ones.  16-byte aligned device memory whose contents mean nothing before or after
+ * the call. */
 size_t mxg_route_workspace_bytes(int64_t tokens, int experts, int k);
 
 /* Errors: INVALID_ARG (nulls, sizes, types, ld < experts, last_dim < 1, or

@@ -1043,6 +1043,7 @@ bool few_serve(int experts, int k) { return k <= 8 && experts <= 512; }
 struct Chunks {
   int n;
   int64_t per;  // tokens each
+  int room;     // no fewer than a smaller batch has: tokens rounded up a chunk can leave n below that
 };
 
 Chunks cut(int64_t tokens, int64_t pass) {
@@ -1050,6 +1051,7 @@ Chunks cut(int64_t tokens, int64_t pass) {
   Chunks c;
   c.per = (tokens + n - 1) / n;
   c.n = static_cast<int>(std::max<int64_t>(2, (tokens + c.per - 1) / c.per));
+  c.room = static_cast<int>(std::max<int64_t>(2, n));
   return c;
 }
 
@@ -1058,14 +1060,14 @@ Chunks cut(int64_t tokens, int64_t pass) {
 Chunks chunks_of(int64_t tokens, int experts, int k) {
   const Shape one = many_lanes(experts, k);
   if (tokens <= 2 * (threads_of(one.lpt, one.vpl, true) / one.lpt) && tokens * k <= kOneItems)
-    return {1, std::max<int64_t>(1, tokens)};
+    return {1, std::max<int64_t>(1, tokens), 1};
   const Shape s = few_serve(experts, k) ? few_lanes(experts) : one;
   return cut(tokens, threads_of(s.lpt, s.vpl, false) / s.lpt);
 }
 
 // For choices made elsewhere, each counted as a token with one.
 Chunks chunks_of_choices(int64_t choices) {
-  if (choices <= 4 * kOneThreads) return {1, std::max<int64_t>(1, choices)};
+  if (choices <= 4 * kOneThreads) return {1, std::max<int64_t>(1, choices), 1};
   return cut(choices, kManyThreads);
 }
 
@@ -1182,8 +1184,9 @@ cudaError_t backward_typed(const mxg_route_grad_t& d, int num_sms, cudaStream_t 
 
 }  // namespace
 
+// Grows with the tokens, so that what is made for the largest batch serves them all.
 size_t route_ws_bytes(int64_t tokens, int experts, int k) {
-  const int64_t n = std::max(chunks_of(tokens, experts, k).n, chunks_of_choices(tokens * k).n);
+  const int64_t n = std::max(chunks_of(tokens, experts, k).room, chunks_of_choices(tokens * k).room);
   return n == 1 ? 16 : static_cast<size_t>((n * (2 * pitch_of(experts) + 1) * 4 + 15) / 16 * 16);
 }
 
